@@ -81,7 +81,11 @@ extern "C" {
 #define SV_ERR_INTERNAL 25          /* an internal capacity invariant failed     */
 #define SV_ERR_DATA_ACCEPT 26       /* KV commit: accept length above k_b         */
 #define SV_ERR_DATA_PAGE 27         /* KV commit: a destination page missing from */
-                                    /* the block table, or a negative kv_len      */
+                                    /* the block table, or a negative kv_len;     */
+                                    /* attention, eviction: a page of the request */
+                                    /* missing from its block table               */
+#define SV_ERR_DATA_LENGTH 28       /* attention, eviction: kv_len negative or    */
+                                    /* longer than the block table or the scores  */
 
 /* ---- limits -------------------------------------------------------------- */
 #define SV_MAX_K 32              /* drafts per request (one warp ballot)       */
@@ -89,8 +93,10 @@ extern "C" {
                                  /* (spec_verify_dump_rows); larger top-k and   */
                                  /* top-p alone keep a threshold instead        */
 #define SV_VOCAB_MAX (1 << 22)   /* largest vocabulary                         */
+#define SV_LOGPROBS_TOP_MAX 32   /* most alternatives per row (spec_logprobs)  */
+#define SV_HEAD_DIM_MAX 256      /* largest attention head (spec_attention)    */
 
-typedef enum { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
+typedef enum { SV_F32 = 0, SV_BF16 = 1, SV_F16 = 2 } sv_dtype; /* logits: the first two */
 
 /* A [rows, vocab] logit matrix in device memory.  `data` must be 16-byte
  * aligned and row_stride * element_size must be a multiple of 16 bytes
@@ -365,6 +371,147 @@ int spec_verify_greedy_from_argmax(const int32_t* target_argmax, const int32_t* 
 int spec_adapt_k(const int32_t* accept_len, const int32_t* k_used, double* succ, double* fail,
                  double decay, double c, int32_t k_min, int32_t k_max, int32_t* k_next,
                  float* alpha, void* stream, int32_t batch);
+
+/* ---- attention over the paged cache ----------------------------------------
+ * The target's pass over the last emitted token and the k_b drafts of every
+ * request (or over one new token: k_b = 0), against the cache and the
+ * speculative entries that spec_kv_commit reads and writes.  For query token j
+ * of request b and head hq, whose keys are those of KV head h = hq / G with
+ * G = q_heads / kv_heads:
+ *   s_p = scale * q . K[p]            lse = ln sum_p exp(s_p)
+ *   out = sum_p exp(s_p - lse) V[p]
+ * over the positions p the token sees.  With `spec`, positions 0 ..
+ * kv_len[b] - 1 are the cache's and kv_len[b] + i is entry i of the request;
+ * token j sits at position kv_len[b] + j.  Without (NULL), the tokens' own
+ * entries are in the cache already and token j sits at kv_len[b] - 1 - k_b + j.
+ * A token sees the positions up to its own and, with window W > 0, only the
+ * last W of them.  A token that sees nothing gets out = 0 and lse = -inf.
+ * Slots past a request's positions are not read into any result, whatever
+ * they hold.
+ *   cache      elem type `dtype` (sv_dtype); entry_elems = kv_heads * head
+ *              size D, D <= SV_HEAD_DIM_MAX, D * element size a multiple of 16
+ *   q          [rows, q_heads, D], element strides q_token_stride and
+ *              q_head_stride, D contiguous, any alignment; rows = sum (k_b + 1)
+ *   spec       [B, spec_slots, n_layers, 2, E] or NULL
+ *   out        [rows, q_heads, D], contiguous
+ *   lse        [rows, q_heads] float
+ *   workspace  >= spec_attention_workspace_size(batch, D) bytes, 256-byte
+ *              aligned (its size depends on the current device's SM count)
+ * A k outside [0, SV_MAX_K] or sum (k + 1) != rows fails the whole batch
+ * (SV_ERR_DATA_K / SV_ERR_DATA_ROWS, every output NaN).  A request whose
+ * kv_len is negative or above max_pages * page_size (SV_ERR_DATA_LENGTH) or
+ * with more than spec_slots tokens (SV_ERR_DATA_K) gets NaN rows; so does a
+ * row of a request that needs a page missing from its block table
+ * (SV_ERR_DATA_PAGE).  Results do not depend on the batch's order in time:
+ * sums have a fixed order on a given device.  Same ownership, stream and
+ * error conventions as spec_verify. */
+size_t spec_attention_workspace_size(int32_t batch, int32_t head_dim);
+
+int spec_attention(const sv_kv_cache* cache, int32_t dtype, int32_t layer, int32_t kv_heads,
+                   const void* q, int64_t q_token_stride, int64_t q_head_stride, int32_t q_heads,
+                   int64_t rows, const void* spec, int32_t spec_slots, const int32_t* k_per_req,
+                   const int32_t* kv_len, const int32_t* block_table, int32_t max_pages,
+                   float scale, int32_t window, void* out, float* lse, void* stream,
+                   int32_t batch, void* workspace, size_t workspace_bytes);
+
+/* ---- accumulated attention weights -----------------------------------------
+ * How much each cached position is attended to, for spec_kv_evict:
+ *   out_score[b][p] = score[b][p] + sum_j sum_hq exp(s_p - lse[j][hq])
+ * over the heads and the query tokens j = 0 .. accept_len[b] (all k_b + 1 when
+ * accept_len is NULL; none, and nothing written, when it is -1), with the q,
+ * lse and lengths of spec_attention before spec_kv_commit.  Positions 0 ..
+ * kv_len[b] - 1 are written, and with `spec` also kv_len[b] .. kv_len[b] +
+ * accept_len[b], the positions that spec_kv_commit appends; positions past
+ * them stay as they are, so scores that start at zero stay zero beyond the
+ * cached length.
+ *   score, out_score  [B, score_cols] float with row strides score_stride and
+ *                     out_stride; they may be the same buffer
+ *   workspace         >= spec_attention_weights_workspace_size(batch)
+ * A request with an accept length above k_b (SV_ERR_DATA_ACCEPT), with
+ * positions past score_cols or its block table (SV_ERR_DATA_LENGTH) or more
+ * than spec_slots tokens (SV_ERR_DATA_K) is left untouched; positions on a
+ * missing page are not written (SV_ERR_DATA_PAGE).  A batch error writes
+ * nothing.  Each score has one writer and a fixed order of its sum. */
+size_t spec_attention_weights_workspace_size(int32_t batch);
+
+int spec_attention_weights(const sv_kv_cache* cache, int32_t dtype, int32_t layer,
+                           int32_t kv_heads, const void* q, int64_t q_token_stride,
+                           int64_t q_head_stride, int32_t q_heads, int64_t rows, const void* spec,
+                           int32_t spec_slots, const int32_t* k_per_req, const int32_t* kv_len,
+                           const int32_t* block_table, int32_t max_pages, float scale,
+                           int32_t window, const float* lse, const int32_t* accept_len,
+                           const float* score, int64_t score_stride, float* out_score,
+                           int64_t out_stride, int32_t score_cols, void* stream, int32_t batch,
+                           void* workspace, size_t workspace_bytes);
+
+/* ---- eviction from the paged cache -----------------------------------------
+ * Keeps at most `budget` positions of every request: its first `sinks`, its
+ * last `recent` and, of the others, those of the largest score (the lowest
+ * position on ties, NaN below every number); sinks + recent <= budget.  A
+ * request of n <= budget positions keeps all.  Kept positions keep their
+ * order: kept position i moves to position i, K and V of every layer, its
+ * score moves to out_score[b][i], scores from there to n become 0 and
+ * out_len[b] the number kept.
+ * In place (dst NULL): entries move within the request's own pages, which no
+ * other request may share; pages past the new length are free.  Else the kept
+ * entries are written to dst at dst_table's pages (another cache of the same
+ * geometry, or other pages of this one) and the source stays as it is.
+ *   score       [B, score_cols] float, row stride score_stride
+ *   out_score   [B, out_cols] float, row stride out_stride; may be score
+ *   kv_len      [B] int32; out_len [B] int32, may be kv_len
+ *   out_kept    [B, budget] int32 or NULL: the kept positions, then -1
+ *   workspace   >= spec_kv_evict_workspace_size(batch, budget) bytes
+ * A request with kv_len negative or past its block table, score_cols or (kept
+ * part) out_cols or dst_table fails with SV_ERR_DATA_LENGTH, one with a
+ * missing page with SV_ERR_DATA_PAGE: nothing of it moves, out_kept is -1,
+ * out_len stays where it is kv_len and is -1 elsewhere.  batch <= 65535. */
+size_t spec_kv_evict_workspace_size(int32_t batch, int32_t budget);
+
+int spec_kv_evict(const sv_kv_cache* cache, const int32_t* block_table, int32_t max_pages,
+                  const sv_kv_cache* dst, const int32_t* dst_table, int32_t dst_max_pages,
+                  const float* score, int64_t score_stride, int32_t score_cols, float* out_score,
+                  int64_t out_stride, int32_t out_cols, const int32_t* kv_len, int32_t* out_len,
+                  int32_t budget, int32_t sinks, int32_t recent, int32_t* out_kept, void* stream,
+                  int32_t batch, void* workspace, size_t workspace_bytes);
+
+/* ---- log probabilities of given tokens -------------------------------------
+ * Per row r of the logits, with z = x / T_r (T_r = temperature[r]; NULL or 0
+ * stands for 1), m = max x and t = tokens[r]:
+ *   out_logsum[r]  = ln sum_y exp((x_y - m) / T)     out_max[r] = m
+ *   out_logprob[r] = (x_t - m) / T - out_logsum[r]
+ *   out_entropy[r] = -sum_y p_y ln p_y
+ *   out_top_tokens[r][i], out_top_logprobs[r][i]: the n_top most likely tokens,
+ *     the largest logit first and the lowest index on ties; tokens of
+ *     probability 0 (-inf) are none: -1 and -inf stand for what is missing
+ * A row with token -1 (spec_verify's mark past the last emitted token) is not
+ * read: NaN, and -1 for tokens.  tokens NULL: no log probability (NaN), the
+ * rest as usual.  Rows may start at any element: `data` needs the alignment of
+ * its element only and row_stride >= vocab is any.
+ *   out_*       [rows] float, each may be NULL; out_top_* [rows, n_top] int32
+ *               and float, needed when n_top > 0; n_top <= SV_LOGPROBS_TOP_MAX
+ *   workspace   >= spec_logprobs_workspace_size(rows) bytes
+ * A row with a temperature that is negative, not finite or below 1e-30
+ * (SV_ERR_DATA_TEMPERATURE), a token below -1 or not below vocab
+ * (SV_ERR_DATA_TOKEN), or a NaN, a +inf or no finite logit (SV_ERR_DATA_LOGIT)
+ * gets NaN and -1. */
+size_t spec_logprobs_workspace_size(int64_t rows);
+
+int spec_logprobs(const sv_logits* logits, const int32_t* tokens, const float* temperature,
+                  int32_t n_top, float* out_logprob, float* out_entropy, float* out_max,
+                  float* out_logsum, int32_t* out_top_tokens, float* out_top_logprobs,
+                  void* stream, void* workspace, size_t workspace_bytes);
+
+/* The gradient of a loss with respect to the logits, given its gradients
+ * g_logprob and g_entropy ([rows] float, either may be NULL for 0) and the
+ * forward call's out_max, out_logsum and (with g_entropy) out_entropy:
+ *   dx_y = (1/T) (g_logprob (1[y = t] - p_y) - g_entropy p_y (ln p_y + H))
+ * out: [rows, vocab] of the logits' type, row stride out_stride, any
+ * alignment; it may be the logits themselves.  A row with token -1 gets 0, one
+ * whose forward results are NaN or whose token or temperature is bad NaN. */
+int spec_logprobs_grad(const sv_logits* logits, const int32_t* tokens, const float* temperature,
+                       const float* max, const float* logsum, const float* entropy,
+                       const float* g_logprob, const float* g_entropy, void* out,
+                       int64_t out_stride, void* stream);
 
 /* Human-readable text of a status code. */
 const char* spec_verify_strerror(int code);

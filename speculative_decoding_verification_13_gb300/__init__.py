@@ -29,7 +29,10 @@ __all__ = ["verify", "Verifier", "workspace_size", "get_error", "dump_rows", "st
            "library_path", "SpecVerifyError", "SV_TOPK_MAX", "SV_MAX_K", "verify_noalloc",
            "noalloc_scratch", "SV_NOALLOC_SCRATCH_BYTES", "DraftSampler", "draft_sample", "kv_commit",
            "kv_commit_error", "lmhead_stats", "lmhead_stats_error",
-           "adapt_k", "verify_greedy_from_argmax", "verify_greedy_error"]
+           "adapt_k", "verify_greedy_from_argmax", "verify_greedy_error",
+           "attention", "attention_error", "attention_weights", "attention_weights_error",
+           "kv_evict", "kv_evict_error", "logprobs", "logprobs_error", "logprobs_grad",
+           "LogProbs", "SV_LOGPROBS_TOP_MAX", "SV_HEAD_DIM_MAX"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_lib", "libspecverify.so")
@@ -46,7 +49,8 @@ ERROR_NAMES = {
     4: "SV_ERR_WORKSPACE", 16: "SV_ERR_DATA_K", 17: "SV_ERR_DATA_TEMPERATURE",
     18: "SV_ERR_DATA_TOP_P", 19: "SV_ERR_DATA_TOP_K", 20: "SV_ERR_DATA_TOKEN",
     21: "SV_ERR_DATA_ROWS", 22: "SV_ERR_DATA_LOGIT", 23: "SV_ERR_DATA_NO_DRAFT",
-    24: "SV_ERR_TIMEOUT", 25: "SV_ERR_INTERNAL",
+    24: "SV_ERR_TIMEOUT", 25: "SV_ERR_INTERNAL", 26: "SV_ERR_DATA_ACCEPT",
+    27: "SV_ERR_DATA_PAGE", 28: "SV_ERR_DATA_LENGTH",
 }
 
 
@@ -620,3 +624,8 @@ def verify_noalloc(target, draft, draft_tokens, k_per_req, temperature, uniforms
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_verify_noalloc")
     return out_accept_len, out_tokens
+
+
+from .operators import (LogProbs, SV_HEAD_DIM_MAX, SV_LOGPROBS_TOP_MAX, attention,  # noqa: E402
+                        attention_error, attention_weights, attention_weights_error, kv_evict,
+                        kv_evict_error, logprobs, logprobs_error, logprobs_grad)

@@ -7,10 +7,12 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 #include <vector>
 
+#include "sv_attn.cuh"
 #include "sv_internal.cuh"
 
 namespace sv {
@@ -69,7 +71,68 @@ int prepare_device(int vocab, DeviceState* out) {
 
 bool misaligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
 
-size_t elem_size(int dtype) { return dtype == SV_BF16 ? 2 : 4; }
+size_t elem_size(int dtype) { return dtype == SV_BF16 || dtype == SV_F16 ? 2 : 4; }
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return sms;
+}
+
+// The checks and arguments that spec_attention and spec_attention_weights share.
+int attn_args(const sv_kv_cache* cache, int32_t dtype, int32_t layer, int32_t kv_heads,
+              const void* q, int64_t q_ts, int64_t q_hs, int32_t q_heads, int64_t rows,
+              const void* spec, int32_t slots, const int32_t* k_per_req, const int32_t* kv_len,
+              const int32_t* table, int32_t max_pages, float scale, int32_t window, int32_t batch,
+              AttnArgs* out) {
+  if (!cache || batch < 0 || rows < 0 || max_pages < 0 || window < 0) return SV_ERR_ARG;
+  const sv_kv_cache& c = *cache;
+  if (dtype != SV_F32 && dtype != SV_BF16 && dtype != SV_F16) return SV_ERR_UNSUPPORTED;
+  if (c.num_pages < 0 || c.n_layers < 1 || c.page_size < 1 || c.entry_elems < 1 ||
+      size_t(c.elem_bytes) != elem_size(dtype) || layer < 0 || layer >= c.n_layers ||
+      kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0 || c.entry_elems % kv_heads != 0)
+    return SV_ERR_ARG;
+  if (!(scale > -INFINITY && scale < INFINITY)) return SV_ERR_ARG;
+  if (rows < batch || rows >= INT_MAX || (rows > 0 && batch == 0)) return SV_ERR_ARG;
+  const int D = c.entry_elems / kv_heads;
+  if (D > SV_HEAD_DIM_MAX || (size_t(D) * c.elem_bytes) % 16 != 0) return SV_ERR_UNSUPPORTED;
+  if (batch > 0) {
+    if (!q || !k_per_req || !kv_len || (max_pages > 0 && !table) ||
+        (c.num_pages > 0 && !c.data) || (spec && slots < 1))
+      return SV_ERR_ARG;
+    if (misaligned(c.data, 16) || misaligned(spec, 16)) return SV_ERR_UNSUPPORTED;
+  }
+  AttnArgs A{};
+  A.q = q;
+  A.q_ts = q_ts;
+  A.q_hs = q_hs;
+  A.entry_bytes = int64_t(c.entry_elems) * c.elem_bytes;
+  A.v_off = A.entry_bytes * c.page_size;
+  A.page_bytes = A.v_off * 2 * c.n_layers;
+  A.cache = static_cast<const char*>(c.data) + A.v_off * 2 * layer;
+  A.num_pages = c.num_pages;
+  A.spec_tok = A.entry_bytes * 2 * c.n_layers;
+  A.spec_req = A.spec_tok * slots;
+  A.spec = spec ? static_cast<const char*>(spec) + A.entry_bytes * 2 * layer : nullptr;
+  A.slots = slots;
+  A.kv_len = kv_len;
+  A.k_per_req = k_per_req;
+  A.table = table;
+  A.S = c.page_size;
+  A.max_pages = max_pages;
+  A.B = batch;
+  A.Hq = q_heads;
+  A.Hkv = kv_heads;
+  A.G = q_heads / kv_heads;
+  A.D = D;
+  A.window = window;
+  A.Rt = rows;
+  A.scale2 = scale * 1.4426950408889634f;
+  *out = A;
+  return SV_OK;
+}
 
 }  // namespace
 
@@ -360,6 +423,187 @@ int spec_verify_greedy_from_argmax(const int32_t* target_argmax, const int32_t* 
              : SV_ERR_CUDA;
 }
 
+size_t spec_attention_workspace_size(int32_t batch, int32_t head_dim) {
+  const int sms = sm_count();
+  if (batch < 0 || head_dim < 1 || head_dim > SV_HEAD_DIM_MAX || sms == 0) return 0;
+  return attn_workspace_bytes(batch, head_dim, sms, false);
+}
+
+int spec_attention(const sv_kv_cache* cache, int32_t dtype, int32_t layer, int32_t kv_heads,
+                   const void* q, int64_t q_token_stride, int64_t q_head_stride, int32_t q_heads,
+                   int64_t rows, const void* spec, int32_t spec_slots, const int32_t* k_per_req,
+                   const int32_t* kv_len, const int32_t* block_table, int32_t max_pages,
+                   float scale, int32_t window, void* out, float* lse, void* stream,
+                   int32_t batch, void* workspace, size_t workspace_bytes) {
+  AttnArgs A;
+  if (int rc = attn_args(cache, dtype, layer, kv_heads, q, q_token_stride, q_head_stride, q_heads,
+                         rows, spec, spec_slots, k_per_req, kv_len, block_table, max_pages, scale,
+                         window, batch, &A))
+    return rc;
+  if (batch == 0) return SV_OK;
+  if (!out || !lse) return SV_ERR_ARG;
+  if (!workspace || misaligned(workspace, 256)) return SV_ERR_WORKSPACE;
+  const int sms = sm_count();
+  if (sms == 0) return SV_ERR_CUDA;
+  if (workspace_bytes < attn_workspace_bytes(batch, A.D, sms, false)) return SV_ERR_WORKSPACE;
+  A.out = out;
+  A.o_hs = A.D;
+  A.o_ts = int64_t(A.D) * q_heads;
+  A.lse = lse;
+  return launch_attn(A, dtype, false, workspace, sms, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
+size_t spec_attention_weights_workspace_size(int32_t batch) {
+  const int sms = sm_count();
+  return batch < 0 || sms == 0 ? 0 : attn_workspace_bytes(batch, 16, sms, true);
+}
+
+int spec_attention_weights(const sv_kv_cache* cache, int32_t dtype, int32_t layer,
+                           int32_t kv_heads, const void* q, int64_t q_token_stride,
+                           int64_t q_head_stride, int32_t q_heads, int64_t rows, const void* spec,
+                           int32_t spec_slots, const int32_t* k_per_req, const int32_t* kv_len,
+                           const int32_t* block_table, int32_t max_pages, float scale,
+                           int32_t window, const float* lse, const int32_t* accept_len,
+                           const float* score, int64_t score_stride, float* out_score,
+                           int64_t out_stride, int32_t score_cols, void* stream, int32_t batch,
+                           void* workspace, size_t workspace_bytes) {
+  AttnArgs A;
+  if (int rc = attn_args(cache, dtype, layer, kv_heads, q, q_token_stride, q_head_stride, q_heads,
+                         rows, spec, spec_slots, k_per_req, kv_len, block_table, max_pages, scale,
+                         window, batch, &A))
+    return rc;
+  if (score_cols < 0 || (batch > 1 && (score_stride < score_cols || out_stride < score_cols)))
+    return SV_ERR_ARG;
+  // one buffer has one row stride
+  if (score == out_score && batch > 1 && score_stride != out_stride) return SV_ERR_ARG;
+  if (batch == 0) return SV_OK;
+  if (!lse || (score_cols > 0 && (!score || !out_score))) return SV_ERR_ARG;
+  if (!workspace || misaligned(workspace, 256)) return SV_ERR_WORKSPACE;
+  const int sms = sm_count();
+  if (sms == 0) return SV_ERR_CUDA;
+  if (workspace_bytes < attn_workspace_bytes(batch, A.D, sms, true)) return SV_ERR_WORKSPACE;
+  A.lse = const_cast<float*>(lse);
+  A.accept_len = accept_len;
+  A.score = score;
+  A.out_score = out_score;
+  A.score_stride = score_stride;
+  A.out_stride = out_stride;
+  A.score_cols = score_cols;
+  return launch_attn(A, dtype, true, workspace, sms, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
+size_t spec_kv_evict_workspace_size(int32_t batch, int32_t budget) {
+  return batch < 0 || budget < 1 ? 0 : evict_workspace_bytes(batch, budget);
+}
+
+int spec_kv_evict(const sv_kv_cache* cache, const int32_t* block_table, int32_t max_pages,
+                  const sv_kv_cache* dst, const int32_t* dst_table, int32_t dst_max_pages,
+                  const float* score, int64_t score_stride, int32_t score_cols, float* out_score,
+                  int64_t out_stride, int32_t out_cols, const int32_t* kv_len, int32_t* out_len,
+                  int32_t budget, int32_t sinks, int32_t recent, int32_t* out_kept, void* stream,
+                  int32_t batch, void* workspace, size_t workspace_bytes) {
+  if (!cache || batch < 0 || max_pages < 0 || budget < 1 || sinks < 0 || recent < 0 ||
+      int64_t(sinks) + recent > budget || score_cols < 0 || out_cols < 0)
+    return SV_ERR_ARG;
+  if (batch > 1 && (score_stride < score_cols || out_stride < out_cols)) return SV_ERR_ARG;
+  if (score == out_score && batch > 1 && score_stride != out_stride) return SV_ERR_ARG;
+  const sv_kv_cache& c = *cache;
+  if (c.num_pages < 0 || c.n_layers < 1 || c.page_size < 1 || c.entry_elems < 1 ||
+      (c.elem_bytes != 2 && c.elem_bytes != 4))
+    return SV_ERR_ARG;
+  if ((int64_t(c.entry_elems) * c.elem_bytes) % 16 != 0 || batch > 65535)
+    return SV_ERR_UNSUPPORTED;
+  const bool in_place = dst == nullptr;
+  if (!in_place) {
+    if (dst->n_layers != c.n_layers || dst->page_size != c.page_size ||
+        dst->entry_elems != c.entry_elems || dst->elem_bytes != c.elem_bytes ||
+        dst->num_pages < 0 || dst_max_pages < 0)
+      return SV_ERR_ARG;
+  }
+  const sv_kv_cache& d = in_place ? c : *dst;
+  const int32_t* dt = in_place ? block_table : dst_table;
+  const int32_t dcols = in_place ? max_pages : dst_max_pages;
+  if (!workspace || misaligned(workspace, 256) ||
+      workspace_bytes < evict_workspace_bytes(batch, budget))
+    return SV_ERR_WORKSPACE;
+  if (batch == 0) return SV_OK;
+  if (!kv_len || !out_len || (max_pages > 0 && !block_table) || (dcols > 0 && !dt) ||
+      (c.num_pages > 0 && !c.data) || (d.num_pages > 0 && !d.data) || (score_cols > 0 && !score) ||
+      (out_cols > 0 && !out_score))
+    return SV_ERR_ARG;
+  if (misaligned(c.data, 16) || misaligned(d.data, 16)) return SV_ERR_UNSUPPORTED;
+  const int sms = sm_count();
+  if (sms == 0) return SV_ERR_CUDA;
+  return launch_evict(c, block_table, max_pages, d, dt, dcols, score, score_stride, score_cols,
+                      out_score, out_stride, out_cols, kv_len, out_len, batch, budget, sinks,
+                      recent, out_kept, in_place, workspace, sms,
+                      static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
+size_t spec_logprobs_workspace_size(int64_t rows) {
+  return rows < 0 || rows >= INT_MAX ? 0 : logprobs_workspace_bytes(rows);
+}
+
+// Logits that may start at any element.
+static int logprobs_check(const sv_logits* logits) {
+  if (!logits) return SV_ERR_ARG;
+  const sv_logits& x = *logits;
+  if (x.dtype != SV_F32 && x.dtype != SV_BF16) return SV_ERR_UNSUPPORTED;
+  if (x.vocab < 1 || x.rows < 0 || x.rows >= INT_MAX || (x.rows > 1 && x.row_stride < x.vocab))
+    return SV_ERR_ARG;
+  if (x.vocab > SV_VOCAB_MAX) return SV_ERR_UNSUPPORTED;
+  if (x.rows > 0 && !x.data) return SV_ERR_ARG;
+  if (misaligned(x.data, elem_size(x.dtype))) return SV_ERR_UNSUPPORTED;
+  return SV_OK;
+}
+
+int spec_logprobs(const sv_logits* logits, const int32_t* tokens, const float* temperature,
+                  int32_t n_top, float* out_logprob, float* out_entropy, float* out_max,
+                  float* out_logsum, int32_t* out_top_tokens, float* out_top_logprobs,
+                  void* stream, void* workspace, size_t workspace_bytes) {
+  if (int rc = logprobs_check(logits)) return rc;
+  if (n_top < 0) return SV_ERR_ARG;
+  if (n_top > SV_LOGPROBS_TOP_MAX) return SV_ERR_UNSUPPORTED;
+  if (n_top > 0 && logits->rows > 0 && (!out_top_tokens || !out_top_logprobs)) return SV_ERR_ARG;
+  if (!workspace || misaligned(workspace, 256) ||
+      workspace_bytes < logprobs_workspace_bytes(logits->rows))
+    return SV_ERR_WORKSPACE;
+  if (logits->rows == 0) return SV_OK;
+  return launch_logprobs(*logits, tokens, temperature, n_top, out_logprob, out_entropy, out_max,
+                         out_logsum, out_top_tokens, out_top_logprobs, workspace,
+                         static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
+int spec_logprobs_grad(const sv_logits* logits, const int32_t* tokens, const float* temperature,
+                       const float* max, const float* logsum, const float* entropy,
+                       const float* g_logprob, const float* g_entropy, void* out,
+                       int64_t out_stride, void* stream) {
+  if (int rc = logprobs_check(logits)) return rc;
+  if (logits->rows > 1 && out_stride < logits->vocab) return SV_ERR_ARG;
+  if (logits->rows == 0) return SV_OK;
+  if (!tokens || !max || !logsum || (g_entropy && !entropy) || !out) return SV_ERR_ARG;
+  if (misaligned(out, elem_size(logits->dtype))) return SV_ERR_UNSUPPORTED;
+  // one buffer has one row stride
+  if (out == logits->data && logits->rows > 1 && out_stride != logits->row_stride)
+    return SV_ERR_ARG;
+  if (logprobs_grad_blocks(*logits) > INT_MAX) return SV_ERR_UNSUPPORTED;
+  return launch_logprobs_grad(*logits, tokens, temperature, max, logsum, entropy, g_logprob,
+                              g_entropy, out, out_stride,
+                              static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
 int spec_verify_get_error(const void* workspace, void* stream, int32_t* code, int32_t* request,
                           int64_t* row) {
   if (!workspace || !code) return SV_ERR_ARG;
@@ -367,6 +611,33 @@ int spec_verify_get_error(const void* workspace, void* stream, int32_t* code, in
   WsHeader h;
   if (cudaMemcpy(&h, workspace, sizeof h, cudaMemcpyDeviceToHost) != cudaSuccess)
     return SV_ERR_CUDA;
+  if (h.err_code == kStatusList) {
+    // one status per row or request: the lowest that failed
+    if (h.err_row < 0 || h.err_row > INT_MAX || h.n_active < 0) return SV_ERR_INTERNAL;
+    const size_t n = size_t(h.err_row), extra = size_t(h.n_active);
+    std::vector<int32_t> st;
+    try {
+      st.resize(n + extra);
+    } catch (...) {
+      return SV_ERR_INTERNAL;
+    }
+    if (!st.empty() &&
+        cudaMemcpy(st.data(), static_cast<const char*>(workspace) + align256(sizeof(WsHeader)),
+                   st.size() * sizeof(int32_t), cudaMemcpyDeviceToHost) != cudaSuccess)
+      return SV_ERR_CUDA;
+    size_t at = 0;
+    while (at < n && st[at] == 0) ++at;
+    int32_t c = at < n ? st[at] : 0;
+    for (size_t i = n; i < n + extra; ++i)
+      if (st[i] >= 0 && size_t(st[i]) < at) {
+        at = size_t(st[i]);
+        c = SV_ERR_DATA_PAGE;
+      }
+    *code = c;
+    if (request) *request = c && h.err_req ? int32_t(at) : -1;
+    if (row) *row = c && !h.err_req ? int64_t(at) : -1;
+    return SV_OK;
+  }
   *code = h.err_code;
   if (request) *request = h.err_req;
   if (row) *row = h.err_row;
@@ -438,7 +709,8 @@ const char* spec_verify_strerror(int code) {
     case SV_ERR_TIMEOUT: return "internal bounded wait expired";
     case SV_ERR_INTERNAL: return "internal capacity invariant failed";
     case SV_ERR_DATA_ACCEPT: return "KV commit: accept length above k";
-    case SV_ERR_DATA_PAGE: return "KV commit: destination page missing or negative kv_len";
+    case SV_ERR_DATA_PAGE: return "a page missing from the block table, or negative kv_len";
+    case SV_ERR_DATA_LENGTH: return "kv_len negative, or past the block table or the scores";
     default: return "unknown status";
   }
 }

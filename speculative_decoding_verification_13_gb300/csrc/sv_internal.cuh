@@ -62,6 +62,13 @@ struct WsHeader {
   int32_t pad[2];
 };
 
+// err_code of a header whose call keeps one status per entry instead (no
+// counter to clear before the call, the lowest failed entry whatever the order
+// of the CTAs): err_row entries follow the header, which are rows (err_req 0)
+// or requests (err_req 1), then n_active entries that name the first request
+// with a missing page, INT32_MAX for none.
+constexpr int32_t kStatusList = -1;
+
 struct RowStat {
   double s;     // softmax normaliser (sampling rows; kept-set weight for filtered rows,
                 // relative to the row max m for kBig rows)
@@ -221,6 +228,27 @@ cudaError_t launch_greedy_from_argmax(const int32_t* argmax, const int32_t* draf
                                       int32_t* out_tokens, int B, int64_t Rt, int V,
                                       void* workspace, cudaStream_t s);
 size_t rowpass_smem_bytes();
+size_t logprobs_workspace_bytes(int64_t rows);
+cudaError_t launch_logprobs(const sv_logits& x, const int32_t* tokens, const float* temperature,
+                            int n_top, float* logprob, float* entropy, float* mx, float* logsum,
+                            int32_t* top_tok, float* top_lp, void* workspace, cudaStream_t s);
+int64_t logprobs_grad_blocks(const sv_logits& x);
+cudaError_t launch_logprobs_grad(const sv_logits& x, const int32_t* tokens,
+                                 const float* temperature, const float* mx, const float* logsum,
+                                 const float* entropy, const float* g_lp, const float* g_ent,
+                                 void* out, int64_t out_stride, cudaStream_t s);
+size_t evict_workspace_bytes(int32_t B, int32_t budget);
+cudaError_t launch_evict(const sv_kv_cache& src, const int32_t* src_table, int src_cols,
+                         const sv_kv_cache& dst, const int32_t* dst_table, int dst_cols,
+                         const float* score, int64_t score_stride, int score_cols,
+                         float* out_score, int64_t out_stride, int out_cols,
+                         const int32_t* kv_len, int32_t* out_len, int B, int budget, int sinks,
+                         int recent, int32_t* out_kept, bool in_place, void* workspace, int sms,
+                         cudaStream_t s);
+struct AttnArgs;
+size_t attn_workspace_bytes(int32_t B, int32_t D, int sms, bool weights);
+cudaError_t launch_attn(AttnArgs A, int dtype, bool weights, void* workspace, int sms,
+                        cudaStream_t s);
 
 // Launch of a kernel that may start while the previous kernel on the stream
 // finishes (programmatic dependent launch): it must execute pdl_wait() before

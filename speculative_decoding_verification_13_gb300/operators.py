@@ -1,0 +1,412 @@
+"""Operators of the serving and drafter-training step around verification:
+attention over the paged KV cache that :func:`kv_commit` fills, the accumulated
+attention weights, eviction from the cache by them, and log probabilities of
+given tokens with their gradient.
+
+Like the rest of the binding this only marshals arguments.  Calls are
+asynchronous on ``stream`` (default: the current stream) and allocate only
+their outputs and, once per stream, a workspace.  Data errors are found by the
+kernels and read back with the ``*_error`` functions.  Nothing here is recorded
+by autograd: the gradient of :func:`logprobs` is :func:`logprobs_grad`.
+"""
+
+from __future__ import annotations
+
+import collections
+import ctypes
+import math
+
+import torch
+
+from . import (SV_BF16, SV_F32, SV_OK, SpecVerifyError, _KvCache, _Logits, _check, _ptr, get_error,
+               load_library)
+
+SV_F16 = 2
+SV_LOGPROBS_TOP_MAX = 32
+SV_HEAD_DIM_MAX = 256
+
+_DTYPES = {torch.float32: SV_F32, torch.bfloat16: SV_BF16, torch.float16: SV_F16}
+
+LogProbs = collections.namedtuple(
+    "LogProbs", ["logprob", "entropy", "max", "logsum", "top_tokens", "top_logprobs"])
+
+_P, _i32, _i64, _sz, _f32 = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t,
+                             ctypes.c_float)
+_KV = ctypes.POINTER(_KvCache)
+_SIGNATURES = {
+    "spec_attention_workspace_size": (_sz, [_i32, _i32]),
+    "spec_attention": (ctypes.c_int, [_KV, _i32, _i32, _i32, _P, _i64, _i64, _i32, _i64, _P, _i32,
+                                      _P, _P, _P, _i32, _f32, _i32, _P, _P, _P, _i32, _P, _sz]),
+    "spec_attention_weights_workspace_size": (_sz, [_i32]),
+    "spec_attention_weights": (ctypes.c_int, [_KV, _i32, _i32, _i32, _P, _i64, _i64, _i32, _i64,
+                                              _P, _i32, _P, _P, _P, _i32, _f32, _i32, _P, _P, _P,
+                                              _i64, _P, _i64, _i32, _P, _i32, _P, _sz]),
+    "spec_kv_evict_workspace_size": (_sz, [_i32, _i32]),
+    "spec_kv_evict": (ctypes.c_int, [_KV, _P, _i32, _KV, _P, _i32, _P, _i64, _i32, _P, _i64, _i32,
+                                     _P, _P, _i32, _i32, _i32, _P, _P, _i32, _P, _sz]),
+    "spec_logprobs_workspace_size": (_sz, [_i64]),
+    "spec_logprobs": (ctypes.c_int, [ctypes.POINTER(_Logits), _P, _P, _i32, _P, _P, _P, _P, _P, _P,
+                                     _P, _P, _sz]),
+    "spec_logprobs_grad": (ctypes.c_int, [ctypes.POINTER(_Logits), _P, _P, _P, _P, _P, _P, _P, _P,
+                                          _i64, _P]),
+}
+_lib = None
+
+
+def _library():
+    global _lib
+    if _lib is None:
+        lib = load_library()
+        for name, (res, args) in _SIGNATURES.items():
+            f = getattr(lib, name)
+            f.restype, f.argtypes = res, args
+        _lib = lib
+    return _lib
+
+
+# ----------------------------------------------------------- streams, workspaces
+_workspaces = {}   # (kind, device, stream) -> workspace: calls of one stream are in order
+_last = {}         # (kind, device) -> (workspace, stream) of the last call
+_sizes = {}        # workspace sizes already asked for
+
+
+def _stream_of(stream, dev):
+    return torch.cuda.current_stream(dev) if stream is None else stream
+
+
+def _scratch(kind, dev, stream, size):
+    """A workspace for a call on ``stream``: one per stream, or one of its own
+    while a graph is being captured (the graph may be replayed next to the
+    stream's other calls)."""
+    size_key = (kind, dev.index, size)
+    need = _sizes.get(size_key)
+    if need is None:
+        with torch.cuda.device(dev):
+            need = int(getattr(_library(), f"spec_{kind}_workspace_size")(*size))
+        if need == 0:
+            raise SpecVerifyError(1, f"spec_{kind}_workspace_size")
+        if len(_sizes) > 4096:
+            _sizes.clear()
+        _sizes[size_key] = need
+    key = (kind, dev.index, stream.cuda_stream)
+    ws = None if torch.cuda.is_current_stream_capturing() else _workspaces.get(key)
+    if ws is None or ws.numel() < need:
+        with torch.cuda.stream(stream):
+            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        if not torch.cuda.is_current_stream_capturing():
+            _workspaces[key] = ws
+    _last[kind, dev.index] = ws, stream
+    return ws
+
+
+def _error(kind, stream, device):
+    d = torch.device(device or "cuda")
+    index = d.index if d.index is not None else torch.cuda.current_device()
+    ws, last = _last[kind, index]
+    return get_error(ws, last if stream is None else stream)
+
+
+def _call(name, dev, *args):
+    f = getattr(_library(), name)
+    if torch.cuda.current_device() == dev.index:
+        rc = f(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args)
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, name)
+
+
+# --------------------------------------------------------------------- checks
+def _vector(t, name, dtype, n, dev, optional=False):
+    if t is None:
+        if optional:
+            return
+        raise ValueError(f"{name} is required")
+    _check(t, name, dtype)
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    if t.numel() < n:
+        raise ValueError(f"{name} holds {t.numel()} elements, {n} are needed")
+
+
+def _matrix(t, name, dtype, shape, dev):
+    """A contiguous tensor of this shape."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev:
+        raise TypeError(f"{name} must be a {dtype} tensor on {dev}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}")
+
+
+def _rows2d(t, name, dtype, rows, dev):
+    """A float matrix with contiguous rows; returns its row stride."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev or t.dim() != 2:
+        raise TypeError(f"{name} must be a 2-D {dtype} tensor on {dev}")
+    if t.shape[0] < rows or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must have {rows} contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _cache_desc(cache, name="cache"):
+    if not isinstance(cache, torch.Tensor) or not cache.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if cache.dim() != 5 or not cache.is_contiguous() or cache.shape[2] != 2:
+        raise ValueError(f"{name} must be contiguous [num_pages, n_layers, 2, page_size, E]")
+    if cache.element_size() not in (2, 4):
+        raise TypeError(f"{name} must have a 2- or 4-byte dtype")
+    return _KvCache(cache.data_ptr() if cache.numel() else None, cache.shape[0], cache.shape[1],
+                    cache.shape[3], cache.shape[4], cache.element_size())
+
+
+def _table(t, name, B, dev):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    _check(t, name, torch.int32, ndim=2)
+    if t.device != dev or not t.is_contiguous() or t.shape[0] != B:
+        raise ValueError(f"{name} must be contiguous with {B} rows on {dev}")
+
+
+def _attention_args(q, cache, layer, kv_len, block_table, k_per_req, spec, scale, window):
+    """The checks that both attention calls share; returns their leading arguments."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3 or q.dtype not in _DTYPES:
+        raise TypeError("q must be a 3-D float32, bfloat16 or float16 CUDA tensor")
+    desc = _cache_desc(cache)
+    dev = q.device
+    if cache.dtype != q.dtype or cache.device != dev:
+        raise TypeError("q and cache must share dtype and device")
+    rows, Hq, D = q.shape
+    E = cache.shape[4]
+    if D < 1 or E % D or Hq < 1 or Hq % (E // D):
+        raise ValueError(f"{Hq} heads of {D} do not fit a cache entry of {E} elements")
+    if D > 1 and q.stride(2) != 1:
+        raise ValueError("the heads of q must be contiguous")
+    if not 0 <= layer < cache.shape[1]:
+        raise ValueError(f"layer {layer} of {cache.shape[1]}")
+    if window < 0:
+        raise ValueError("window must be 0 (off) or positive")
+    B = int(k_per_req.shape[0])
+    _vector(k_per_req, "k_per_req", torch.int32, B, dev)
+    _vector(kv_len, "kv_len", torch.int32, B, dev)
+    _table(block_table, "block_table", B, dev)
+    slots = 0
+    if spec is not None:
+        if not isinstance(spec, torch.Tensor) or spec.dim() != 5 or spec.shape[1] < 1:
+            raise ValueError("spec must be [B, slots, n_layers, 2, E]")
+        slots = spec.shape[1]
+        if spec.dtype != q.dtype or spec.device != dev:
+            raise TypeError("spec must share q's dtype and device")
+        if tuple(spec.shape) != (B, slots, cache.shape[1], 2, E) or not spec.is_contiguous():
+            raise ValueError("spec must be contiguous [B, slots, n_layers, 2, E] matching the cache")
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    return dev, B, rows, Hq, D, (
+        ctypes.byref(desc), _DTYPES[q.dtype], int(layer), E // D, _ptr(q), q.stride(0),
+        q.stride(1), Hq, rows, _ptr(spec), slots, _ptr(k_per_req), _ptr(kv_len),
+        _ptr(block_table), block_table.shape[1], scale, int(window))
+
+
+# ------------------------------------------------------------------ operators
+def attention(q, cache, layer, kv_len, block_table, k_per_req, spec=None, *, scale=None, window=0,
+              out=None, out_lse=None, stream=None):
+    """Attention of every request's query tokens over its paged cache.
+
+    q: [rows, q_heads, D] (bf16, fp16 or fp32; token and head strides are free),
+    request b owning the k_b + 1 rows that it owns among the verifier's target
+    rows; cache: [num_pages, n_layers, 2, page_size, kv_heads * D] as in
+    :func:`kv_commit`, of which ``layer`` is read; kv_len, k_per_req: [B] int32;
+    block_table: [B, max_pages] int32; spec: [B, slots, n_layers, 2, E], the
+    entries of the query tokens that :func:`kv_commit` will append (token j then
+    sits at position kv_len + j), or None when the cache holds them already
+    (token j sits at kv_len - 1 - k + j).  A token sees the positions up to its
+    own, with ``window`` > 0 only the last ``window`` of them.
+
+    Returns ``(out [rows, q_heads, D], lse [rows, q_heads] float32)``; a token
+    that sees nothing has out 0 and lse -inf."""
+    dev, B, rows, Hq, D, args = _attention_args(q, cache, layer, kv_len, block_table, k_per_req,
+                                                spec, scale, window)
+    if out is None:
+        out = torch.empty((rows, Hq, D), dtype=q.dtype, device=dev)
+    else:
+        _matrix(out, "out", q.dtype, (rows, Hq, D), dev)
+    if out_lse is None:
+        out_lse = torch.empty((rows, Hq), dtype=torch.float32, device=dev)
+    else:
+        _matrix(out_lse, "out_lse", torch.float32, (rows, Hq), dev)
+    s = _stream_of(stream, dev)
+    ws = _scratch("attention", dev, s, (B, D))
+    _call("spec_attention", dev, *args, _ptr(out), _ptr(out_lse), s.cuda_stream, B, _ptr(ws),
+          ws.numel())
+    return out, out_lse
+
+
+def attention_weights(q, cache, layer, kv_len, block_table, k_per_req, lse, score, spec=None,
+                      accept_len=None, *, scale=None, window=0, out_score=None, stream=None):
+    """Add the attention weights of one layer to the positions' running scores.
+
+    The arguments of :func:`attention` and its ``lse``, before :func:`kv_commit`
+    moves kv_len; score: [B, cols] float32.  Only the query tokens 0 ..
+    accept_len[b] count (all without it; a request with -1 is left alone), so
+    rejected drafts leave no trace.  Positions 0 .. kv_len - 1 and, with
+    ``spec``, those that the commit will append are written to ``out_score``
+    (default: ``score`` itself).  Returns ``out_score``."""
+    dev, B, rows, Hq, D, args = _attention_args(q, cache, layer, kv_len, block_table, k_per_req,
+                                                spec, scale, window)
+    _matrix(lse, "lse", torch.float32, (rows, Hq), dev)
+    _vector(accept_len, "accept_len", torch.int32, B, dev, optional=True)
+    stride = _rows2d(score, "score", torch.float32, B, dev)
+    if out_score is None:
+        out_score = score
+    out_stride = _rows2d(out_score, "out_score", torch.float32, B, dev)
+    if out_score.shape[1] != score.shape[1]:
+        raise ValueError("score and out_score must have the same columns")
+    s = _stream_of(stream, dev)
+    ws = _scratch("attention_weights", dev, s, (B,))
+    _call("spec_attention_weights", dev, *args, _ptr(lse), _ptr(accept_len), _ptr(score), stride,
+          _ptr(out_score), out_stride, score.shape[1], s.cuda_stream, B, _ptr(ws), ws.numel())
+    return out_score
+
+
+def kv_evict(cache, score, kv_len, block_table, budget, sinks=0, recent=0, *, out_cache=None,
+             out_table=None, out_score=None, out_len=None, out_kept=None, with_kept=False,
+             stream=None):
+    """Keep at most ``budget`` positions of every request, by attention weight.
+
+    A request with more keeps its first ``sinks``, its last ``recent`` and, of
+    the others, those of the largest score (lowest position on ties), in their
+    order: every layer's K and V move to positions 0 .. budget - 1, scores
+    (:func:`attention_weights`) with them, and the length becomes the number
+    kept.  Without ``out_table`` the entries move inside the request's own
+    pages, which no other request may share; with it they are written to those
+    pages of ``out_cache`` (default: the same cache) and the source stays.
+    ``out_score`` and ``out_len`` default to score and kv_len, in place.
+
+    Returns ``(out_len [B] int32, kept [B, budget] int32 or None)``."""
+    desc = _cache_desc(cache)
+    dev = cache.device
+    B = int(kv_len.shape[0])
+    _vector(kv_len, "kv_len", torch.int32, B, dev)
+    _table(block_table, "block_table", B, dev)
+    budget, sinks, recent = int(budget), int(sinks), int(recent)
+    if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget:
+        raise ValueError("budget must be positive and hold sinks and recent")
+    stride = _rows2d(score, "score", torch.float32, B, dev)
+    if out_score is None:
+        out_score = score
+    out_stride = _rows2d(out_score, "out_score", torch.float32, B, dev)
+    if out_len is None:
+        out_len = kv_len
+    _vector(out_len, "out_len", torch.int32, B, dev)
+    out_desc, out_cols = None, 0
+    if out_table is not None:
+        _table(out_table, "out_table", B, dev)
+        dst = cache if out_cache is None else out_cache
+        out_desc = _cache_desc(dst, "out_cache")
+        if dst.dtype != cache.dtype or dst.device != dev or dst.shape[1:] != cache.shape[1:]:
+            raise ValueError("out_cache must match the cache in all but its pages")
+        out_cols = out_table.shape[1]
+    elif out_cache is not None:
+        raise ValueError("out_cache needs out_table")
+    if out_kept is None and with_kept:
+        out_kept = torch.empty((B, budget), dtype=torch.int32, device=dev)
+    if out_kept is not None:
+        _matrix(out_kept, "out_kept", torch.int32, (B, budget), dev)
+    s = _stream_of(stream, dev)
+    ws = _scratch("kv_evict", dev, s, (B, budget))
+    _call("spec_kv_evict", dev, ctypes.byref(desc), _ptr(block_table), block_table.shape[1],
+          ctypes.byref(out_desc) if out_desc is not None else None, _ptr(out_table), out_cols,
+          _ptr(score), stride, score.shape[1], _ptr(out_score), out_stride, out_score.shape[1],
+          _ptr(kv_len), _ptr(out_len), budget, sinks, recent, _ptr(out_kept), s.cuda_stream, B,
+          _ptr(ws), ws.numel())
+    return out_len, out_kept
+
+
+def _rows_desc(x):
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() != 2:
+        raise TypeError("logits must be a 2-D CUDA tensor")
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits must be float32 or bfloat16, got {x.dtype}")
+    if x.shape[1] > 1 and x.stride(1) != 1:
+        raise ValueError("logit rows must be contiguous")
+    return _Logits(x.data_ptr() if x.numel() else None, _DTYPES[x.dtype], x.shape[1], x.shape[0],
+                   x.stride(0) if x.shape[0] > 1 else x.shape[1])
+
+
+def logprobs(logits, tokens, temperature=None, n_top=0, *, stream=None):
+    """Log probability of each row's token, entropy and the ``n_top`` (at most
+    32) most likely tokens, in one pass over the logits.
+
+    logits: [rows, V] float32 or bfloat16, any row stride; tokens: [rows] int32
+    (-1: skip the row; None: no log probabilities); temperature: [rows] float32
+    or None, 0 standing for 1.  Returns a :class:`LogProbs`: logprob, entropy,
+    max, logsum [rows] float32 and top_tokens, top_logprobs [rows, n_top] (None
+    without n_top; ties go to the lowest index; -1 and -inf where a row has
+    fewer tokens of nonzero probability)."""
+    x = _rows_desc(logits)
+    dev, R = logits.device, logits.shape[0]
+    _vector(tokens, "tokens", torch.int32, R, dev, optional=True)
+    _vector(temperature, "temperature", torch.float32, R, dev, optional=True)
+    n_top = int(n_top)
+    if not 0 <= n_top <= SV_LOGPROBS_TOP_MAX:
+        raise ValueError(f"n_top must be in [0, {SV_LOGPROBS_TOP_MAX}]")
+    f = torch.empty((4, R), dtype=torch.float32, device=dev)
+    tok = top = None
+    if n_top:
+        tok = torch.empty((R, n_top), dtype=torch.int32, device=dev)
+        top = torch.empty((R, n_top), dtype=torch.float32, device=dev)
+    s = _stream_of(stream, dev)
+    ws = _scratch("logprobs", dev, s, (R,))
+    at = f.data_ptr()
+    _call("spec_logprobs", dev, ctypes.byref(x), _ptr(tokens), _ptr(temperature), n_top, at,
+          at + 4 * R, at + 8 * R, at + 12 * R, _ptr(tok), _ptr(top), s.cuda_stream, _ptr(ws),
+          ws.numel())
+    return LogProbs(f[0], f[1], f[2], f[3], tok, top)
+
+
+def logprobs_grad(logits, tokens, max, logsum, entropy, grad_logprob, grad_entropy=None,
+                  temperature=None, *, out=None, stream=None):
+    """Gradient of a loss with respect to the logits, from its gradients with
+    respect to :func:`logprobs`' logprob and entropy ([rows] float32, either may
+    be None) and that call's max, logsum and entropy (needed with grad_entropy).
+
+    Returns ``out`` [rows, V] of the logits' dtype; it may be the logits
+    themselves.  Rows with token -1 get 0."""
+    x = _rows_desc(logits)
+    dev, (R, V) = logits.device, logits.shape
+    _vector(tokens, "tokens", torch.int32, R, dev)
+    _vector(max, "max", torch.float32, R, dev)
+    _vector(logsum, "logsum", torch.float32, R, dev)
+    _vector(entropy, "entropy", torch.float32, R, dev, optional=grad_entropy is None)
+    _vector(grad_logprob, "grad_logprob", torch.float32, R, dev, optional=True)
+    _vector(grad_entropy, "grad_entropy", torch.float32, R, dev, optional=True)
+    _vector(temperature, "temperature", torch.float32, R, dev, optional=True)
+    if out is None:
+        out = torch.empty((R, V), dtype=logits.dtype, device=dev)
+    out_stride = _rows2d(out, "out", logits.dtype, R, dev)
+    if tuple(out.shape) != (R, V):
+        raise ValueError(f"out must be {(R, V)}")
+    s = _stream_of(stream, dev)
+    _call("spec_logprobs_grad", dev, ctypes.byref(x), _ptr(tokens), _ptr(temperature), _ptr(max),
+          _ptr(logsum), _ptr(entropy), _ptr(grad_logprob), _ptr(grad_entropy), _ptr(out),
+          out_stride, s.cuda_stream)
+    return out
+
+
+# --------------------------------------------------------------------- errors
+def attention_error(stream=None, device=None):
+    """``(code, request, row)`` of the first failed request of the last
+    attention on this device (code 0: none).  Synchronises."""
+    return _error("attention", stream, device)
+
+
+def attention_weights_error(stream=None, device=None):
+    """The same of the last attention_weights."""
+    return _error("attention_weights", stream, device)
+
+
+def kv_evict_error(stream=None, device=None):
+    """The same of the last kv_evict."""
+    return _error("kv_evict", stream, device)
+
+
+def logprobs_error(stream=None, device=None):
+    """The same of the last logprobs; ``row`` is the first failed row."""
+    return _error("logprobs", stream, device)
