@@ -629,7 +629,12 @@ int spec_verify_get_error(const void* workspace, void* stream, int32_t* code, in
     while (at < n && st[at] == 0) ++at;
     int32_t c = at < n ? st[at] : 0;
     for (size_t i = n; i < n + extra; ++i)
-      if (st[i] >= 0 && size_t(st[i]) < at) {
+      if (st[i] < 0) {  // a CTA's failure, no request's
+        *code = -st[i];
+        if (request) *request = -1;
+        if (row) *row = -1;
+        return SV_OK;
+      } else if (size_t(st[i]) < at) {
         at = size_t(st[i]);
         c = SV_ERR_DATA_PAGE;
       }

@@ -10,6 +10,8 @@
 // one pass with the running maximum and sum of the softmax.  Positions outside
 // a request's keys are zero-filled, and a masked weight takes no part in the
 // product with V, so that what unused slots hold does not matter.
+#include <cmath>
+
 #include "sv_attn.cuh"
 
 namespace sv {
@@ -85,20 +87,6 @@ __device__ __forceinline__ void load_q(const AttnArgs& A, int t_off, int h, int 
       v = to_float<T>(q[int64_t(t_off + row / A.G) * A.q_ts +
                         int64_t(h * A.G + row % A.G) * A.q_hs + d]);
     sq[i] = v;
-  }
-}
-
-template <class T>
-__device__ void fail_all(const AttnArgs& A) {
-  // a batch whose rows cannot be told apart: every output is NaN
-  const float nan = __int_as_float(0x7fc00000);
-  const int64_t n = A.Rt * A.Hq;
-  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
-       i += int64_t(gridDim.x) * blockDim.x) {
-    const int64_t t = i / A.Hq, hq = i % A.Hq;
-    A.lse[i] = nan;
-    T* o = static_cast<T*>(A.out) + t * A.o_ts + hq * A.o_hs;
-    for (int d = 0; d < A.D; ++d) o[d] = from_float<T>(nan);
   }
 }
 
@@ -414,6 +402,13 @@ cudaError_t run_attn(const AttnArgs& A, bool weights, cudaStream_t s) {
 }
 
 constexpr int kCtasPerSm = 2;  // shared memory of the widest heads
+constexpr int kTcRows = 128;   // rows a unit of the tensor-core kernel
+
+// Heads and types that the tensor-core kernel takes.  A scale of 0 would turn
+// its masked scores into NaN.
+bool on_tensor_cores(const AttnArgs& A, int dtype) {
+  return dtype != SV_F32 && (A.D == 64 || A.D == 128 || A.D == 256) && A.scale2 != 0.0f;
+}
 
 struct AttnLayout {
   size_t status, split, ml, o, total;
@@ -437,19 +432,36 @@ AttnLayout attn_layout(int B, int D, int ctas, int mr) {
 
 size_t attn_workspace_bytes(int32_t B, int32_t D, int sms, bool weights) {
   const AttnLayout L = attn_layout(B, D, sms * kCtasPerSm, kMr);
-  return weights ? L.split : L.total;
+  if (weights) return L.split;
+  const AttnLayout T = attn_layout(B, D, sms, kTcRows);
+  return L.total > T.total ? L.total : T.total;
 }
 
 cudaError_t launch_attn(AttnArgs A, int dtype, bool weights, void* workspace, int sms,
                         cudaStream_t s) {
-  A.ctas = sms * kCtasPerSm;
-  const AttnLayout L = attn_layout(A.B, A.D, A.ctas, kMr);
+  const bool tc = !weights && on_tensor_cores(A, dtype);
+  A.ctas = tc ? sms : sms * kCtasPerSm;
+  const AttnLayout L = attn_layout(A.B, A.D, A.ctas, tc ? kTcRows : kMr);
   char* w = static_cast<char*>(workspace);
   A.hdr = reinterpret_cast<WsHeader*>(w);
   A.status = reinterpret_cast<int32_t*>(w + L.status);
   A.split = reinterpret_cast<AttnSplit*>(w + L.split);
   A.part_ml = reinterpret_cast<float2*>(w + L.ml);
   A.part_o = reinterpret_cast<float*>(w + L.o);
+  if (tc) {
+    auto aligned = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+    A.s_shift = -1;
+    for (int i = 0; i < 31; ++i)
+      if (A.S == 1 << i) A.s_shift = i;
+    A.q_vec = aligned(A.q) && A.q_ts % 8 == 0 && A.q_hs % 8 == 0;
+    A.out_vec = aligned(A.out);
+    A.q_flip = A.scale2 < 0.0f;
+    A.scale2 = fabsf(A.scale2);
+    const cudaError_t e = launch_attn_tc(A, dtype, s);
+    if (e != cudaSuccess) return e;
+    return dtype == SV_BF16 ? launch_join(attn_join_kernel<__nv_bfloat16, kTcRows>, A, s)
+                            : launch_join(attn_join_kernel<__half, kTcRows>, A, s);
+  }
   switch (dtype) {
     case SV_F32: return run_attn<float>(A, weights, s);
     case SV_BF16: return run_attn<__nv_bfloat16>(A, weights, s);

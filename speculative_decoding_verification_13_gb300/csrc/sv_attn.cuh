@@ -53,6 +53,10 @@ struct AttnArgs {
   int64_t score_stride, out_stride;
   int32_t score_cols;
   int32_t ctas;                   // grid of the main kernel
+  // the tensor-core kernel
+  int32_t s_shift;                // log2 of the page size, or -1
+  int32_t q_vec, out_vec;         // 16-byte aligned heads
+  int32_t q_flip;                 // the scale was negative: scale2 is its magnitude
 };
 
 #ifdef __CUDACC__
@@ -254,6 +258,23 @@ __device__ __forceinline__ const char* attn_key(const AttnArgs& A, int b, int n,
   return A.cache + page * A.page_bytes + int64_t(p % A.S) * A.entry_bytes;
 }
 
+template <class T>
+__device__ void fail_all(const AttnArgs& A) {
+  // a batch whose rows cannot be told apart: every output is NaN
+  const float nan = __int_as_float(0x7fc00000);
+  const int64_t n = A.Rt * A.Hq;
+  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+       i += int64_t(gridDim.x) * blockDim.x) {
+    const int64_t t = i / A.Hq, hq = i % A.Hq;
+    A.lse[i] = nan;
+    T* o = static_cast<T*>(A.out) + t * A.o_ts + hq * A.o_hs;
+    for (int d = 0; d < A.D; ++d) o[d] = from_float<T>(nan);
+  }
+}
+
 #endif  // __CUDACC__
+
+// The tensor-core kernel's share of a call (MR = 128, one CTA per SM).
+cudaError_t launch_attn_tc(const AttnArgs& A, int dtype, cudaStream_t s);
 
 }  // namespace sv

@@ -1,0 +1,754 @@
+// Attention over the paged KV cache on the fifth-generation tensor cores, for
+// bf16 and fp16 and heads of 64, 128 and 256.
+//
+// A unit is up to 128 query rows of one KV head, the M of the products:
+// S = Q K^T (128 x TN x D) and O += P V (128 x D x TN) per tile of TN = 8192/D
+// positions, so that a tile of K or of V is 16 KB.  Few rows leave most of M
+// idle, which costs nothing that matters: a tile's two products take about 500
+// cycles of the tensor cores, its 32 KB of K and V take about 1400 of an SM's
+// share of the HBM.
+//
+// One CTA per SM, over its piece of the line of tiles (sv_attn.cuh):
+//   warps 4-5  load: Q of a unit (two buffers) and, tile by tile, K and V rows
+//              gathered from their pages with 16-byte asynchronous copies into a
+//              ring of 16 KB slots, in the 128-byte swizzled layout that the
+//              tensor cores read (K along the head: K-major; V along the head:
+//              MN-major).  Positions outside the request's keys are zero-filled.
+//   warp 6     issues the products (one lane).  S has two accumulators: S of the
+//              next tile is computed while the softmax of this one runs.
+//   warps 0-3  softmax, one row a thread (the lanes of TMEM): scores from TMEM,
+//              running maximum, P rounded to the type (half a step of it, the
+//              one rounding of a weight; sums stay in 32 bits) back to TMEM over
+//              the scores, where the second product reads it as its A operand.
+//              O is rescaled only when a row's maximum has grown by more than
+//              2^8 since the last time: the stored maximum is then exact enough
+//              for P and the sum to stay in range, and most tiles skip it.
+// A warp without live rows only keeps the barriers' count.
+//
+// Tiles that some row of the unit sees in part (the drafts' triangle, a
+// window's edge): the masked weights are 0, but 0 times an infinite or NaN
+// value would still reach the row.  The softmax warps look through V of such a
+// tile; if it holds any, each row collects the signs of those that it sees,
+// they are replaced by 0 in the tile, and added to the row's O afterwards.
+//
+// Every wait is bounded; on expiry the CTA's status records it, its copies and
+// products land, and TMEM is freed.
+#include "sv_attn.cuh"
+#include "sv_tcgen05.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kTcThreads = 224;   // 4 softmax, 2 load, 1 product warp
+constexpr int kTcMr = 128;
+constexpr int kSlotBytes = 16384;
+constexpr int kLoaders = 64;
+constexpr int kLoadWarp = 4, kMmaWarp = 6;
+constexpr float kRescaleLog2 = 8.0f;
+
+template <int D>
+struct Shape {
+  static constexpr int TN = 8192 / D;
+  static constexpr int kQBytes = kTcMr * D * 2;
+  static constexpr int kSlots = D == 64 ? 11 : D == 128 ? 10 : 6;  // what shared memory holds
+  static constexpr int kLag = kSlots - 3;       // slots in flight before the oldest is awaited
+  static constexpr uint32_t kOCol = 2 * TN;     // TMEM columns: S0, S1, O
+  static constexpr uint32_t kTmemCols = 2 * TN + D <= 256 ? 256 : 512;
+  static constexpr size_t kSmem = 1024 + 2 * size_t(kQBytes) + size_t(kSlots) * kSlotBytes;
+};
+
+struct TcShared {
+  uint64_t full[11], empty[11];
+  uint64_t qfull[2], qempty[2], sfull[2], pfull[2], pvdone[2], ofree;
+  uint64_t rows, looked[2], drain;  // loaders among themselves; softmax warps among themselves
+  uint32_t tmem;
+  int abort;
+  int first_bad;
+  int bad[8];        // per unit, a ring: the unit needs a missing page
+  int dirty[2];      // per tile parity: 1 + the tile whose V holds a non-finite value
+};
+
+// One unit's part of a CTA's piece.
+struct Seg {
+  int b, t_off, h, row0, rows, first, count;
+  bool whole;
+  int64_t unit_end;   // tile of the line after the unit's last
+  AttnReq R;
+};
+
+template <int TN>
+struct Walk {
+  int64_t pos, end, base;
+  int b, t_off;
+  AttnReq R;
+  __device__ __forceinline__ Walk(const AttnArgs& A, const AttnPlan& P)
+      : pos(P.start), end(P.end), base(P.base), b(P.b), t_off(P.t_off) {
+    if (pos < end) R = attn_request<TN, kTcMr, false>(A, b);
+  }
+  __device__ __forceinline__ bool next(const AttnArgs& A, Seg& s) {
+    if (pos >= end) return false;
+    int64_t nt = attn_tiles<TN, kTcMr, false>(A, R);
+    while (pos >= base + nt) {
+      base += nt;
+      t_off += R.k + 1;
+      R = attn_request<TN, kTcMr, false>(A, ++b);
+      nt = attn_tiles<TN, kTcMr, false>(A, R);
+    }
+    const int64_t local = pos - base;
+    const int unit = int(local / R.ntiles);
+    s.b = b;
+    s.t_off = t_off;
+    s.first = int(local % R.ntiles);
+    const int64_t left = end - pos;
+    s.count = int(left < R.ntiles - s.first ? left : R.ntiles - s.first);
+    s.h = unit / R.mtiles;
+    s.row0 = (unit % R.mtiles) * kTcMr;
+    s.rows = min(kTcMr, (R.k + 1) * A.G - s.row0);
+    s.whole = s.first == 0 && s.count == R.ntiles;
+    s.unit_end = pos - s.first + R.ntiles;
+    s.R = R;
+    pos += s.count;
+    return true;
+  }
+};
+
+template <class T> struct Bits;
+template <> struct Bits<__nv_bfloat16> {
+  static constexpr uint32_t kFmt = 1, kExp = 0x7f807f80u, kOne = 0x00800080u, kExp1 = 0x7f80u,
+                            kMan1 = 0x007fu;
+  __device__ static uint32_t pack(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+template <> struct Bits<__half> {
+  static constexpr uint32_t kFmt = 0, kExp = 0x7c007c00u, kOne = 0x04000400u, kExp1 = 0x7c00u,
+                            kMan1 = 0x03ffu;
+  __device__ static uint32_t pack(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+// any of the two 16-bit values of w infinite or NaN
+template <class T>
+__device__ __forceinline__ bool any_nonfinite(uint32_t w) {
+  return (((w & Bits<T>::kExp) + Bits<T>::kOne) & 0x80008000u) != 0;
+}
+
+// Descriptor of an MN-major 16-bit tile with 128-byte swizzling: rows (of K)
+// of 128 bytes, 8-row groups 1024 bytes apart, blocks of 64 elements of MN
+// `block` bytes apart.
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t addr, uint32_t block) {
+  return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(block >> 4) << 16) |
+         (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Bounded wait; false, with the CTA's abort flag set, on expiry.
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, TcShared& S) {
+  if (mbar_wait_for(smem_addr(bar), parity, kWaitNs, &S.abort)) return true;
+  *reinterpret_cast<volatile int*>(&S.abort) = 1;
+  return false;
+}
+// The same for a whole warp, one answer for all its lanes.
+__device__ __forceinline__ bool tc_wait_warp(uint64_t* bar, uint32_t parity, TcShared& S) {
+  return __all_sync(0xffffffffu, tc_wait(bar, parity, S));
+}
+// Barrier of the four warps that count on `bar`, bounded like every other wait
+// (a warp that gave up would leave a hardware barrier waiting for ever).
+__device__ __forceinline__ bool tc_sync(uint64_t* bar, uint32_t parity, TcShared& S) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(bar));
+  return tc_wait_warp(bar, parity, S);
+}
+
+template <class T, int D>
+__global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnArgs A) {
+  using C = Shape<D>;
+  constexpr int TN = C::TN;
+  extern __shared__ unsigned char tc_smem_raw[];
+  __shared__ TcShared S;
+  __shared__ uint64_t s_addr[2][TN];   // a tile's row addresses (bit 0: a speculative entry)
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t smem0 = (smem_addr(tc_smem_raw) + 1023u) & ~1023u;
+  unsigned char* smem_p = tc_smem_raw + (smem0 - smem_addr(tc_smem_raw));
+  const uint32_t ring0 = smem0 + 2 * C::kQBytes;
+
+  if (tid == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(smem_addr(&S.full[i]), kLoaders / 32);
+      mbar_init(smem_addr(&S.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&S.qfull[i]), kLoaders / 32);
+      mbar_init(smem_addr(&S.qempty[i]), 1);
+      mbar_init(smem_addr(&S.sfull[i]), 1);
+      mbar_init(smem_addr(&S.pfull[i]), 4);
+      mbar_init(smem_addr(&S.pvdone[i]), 1);
+      S.dirty[i] = 0;
+    }
+    mbar_init(smem_addr(&S.ofree), 4);
+    mbar_init(smem_addr(&S.rows), kLoaders / 32);
+    mbar_init(smem_addr(&S.looked[0]), 4);
+    mbar_init(smem_addr(&S.looked[1]), 4);
+    mbar_init(smem_addr(&S.drain), 1);
+    fence_mbar_init();
+    S.abort = 0;
+    S.first_bad = INT32_MAX;
+    A.split[blockIdx.x].valid = 0;
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(&S.tmem)),
+                 "r"(C::kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  const AttnPlan P = attn_plan<TN, kTcMr, false, kTcThreads>(A);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem;
+  if (P.code) fail_all<T>(A);
+  const bool go = P.code == 0 && P.start < P.end;
+
+  if (go && warp >= kLoadWarp && warp < kMmaWarp) {
+    // ----------------------------------------------------------------- loads
+    const int lt = tid - kLoadWarp * 32;
+    constexpr int kChunks = D / 8;               // 16-byte chunks per row
+    constexpr int kRowStep = kLoaders / kChunks;  // rows per round
+    const int ch = lt % kChunks, row_in = lt / kChunks;
+    Walk<TN> walk(A, P);
+    Seg s;
+    uint32_t slot = 0, phase = 1;   // empty barriers: the first round passes at once
+    // Slots filled, and handed on to the consumers: a slot is handed on once it
+    // has landed, kLag slots behind the one being issued.
+    int64_t issued = 0, handed = 0;
+    uint32_t hand_slot = 0;
+    int unit = 0, tile_buf = 0;
+    uint32_t rows_phase = 0;
+    bool stop = false;
+    auto hand_on = [&]() {
+      fence_async_proxy();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&S.full[hand_slot]));
+      if (++hand_slot == C::kSlots) hand_slot = 0;
+      ++handed;
+    };
+    while (!stop && walk.next(A, s)) {
+      // Q: rows of a row-major swizzled tile per 64 elements of the head
+      const int qb = unit & 1;
+      if (lt == 0) S.bad[unit & 7] = s.R.code != 0;
+      if (unit >= 2 && handed < issued) {
+        // the buffer comes free by the products of slots that are still held
+        // back: hand them on rather than wait for it with them
+        const bool ready = __all_sync(
+            0xffffffffu, mbar_try_wait(smem_addr(&S.qempty[qb]), ((unit >> 1) & 1) ^ 1));
+        if (!ready) {
+          cp_async_wait<0>();
+          while (handed < issued) hand_on();
+        }
+      }
+      stop = !tc_wait_warp(&S.qempty[qb], ((unit >> 1) & 1) ^ 1, S) ||
+             !tc_sync(&S.rows, rows_phase, S);
+      if (stop) break;
+      rows_phase ^= 1;
+      {
+        const T* q = static_cast<const T*>(A.q);
+        const int live = (s.rows + 31) & ~31;
+        for (int r = row_in; r < live; r += kRowStep) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (r < s.rows) {
+            const int row = s.row0 + r;
+            const T* src = q + int64_t(s.t_off + row / A.G) * A.q_ts +
+                           int64_t(s.h * A.G + row % A.G) * A.q_hs + ch * 8;
+            if (A.q_vec) {
+              v = __ldg(reinterpret_cast<const uint4*>(src));
+            } else {
+              T e[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) e[i] = src[i];
+              v = *reinterpret_cast<uint4*>(e);
+            }
+            if (A.q_flip) {  // a negative scale: S of -q with its magnitude
+              v.x ^= 0x80008000u;
+              v.y ^= 0x80008000u;
+              v.z ^= 0x80008000u;
+              v.w ^= 0x80008000u;
+            }
+          }
+          *reinterpret_cast<uint4*>(smem_p + qb * C::kQBytes + (ch >> 3) * (kTcMr * 128) +
+                                    r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+        }
+        fence_async_proxy();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&S.qfull[qb]));
+      }
+      const int hi = s.R.code ? 0 : s.R.hi;
+      // address of a row; a tile's are found one tile ahead
+      constexpr int kAddr = (TN + kLoaders - 1) / kLoaders;  // rows per thread
+      auto address = [&](int p) -> uint64_t {
+        if (p >= hi) return 0;
+        const int64_t head = int64_t(s.h) * D * 2;
+        if (p >= s.R.n)
+          return reinterpret_cast<uint64_t>(A.spec + int64_t(s.b) * A.spec_req +
+                                            int64_t(p - s.R.n) * A.spec_tok + head) | 1;
+        const int col = A.s_shift >= 0 ? p >> A.s_shift : p / A.S;
+        const int page = __ldg(A.table + int64_t(s.b) * A.max_pages + col);
+        if (page < 0 || page >= A.num_pages) {
+          S.bad[unit & 7] = 1;
+          atomicMin(&S.first_bad, s.b);
+          return 0;
+        }
+        return reinterpret_cast<uint64_t>(A.cache + page * A.page_bytes +
+                                          int64_t(p - col * A.S) * A.entry_bytes + head);
+      };
+      const int p0 = (s.R.tile0 + s.first) * TN;
+      uint64_t next[kAddr];
+#pragma unroll
+      for (int i = 0; i < kAddr; ++i)
+        next[i] = i * kLoaders + lt < TN ? address(p0 + i * kLoaders + lt) : 0;
+      for (int t = 0; t < s.count && !stop; ++t) {
+#pragma unroll
+        for (int i = 0; i < kAddr; ++i)
+          if (i * kLoaders + lt < TN) s_addr[tile_buf][i * kLoaders + lt] = next[i];
+        if (!tc_sync(&S.rows, rows_phase, S)) {
+          stop = true;
+          break;
+        }
+        rows_phase ^= 1;
+        if (t + 1 < s.count) {
+#pragma unroll
+          for (int i = 0; i < kAddr; ++i)
+            next[i] =
+                i * kLoaders + lt < TN ? address(p0 + (t + 1) * TN + i * kLoaders + lt) : 0;
+        }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          if (!tc_wait_warp(&S.empty[slot], phase, S)) {
+            stop = true;
+            break;
+          }
+          const uint32_t dst0 = ring0 + slot * kSlotBytes + (ch >> 3) * (TN * 128);
+#pragma unroll
+          for (int i = 0; i < TN / kRowStep; ++i) {
+            const int r = row_in + i * kRowStep;
+            const uint64_t a = s_addr[tile_buf][r];
+            const uint64_t off = kv ? ((a & 1) ? A.entry_bytes : A.v_off) : 0;
+            const char* src = reinterpret_cast<const char*>((a & ~uint64_t(1)) + off) + ch * 16;
+            cp_async16(dst0 + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                       a ? src : reinterpret_cast<const char*>(A.k_per_req), a ? 16u : 0u);
+          }
+          cp_async_commit();
+          ++issued;
+          if (issued - handed > C::kLag) {
+            cp_async_wait<C::kLag>();
+            hand_on();
+          }
+          if (++slot == C::kSlots) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+        tile_buf ^= 1;
+      }
+      ++unit;
+    }
+    // the last slots, one by one: empty groups behind them move the wait along
+    for (int64_t groups = issued + 1; !stop && handed < issued; ++groups) {
+      cp_async_commit();
+      if (groups - C::kLag > handed) {
+        cp_async_wait<C::kLag>();
+        hand_on();
+      }
+    }
+    cp_async_wait<0>();
+  } else if (go && warp == kMmaWarp && lane == 0) {
+    // -------------------------------------------------------------- products
+    constexpr uint32_t kBase = (1u << 4) | (Bits<T>::kFmt << 7) | (Bits<T>::kFmt << 10) |
+                               (uint32_t(kTcMr >> 4) << 24);
+    constexpr uint32_t kIdescS = kBase | (uint32_t(TN >> 3) << 17);
+    constexpr uint32_t kIdescO = kBase | (uint32_t(D >> 3) << 17) | (1u << 16);
+    Walk<TN> walk(A, P);
+    Seg s;
+    int left = 0, unit = -1;     // tiles of the unit whose S is issued next, the unit
+    int64_t gs = 0;              // S products issued
+    auto issue_s = [&]() -> int {  // 0: no tile left, 1: issued, 2: the first of its unit, -1: gave up
+      int kind = 1;
+      if (left == 0) {
+        if (!walk.next(A, s)) return 0;
+        left = s.count;
+        ++unit;
+        kind = 2;
+        if (!tc_wait(&S.qfull[unit & 1], (unit >> 1) & 1, S)) return -1;
+      }
+      if (gs >= 2 && !tc_wait(&S.pvdone[gs & 1], ((gs - 2) >> 1) & 1, S)) return -1;
+      const int64_t use = 2 * gs;
+      const uint32_t slot = uint32_t(use % C::kSlots);
+      if (!tc_wait(&S.full[slot], (use / C::kSlots) & 1, S)) return -1;
+      tc_fence_after();
+      const uint32_t q = smem0 + (unit & 1) * C::kQBytes, k = ring0 + slot * kSlotBytes;
+      const uint32_t d = tmem + uint32_t(gs & 1) * TN;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+        mma_ss(d, sw128_desc(q + (c >> 2) * (kTcMr * 128) + (c & 3) * 32),
+               sw128_desc(k + (c >> 2) * (TN * 128) + (c & 3) * 32), kIdescS, c != 0);
+      umma_commit(smem_addr(&S.sfull[gs & 1]));
+      umma_commit(smem_addr(&S.empty[slot]));
+      if (--left == 0) umma_commit(smem_addr(&S.qempty[unit & 1]));
+      ++gs;
+      return kind;
+    };
+    int kind = issue_s();
+    int unit_pv = -1;
+    bool ok = kind > 0;
+    for (int64_t g = 0; ok; ++g) {
+      const int next = issue_s();
+      if (next < 0) break;
+      const int64_t use = 2 * g + 1;
+      const uint32_t slot = uint32_t(use % C::kSlots);
+      if (kind == 2) {
+        ++unit_pv;
+        // O still holds the unit before until its rows have been read
+        if (unit_pv > 0 && !tc_wait(&S.ofree, (unit_pv - 1) & 1, S)) break;
+      }
+      if (!tc_wait(&S.full[slot], (use / C::kSlots) & 1, S)) break;
+      if (!tc_wait(&S.pfull[g & 1], (g >> 1) & 1, S)) break;
+      tc_fence_after();
+      const uint32_t v = ring0 + slot * kSlotBytes, p = tmem + uint32_t(g & 1) * TN;
+#pragma unroll
+      for (int c = 0; c < TN / 16; ++c)
+        mma_ts(tmem + C::kOCol, p + c * 8, sw128_mn_desc(v + c * 2048, TN * 128), kIdescO,
+               (c != 0) || kind != 2);
+      umma_commit(smem_addr(&S.pvdone[g & 1]));
+      umma_commit(smem_addr(&S.empty[slot]));
+      kind = next;
+      ok = next > 0;
+    }
+    if (*reinterpret_cast<volatile int*>(&S.abort)) {
+      // every product issued must finish before TMEM is freed
+      umma_commit(smem_addr(&S.drain));
+      mbar_wait_for(smem_addr(&S.drain), 0);
+    }
+  } else if (go && warp < kLoadWarp) {
+    // --------------------------------------------------------------- softmax
+    const uint32_t lanes = tmem + (uint32_t(warp * 32) << 16);
+    Walk<TN> walk(A, P);
+    Seg s;
+    int64_t g = 0;
+    int unit = 0;
+    uint32_t looked = 0, collected = 0;
+    bool stop = false;
+    while (!stop && walk.next(A, s)) {
+      const bool active = warp * 32 < s.rows;
+      const bool live = tid < s.rows;
+      const int row = s.row0 + tid;
+      const int tok = row / A.G;
+      const int at = s.R.at0 + tok;
+      const int row_hi = live ? (s.R.code ? 0 : min(at + 1, s.R.hi)) : INT32_MAX;
+      const int row_lo = live && A.window > 0 ? max(0, at - A.window + 1) : 0;
+      // the range that every row of the unit sees: tiles inside it need no mask
+      const int at_first = s.R.at0 + s.row0 / A.G;
+      const int at_last = s.R.at0 + (s.row0 + s.rows - 1) / A.G;
+      const int all_hi = s.R.code ? 0 : min(at_first + 1, s.R.hi);
+      const int all_lo = A.window > 0 ? max(0, at_last - A.window + 1) : 0;
+      float m = -INFINITY, l = 0.f;   // m: the maximum that the sum and O refer to
+      for (int t = 0; t < s.count; ++t, ++g) {
+        const int p0 = (s.R.tile0 + s.first + t) * TN;
+        const int buf = int(g & 1);
+        const bool edge = p0 < all_lo || p0 + TN > all_hi;
+        const uint32_t scol = lanes + uint32_t(buf) * TN;
+        if (!tc_wait_warp(&S.sfull[buf], (g >> 1) & 1, S)) {
+          stop = true;
+          break;
+        }
+        tc_fence_after();
+        uint32_t plus[D / 32], minus[D / 32];   // non-finite values that the row sees
+        bool dirty = false;
+        if (edge) {
+          // V of this tile: 128 bytes a thread
+          const int64_t use = 2 * g + 1;
+          const uint32_t slot = uint32_t(use % C::kSlots);
+          if (!tc_wait_warp(&S.full[slot], (use / C::kSlots) & 1, S)) {
+            stop = true;
+            break;
+          }
+          uint4* v = reinterpret_cast<uint4*>(smem_p + 2 * C::kQBytes + slot * kSlotBytes);
+          bool found = false;
+#pragma unroll
+          for (int i = 0; i < kSlotBytes / 16 / 128; ++i) {
+            const uint4 w = v[i * 128 + tid];
+            found |= any_nonfinite<T>(w.x) | any_nonfinite<T>(w.y) | any_nonfinite<T>(w.z) |
+                     any_nonfinite<T>(w.w);
+          }
+          if (found) S.dirty[buf] = int(g) + 1;
+          if (!tc_sync(&S.looked[0], looked, S)) {
+            stop = true;
+            break;
+          }
+          looked ^= 1;
+          dirty = *reinterpret_cast<volatile int*>(&S.dirty[buf]) == int(g) + 1;
+          if (dirty) {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) plus[i] = minus[i] = 0;
+            const uint32_t* vw = reinterpret_cast<const uint32_t*>(v);
+            for (int c = 0; c < TN; ++c) {
+              if (p0 + c < row_lo || p0 + c >= row_hi) continue;
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i)
+                for (int e = 0; e < 32; e += 2) {
+                  const int d = i * 32 + e;
+                  const uint32_t w = vw[(d >> 6) * (TN * 32) + c * 32 +
+                                        ((((d & 63) >> 3) ^ (c & 7)) << 2) + ((d & 7) >> 1)];
+                  if (!any_nonfinite<T>(w)) continue;
+#pragma unroll
+                  for (int x = 0; x < 2; ++x) {
+                    const uint32_t y = (w >> (16 * x)) & 0xffffu;
+                    if ((y & Bits<T>::kExp1) != Bits<T>::kExp1) continue;
+                    const bool isnan = (y & Bits<T>::kMan1) != 0;
+                    if (isnan || !(y & 0x8000u)) plus[i] |= 1u << (e + x);
+                    if (isnan || (y & 0x8000u)) minus[i] |= 1u << (e + x);
+                  }
+                }
+            }
+            if (!tc_sync(&S.looked[1], collected, S)) {
+              stop = true;
+              break;
+            }
+            collected ^= 1;
+            for (int i = 0; i < kSlotBytes / 16 / 128; ++i) {
+              uint32_t* w = reinterpret_cast<uint32_t*>(v + i * 128 + tid);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const uint32_t e = ((w[x] & Bits<T>::kExp) + Bits<T>::kOne) & 0x80008000u;
+                w[x] &= ~((e >> 15) * 0xffffu);
+              }
+            }
+            fence_async_proxy();
+          }
+        }
+        if (active) {
+          float x[TN];
+#pragma unroll
+          for (int c = 0; c < TN / 32; ++c)
+            tmem_ld32(scol + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[c * 32]));
+          tmem_ld_wait();
+          if (edge) {
+#pragma unroll
+            for (int c = 0; c < TN; ++c)
+              x[c] = p0 + c >= row_lo && p0 + c < row_hi ? x[c] : -INFINITY;
+          }
+          float top = x[0];
+#pragma unroll
+          for (int c = 1; c < TN; ++c) top = fmaxf(top, x[c]);
+          top *= A.scale2;   // scale2 >= 0; 0 times an infinite score is NaN and ignored here
+          const float grown = fmaxf(m, top);
+          const bool rescale = live && grown > m + kRescaleLog2;
+          if (__any_sync(0xffffffffu, rescale)) {
+            // all rows of the warp move to their present maximum
+            const float f = m == -INFINITY ? 0.f : exp2f(m - grown);
+            if (t > 0) {
+              if (!tc_wait_warp(&S.pvdone[(g - 1) & 1], ((g - 1) >> 1) & 1, S)) {
+                stop = true;
+                break;
+              }
+              tc_fence_after();
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(lanes + C::kOCol + c * 32, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st32(lanes + C::kOCol + c * 32, o);
+              }
+            }
+            l *= f;
+            m = grown;
+          }
+          const float sh = m == -INFINITY ? 0.f : m;
+          const uint64_t sc2 = pk2(A.scale2, A.scale2), sh2 = pk2(-sh, -sh);
+          uint64_t sum = pk2(0.f, 0.f);
+          uint32_t pw[TN / 2];
+#pragma unroll
+          for (int c = 0; c < TN; c += 2) {
+            float a, b2;
+            upk2(fma2(pk2(x[c], x[c + 1]), sc2, sh2), a, b2);
+            a = ex2_approx(a);
+            b2 = ex2_approx(b2);
+            sum = add2(sum, pk2(a, b2));
+            pw[c / 2] = Bits<T>::pack(a, b2);
+          }
+          float s0, s1;
+          upk2(sum, s0, s1);
+          l += s0 + s1;
+          if constexpr (TN / 2 >= 32) {
+#pragma unroll
+            for (int c = 0; c < TN / 64; ++c)
+              tmem_st32(scol + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&pw[c * 32]));
+          } else {
+            tmem_st16(scol, *reinterpret_cast<uint32_t(*)[16]>(&pw[0]));
+          }
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&S.pfull[buf]));
+        if (dirty) {
+          if (!tc_wait_warp(&S.pvdone[buf], (g >> 1) & 1, S)) {
+            stop = true;
+            break;
+          }
+          tc_fence_after();
+          if (active) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(lanes + C::kOCol + c * 32, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                float v = __uint_as_float(o[e]);
+                if ((plus[c] >> e) & 1) v += INFINITY;
+                if ((minus[c] >> e) & 1) v -= INFINITY;
+                o[e] = __float_as_uint(v);
+              }
+              tmem_st32(lanes + C::kOCol + c * 32, o);
+            }
+            tmem_st_wait();
+          }
+          tc_fence_before();
+        }
+      }
+      if (stop) break;
+      // ------------------------------------------------- the unit's rows
+      if (!tc_wait_warp(&S.pvdone[(g - 1) & 1], ((g - 1) >> 1) & 1, S)) break;
+      tc_fence_after();
+      if (active) {
+        const bool bad = *reinterpret_cast<volatile int*>(&S.bad[unit & 7]) != 0;
+        const float nan = __int_as_float(0x7fc00000);
+        const int slot = s.first == 0 ? 1 : 0;
+        const int64_t pr = (int64_t(blockIdx.x) * 2 + slot) * kTcMr + tid;
+        const int hq = s.h * A.G + row % A.G;
+        const int64_t trow = int64_t(s.t_off) + tok;
+        T* out = static_cast<T*>(A.out) + trow * A.o_ts + int64_t(hq) * A.o_hs;
+        const float inv = bad ? nan : l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(lanes + C::kOCol + c * 32, o);
+          tmem_ld_wait();
+          if (!live) continue;
+          if (s.whole) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              w[e] = Bits<T>::pack(__uint_as_float(o[2 * e]) * inv,
+                                   __uint_as_float(o[2 * e + 1]) * inv);
+            if (A.out_vec) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<uint4*>(out + c * 32 + e * 8) =
+                    make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const uint16_t h = uint16_t(w[e / 2] >> (16 * (e & 1)));
+                out[c * 32 + e] = *reinterpret_cast<const T*>(&h);
+              }
+            }
+          } else {
+            uint4* po = reinterpret_cast<uint4*>(A.part_o + pr * D + c * 32);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              po[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        }
+        if (live) {
+          if (s.whole)
+            A.lse[trow * A.Hq + hq] =
+                bad ? nan : (m == -INFINITY ? 0.f : m * kAttnLn2) + logf(l);
+          else
+            A.part_ml[pr] = make_float2(bad ? nan : m, l);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&S.ofree));
+      if (tid == 0 && !s.whole && s.first == 0) {
+        AttnSplit& u = A.split[blockIdx.x];
+        u.last = attn_owner(P, s.unit_end - 1);
+        u.t_off = s.t_off;
+        u.h = s.h;
+        u.row0 = s.row0;
+        u.rows = s.rows;
+        u.valid = 1;
+      }
+      ++unit;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0)
+    A.status[A.B + blockIdx.x] = S.abort ? -SV_ERR_TIMEOUT : S.first_bad;
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(C::kTmemCols));
+  }
+}
+
+template <class T, int D>
+cudaError_t run(const AttnArgs& A, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(
+      attn_tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Shape<D>::kSmem));
+  if (e != cudaSuccess) return e;
+  attn_tc_kernel<T, D><<<A.ctas, kTcThreads, Shape<D>::kSmem, s>>>(A);
+  return cudaGetLastError();
+}
+
+template <class T>
+cudaError_t run_dim(const AttnArgs& A, cudaStream_t s) {
+  switch (A.D) {
+    case 64: return run<T, 64>(A, s);
+    case 128: return run<T, 128>(A, s);
+    default: return run<T, 256>(A, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc(const AttnArgs& A, int dtype, cudaStream_t s) {
+  return dtype == SV_BF16 ? run_dim<__nv_bfloat16>(A, s) : run_dim<__half>(A, s);
+}
+
+}  // namespace sv

@@ -66,7 +66,7 @@ struct WsHeader {
 // counter to clear before the call, the lowest failed entry whatever the order
 // of the CTAs): err_row entries follow the header, which are rows (err_req 0)
 // or requests (err_req 1), then n_active entries that name the first request
-// with a missing page, INT32_MAX for none.
+// with a missing page (INT32_MAX for none) or, negative, their own error.
 constexpr int32_t kStatusList = -1;
 
 struct RowStat {
