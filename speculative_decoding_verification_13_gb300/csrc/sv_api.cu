@@ -112,6 +112,7 @@ int attn_args(const sv_kv_cache* cache, int32_t dtype, int32_t layer, int32_t kv
   A.v_off = A.entry_bytes * c.page_size;
   A.page_bytes = A.v_off * 2 * c.n_layers;
   A.cache = static_cast<const char*>(c.data) + A.v_off * 2 * layer;
+  A.layer_row = 2 * layer * c.page_size;
   A.num_pages = c.num_pages;
   A.spec_tok = A.entry_bytes * 2 * c.n_layers;
   A.spec_req = A.spec_tok * slots;

@@ -9,11 +9,18 @@
 // share of the HBM.
 //
 // One CTA per SM, over its piece of the line of tiles (sv_attn.cuh):
-//   warps 4-5  load: Q of a unit (two buffers) and, tile by tile, K and V rows
-//              gathered from their pages with 16-byte asynchronous copies into a
-//              ring of 16 KB slots, in the 128-byte swizzled layout that the
-//              tensor cores read (K along the head: K-major; V along the head:
-//              MN-major).  Positions outside the request's keys are zero-filled.
+//   warps 4-5  load: Q of a unit (two buffers, plain loads) and, tile by tile, K
+//              (warp 4) and V (warp 5) into a ring of 16 KB slots, in the
+//              128-byte swizzled layout that the tensor cores read (K along the
+//              head: K-major; V along the head: MN-major).  Rows are gathered
+//              by the copy engine, four rows of 128 bytes an instruction, one
+//              instruction a lane: pages of any size, and a row number of -1
+//              (a position outside the request's keys, a missing page) is
+//              filled with zeros.  A tile that holds speculative entries comes
+//              by 16-byte copies of the lanes instead.  (All tiles came that way
+//              at first: the fence that such copies need before the tensor
+//              cores may read them waits for every copy in flight, and 32
+//              requests with up to 15 drafts took 229 us.)
 //   warp 6     issues the products (one lane).  S has two accumulators: S of the
 //              next tile is computed while the softmax of this one runs.
 //   warps 0-3  softmax, one row a thread (the lanes of TMEM): scores from TMEM,
@@ -51,7 +58,6 @@ struct Shape {
   static constexpr int TN = 8192 / D;
   static constexpr int kQBytes = kTcMr * D * 2;
   static constexpr int kSlots = D == 64 ? 11 : D == 128 ? 10 : 6;  // what shared memory holds
-  static constexpr int kLag = kSlots - 3;       // slots in flight before the oldest is awaited
   static constexpr uint32_t kOCol = 2 * TN;     // TMEM columns: S0, S1, O
   static constexpr uint32_t kTmemCols = 2 * TN + D <= 256 ? 256 : 512;
   static constexpr size_t kSmem = 1024 + 2 * size_t(kQBytes) + size_t(kSlots) * kSlotBytes;
@@ -60,7 +66,7 @@ struct Shape {
 struct TcShared {
   uint64_t full[11], empty[11];
   uint64_t qfull[2], qempty[2], sfull[2], pfull[2], pvdone[2], ofree;
-  uint64_t rows, looked[2], drain;  // loaders among themselves; softmax warps among themselves
+  uint64_t rows, looked[2], drain;  // load warps among themselves, softmax warps among themselves
   uint32_t tmem;
   int abort;
   int first_bad;
@@ -164,17 +170,29 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Bounded wait; false, with the CTA's abort flag set, on expiry.
+// Four rows of the tensor map's matrix, 128 bytes from column x of each.
+__device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, int x,
+                                        const int (&row)[4], uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]),
+      "r"(row[3]), "r"(bar)
+      : "memory");
+}
+
+// Bounded wait; false, with the CTA's abort flag set, on expiry.  The clock of
+// the bound is read only after a number of polls: a wait here is short, and
+// reading the global timer would be most of it.
 __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, TcShared& S) {
-  if (mbar_wait_for(smem_addr(bar), parity, kWaitNs, &S.abort)) return true;
+  const uint32_t at = smem_addr(bar);
+  for (int i = 0; i < 128; ++i)
+    if (mbar_try_wait(at, parity)) return true;
+  if (mbar_wait_for(at, parity, kWaitNs, &S.abort)) return true;
   *reinterpret_cast<volatile int*>(&S.abort) = 1;
   return false;
 }
@@ -191,12 +209,13 @@ __device__ __forceinline__ bool tc_sync(uint64_t* bar, uint32_t parity, TcShared
 }
 
 template <class T, int D>
-__global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnArgs A) {
+__global__ void __launch_bounds__(kTcThreads, 1)
+    attn_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const AttnArgs A) {
   using C = Shape<D>;
   constexpr int TN = C::TN;
   extern __shared__ unsigned char tc_smem_raw[];
   __shared__ TcShared S;
-  __shared__ uint64_t s_addr[2][TN];   // a tile's row addresses (bit 0: a speculative entry)
+  __shared__ const char* s_addr[2][TN];   // row addresses of a tile with speculative entries
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t smem0 = (smem_addr(tc_smem_raw) + 1023u) & ~1023u;
   unsigned char* smem_p = tc_smem_raw + (smem0 - smem_addr(tc_smem_raw));
@@ -204,7 +223,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnArgs A
 
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(smem_addr(&S.full[i]), kLoaders / 32);
+      mbar_init(smem_addr(&S.full[i]), 1);
       mbar_init(smem_addr(&S.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -241,41 +260,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnArgs A
 
   if (go && warp >= kLoadWarp && warp < kMmaWarp) {
     // ----------------------------------------------------------------- loads
-    const int lt = tid - kLoadWarp * 32;
-    constexpr int kChunks = D / 8;               // 16-byte chunks per row
-    constexpr int kRowStep = kLoaders / kChunks;  // rows per round
-    const int ch = lt % kChunks, row_in = lt / kChunks;
+    const int kv = warp - kLoadWarp;              // 0: K, 1: V
+    constexpr int kParts = D / 64;                // 128-byte parts of a row
+    const int group = lane / kParts, part = lane % kParts;  // this lane's four rows, and part
+    constexpr int kChunks = D / 8;                // 16-byte chunks of a row
     Walk<TN> walk(A, P);
     Seg s;
-    uint32_t slot = 0, phase = 1;   // empty barriers: the first round passes at once
-    // Slots filled, and handed on to the consumers: a slot is handed on once it
-    // has landed, kLag slots behind the one being issued.
-    int64_t issued = 0, handed = 0;
-    uint32_t hand_slot = 0;
-    int unit = 0, tile_buf = 0;
+    uint32_t slot = kv, phase = 1;  // empty barriers: the first round passes at once
+    int unit = 0;
     uint32_t rows_phase = 0;
     bool stop = false;
-    auto hand_on = [&]() {
-      fence_async_proxy();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&S.full[hand_slot]));
-      if (++hand_slot == C::kSlots) hand_slot = 0;
-      ++handed;
-    };
     while (!stop && walk.next(A, s)) {
       // Q: rows of a row-major swizzled tile per 64 elements of the head
       const int qb = unit & 1;
-      if (lt == 0) S.bad[unit & 7] = s.R.code != 0;
-      if (unit >= 2 && handed < issued) {
-        // the buffer comes free by the products of slots that are still held
-        // back: hand them on rather than wait for it with them
-        const bool ready = __all_sync(
-            0xffffffffu, mbar_try_wait(smem_addr(&S.qempty[qb]), ((unit >> 1) & 1) ^ 1));
-        if (!ready) {
-          cp_async_wait<0>();
-          while (handed < issued) hand_on();
-        }
-      }
+      if (tid == kLoadWarp * 32) S.bad[unit & 7] = s.R.code != 0;
       stop = !tc_wait_warp(&S.qempty[qb], ((unit >> 1) & 1) ^ 1, S) ||
              !tc_sync(&S.rows, rows_phase, S);
       if (stop) break;
@@ -283,7 +281,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnArgs A
       {
         const T* q = static_cast<const T*>(A.q);
         const int live = (s.rows + 31) & ~31;
-        for (int r = row_in; r < live; r += kRowStep) {
+        const int lt = tid - kLoadWarp * 32, ch = lt % kChunks;
+        for (int r = lt / kChunks; r < live; r += kLoaders / kChunks) {
           uint4 v = make_uint4(0, 0, 0, 0);
           if (r < s.rows) {
             const int row = s.row0 + r;
@@ -312,84 +311,87 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnArgs A
         if (lane == 0) mbar_arrive(smem_addr(&S.qfull[qb]));
       }
       const int hi = s.R.code ? 0 : s.R.hi;
-      // address of a row; a tile's are found one tile ahead
-      constexpr int kAddr = (TN + kLoaders - 1) / kLoaders;  // rows per thread
-      auto address = [&](int p) -> uint64_t {
-        if (p >= hi) return 0;
-        const int64_t head = int64_t(s.h) * D * 2;
-        if (p >= s.R.n)
-          return reinterpret_cast<uint64_t>(A.spec + int64_t(s.b) * A.spec_req +
-                                            int64_t(p - s.R.n) * A.spec_tok + head) | 1;
-        const int col = A.s_shift >= 0 ? p >> A.s_shift : p / A.S;
-        const int page = __ldg(A.table + int64_t(s.b) * A.max_pages + col);
-        if (page < 0 || page >= A.num_pages) {
-          S.bad[unit & 7] = 1;
-          atomicMin(&S.first_bad, s.b);
-          return 0;
-        }
-        return reinterpret_cast<uint64_t>(A.cache + page * A.page_bytes +
-                                          int64_t(p - col * A.S) * A.entry_bytes + head);
-      };
+      const int cached = min(s.R.n, hi);
       const int p0 = (s.R.tile0 + s.first) * TN;
-      uint64_t next[kAddr];
+      const int32_t* table = A.table + int64_t(s.b) * A.max_pages;
+      auto column = [&](int p) { return A.s_shift >= 0 ? p >> A.s_shift : p / A.S; };
+      auto missing = [&](int page) {
+        if (page >= 0 && page < A.num_pages) return false;
+        S.bad[unit & 7] = 1;
+        atomicMin(&S.first_bad, s.b);
+        return true;
+      };
+      // The pages of a tile's rows are read one tile ahead, so that nothing
+      // waits for the block table.  Pages of a multiple of four positions: the
+      // lane's four rows share one.
+      int page[4];
+      auto pages = [&](int t) {
+        const int p = p0 + t * TN + group * 4;
 #pragma unroll
-      for (int i = 0; i < kAddr; ++i)
-        next[i] = i * kLoaders + lt < TN ? address(p0 + i * kLoaders + lt) : 0;
-      for (int t = 0; t < s.count && !stop; ++t) {
+        for (int j = 0; j < 4; ++j)
+          if ((j == 0 || A.s_odd) && p + j < cached) page[j] = __ldg(table + column(p + j));
+      };
+      pages(0);
+      for (int t = 0; t < s.count; ++t) {
+        const int pt = p0 + t * TN;
+        int row[4];
 #pragma unroll
-        for (int i = 0; i < kAddr; ++i)
-          if (i * kLoaders + lt < TN) s_addr[tile_buf][i * kLoaders + lt] = next[i];
-        if (!tc_sync(&S.rows, rows_phase, S)) {
+        for (int j = 0; j < 4; ++j) {
+          const int p = pt + group * 4 + j;
+          const int pg = A.s_odd ? page[j] : page[0];
+          row[j] = -1;
+          if (p < cached && !missing(pg))
+            row[j] = pg * A.page_rows + kv * A.S + (p - column(p) * A.S);
+        }
+        if (t + 1 < s.count) pages(t + 1);
+        if (!tc_wait_warp(&S.empty[slot], phase, S)) {
           stop = true;
           break;
         }
-        rows_phase ^= 1;
-        if (t + 1 < s.count) {
-#pragma unroll
-          for (int i = 0; i < kAddr; ++i)
-            next[i] =
-                i * kLoaders + lt < TN ? address(p0 + (t + 1) * TN + i * kLoaders + lt) : 0;
+        const uint32_t dst = ring0 + slot * kSlotBytes, bar = smem_addr(&S.full[slot]);
+        if (pt + TN <= cached || hi <= cached) {
+          if (lane == 0) mbar_arrive_expect_tx(bar, kSlotBytes);
+          __syncwarp();
+          gather4(dst + part * (TN * 128) + group * 512, &rows_map, s.h * D + part * 64, row, bar);
+        } else {
+          // some rows are speculative entries
+          for (int r = lane; r < TN; r += 32) {
+            const int p = pt + r;
+            const char* a = nullptr;
+            if (p >= cached) {
+              if (p < hi)
+                a = A.spec + int64_t(s.b) * A.spec_req + int64_t(p - s.R.n) * A.spec_tok +
+                    kv * A.entry_bytes;
+            } else {
+              const int pg = __ldg(table + column(p));
+              if (!missing(pg))
+                a = A.cache + pg * A.page_bytes + kv * A.v_off +
+                    (p - column(p) * A.S) * A.entry_bytes;
+            }
+            s_addr[kv][r] = a ? a + int64_t(s.h) * D * 2 : nullptr;
+          }
+          __syncwarp();
+          const int ch = lane % kChunks;
+#pragma unroll 8
+          for (int r = lane / kChunks; r < TN; r += 32 / kChunks) {
+            const char* src = s_addr[kv][r];
+            cp_async16(dst + (ch >> 3) * (TN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                       src ? src + ch * 16 : reinterpret_cast<const char*>(A.k_per_req),
+                       src ? 16u : 0u);
+          }
+          cp_async_wait_all();
+          fence_async_proxy();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar);
         }
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          if (!tc_wait_warp(&S.empty[slot], phase, S)) {
-            stop = true;
-            break;
-          }
-          const uint32_t dst0 = ring0 + slot * kSlotBytes + (ch >> 3) * (TN * 128);
-#pragma unroll
-          for (int i = 0; i < TN / kRowStep; ++i) {
-            const int r = row_in + i * kRowStep;
-            const uint64_t a = s_addr[tile_buf][r];
-            const uint64_t off = kv ? ((a & 1) ? A.entry_bytes : A.v_off) : 0;
-            const char* src = reinterpret_cast<const char*>((a & ~uint64_t(1)) + off) + ch * 16;
-            cp_async16(dst0 + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                       a ? src : reinterpret_cast<const char*>(A.k_per_req), a ? 16u : 0u);
-          }
-          cp_async_commit();
-          ++issued;
-          if (issued - handed > C::kLag) {
-            cp_async_wait<C::kLag>();
-            hand_on();
-          }
-          if (++slot == C::kSlots) {
-            slot = 0;
-            phase ^= 1;
-          }
+        slot += 2;
+        if (slot >= C::kSlots) {
+          slot -= C::kSlots;
+          phase ^= 1;
         }
-        tile_buf ^= 1;
       }
       ++unit;
     }
-    // the last slots, one by one: empty groups behind them move the wait along
-    for (int64_t groups = issued + 1; !stop && handed < issued; ++groups) {
-      cp_async_commit();
-      if (groups - C::kLag > handed) {
-        cp_async_wait<C::kLag>();
-        hand_on();
-      }
-    }
-    cp_async_wait<0>();
   } else if (go && warp == kMmaWarp && lane == 0) {
     // -------------------------------------------------------------- products
     constexpr uint32_t kBase = (1u << 4) | (Bits<T>::kFmt << 7) | (Bits<T>::kFmt << 10) |
@@ -727,12 +729,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnArgs A
   }
 }
 
+// The whole cache as a matrix of entries, [pages * layers * 2 * page size, E],
+// for gathers of 128 bytes from four rows.
+bool rows_map(CUtensorMap* map, const AttnArgs& A, bool bf16) {
+  const EncodeTiledFn fn = tensor_map_encoder();
+  if (!fn) return false;
+  const uint64_t elems = uint64_t(A.entry_bytes) / 2;
+  const cuuint64_t dims[2] = {elems, cuuint64_t(A.num_pages > 0 ? A.num_pages : 1) *
+                                         cuuint64_t(A.page_rows) - cuuint64_t(A.layer_row)};
+  const cuuint64_t strides[1] = {cuuint64_t(A.entry_bytes)};
+  const cuuint32_t box[2] = {64, 1}, step[2] = {1, 1};
+  // an empty pool has no page that a row could come from: any address will do
+  const void* base = A.num_pages > 0 ? static_cast<const void*>(A.cache) : A.spec;
+  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+            const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <class T, int D>
 cudaError_t run(const AttnArgs& A, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(
       attn_tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Shape<D>::kSmem));
   if (e != cudaSuccess) return e;
-  attn_tc_kernel<T, D><<<A.ctas, kTcThreads, Shape<D>::kSmem, s>>>(A);
+  CUtensorMap map;
+  if (!rows_map(&map, A, Bits<T>::kFmt != 0)) return cudaErrorInvalidValue;
+  attn_tc_kernel<T, D><<<A.ctas, kTcThreads, Shape<D>::kSmem, s>>>(map, A);
   return cudaGetLastError();
 }
 

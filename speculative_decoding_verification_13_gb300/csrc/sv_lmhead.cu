@@ -19,8 +19,6 @@
 // exp((z - max) / T).  Per-chunk partial statistics go to global memory and a
 // second kernel combines them per row.  Every wait is bounded; on expiry the
 // kernel records SV_ERR_TIMEOUT, lets its copies and MMAs land and frees TMEM.
-#include <cuda.h>
-
 #include "sv_internal.cuh"
 #include "sv_tcgen05.cuh"
 
@@ -294,28 +292,9 @@ __global__ void lmhead_combine_kernel(const LmArgs A, float* out_m, double* out_
   out_xt[r] = xt;
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    fn = reinterpret_cast<EncodeTiledFn>(p);
-  }
-  return fn;
-}
-
 // A [rows, K] bf16 row-major matrix as TMA tiles of box_rows x 64, 128-byte swizzled.
 bool make_map(CUtensorMap* map, const void* data, int rows, int K, int box_rows) {
-  EncodeTiledFn fn = encode_fn();
+  EncodeTiledFn fn = tensor_map_encoder();
   if (!fn) return false;
   const cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(rows)};
   const cuuint64_t strides[1] = {cuuint64_t(K) * 2};

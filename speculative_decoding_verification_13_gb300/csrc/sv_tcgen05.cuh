@@ -1,10 +1,32 @@
-// Small wrappers of the fifth-generation tensor cores' instructions (tcgen05),
-// shared by the kernels that use them.
+// Small wrappers of the fifth-generation tensor cores' instructions (tcgen05)
+// and of tensor maps, shared by the kernels that use them.
 #pragma once
+
+#include <cuda.h>
 
 #include "sv_internal.cuh"
 
 namespace sv {
+
+// The driver's encoder of tensor maps, null if it cannot be had.
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiledFn tensor_map_encoder() {
+  static EncodeTiledFn fn = nullptr;
+  if (!fn) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    fn = reinterpret_cast<EncodeTiledFn>(p);
+  }
+  return fn;
+}
 
 // Shared-memory matrix descriptor of a K-major 16-bit tile with 128-byte
 // swizzling: rows of 128 bytes, 8-row groups 1024 bytes apart.
