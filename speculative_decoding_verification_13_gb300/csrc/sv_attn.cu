@@ -405,7 +405,7 @@ constexpr int kCtasPerSm = 2;  // shared memory of the widest heads
 constexpr int kTcRows = 128;   // rows a unit of the tensor-core kernel
 
 // Heads and types that the tensor-core kernel takes.  A scale of 0 would turn
-// its masked scores into NaN; its rows are gathered by 32-bit numbers.
+// its masked scores into NaN; its entries are numbered in 32 bits.
 bool on_tensor_cores(const AttnArgs& A, int dtype) {
   return dtype != SV_F32 && (A.D == 64 || A.D == 128 || A.D == 256) && A.scale2 != 0.0f &&
          (A.num_pages > 0 || A.spec) &&
@@ -455,7 +455,6 @@ cudaError_t launch_attn(AttnArgs A, int dtype, bool weights, void* workspace, in
     A.s_shift = -1;
     for (int i = 0; i < 31; ++i)
       if (A.S == 1 << i) A.s_shift = i;
-    A.s_odd = A.S % 4 != 0;
     A.page_rows = int32_t(A.page_bytes / A.entry_bytes);
     A.q_vec = aligned(A.q) && A.q_ts % 8 == 0 && A.q_hs % 8 == 0;
     A.out_vec = aligned(A.out);

@@ -55,7 +55,7 @@ struct AttnArgs {
   int32_t ctas;                   // grid of the main kernel
   // the tensor-core kernel
   int32_t s_shift;                // log2 of the page size, or -1
-  int32_t s_odd;                  // pages that are no multiple of four positions
+  int32_t box_rows;               // entries per box of the copy engine, 0: no boxes
   int32_t page_rows, layer_row;   // entries per page, entries before the layer's first
   int32_t q_vec, out_vec;         // 16-byte aligned heads
   int32_t q_flip;                 // the scale was negative: scale2 is its magnitude

@@ -12,15 +12,18 @@
 //   warps 4-5  load: Q of a unit (two buffers, plain loads) and, tile by tile, K
 //              (warp 4) and V (warp 5) into a ring of 16 KB slots, in the
 //              128-byte swizzled layout that the tensor cores read (K along the
-//              head: K-major; V along the head: MN-major).  Rows are gathered
-//              by the copy engine, four rows of 128 bytes an instruction, one
-//              instruction a lane: pages of any size, and a row number of -1
-//              (a position outside the request's keys, a missing page) is
-//              filled with zeros.  A tile that holds speculative entries comes
-//              by 16-byte copies of the lanes instead.  (All tiles came that way
-//              at first: the fence that such copies need before the tensor
-//              cores may read them waits for every copy in flight, and 32
-//              requests with up to 15 drafts took 229 us.)
+//              head: K-major; V along the head: MN-major).  The copy engine
+//              moves what a page has of the tile in boxes of 128 bytes by the
+//              page's rows, one box a lane.  Tiles that are not whole (the end
+//              of the cache, speculative entries) and pages of other than a
+//              multiple of 8 positions come by 16-byte asynchronous copies of
+//              the lanes, which fill positions outside the request's keys with
+//              zeros; the product warp's fence orders them before its reads.
+//              Measured on 32 requests with up to 15 drafts: all tiles by
+//              16-byte copies with the fence on the writing side, which waits
+//              for every copy in flight, 229 us; rows gathered by the copy
+//              engine, four an instruction, of which it takes one in about 50
+//              cycles, 264 us.
 //   warp 6     issues the products (one lane).  S has two accumulators: S of the
 //              next tile is computed while the softmax of this one runs.
 //   warps 0-3  softmax, one row a thread (the lanes of TMEM): scores from TMEM,
@@ -170,18 +173,17 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ void cp_async_wait_all() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
+// This lane's arrival on a barrier, made when its copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// Four rows of the tensor map's matrix, 128 bytes from column x of each.
-__device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, int x,
-                                        const int (&row)[4], uint32_t bar) {
+__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                         uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]),
-      "r"(row[3]), "r"(bar)
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
 
@@ -223,7 +225,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(smem_addr(&S.full[i]), 1);
+      mbar_init(smem_addr(&S.full[i]), 32);  // the lanes of a load warp
       mbar_init(smem_addr(&S.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -262,7 +264,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ----------------------------------------------------------------- loads
     const int kv = warp - kLoadWarp;              // 0: K, 1: V
     constexpr int kParts = D / 64;                // 128-byte parts of a row
-    const int group = lane / kParts, part = lane % kParts;  // this lane's four rows, and part
+    const int part = lane % kParts, box0 = lane / kParts * A.box_rows;  // this lane's box
+    const bool boxes = A.box_rows > 0 && box0 < TN;
     constexpr int kChunks = D / 8;                // 16-byte chunks of a row
     Walk<TN> walk(A, P);
     Seg s;
@@ -321,68 +324,71 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         atomicMin(&S.first_bad, s.b);
         return true;
       };
-      // The pages of a tile's rows are read one tile ahead, so that nothing
-      // waits for the block table.  Pages of a multiple of four positions: the
-      // lane's four rows share one.
-      int page[4];
-      auto pages = [&](int t) {
-        const int p = p0 + t * TN + group * 4;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if ((j == 0 || A.s_odd) && p + j < cached) page[j] = __ldg(table + column(p + j));
+      // The page of a tile's box is read one tile ahead, so that nothing waits
+      // for the block table.
+      int page = -1;
+      auto next_page = [&](int t) {
+        const int p = p0 + t * TN + box0;
+        if (boxes && p < cached) page = __ldg(table + column(p));
       };
-      pages(0);
+      next_page(0);
       for (int t = 0; t < s.count; ++t) {
         const int pt = p0 + t * TN;
-        int row[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int p = pt + group * 4 + j;
-          const int pg = A.s_odd ? page[j] : page[0];
-          row[j] = -1;
-          if (p < cached && !missing(pg))
-            row[j] = pg * A.page_rows + kv * A.S + (p - column(p) * A.S);
-        }
-        if (t + 1 < s.count) pages(t + 1);
+        const int pg = page;
+        if (t + 1 < s.count) next_page(t + 1);
         if (!tc_wait_warp(&S.empty[slot], phase, S)) {
           stop = true;
           break;
         }
         const uint32_t dst = ring0 + slot * kSlotBytes, bar = smem_addr(&S.full[slot]);
-        if (pt + TN <= cached || hi <= cached) {
+        if (A.box_rows > 0 && pt + TN <= cached) {
           if (lane == 0) mbar_arrive_expect_tx(bar, kSlotBytes);
+          else mbar_arrive(bar);
           __syncwarp();
-          gather4(dst + part * (TN * 128) + group * 512, &rows_map, s.h * D + part * 64, row, bar);
+          if (boxes) {
+            const int p = pt + box0;
+            // a missing page: a box outside the matrix is all zeros
+            const int row = missing(pg) ? -A.box_rows
+                                        : pg * A.page_rows + kv * A.S + (p - column(p) * A.S);
+            box_load(dst + part * (TN * 128) + box0 * 128, &rows_map, s.h * D + part * 64, row,
+                     bar);
+          }
         } else {
-          // some rows are speculative entries
+          __syncwarp();
           for (int r = lane; r < TN; r += 32) {
             const int p = pt + r;
-            const char* a = nullptr;
+            const char* a = nullptr;   // stays null for a row that is filled with zeros
             if (p >= cached) {
               if (p < hi)
                 a = A.spec + int64_t(s.b) * A.spec_req + int64_t(p - s.R.n) * A.spec_tok +
                     kv * A.entry_bytes;
             } else {
-              const int pg = __ldg(table + column(p));
-              if (!missing(pg))
-                a = A.cache + pg * A.page_bytes + kv * A.v_off +
+              const int one = __ldg(table + column(p));
+              if (!missing(one))
+                a = A.cache + one * A.page_bytes + kv * A.v_off +
                     (p - column(p) * A.S) * A.entry_bytes;
             }
             s_addr[kv][r] = a ? a + int64_t(s.h) * D * 2 : nullptr;
           }
           __syncwarp();
           const int ch = lane % kChunks;
-#pragma unroll 8
-          for (int r = lane / kChunks; r < TN; r += 32 / kChunks) {
-            const char* src = s_addr[kv][r];
-            cp_async16(dst + (ch >> 3) * (TN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                       src ? src + ch * 16 : reinterpret_cast<const char*>(A.k_per_req),
-                       src ? 16u : 0u);
+          // addresses of eight rounds first: the copies keep their order, so a
+          // load between two of them would be waited for each time
+          constexpr int kStep = 32 / kChunks;   // rows per round
+#pragma unroll
+          for (int r0 = 0; r0 < TN; r0 += 8 * kStep) {
+            const char* src[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) src[i] = s_addr[kv][r0 + i * kStep + lane / kChunks];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = r0 + i * kStep + lane / kChunks;
+              cp_async16(dst + (ch >> 3) * (TN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                         src[i] ? src[i] + ch * 16 : reinterpret_cast<const char*>(A.k_per_req),
+                         src[i] ? 16u : 0u);
+            }
           }
-          cp_async_wait_all();
-          fence_async_proxy();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar);
+          cp_async_arrive(bar);
         }
         slot += 2;
         if (slot >= C::kSlots) {
@@ -392,6 +398,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       ++unit;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (go && warp == kMmaWarp && lane == 0) {
     // -------------------------------------------------------------- products
     constexpr uint32_t kBase = (1u << 4) | (Bits<T>::kFmt << 7) | (Bits<T>::kFmt << 10) |
@@ -415,6 +422,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int64_t use = 2 * gs;
       const uint32_t slot = uint32_t(use % C::kSlots);
       if (!tc_wait(&S.full[slot], (use / C::kSlots) & 1, S)) return -1;
+      fence_async_proxy();
       tc_fence_after();
       const uint32_t q = smem0 + (unit & 1) * C::kQBytes, k = ring0 + slot * kSlotBytes;
       const uint32_t d = tmem + uint32_t(gs & 1) * TN;
@@ -443,6 +451,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (!tc_wait(&S.full[slot], (use / C::kSlots) & 1, S)) break;
       if (!tc_wait(&S.pfull[g & 1], (g >> 1) & 1, S)) break;
+      fence_async_proxy();
       tc_fence_after();
       const uint32_t v = ring0 + slot * kSlotBytes, p = tmem + uint32_t(g & 1) * TN;
 #pragma unroll
@@ -729,8 +738,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-// The whole cache as a matrix of entries, [pages * layers * 2 * page size, E],
-// for gathers of 128 bytes from four rows.
+// The cache from the layer's first entry on as a matrix of entries of E
+// elements, moved in boxes of 128 bytes by box_rows entries.
 bool rows_map(CUtensorMap* map, const AttnArgs& A, bool bf16) {
   const EncodeTiledFn fn = tensor_map_encoder();
   if (!fn) return false;
@@ -738,7 +747,7 @@ bool rows_map(CUtensorMap* map, const AttnArgs& A, bool bf16) {
   const cuuint64_t dims[2] = {elems, cuuint64_t(A.num_pages > 0 ? A.num_pages : 1) *
                                          cuuint64_t(A.page_rows) - cuuint64_t(A.layer_row)};
   const cuuint64_t strides[1] = {cuuint64_t(A.entry_bytes)};
-  const cuuint32_t box[2] = {64, 1}, step[2] = {1, 1};
+  const cuuint32_t box[2] = {64, cuuint32_t(A.box_rows > 0 ? A.box_rows : 8)}, step[2] = {1, 1};
   // an empty pool has no page that a row could come from: any address will do
   const void* base = A.num_pages > 0 ? static_cast<const void*>(A.cache) : A.spec;
   return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
@@ -753,8 +762,17 @@ cudaError_t run(const AttnArgs& A, cudaStream_t s) {
       attn_tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Shape<D>::kSmem));
   if (e != cudaSuccess) return e;
   CUtensorMap map;
-  if (!rows_map(&map, A, Bits<T>::kFmt != 0)) return cudaErrorInvalidValue;
-  attn_tc_kernel<T, D><<<A.ctas, kTcThreads, Shape<D>::kSmem, s>>>(map, A);
+  AttnArgs B = A;
+  // rows of a page that lie in one tile, whole groups of 8 of the swizzled layout
+  int rows = A.S, rest = Shape<D>::TN;
+  while (rest) {
+    const int r = rows % rest;
+    rows = rest;
+    rest = r;
+  }
+  B.box_rows = rows % 8 == 0 ? rows : 0;
+  if (!rows_map(&map, B, Bits<T>::kFmt != 0)) return cudaErrorInvalidValue;
+  attn_tc_kernel<T, D><<<A.ctas, kTcThreads, Shape<D>::kSmem, s>>>(map, B);
   return cudaGetLastError();
 }
 
