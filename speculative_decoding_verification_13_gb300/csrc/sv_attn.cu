@@ -11,6 +11,7 @@
 // a request's keys are zero-filled, and a masked weight takes no part in the
 // product with V, so that what unused slots hold does not matter.
 #include <cmath>
+#include <numeric>
 
 #include "sv_attn.cuh"
 
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const AttnArgs A) {
     }
     if (!whole && first == 0 && tid == 0) {
       AttnSplit& sp_ = A.split[blockIdx.x];
-      sp_.last = attn_owner(P, pos + R.ntiles - 1);
+      sp_.last = attn_owner(A, P, pos + R.ntiles - 1);
       sp_.t_off = t_off;
       sp_.h = h;
       sp_.row0 = row0;
@@ -256,10 +257,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   const AttnSplit u = A.split[c0];
   if (!u.valid) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int nseg = u.last - c0 + 1;
+  const int nseg = (u.last - c0) / A.hg + 1;
   for (int r = blockIdx.y * (kJoinThreads / 32) + warp; r < u.rows;
        r += kJoinSplit * (kJoinThreads / 32)) {
-    auto slot = [&](int s) { return (int64_t(c0 + s) * 2 + (s == 0 ? 1 : 0)) * MR + r; };
+    auto slot = [&](int s) { return (int64_t(c0 + s * A.hg) * 2 + (s == 0 ? 1 : 0)) * MR + r; };
     float m = -INFINITY;
     for (int s = lane; s < nseg; s += 32) m = fmax_nan(m, A.part_ml[slot(s)].x);
 #pragma unroll
@@ -443,6 +444,7 @@ cudaError_t launch_attn(AttnArgs A, int dtype, bool weights, void* workspace, in
                         cudaStream_t s) {
   const bool tc = !weights && on_tensor_cores(A, dtype);
   A.ctas = tc ? sms : sms * kCtasPerSm;
+  A.hg = tc ? std::gcd(A.ctas, A.Hkv) : 1;
   const AttnLayout L = attn_layout(A.B, A.D, A.ctas, tc ? kTcRows : kMr);
   char* w = static_cast<char*>(workspace);
   A.hdr = reinterpret_cast<WsHeader*>(w);

@@ -12,6 +12,11 @@
 // kernel in order of position.  A CTA holds at most two partials: of the unit
 // it begins in (slot 0, begun by an earlier CTA) and of the unit it ends in
 // (slot 1, begun by itself).
+//
+// hg KV heads (a divisor of their number and of the CTAs') can have a line of
+// their own each: hg neighbouring CTAs then walk the same positions of
+// different heads at the same time, and the pieces of an entry that lie side by
+// side in memory are read together.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -53,6 +58,7 @@ struct AttnArgs {
   int64_t score_stride, out_stride;
   int32_t score_cols;
   int32_t ctas;                   // grid of the main kernel
+  int32_t hg;                     // heads with a line of their own, 1 or more
   // the tensor-core kernel
   int32_t s_shift;                // log2 of the page size, or -1
   int32_t box_rows;               // entries per box of the copy engine, 0: no boxes
@@ -136,13 +142,13 @@ struct AttnPlan {
   int64_t start, end;  // this CTA's
   int64_t base;      // tiles before request b
   int b, t_off;      // the request `start` lies in, query tokens before it
-  int ctas;          // CTAs that have tiles
+  int ctas;          // pieces that have tiles
   int code, code_b;  // a data error of the whole batch, and its request
 };
 
 template <int TN, int MR, bool WEIGHTS>
 __device__ __forceinline__ int64_t attn_tiles(const AttnArgs& A, const AttnReq& r) {
-  return WEIGHTS ? int64_t(r.ntiles) : int64_t(A.Hkv) * r.mtiles * r.ntiles;
+  return WEIGHTS ? int64_t(r.ntiles) : int64_t(A.Hkv / A.hg) * r.mtiles * r.ntiles;
 }
 
 // All threads of the block call this.  CTA 0 records the requests' errors.
@@ -200,8 +206,9 @@ __device__ AttnPlan attn_plan(const AttnArgs& A) {
   }
   AttnPlan P;
   P.total = total;
-  P.ctas = int(total < A.ctas ? total : int64_t(A.ctas));
-  const int c = blockIdx.x;
+  const int pieces = A.ctas / A.hg;
+  P.ctas = int(total < pieces ? total : int64_t(pieces));
+  const int c = blockIdx.x / A.hg;
   P.start = c < P.ctas ? total * c / P.ctas : total;
   P.end = c < P.ctas ? total * (c + 1) / P.ctas : total;
   int64_t base = wt + it - tiles;
@@ -242,9 +249,9 @@ __device__ AttnPlan attn_plan(const AttnArgs& A) {
   return P;
 }
 
-// The CTA that owns tile x of the line.
-__device__ __forceinline__ int attn_owner(const AttnPlan& P, int64_t x) {
-  return int(((x + 1) * P.ctas - 1) / P.total);
+// The CTA of this one's heads that owns tile x of the line.
+__device__ __forceinline__ int attn_owner(const AttnArgs& A, const AttnPlan& P, int64_t x) {
+  return int(((x + 1) * P.ctas - 1) / P.total) * A.hg + int(blockIdx.x) % A.hg;
 }
 
 // Address of key p of request b (head 0, K), null where its page is missing.

@@ -10,7 +10,7 @@
 //
 // One CTA per SM, over its piece of the line of tiles (sv_attn.cuh):
 //   warps 4-5  load: Q of a unit (two buffers, plain loads) and, tile by tile, K
-//              (warp 4) and V (warp 5) into a ring of 16 KB slots, in the
+//              (warp 4) and V (warp 5) into a ring of slots, in the
 //              128-byte swizzled layout that the tensor cores read (K along the
 //              head: K-major; V along the head: MN-major).  The copy engine
 //              moves what a page has of the tile in boxes of 128 bytes by the
@@ -24,8 +24,8 @@
 //              for every copy in flight, 229 us; rows gathered by the copy
 //              engine, four an instruction, of which it takes one in about 50
 //              cycles, 264 us.
-//   warp 6     issues the products (one lane).  S has two accumulators: S of the
-//              next tile is computed while the softmax of this one runs.
+//   warp 6     issues the products (one lane).  S has three accumulators, so that
+//              S of the next tiles does not wait for the product of this one.
 //   warps 0-3  softmax, one row a thread (the lanes of TMEM): scores from TMEM,
 //              running maximum, P rounded to the type (half a step of it, the
 //              one rounding of a weight; sums stay in 32 bits) back to TMEM over
@@ -51,30 +51,58 @@ namespace {
 
 constexpr int kTcThreads = 224;   // 4 softmax, 2 load, 1 product warp
 constexpr int kTcMr = 128;
-constexpr int kSlotBytes = 16384;
+constexpr int kBufs = 3;          // S accumulators, each then the P of its tile
 constexpr int kLoaders = 64;
 constexpr int kLoadWarp = 4, kMmaWarp = 6;
 constexpr float kRescaleLog2 = 8.0f;
 
 template <int D>
 struct Shape {
-  static constexpr int TN = 8192 / D;
+  static constexpr int TN = D == 256 ? 64 : 128;
+  static constexpr int kSlotBytes = TN * D * 2;
   static constexpr int kQBytes = kTcMr * D * 2;
-  static constexpr int kSlots = D == 64 ? 11 : D == 128 ? 10 : 6;  // what shared memory holds
-  static constexpr uint32_t kOCol = 2 * TN;     // TMEM columns: S0, S1, O
-  static constexpr uint32_t kTmemCols = 2 * TN + D <= 256 ? 256 : 512;
-  static constexpr size_t kSmem = 1024 + 2 * size_t(kQBytes) + size_t(kSlots) * kSlotBytes;
+  static constexpr int kQBufs = D == 256 ? 1 : 2;
+  static constexpr int kSlots = D == 64 ? 11 : 5;  // what shared memory holds
+  static constexpr uint32_t kOCol = kBufs * TN;     // TMEM columns: the S accumulators, then O
+  static constexpr size_t kSmem =
+      1024 + kQBufs * size_t(kQBytes) + size_t(kSlots) * kSlotBytes;
 };
+constexpr uint32_t kTmemCols = 512;
 
 struct TcShared {
   uint64_t full[11], empty[11];
-  uint64_t qfull[2], qempty[2], sfull[2], pfull[2], pvdone[2], ofree;
+  uint64_t qfull[2], qempty[2], sfull[kBufs], pfull[kBufs], pvdone[kBufs], ofree;
   uint64_t rows, looked[2], drain;  // load warps among themselves, softmax warps among themselves
   uint32_t tmem;
   int abort;
   int first_bad;
   int bad[8];        // per unit, a ring: the unit needs a missing page
-  int dirty[2];      // per tile parity: 1 + the tile whose V holds a non-finite value
+  int copied[11];    // per slot: filled by the lanes' copies, not by the copy engine
+  int dirty[kBufs];  // per S buffer: 1 + the tile whose V holds a non-finite value
+};
+
+// A place in the ring and the phase of its barriers, one tile (K and V) a step.
+template <int N>
+struct Slot {
+  uint32_t at, phase;
+  __device__ __forceinline__ void step() {
+    at += 2;
+    if (at >= N) {
+      at -= N;
+      phase ^= 1;
+    }
+  }
+};
+
+// One of the S buffers and the phase of its barriers, one tile a step.
+struct Buf {
+  uint32_t at = 0, phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++at == kBufs) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
 };
 
 // One unit's part of a CTA's piece.
@@ -110,7 +138,7 @@ struct Walk {
     s.first = int(local % R.ntiles);
     const int64_t left = end - pos;
     s.count = int(left < R.ntiles - s.first ? left : R.ntiles - s.first);
-    s.h = unit / R.mtiles;
+    s.h = unit / R.mtiles * A.hg + int(blockIdx.x) % A.hg;
     s.row0 = (unit % R.mtiles) * kTcMr;
     s.rows = min(kTcMr, (R.k + 1) * A.G - s.row0);
     s.whole = s.first == 0 && s.count == R.ntiles;
@@ -152,20 +180,32 @@ __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t addr, uint32_t block)
          (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t acc) {
+// The products and their commits are issued by one lane of a warp that runs
+// them as a whole: predicated instructions, no branch, so that descriptors stay
+// in the warp's uniform registers (one lane in a branch of its own had to move
+// every operand there: about 100 cycles a product).
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b,
+                                       uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n.reg .pred p, e;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 e, %5, 0;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b,
+                                       uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n.reg .pred p, e;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 e, %5, 0;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n.reg .pred e;\nsetp.ne.b32 e, %1, 0;\n"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          smem_addr(bar)),
+      "r"(lead)
       : "memory");
 }
 
@@ -217,11 +257,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   constexpr int TN = C::TN;
   extern __shared__ unsigned char tc_smem_raw[];
   __shared__ TcShared S;
-  __shared__ const char* s_addr[2][TN];   // row addresses of a tile with speculative entries
+  __shared__ const char* s_addr[2][64];   // row addresses of a tile with speculative entries
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t smem0 = (smem_addr(tc_smem_raw) + 1023u) & ~1023u;
   unsigned char* smem_p = tc_smem_raw + (smem0 - smem_addr(tc_smem_raw));
-  const uint32_t ring0 = smem0 + 2 * C::kQBytes;
+  const uint32_t ring0 = smem0 + C::kQBufs * C::kQBytes;
+  constexpr int kSlotBytes = C::kSlotBytes;
 
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
@@ -231,6 +272,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&S.qfull[i]), kLoaders / 32);
       mbar_init(smem_addr(&S.qempty[i]), 1);
+    }
+    for (int i = 0; i < kBufs; ++i) {
       mbar_init(smem_addr(&S.sfull[i]), 1);
       mbar_init(smem_addr(&S.pfull[i]), 4);
       mbar_init(smem_addr(&S.pvdone[i]), 1);
@@ -249,7 +292,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(&S.tmem)),
-                 "r"(C::kTmemCols));
+                 "r"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   const AttnPlan P = attn_plan<TN, kTcMr, false, kTcThreads>(A);
@@ -269,15 +312,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr int kChunks = D / 8;                // 16-byte chunks of a row
     Walk<TN> walk(A, P);
     Seg s;
-    uint32_t slot = kv, phase = 1;  // empty barriers: the first round passes at once
+    Slot<C::kSlots> at{uint32_t(kv), 1};  // empty barriers: the first round passes at once
     int unit = 0;
     uint32_t rows_phase = 0;
     bool stop = false;
     while (!stop && walk.next(A, s)) {
       // Q: rows of a row-major swizzled tile per 64 elements of the head
-      const int qb = unit & 1;
+      const int qb = unit % C::kQBufs;
       if (tid == kLoadWarp * 32) S.bad[unit & 7] = s.R.code != 0;
-      stop = !tc_wait_warp(&S.qempty[qb], ((unit >> 1) & 1) ^ 1, S) ||
+      stop = !tc_wait_warp(&S.qempty[qb], ((unit / C::kQBufs) & 1) ^ 1, S) ||
              !tc_sync(&S.rows, rows_phase, S);
       if (stop) break;
       rows_phase ^= 1;
@@ -336,14 +379,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int pt = p0 + t * TN;
         const int pg = page;
         if (t + 1 < s.count) next_page(t + 1);
-        if (!tc_wait_warp(&S.empty[slot], phase, S)) {
+        const uint32_t slot = at.at;
+        if (!tc_wait_warp(&S.empty[slot], at.phase, S)) {
           stop = true;
           break;
         }
         const uint32_t dst = ring0 + slot * kSlotBytes, bar = smem_addr(&S.full[slot]);
         if (A.box_rows > 0 && pt + TN <= cached) {
-          if (lane == 0) mbar_arrive_expect_tx(bar, kSlotBytes);
-          else mbar_arrive(bar);
+          if (lane == 0) {
+            S.copied[slot] = 0;
+            mbar_arrive_expect_tx(bar, kSlotBytes);
+          } else {
+            mbar_arrive(bar);
+          }
           __syncwarp();
           if (boxes) {
             const int p = pt + box0;
@@ -354,61 +402,72 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                      bar);
           }
         } else {
-          __syncwarp();
-          for (int r = lane; r < TN; r += 32) {
-            const int p = pt + r;
-            const char* a = nullptr;   // stays null for a row that is filled with zeros
-            if (p >= cached) {
-              if (p < hi)
-                a = A.spec + int64_t(s.b) * A.spec_req + int64_t(p - s.R.n) * A.spec_tok +
-                    kv * A.entry_bytes;
-            } else {
-              const int one = __ldg(table + column(p));
-              if (!missing(one))
-                a = A.cache + one * A.page_bytes + kv * A.v_off +
-                    (p - column(p) * A.S) * A.entry_bytes;
-            }
-            s_addr[kv][r] = a ? a + int64_t(s.h) * D * 2 : nullptr;
-          }
-          __syncwarp();
           const int ch = lane % kChunks;
-          // addresses of eight rounds first: the copies keep their order, so a
-          // load between two of them would be waited for each time
           constexpr int kStep = 32 / kChunks;   // rows per round
 #pragma unroll
-          for (int r0 = 0; r0 < TN; r0 += 8 * kStep) {
-            const char* src[8];
+          for (int half = 0; half < TN; half += 64) {
+            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) src[i] = s_addr[kv][r0 + i * kStep + lane / kChunks];
+            for (int r = lane; r < 64; r += 32) {
+              const int p = pt + half + r;
+              const char* a = nullptr;   // stays null for a row that is filled with zeros
+              if (p >= cached) {
+                if (p < hi)
+                  a = A.spec + int64_t(s.b) * A.spec_req + int64_t(p - s.R.n) * A.spec_tok +
+                      kv * A.entry_bytes;
+              } else {
+                const int one = __ldg(table + column(p));
+                if (!missing(one))
+                  a = A.cache + one * A.page_bytes + kv * A.v_off +
+                      (p - column(p) * A.S) * A.entry_bytes;
+              }
+              s_addr[kv][r] = a ? a + int64_t(s.h) * D * 2 : nullptr;
+            }
+            __syncwarp();
+            // addresses of eight rounds first: the copies keep their order, so a
+            // load between two of them would be waited for each time
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = r0 + i * kStep + lane / kChunks;
-              cp_async16(dst + (ch >> 3) * (TN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                         src[i] ? src[i] + ch * 16 : reinterpret_cast<const char*>(A.k_per_req),
-                         src[i] ? 16u : 0u);
+            for (int r0 = 0; r0 < 64; r0 += 8 * kStep) {
+              const char* src[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) src[i] = s_addr[kv][r0 + i * kStep + lane / kChunks];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int r = half + r0 + i * kStep + lane / kChunks;
+                cp_async16(dst + (ch >> 3) * (TN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                           src[i] ? src[i] + ch * 16 : reinterpret_cast<const char*>(A.k_per_req),
+                           src[i] ? 16u : 0u);
+              }
             }
           }
+          if (lane == 0) S.copied[slot] = 1;
           cp_async_arrive(bar);
         }
-        slot += 2;
-        if (slot >= C::kSlots) {
-          slot -= C::kSlots;
-          phase ^= 1;
-        }
+        at.step();
       }
       ++unit;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (go && warp == kMmaWarp && lane == 0) {
+  } else if (go && warp == kMmaWarp) {
     // -------------------------------------------------------------- products
     constexpr uint32_t kBase = (1u << 4) | (Bits<T>::kFmt << 7) | (Bits<T>::kFmt << 10) |
                                (uint32_t(kTcMr >> 4) << 24);
     constexpr uint32_t kIdescS = kBase | (uint32_t(TN >> 3) << 17);
     constexpr uint32_t kIdescO = kBase | (uint32_t(D >> 3) << 17) | (1u << 16);
+    const uint32_t lead = lane == 0;
+    Slot<C::kSlots> k_slot{0, 0}, v_slot{1, 0};
     Walk<TN> walk(A, P);
     Seg s;
     int left = 0, unit = -1;     // tiles of the unit whose S is issued next, the unit
-    int64_t gs = 0;              // S products issued
+    Buf sb, pb;                  // buffers of the next S and of the next P
+    // The fence that orders the lanes' copies before the products' reads takes
+    // as long as the products in flight: only slots that were filled by them.
+    auto slot_copied = [&](uint32_t i) {
+      return *reinterpret_cast<volatile int*>(&S.copied[i]) != 0;
+    };
+    // descriptors of the first Q buffer and slot; others lie a constant away
+    const uint64_t q_desc = sw128_desc(smem0), k_desc = sw128_desc(ring0);
+    const uint64_t v_desc = sw128_mn_desc(ring0, TN * 128);
     auto issue_s = [&]() -> int {  // 0: no tile left, 1: issued, 2: the first of its unit, -1: gave up
       int kind = 1;
       if (left == 0) {
@@ -416,66 +475,73 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         left = s.count;
         ++unit;
         kind = 2;
-        if (!tc_wait(&S.qfull[unit & 1], (unit >> 1) & 1, S)) return -1;
+        if (!tc_wait_warp(&S.qfull[unit % C::kQBufs], (unit / C::kQBufs) & 1, S)) return -1;
       }
-      if (gs >= 2 && !tc_wait(&S.pvdone[gs & 1], ((gs - 2) >> 1) & 1, S)) return -1;
-      const int64_t use = 2 * gs;
-      const uint32_t slot = uint32_t(use % C::kSlots);
-      if (!tc_wait(&S.full[slot], (use / C::kSlots) & 1, S)) return -1;
-      fence_async_proxy();
+      // the buffer's last P has been read (the first round passes at once)
+      if (!tc_wait_warp(&S.pvdone[sb.at], sb.phase ^ 1, S)) return -1;
+      const uint32_t slot = k_slot.at;
+      if (!tc_wait_warp(&S.full[slot], k_slot.phase, S)) return -1;
+      if (slot_copied(slot)) fence_async_proxy();
       tc_fence_after();
-      const uint32_t q = smem0 + (unit & 1) * C::kQBytes, k = ring0 + slot * kSlotBytes;
-      const uint32_t d = tmem + uint32_t(gs & 1) * TN;
+      const uint64_t q = q_desc + uint32_t((unit % C::kQBufs) * (C::kQBytes >> 4));
+      const uint64_t k = k_desc + slot * (kSlotBytes >> 4);
+      const uint32_t d = tmem + sb.at * TN;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c)
-        mma_ss(d, sw128_desc(q + (c >> 2) * (kTcMr * 128) + (c & 3) * 32),
-               sw128_desc(k + (c >> 2) * (TN * 128) + (c & 3) * 32), kIdescS, c != 0);
-      umma_commit(smem_addr(&S.sfull[gs & 1]));
-      umma_commit(smem_addr(&S.empty[slot]));
-      if (--left == 0) umma_commit(smem_addr(&S.qempty[unit & 1]));
-      ++gs;
+        mma_ss(lead, d, q + (((c >> 2) * (kTcMr * 128) + (c & 3) * 32) >> 4),
+               k + (((c >> 2) * (TN * 128) + (c & 3) * 32) >> 4), kIdescS, c != 0);
+      mma_commit(lead, &S.sfull[sb.at]);
+      mma_commit(lead, &S.empty[slot]);
+      if (--left == 0) mma_commit(lead, &S.qempty[unit % C::kQBufs]);
+      k_slot.step();
+      sb.step();
       return kind;
     };
     int kind = issue_s();
     int unit_pv = -1;
     bool ok = kind > 0;
-    for (int64_t g = 0; ok; ++g) {
+    while (ok) {
       const int next = issue_s();
       if (next < 0) break;
-      const int64_t use = 2 * g + 1;
-      const uint32_t slot = uint32_t(use % C::kSlots);
+      const uint32_t slot = v_slot.at;
       if (kind == 2) {
         ++unit_pv;
         // O still holds the unit before until its rows have been read
-        if (unit_pv > 0 && !tc_wait(&S.ofree, (unit_pv - 1) & 1, S)) break;
+        if (unit_pv > 0 && !tc_wait_warp(&S.ofree, (unit_pv - 1) & 1, S)) break;
       }
-      if (!tc_wait(&S.full[slot], (use / C::kSlots) & 1, S)) break;
-      if (!tc_wait(&S.pfull[g & 1], (g >> 1) & 1, S)) break;
-      fence_async_proxy();
+      if (!tc_wait_warp(&S.full[slot], v_slot.phase, S)) break;
+      if (!tc_wait_warp(&S.pfull[pb.at], pb.phase, S)) break;
+      if (slot_copied(slot)) fence_async_proxy();
       tc_fence_after();
-      const uint32_t v = ring0 + slot * kSlotBytes, p = tmem + uint32_t(g & 1) * TN;
+      const uint64_t v = v_desc + slot * (kSlotBytes >> 4);
+      const uint32_t p = tmem + pb.at * TN;
 #pragma unroll
       for (int c = 0; c < TN / 16; ++c)
-        mma_ts(tmem + C::kOCol, p + c * 8, sw128_mn_desc(v + c * 2048, TN * 128), kIdescO,
+        mma_ts(lead, tmem + C::kOCol, p + c * 8, v + c * (2048 >> 4), kIdescO,
                (c != 0) || kind != 2);
-      umma_commit(smem_addr(&S.pvdone[g & 1]));
-      umma_commit(smem_addr(&S.empty[slot]));
+      mma_commit(lead, &S.pvdone[pb.at]);
+      mma_commit(lead, &S.empty[slot]);
+      v_slot.step();
+      pb.step();
       kind = next;
       ok = next > 0;
     }
     if (*reinterpret_cast<volatile int*>(&S.abort)) {
       // every product issued must finish before TMEM is freed
-      umma_commit(smem_addr(&S.drain));
+      mma_commit(lead, &S.drain);
       mbar_wait_for(smem_addr(&S.drain), 0);
+      __syncwarp();
     }
   } else if (go && warp < kLoadWarp) {
     // --------------------------------------------------------------- softmax
     const uint32_t lanes = tmem + (uint32_t(warp * 32) << 16);
     Walk<TN> walk(A, P);
     Seg s;
-    int64_t g = 0;
+    int g = 0;
     int unit = 0;
     uint32_t looked = 0, collected = 0;
+    Slot<C::kSlots> v_slot{1, 0};
+    Buf bf, done;                // of this tile, and of the one before (its product with V)
     bool stop = false;
     while (!stop && walk.next(A, s)) {
       const bool active = warp * 32 < s.rows;
@@ -491,12 +557,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int all_hi = s.R.code ? 0 : min(at_first + 1, s.R.hi);
       const int all_lo = A.window > 0 ? max(0, at_last - A.window + 1) : 0;
       float m = -INFINITY, l = 0.f;   // m: the maximum that the sum and O refer to
-      for (int t = 0; t < s.count; ++t, ++g) {
+      for (int t = 0; t < s.count; ++t, ++g, v_slot.step(), done = bf, bf.step()) {
         const int p0 = (s.R.tile0 + s.first + t) * TN;
-        const int buf = int(g & 1);
+        const int buf = bf.at;
         const bool edge = p0 < all_lo || p0 + TN > all_hi;
         const uint32_t scol = lanes + uint32_t(buf) * TN;
-        if (!tc_wait_warp(&S.sfull[buf], (g >> 1) & 1, S)) {
+        if (!tc_wait_warp(&S.sfull[buf], bf.phase, S)) {
           stop = true;
           break;
         }
@@ -505,13 +571,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bool dirty = false;
         if (edge) {
           // V of this tile: 128 bytes a thread
-          const int64_t use = 2 * g + 1;
-          const uint32_t slot = uint32_t(use % C::kSlots);
-          if (!tc_wait_warp(&S.full[slot], (use / C::kSlots) & 1, S)) {
+          const uint32_t slot = v_slot.at;
+          if (!tc_wait_warp(&S.full[slot], v_slot.phase, S)) {
             stop = true;
             break;
           }
-          uint4* v = reinterpret_cast<uint4*>(smem_p + 2 * C::kQBytes + slot * kSlotBytes);
+          uint4* v = reinterpret_cast<uint4*>(smem_p + C::kQBufs * C::kQBytes + slot * kSlotBytes);
           bool found = false;
 #pragma unroll
           for (int i = 0; i < kSlotBytes / 16 / 128; ++i) {
@@ -519,13 +584,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             found |= any_nonfinite<T>(w.x) | any_nonfinite<T>(w.y) | any_nonfinite<T>(w.z) |
                      any_nonfinite<T>(w.w);
           }
-          if (found) S.dirty[buf] = int(g) + 1;
+          if (found) S.dirty[buf] = g + 1;
           if (!tc_sync(&S.looked[0], looked, S)) {
             stop = true;
             break;
           }
           looked ^= 1;
-          dirty = *reinterpret_cast<volatile int*>(&S.dirty[buf]) == int(g) + 1;
+          dirty = *reinterpret_cast<volatile int*>(&S.dirty[buf]) == g + 1;
           if (dirty) {
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) plus[i] = minus[i] = 0;
@@ -586,7 +651,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // all rows of the warp move to their present maximum
             const float f = m == -INFINITY ? 0.f : exp2f(m - grown);
             if (t > 0) {
-              if (!tc_wait_warp(&S.pvdone[(g - 1) & 1], ((g - 1) >> 1) & 1, S)) {
+              if (!tc_wait_warp(&S.pvdone[done.at], done.phase, S)) {
                 stop = true;
                 break;
               }
@@ -634,7 +699,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&S.pfull[buf]));
         if (dirty) {
-          if (!tc_wait_warp(&S.pvdone[buf], (g >> 1) & 1, S)) {
+          if (!tc_wait_warp(&S.pvdone[buf], bf.phase, S)) {
             stop = true;
             break;
           }
@@ -661,7 +726,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (stop) break;
       // ------------------------------------------------- the unit's rows
-      if (!tc_wait_warp(&S.pvdone[(g - 1) & 1], ((g - 1) >> 1) & 1, S)) break;
+      if (!tc_wait_warp(&S.pvdone[done.at], done.phase, S)) break;
       tc_fence_after();
       if (active) {
         const bool bad = *reinterpret_cast<volatile int*>(&S.bad[unit & 7]) != 0;
@@ -716,7 +781,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (lane == 0) mbar_arrive(smem_addr(&S.ofree));
       if (tid == 0 && !s.whole && s.first == 0) {
         AttnSplit& u = A.split[blockIdx.x];
-        u.last = attn_owner(P, s.unit_end - 1);
+        u.last = attn_owner(A, P, s.unit_end - 1);
         u.t_off = s.t_off;
         u.h = s.h;
         u.row0 = s.row0;
@@ -734,7 +799,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(C::kTmemCols));
+                 "r"(kTmemCols));
   }
 }
 
