@@ -9,8 +9,9 @@
 // share of the HBM.
 //
 // One CTA per SM, over its piece of the line of tiles (sv_attn.cuh):
-//   warps 4-5  load: Q of a unit (two buffers, plain loads) and, tile by tile, K
-//              (warp 4) and V (warp 5) into a ring of slots, in the
+//   warp 7     finds the CTA's units, announces them and loads their Q, one ahead
+//              where two fit.
+//   warps 4-5  load, tile by tile, K (warp 4) and V (warp 5) into a ring of slots, in the
 //              128-byte swizzled layout that the tensor cores read (K along the
 //              head: K-major; V along the head: MN-major).  The copy engine
 //              moves what a page has of the tile in boxes of 128 bytes by the
@@ -49,11 +50,11 @@
 namespace sv {
 namespace {
 
-constexpr int kTcThreads = 224;   // 4 softmax, 2 load, 1 product warp
+constexpr int kTcThreads = 256;   // 4 softmax, 2 load, 1 product, 1 query warp
 constexpr int kTcMr = 128;
 constexpr int kBufs = 3;          // S accumulators, each then the P of its tile
-constexpr int kLoaders = 64;
-constexpr int kLoadWarp = 4, kMmaWarp = 6;
+constexpr int kLoadWarp = 4, kMmaWarp = 6, kQueryWarp = 7;
+constexpr int kSegs = 8;          // parts announced ahead of the warp that is furthest back
 constexpr float kRescaleLog2 = 8.0f;
 
 template <int D>
@@ -69,14 +70,25 @@ struct Shape {
 };
 constexpr uint32_t kTmemCols = 512;
 
+// One unit's part of a CTA's piece.  The query warp finds them, a few ahead, and
+// announces them to the others; count 0 is the end.
+struct Seg {
+  int b, t_off, h, row0, rows, first, count;
+  bool whole;
+  int64_t unit_end;   // tile of the line after the unit's last
+  AttnReq R;
+};
+
 struct TcShared {
+  Seg seg[kSegs];
+  uint64_t announced[kSegs];
   uint64_t full[11], empty[11];
   uint64_t qfull[2], qempty[2], sfull[kBufs], pfull[kBufs], pvdone[kBufs], ofree;
-  uint64_t rows, looked[2], drain;  // load warps among themselves, softmax warps among themselves
+  uint64_t looked[2], drain;  // softmax warps among themselves
   uint32_t tmem;
   int abort;
   int first_bad;
-  int bad[8];        // per unit, a ring: the unit needs a missing page
+  int bad[kSegs];    // the part needs a missing page
   int copied[11];    // per slot: filled by the lanes' copies, not by the copy engine
   int dirty[kBufs];  // per S buffer: 1 + the tile whose V holds a non-finite value
 };
@@ -103,14 +115,6 @@ struct Buf {
       phase ^= 1;
     }
   }
-};
-
-// One unit's part of a CTA's piece.
-struct Seg {
-  int b, t_off, h, row0, rows, first, count;
-  bool whole;
-  int64_t unit_end;   // tile of the line after the unit's last
-  AttnReq R;
 };
 
 template <int TN>
@@ -250,6 +254,13 @@ __device__ __forceinline__ bool tc_sync(uint64_t* bar, uint32_t parity, TcShared
   return tc_wait_warp(bar, parity, S);
 }
 
+// The part that warp comes to next; false at the end, or when the CTA gave up.
+__device__ __forceinline__ bool next_seg(TcShared& S, int unit, Seg& s) {
+  if (!tc_wait_warp(&S.announced[unit % kSegs], (unit / kSegs) & 1, S)) return false;
+  s = S.seg[unit % kSegs];
+  return s.count > 0;
+}
+
 template <class T, int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const AttnArgs A) {
@@ -257,7 +268,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   constexpr int TN = C::TN;
   extern __shared__ unsigned char tc_smem_raw[];
   __shared__ TcShared S;
-  __shared__ const char* s_addr[2][64];   // row addresses of a tile with speculative entries
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t smem0 = (smem_addr(tc_smem_raw) + 1023u) & ~1023u;
   unsigned char* smem_p = tc_smem_raw + (smem0 - smem_addr(tc_smem_raw));
@@ -270,7 +280,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(smem_addr(&S.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_addr(&S.qfull[i]), kLoaders / 32);
+      mbar_init(smem_addr(&S.qfull[i]), 1);
       mbar_init(smem_addr(&S.qempty[i]), 1);
     }
     for (int i = 0; i < kBufs; ++i) {
@@ -280,7 +290,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       S.dirty[i] = 0;
     }
     mbar_init(smem_addr(&S.ofree), 4);
-    mbar_init(smem_addr(&S.rows), kLoaders / 32);
+    for (int i = 0; i < kSegs; ++i) mbar_init(smem_addr(&S.announced[i]), 1);
     mbar_init(smem_addr(&S.looked[0]), 4);
     mbar_init(smem_addr(&S.looked[1]), 4);
     mbar_init(smem_addr(&S.drain), 1);
@@ -310,52 +320,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int part = lane % kParts, box0 = lane / kParts * A.box_rows;  // this lane's box
     const bool boxes = A.box_rows > 0 && box0 < TN;
     constexpr int kChunks = D / 8;                // 16-byte chunks of a row
-    Walk<TN> walk(A, P);
     Seg s;
     Slot<C::kSlots> at{uint32_t(kv), 1};  // empty barriers: the first round passes at once
-    int unit = 0;
-    uint32_t rows_phase = 0;
     bool stop = false;
-    while (!stop && walk.next(A, s)) {
-      // Q: rows of a row-major swizzled tile per 64 elements of the head
-      const int qb = unit % C::kQBufs;
-      if (tid == kLoadWarp * 32) S.bad[unit & 7] = s.R.code != 0;
-      stop = !tc_wait_warp(&S.qempty[qb], ((unit / C::kQBufs) & 1) ^ 1, S) ||
-             !tc_sync(&S.rows, rows_phase, S);
-      if (stop) break;
-      rows_phase ^= 1;
-      {
-        const T* q = static_cast<const T*>(A.q);
-        const int live = (s.rows + 31) & ~31;
-        const int lt = tid - kLoadWarp * 32, ch = lt % kChunks;
-        for (int r = lt / kChunks; r < live; r += kLoaders / kChunks) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (r < s.rows) {
-            const int row = s.row0 + r;
-            const T* src = q + int64_t(s.t_off + row / A.G) * A.q_ts +
-                           int64_t(s.h * A.G + row % A.G) * A.q_hs + ch * 8;
-            if (A.q_vec) {
-              v = __ldg(reinterpret_cast<const uint4*>(src));
-            } else {
-              T e[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) e[i] = src[i];
-              v = *reinterpret_cast<uint4*>(e);
-            }
-            if (A.q_flip) {  // a negative scale: S of -q with its magnitude
-              v.x ^= 0x80008000u;
-              v.y ^= 0x80008000u;
-              v.z ^= 0x80008000u;
-              v.w ^= 0x80008000u;
-            }
-          }
-          *reinterpret_cast<uint4*>(smem_p + qb * C::kQBytes + (ch >> 3) * (kTcMr * 128) +
-                                    r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
-        }
-        fence_async_proxy();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&S.qfull[qb]));
-      }
+    for (int unit = 0; !stop && next_seg(S, unit, s); ++unit) {
       const int hi = s.R.code ? 0 : s.R.hi;
       const int cached = min(s.R.n, hi);
       const int p0 = (s.R.tile0 + s.first) * TN;
@@ -363,21 +331,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       auto column = [&](int p) { return A.s_shift >= 0 ? p >> A.s_shift : p / A.S; };
       auto missing = [&](int page) {
         if (page >= 0 && page < A.num_pages) return false;
-        S.bad[unit & 7] = 1;
+        S.bad[unit % kSegs] = 1;
         atomicMin(&S.first_bad, s.b);
         return true;
       };
-      // The page of a tile's box is read one tile ahead, so that nothing waits
-      // for the block table.
-      int page = -1;
+      // A tile comes in boxes, or row by row; the pages of its box, or of its
+      // rows (row lane + 32 i of the tile), are read one tile ahead, so that
+      // nothing waits for the block table.
+      constexpr int kOwn = TN / 32;
+      int page[kOwn];
+      auto boxed = [&](int t) { return A.box_rows > 0 && p0 + (t + 1) * TN <= cached; };
       auto next_page = [&](int t) {
-        const int p = p0 + t * TN + box0;
-        if (boxes && p < cached) page = __ldg(table + column(p));
+        if (boxed(t)) {
+          if (boxes) page[0] = __ldg(table + column(p0 + t * TN + box0));
+        } else {
+#pragma unroll
+          for (int i = 0; i < kOwn; ++i) {
+            const int p = p0 + t * TN + lane + 32 * i;
+            if (p < cached) page[i] = __ldg(table + column(p));
+          }
+        }
       };
       next_page(0);
       for (int t = 0; t < s.count; ++t) {
         const int pt = p0 + t * TN;
-        const int pg = page;
+        int pg[kOwn];
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) pg[i] = page[i];
         if (t + 1 < s.count) next_page(t + 1);
         const uint32_t slot = at.at;
         if (!tc_wait_warp(&S.empty[slot], at.phase, S)) {
@@ -385,7 +365,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           break;
         }
         const uint32_t dst = ring0 + slot * kSlotBytes, bar = smem_addr(&S.full[slot]);
-        if (A.box_rows > 0 && pt + TN <= cached) {
+        if (boxed(t)) {
           if (lane == 0) {
             S.copied[slot] = 0;
             mbar_arrive_expect_tx(bar, kSlotBytes);
@@ -396,58 +376,109 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (boxes) {
             const int p = pt + box0;
             // a missing page: a box outside the matrix is all zeros
-            const int row = missing(pg) ? -A.box_rows
-                                        : pg * A.page_rows + kv * A.S + (p - column(p) * A.S);
+            const int row = missing(pg[0])
+                                ? -A.box_rows
+                                : pg[0] * A.page_rows + kv * A.S + (p - column(p) * A.S);
             box_load(dst + part * (TN * 128) + box0 * 128, &rows_map, s.h * D + part * 64, row,
                      bar);
           }
         } else {
+          // addresses of the lane's own rows; each round's lanes then fetch
+          // theirs from the lane that has it
+          uint64_t own[kOwn];
+#pragma unroll
+          for (int i = 0; i < kOwn; ++i) {
+            const int p = pt + lane + 32 * i;
+            const char* a = nullptr;   // stays null for a row that is filled with zeros
+            if (p >= cached) {
+              if (p < hi)
+                a = A.spec + int64_t(s.b) * A.spec_req + int64_t(p - s.R.n) * A.spec_tok +
+                    kv * A.entry_bytes;
+            } else if (!missing(pg[i])) {
+              a = A.cache + pg[i] * A.page_bytes + kv * A.v_off +
+                  (p - column(p) * A.S) * A.entry_bytes;
+            }
+            own[i] = a ? reinterpret_cast<uint64_t>(a + int64_t(s.h) * D * 2) : 0;
+          }
           const int ch = lane % kChunks;
           constexpr int kStep = 32 / kChunks;   // rows per round
 #pragma unroll
-          for (int half = 0; half < TN; half += 64) {
-            __syncwarp();
+          for (int i = 0; i < kOwn; ++i)
 #pragma unroll
-            for (int r = lane; r < 64; r += 32) {
-              const int p = pt + half + r;
-              const char* a = nullptr;   // stays null for a row that is filled with zeros
-              if (p >= cached) {
-                if (p < hi)
-                  a = A.spec + int64_t(s.b) * A.spec_req + int64_t(p - s.R.n) * A.spec_tok +
-                      kv * A.entry_bytes;
-              } else {
-                const int one = __ldg(table + column(p));
-                if (!missing(one))
-                  a = A.cache + one * A.page_bytes + kv * A.v_off +
-                      (p - column(p) * A.S) * A.entry_bytes;
-              }
-              s_addr[kv][r] = a ? a + int64_t(s.h) * D * 2 : nullptr;
+            for (int j = 0; j < 32; j += kStep) {
+              const int from = j + lane / kChunks, r = 32 * i + from;
+              const uint64_t a =
+                  (uint64_t(__shfl_sync(0xffffffffu, uint32_t(own[i] >> 32), from)) << 32) |
+                  __shfl_sync(0xffffffffu, uint32_t(own[i]), from);
+              cp_async16(dst + (ch >> 3) * (TN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                         a ? reinterpret_cast<const char*>(a) + ch * 16
+                           : reinterpret_cast<const char*>(A.k_per_req),
+                         a ? 16u : 0u);
             }
-            __syncwarp();
-            // addresses of eight rounds first: the copies keep their order, so a
-            // load between two of them would be waited for each time
-#pragma unroll
-            for (int r0 = 0; r0 < 64; r0 += 8 * kStep) {
-              const char* src[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) src[i] = s_addr[kv][r0 + i * kStep + lane / kChunks];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int r = half + r0 + i * kStep + lane / kChunks;
-                cp_async16(dst + (ch >> 3) * (TN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                           src[i] ? src[i] + ch * 16 : reinterpret_cast<const char*>(A.k_per_req),
-                           src[i] ? 16u : 0u);
-              }
-            }
-          }
           if (lane == 0) S.copied[slot] = 1;
           cp_async_arrive(bar);
         }
         at.step();
       }
-      ++unit;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (go && warp == kQueryWarp) {
+    // --------------------------------------------- parts, and their queries
+    constexpr int kChunks = D / 8, kStep = 32 / kChunks, kBatch = 16;
+    const int ch = lane % kChunks;
+    const T* q = static_cast<const T*>(A.q);
+    Walk<TN> walk(A, P);
+    for (int unit = 0;; ++unit) {
+      Seg s;
+      s.count = 0;
+      walk.next(A, s);
+      // This entry's part before is done with everywhere: the wait for a query
+      // buffer in the last round saw the scores of the third part before this
+      // one, and the softmax warps are at most three tiles behind those.
+      if (lane == 0) {
+        S.seg[unit % kSegs] = s;
+        S.bad[unit % kSegs] = s.count && s.R.code != 0;
+        mbar_arrive(smem_addr(&S.announced[unit % kSegs]));
+      }
+      if (s.count == 0) break;
+      const int qb = unit % C::kQBufs;
+      if (!tc_wait_warp(&S.qempty[qb], ((unit / C::kQBufs) & 1) ^ 1, S)) break;
+      // rows of a row-major swizzled tile per 64 elements of the head
+      const int live = (s.rows + 31) & ~31;
+      for (int r0 = lane / kChunks; r0 < live; r0 += kStep * kBatch) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = r0 + i * kStep;
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (r < s.rows) {
+            const int row = s.row0 + r;
+            const T* src = q + int64_t(s.t_off + row / A.G) * A.q_ts +
+                           int64_t(s.h * A.G + row % A.G) * A.q_hs + ch * 8;
+            if (A.q_vec) {
+              v[i] = __ldg(reinterpret_cast<const uint4*>(src));
+            } else {
+              T e[8];
+#pragma unroll
+              for (int x = 0; x < 8; ++x) e[x] = src[x];
+              v[i] = *reinterpret_cast<uint4*>(e);
+            }
+          }
+        }
+        const uint32_t flip = A.q_flip ? 0x80008000u : 0u;  // a negative scale: S of -q
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = r0 + i * kStep;
+          if (r < live)
+            *reinterpret_cast<uint4*>(smem_p + qb * C::kQBytes + (ch >> 3) * (kTcMr * 128) +
+                                      r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
+                make_uint4(v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip);
+        }
+      }
+      fence_async_proxy();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&S.qfull[qb]));
+    }
   } else if (go && warp == kMmaWarp) {
     // -------------------------------------------------------------- products
     constexpr uint32_t kBase = (1u << 4) | (Bits<T>::kFmt << 7) | (Bits<T>::kFmt << 10) |
@@ -456,8 +487,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr uint32_t kIdescO = kBase | (uint32_t(D >> 3) << 17) | (1u << 16);
     const uint32_t lead = lane == 0;
     Slot<C::kSlots> k_slot{0, 0}, v_slot{1, 0};
-    Walk<TN> walk(A, P);
-    Seg s;
     int left = 0, unit = -1;     // tiles of the unit whose S is issued next, the unit
     Buf sb, pb;                  // buffers of the next S and of the next P
     // The fence that orders the lanes' copies before the products' reads takes
@@ -471,9 +500,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto issue_s = [&]() -> int {  // 0: no tile left, 1: issued, 2: the first of its unit, -1: gave up
       int kind = 1;
       if (left == 0) {
-        if (!walk.next(A, s)) return 0;
-        left = s.count;
         ++unit;
+        Seg s;
+        if (!next_seg(S, unit, s)) return 0;
+        left = s.count;
         kind = 2;
         if (!tc_wait_warp(&S.qfull[unit % C::kQBufs], (unit / C::kQBufs) & 1, S)) return -1;
       }
@@ -535,15 +565,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else if (go && warp < kLoadWarp) {
     // --------------------------------------------------------------- softmax
     const uint32_t lanes = tmem + (uint32_t(warp * 32) << 16);
-    Walk<TN> walk(A, P);
     Seg s;
     int g = 0;
-    int unit = 0;
     uint32_t looked = 0, collected = 0;
     Slot<C::kSlots> v_slot{1, 0};
     Buf bf, done;                // of this tile, and of the one before (its product with V)
     bool stop = false;
-    while (!stop && walk.next(A, s)) {
+    for (int unit = 0; !stop && next_seg(S, unit, s); ++unit) {
       const bool active = warp * 32 < s.rows;
       const bool live = tid < s.rows;
       const int row = s.row0 + tid;
@@ -729,7 +757,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!tc_wait_warp(&S.pvdone[done.at], done.phase, S)) break;
       tc_fence_after();
       if (active) {
-        const bool bad = *reinterpret_cast<volatile int*>(&S.bad[unit & 7]) != 0;
+        const bool bad = *reinterpret_cast<volatile int*>(&S.bad[unit % kSegs]) != 0;
         const float nan = __int_as_float(0x7fc00000);
         const int slot = s.first == 0 ? 1 : 0;
         const int64_t pr = (int64_t(blockIdx.x) * 2 + slot) * kTcMr + tid;
@@ -788,7 +816,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         u.rows = s.rows;
         u.valid = 1;
       }
-      ++unit;
     }
   }
   __syncwarp();
