@@ -405,10 +405,10 @@ cudaError_t run_attn(const AttnArgs& A, bool weights, cudaStream_t s) {
 constexpr int kCtasPerSm = 2;  // shared memory of the widest heads
 constexpr int kTcRows = 128;   // rows a unit of the tensor-core kernel
 
-// Heads and types that the tensor-core kernel takes.  A scale of 0 would turn
-// its masked scores into NaN; its entries are numbered in 32 bits.
+// Heads and types that the tensor-core kernel takes.  The largest score is
+// found before the scaling, so the scale has to be positive; its entries are numbered in 32 bits.
 bool on_tensor_cores(const AttnArgs& A, int dtype) {
-  return dtype != SV_F32 && (A.D == 64 || A.D == 128 || A.D == 256) && A.scale2 != 0.0f &&
+  return dtype != SV_F32 && (A.D == 64 || A.D == 128 || A.D == 256) && A.scale2 > 0.0f &&
          (A.num_pages > 0 || A.spec) &&
          A.num_pages * (A.page_bytes / A.entry_bytes) <= INT32_MAX;
 }
@@ -460,8 +460,6 @@ cudaError_t launch_attn(AttnArgs A, int dtype, bool weights, void* workspace, in
     A.page_rows = int32_t(A.page_bytes / A.entry_bytes);
     A.q_vec = aligned(A.q) && A.q_ts % 8 == 0 && A.q_hs % 8 == 0;
     A.out_vec = aligned(A.out);
-    A.q_flip = A.scale2 < 0.0f;
-    A.scale2 = fabsf(A.scale2);
     const cudaError_t e = launch_attn_tc(A, dtype, s);
     if (e != cudaSuccess) return e;
     return dtype == SV_BF16 ? launch_join(attn_join_kernel<__nv_bfloat16, kTcRows>, A, s)

@@ -44,6 +44,8 @@
 //
 // Every wait is bounded; on expiry the CTA's status records it, its copies and
 // products land, and TMEM is freed.
+#include <type_traits>
+
 #include "sv_attn.cuh"
 #include "sv_tcgen05.cuh"
 
@@ -57,16 +59,28 @@ constexpr int kLoadWarp = 4, kMmaWarp = 6, kQueryWarp = 7;
 constexpr int kSegs = 8;          // parts announced ahead of the warp that is furthest back
 constexpr float kRescaleLog2 = 8.0f;
 
+// Copies' sums meet in shared memory: maximum and sum of each row of M, what
+// its row is divided by, and twice 16 columns of O.
+constexpr int kStageCols = 16, kStageRow = kStageCols + 1;  // floats, one for the banks
+struct Stage {
+  float2 ml[kTcMr];
+  float inv[kTcMr];
+  float o[2][kTcMr * kStageRow];
+};
+constexpr size_t kStageBytes = (sizeof(Stage) + 127) / 128 * 128;
+
 template <int D>
 struct Shape {
   static constexpr int TN = D == 256 ? 64 : 128;
   static constexpr int kSlotBytes = TN * D * 2;
   static constexpr int kQBytes = kTcMr * D * 2;
   static constexpr int kQBufs = D == 256 ? 1 : 2;
-  static constexpr int kSlots = D == 64 ? 11 : 5;  // what shared memory holds
+  static constexpr int kSlots = D == 64 ? 10 : 5;  // what shared memory holds
   static constexpr uint32_t kOCol = kBufs * TN;     // TMEM columns: the S accumulators, then O
-  static constexpr size_t kSmem =
-      1024 + kQBufs * size_t(kQBytes) + size_t(kSlots) * kSlotBytes;
+  // where copies of rows are added up: a query buffer, or a place of its own
+  static constexpr bool kOwnStage = kQBytes < int(kStageBytes);
+  static constexpr size_t kSmem = 1024 + kQBufs * size_t(kQBytes) + size_t(kSlots) * kSlotBytes +
+                                  (kOwnStage ? kStageBytes : 0);
 };
 constexpr uint32_t kTmemCols = 512;
 
@@ -74,6 +88,7 @@ constexpr uint32_t kTmemCols = 512;
 // announces them to the others; count 0 is the end.
 struct Seg {
   int b, t_off, h, row0, rows, first, count;
+  int copies;         // of the rows in the M of the products
   bool whole;
   int64_t unit_end;   // tile of the line after the unit's last
   AttnReq R;
@@ -84,7 +99,7 @@ struct TcShared {
   uint64_t announced[kSegs];
   uint64_t full[11], empty[11];
   uint64_t qfull[2], qempty[2], sfull[kBufs], pfull[kBufs], pvdone[kBufs], ofree;
-  uint64_t looked[2], drain;  // softmax warps among themselves
+  uint64_t looked[2], ends, drain;  // softmax warps among themselves
   uint32_t tmem;
   int abort;
   int first_bad;
@@ -145,6 +160,7 @@ struct Walk {
     s.h = unit / R.mtiles * A.hg + int(blockIdx.x) % A.hg;
     s.row0 = (unit % R.mtiles) * kTcMr;
     s.rows = min(kTcMr, (R.k + 1) * A.G - s.row0);
+    s.copies = s.rows <= 32 && TN == 128 ? 4 : s.rows <= 64 ? 2 : 1;
     s.whole = s.first == 0 && s.count == R.ntiles;
     s.unit_end = pos - s.first + R.ntiles;
     s.R = R;
@@ -223,12 +239,17 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 }
 
 __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                         uint32_t bar) {
+                                         uint32_t bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
-      "{%2, %3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
       : "memory");
+}
+__device__ __forceinline__ uint64_t l2_evict_normal_policy() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
 }
 
 // Bounded wait; false, with the CTA's abort flag set, on expiry.  The clock of
@@ -281,7 +302,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&S.qfull[i]), 1);
-      mbar_init(smem_addr(&S.qempty[i]), 1);
+      mbar_init(smem_addr(&S.qempty[i]), 4);
     }
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(smem_addr(&S.sfull[i]), 1);
@@ -293,6 +314,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int i = 0; i < kSegs; ++i) mbar_init(smem_addr(&S.announced[i]), 1);
     mbar_init(smem_addr(&S.looked[0]), 4);
     mbar_init(smem_addr(&S.looked[1]), 4);
+    mbar_init(smem_addr(&S.ends), 4);
     mbar_init(smem_addr(&S.drain), 1);
     fence_mbar_init();
     S.abort = 0;
@@ -320,6 +342,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int part = lane % kParts, box0 = lane / kParts * A.box_rows;  // this lane's box
     const bool boxes = A.box_rows > 0 && box0 < TN;
     constexpr int kChunks = D / 8;                // 16-byte chunks of a row
+    // keys that no other unit of the call reads leave the L2 first
+    const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
     Seg s;
     Slot<C::kSlots> at{uint32_t(kv), 1};  // empty barriers: the first round passes at once
     bool stop = false;
@@ -380,7 +404,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 ? -A.box_rows
                                 : pg[0] * A.page_rows + kv * A.S + (p - column(p) * A.S);
             box_load(dst + part * (TN * 128) + box0 * 128, &rows_map, s.h * D + part * 64, row,
-                     bar);
+                     bar, s.R.mtiles > 1 ? again : once);
           }
         } else {
           // addresses of the lane's own rows; each round's lanes then fetch
@@ -404,7 +428,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           constexpr int kStep = 32 / kChunks;   // rows per round
 #pragma unroll
           for (int i = 0; i < kOwn; ++i)
-#pragma unroll
+#pragma unroll 4
             for (int j = 0; j < 32; j += kStep) {
               const int from = j + lane / kChunks, r = 32 * i + from;
               const uint64_t a =
@@ -424,7 +448,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (go && warp == kQueryWarp) {
     // --------------------------------------------- parts, and their queries
-    constexpr int kChunks = D / 8, kStep = 32 / kChunks, kBatch = 16;
+    constexpr int kChunks = D / 8, kStep = 32 / kChunks;
     const int ch = lane % kChunks;
     const T* q = static_cast<const T*>(A.q);
     Walk<TN> walk(A, P);
@@ -433,8 +457,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       s.count = 0;
       walk.next(A, s);
       // This entry's part before is done with everywhere: the wait for a query
-      // buffer in the last round saw the scores of the third part before this
-      // one, and the softmax warps are at most three tiles behind those.
+      // buffer in the last round saw the end of the third part before this one.
       if (lane == 0) {
         S.seg[unit % kSegs] = s;
         S.bad[unit % kSegs] = s.count && s.R.code != 0;
@@ -443,38 +466,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (s.count == 0) break;
       const int qb = unit % C::kQBufs;
       if (!tc_wait_warp(&S.qempty[qb], ((unit / C::kQBufs) & 1) ^ 1, S)) break;
-      // rows of a row-major swizzled tile per 64 elements of the head
-      const int live = (s.rows + 31) & ~31;
-      for (int r0 = lane / kChunks; r0 < live; r0 += kStep * kBatch) {
-        uint4 v[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int r = r0 + i * kStep;
-          v[i] = make_uint4(0, 0, 0, 0);
-          if (r < s.rows) {
-            const int row = s.row0 + r;
-            const T* src = q + int64_t(s.t_off + row / A.G) * A.q_ts +
-                           int64_t(s.h * A.G + row % A.G) * A.q_hs + ch * 8;
-            if (A.q_vec) {
-              v[i] = __ldg(reinterpret_cast<const uint4*>(src));
-            } else {
-              T e[8];
-#pragma unroll
-              for (int x = 0; x < 8; ++x) e[x] = src[x];
-              v[i] = *reinterpret_cast<uint4*>(e);
-            }
-          }
-        }
-        const uint32_t flip = A.q_flip ? 0x80008000u : 0u;  // a negative scale: S of -q
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int r = r0 + i * kStep;
-          if (r < live)
-            *reinterpret_cast<uint4*>(smem_p + qb * C::kQBytes + (ch >> 3) * (kTcMr * 128) +
-                                      r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
-                make_uint4(v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip);
+      // Rows of a row-major swizzled tile per 64 elements of the head, copies of
+      // them 128 / copies rows apart; rows between them stay as they are (what
+      // a row of S or O holds reaches no other row).
+      const int apart = kTcMr / s.copies;
+      for (int i = lane / kChunks; i < s.rows * s.copies; i += kStep) {
+        const int rr = i / s.copies, r = rr + i % s.copies * apart, row = s.row0 + rr;
+        const T* src = q + int64_t(s.t_off + row / A.G) * A.q_ts +
+                       int64_t(s.h * A.G + row % A.G) * A.q_hs + ch * 8;
+        const uint32_t at = uint32_t(qb * C::kQBytes + (ch >> 3) * (kTcMr * 128) + r * 128 +
+                                     (((ch & 7) ^ (r & 7)) << 4));
+        if (A.q_vec) {
+          cp_async16(smem0 + at, src, 16);
+        } else {
+          T* dst = reinterpret_cast<T*>(smem_p + at);
+          for (int x = 0; x < 8; ++x) dst[x] = src[x];
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       fence_async_proxy();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&S.qfull[qb]));
@@ -522,7 +531,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                k + (((c >> 2) * (TN * 128) + (c & 3) * 32) >> 4), kIdescS, c != 0);
       mma_commit(lead, &S.sfull[sb.at]);
       mma_commit(lead, &S.empty[slot]);
-      if (--left == 0) mma_commit(lead, &S.qempty[unit % C::kQBufs]);
+      --left;
       k_slot.step();
       sb.step();
       return kind;
@@ -567,14 +576,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t lanes = tmem + (uint32_t(warp * 32) << 16);
     Seg s;
     int g = 0;
-    uint32_t looked = 0, collected = 0;
+    uint32_t looked = 0, collected = 0, ends = 0;
     Slot<C::kSlots> v_slot{1, 0};
     Buf bf, done;                // of this tile, and of the one before (its product with V)
     bool stop = false;
     for (int unit = 0; !stop && next_seg(S, unit, s); ++unit) {
-      const bool active = warp * 32 < s.rows;
-      const bool live = tid < s.rows;
-      const int row = s.row0 + tid;
+      const int apart = kTcMr / s.copies;
+      const int copy = tid / apart, rr = tid % apart;   // warps lie in one copy
+      const bool active = warp * 32 % apart < s.rows;
+      const bool live = rr < s.rows;
+      const int row = s.row0 + rr;
       const int tok = row / A.G;
       const int at = s.R.at0 + tok;
       const int row_hi = live ? (s.R.code ? 0 : min(at + 1, s.R.hi)) : INT32_MAX;
@@ -623,7 +634,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) plus[i] = minus[i] = 0;
             const uint32_t* vw = reinterpret_cast<const uint32_t*>(v);
-            for (int c = 0; c < TN; ++c) {
+            for (int c = 0; live && copy == 0 && c < TN; ++c) {
               if (p0 + c < row_lo || p0 + c >= row_hi) continue;
 #pragma unroll
               for (int i = 0; i < D / 32; ++i)
@@ -658,33 +669,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             fence_async_proxy();
           }
         }
-        if (active) {
-          float x[TN];
+        // N columns of the tile, the warp's copy's share
+        auto weigh = [&](auto width) -> bool {
+          constexpr int N = decltype(width)::value;
+          const int c0 = copy * N;
+          float x[N];
 #pragma unroll
-          for (int c = 0; c < TN / 32; ++c)
-            tmem_ld32(scol + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[c * 32]));
+          for (int c = 0; c < N / 32; ++c)
+            tmem_ld32(scol + c0 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[c * 32]));
           tmem_ld_wait();
           if (edge) {
 #pragma unroll
-            for (int c = 0; c < TN; ++c)
-              x[c] = p0 + c >= row_lo && p0 + c < row_hi ? x[c] : -INFINITY;
+            for (int c = 0; c < N; ++c)
+              x[c] = p0 + c0 + c >= row_lo && p0 + c0 + c < row_hi ? x[c] : -INFINITY;
           }
           float top = x[0];
 #pragma unroll
-          for (int c = 1; c < TN; ++c) top = fmaxf(top, x[c]);
-          top *= A.scale2;   // scale2 >= 0; 0 times an infinite score is NaN and ignored here
-          const float grown = fmaxf(m, top);
+          for (int c = 1; c < N; ++c) top = fmaxf(top, x[c]);
+          const float grown = fmaxf(m, top * A.scale2);   // scale2 > 0
           const bool rescale = live && grown > m + kRescaleLog2;
           if (__any_sync(0xffffffffu, rescale)) {
             // all rows of the warp move to their present maximum
             const float f = m == -INFINITY ? 0.f : exp2f(m - grown);
             if (t > 0) {
-              if (!tc_wait_warp(&S.pvdone[done.at], done.phase, S)) {
-                stop = true;
-                break;
-              }
+              if (!tc_wait_warp(&S.pvdone[done.at], done.phase, S)) return false;
               tc_fence_after();
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 tmem_ld32(lanes + C::kOCol + c * 32, o);
@@ -701,27 +711,43 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const float sh = m == -INFINITY ? 0.f : m;
           const uint64_t sc2 = pk2(A.scale2, A.scale2), sh2 = pk2(-sh, -sh);
           uint64_t sum = pk2(0.f, 0.f);
-          uint32_t pw[TN / 2];
+          uint32_t pw[N / 2];
 #pragma unroll
-          for (int c = 0; c < TN; c += 2) {
-            float a, b2;
-            upk2(fma2(pk2(x[c], x[c + 1]), sc2, sh2), a, b2);
-            a = ex2_approx(a);
-            b2 = ex2_approx(b2);
-            sum = add2(sum, pk2(a, b2));
-            pw[c / 2] = Bits<T>::pack(a, b2);
+          for (int c = 0; c < N; c += 2) {
+            float e0, e1;
+            upk2(fma2(pk2(x[c], x[c + 1]), sc2, sh2), e0, e1);
+            e0 = ex2_approx(e0);
+            e1 = ex2_approx(e1);
+            sum = add2(sum, pk2(e0, e1));
+            pw[c / 2] = Bits<T>::pack(e0, e1);
           }
           float s0, s1;
           upk2(sum, s0, s1);
           l += s0 + s1;
-          if constexpr (TN / 2 >= 32) {
+          // the other copies' columns are theirs: zeros here
+          uint32_t zero[16];
 #pragma unroll
-            for (int c = 0; c < TN / 64; ++c)
-              tmem_st32(scol + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&pw[c * 32]));
-          } else {
-            tmem_st16(scol, *reinterpret_cast<uint32_t(*)[16]>(&pw[0]));
-          }
+          for (int c = 0; c < 16; ++c) zero[c] = 0;
+#pragma unroll
+          for (int i = 0; i < TN / N; ++i)
+#pragma unroll
+            for (int c = 0; c < N / 32; ++c) {
+              const uint32_t to = scol + i * (N / 2) + c * 16;
+              if (i == copy) tmem_st16(to, *reinterpret_cast<uint32_t(*)[16]>(&pw[c * 16]));
+              else tmem_st16(to, zero);
+            }
           tmem_st_wait();
+          return true;
+        };
+        if (active) {
+          bool ok;
+          if (s.copies == 1) ok = weigh(std::integral_constant<int, TN>());
+          else if (s.copies == 2) ok = weigh(std::integral_constant<int, TN / 2>());
+          else ok = weigh(std::integral_constant<int, TN == 128 ? 32 : TN / 2>());
+          if (!ok) {
+            stop = true;
+            break;
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -756,57 +782,134 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // ------------------------------------------------- the unit's rows
       if (!tc_wait_warp(&S.pvdone[done.at], done.phase, S)) break;
       tc_fence_after();
-      if (active) {
-        const bool bad = *reinterpret_cast<volatile int*>(&S.bad[unit % kSegs]) != 0;
-        const float nan = __int_as_float(0x7fc00000);
-        const int slot = s.first == 0 ? 1 : 0;
-        const int64_t pr = (int64_t(blockIdx.x) * 2 + slot) * kTcMr + tid;
-        const int hq = s.h * A.G + row % A.G;
-        const int64_t trow = int64_t(s.t_off) + tok;
-        T* out = static_cast<T*>(A.out) + trow * A.o_ts + int64_t(hq) * A.o_hs;
-        const float inv = bad ? nan : l == 0.f ? 0.f : 1.f / l;
+      const bool bad = *reinterpret_cast<volatile int*>(&S.bad[unit % kSegs]) != 0;
+      const float nan = __int_as_float(0x7fc00000);
+      const int slot = s.first == 0 ? 1 : 0;
+      const int64_t pr = (int64_t(blockIdx.x) * 2 + slot) * kTcMr;
+      float top = m, total = l;
+      auto place = [&](int r, int64_t* t, int* hq) {   // token and head of row r of the unit
+        const int x = s.row0 + r;
+        *t = int64_t(s.t_off) + x / A.G;
+        *hq = s.h * A.G + x % A.G;
+      };
+      if (s.copies == 1) {
+        const float inv = bad ? nan : total == 0.f ? 0.f : 1.f / total;
+        int64_t trow;
+        int hq;
+        place(rr, &trow, &hq);
+        if (active) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(lanes + C::kOCol + c * 32, o);
+            tmem_ld_wait();
+            if (!live) continue;
+            if (s.whole) {
+              T* out = static_cast<T*>(A.out) + trow * A.o_ts + int64_t(hq) * A.o_hs + c * 32;
+              uint32_t w[16];
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(lanes + C::kOCol + c * 32, o);
-          tmem_ld_wait();
-          if (!live) continue;
-          if (s.whole) {
-            uint32_t w[16];
+              for (int e = 0; e < 16; ++e)
+                w[e] = Bits<T>::pack(__uint_as_float(o[2 * e]) * inv,
+                                     __uint_as_float(o[2 * e + 1]) * inv);
+              if (A.out_vec) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              w[e] = Bits<T>::pack(__uint_as_float(o[2 * e]) * inv,
-                                   __uint_as_float(o[2 * e + 1]) * inv);
-            if (A.out_vec) {
+                for (int e = 0; e < 4; ++e)
+                  *reinterpret_cast<uint4*>(out + e * 8) =
+                      make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+              } else {
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                *reinterpret_cast<uint4*>(out + c * 32 + e * 8) =
-                    make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const uint16_t h = uint16_t(w[e / 2] >> (16 * (e & 1)));
-                out[c * 32 + e] = *reinterpret_cast<const T*>(&h);
+                for (int e = 0; e < 32; ++e) {
+                  const uint16_t h = uint16_t(w[e / 2] >> (16 * (e & 1)));
+                  out[e] = *reinterpret_cast<const T*>(&h);
+                }
               }
-            }
-          } else {
-            uint4* po = reinterpret_cast<uint4*>(A.part_o + pr * D + c * 32);
+            } else {
+              uint4* po = reinterpret_cast<uint4*>(A.part_o + (pr + rr) * D + c * 32);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              po[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              for (int e = 0; e < 8; ++e)
+                po[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
           }
         }
-        if (live) {
-          if (s.whole)
-            A.lse[trow * A.Hq + hq] =
-                bad ? nan : (m == -INFINITY ? 0.f : m * kAttnLn2) + logf(l);
-          else
-            A.part_ml[pr] = make_float2(bad ? nan : m, l);
+      } else {
+        // The copies' sums and outputs add up at their common maximum, 16
+        // columns of O at a time; all threads then write what is live of them.
+        Stage& stage = *reinterpret_cast<Stage*>(
+            smem_p + (C::kOwnStage ? C::kQBufs * C::kQBytes + C::kSlots * kSlotBytes
+                                   : unit % C::kQBufs * C::kQBytes));
+        stage.ml[tid] = make_float2(m, l);
+        if (!tc_sync(&S.ends, ends, S)) break;
+        ends ^= 1;
+        for (int c = 0; c < s.copies; ++c) top = fmaxf(top, stage.ml[rr + c * apart].x);
+        total = 0.f;
+        for (int c = 0; c < s.copies; ++c) {
+          const float2 x = stage.ml[rr + c * apart];
+          if (x.x > -INFINITY || x.y != x.y) total = fmaf(x.y, exp2f(x.x - top), total);
         }
+        const float f = m > -INFINITY ? exp2f(m - top) : 0.f;
+        if (copy == 0) stage.inv[rr] = bad ? nan : total == 0.f ? 0.f : 1.f / total;
+#pragma unroll 1
+        for (int c = 0; c < D / kStageCols; ++c) {
+          float* buf = stage.o[c & 1];
+          if (active) {
+            uint32_t o[16];
+            tmem_ld16(lanes + C::kOCol + c * kStageCols, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              buf[tid * kStageRow + e] = __uint_as_float(o[e]) * f;
+          }
+          if (!tc_sync(&S.ends, ends, S)) {
+            stop = true;
+            break;
+          }
+          ends ^= 1;
+          for (int i = tid; i < s.rows * (kStageCols / 2); i += 128) {
+            const int r = i / (kStageCols / 2), e = i % (kStageCols / 2) * 2;
+            float v0 = 0.f, v1 = 0.f;
+            for (int k = 0; k < s.copies; ++k) {
+              const float* from = buf + (k * apart + r) * kStageRow + e;
+              v0 += from[0];
+              v1 += from[1];
+            }
+            if (s.whole) {
+              int64_t t;
+              int hq;
+              place(r, &t, &hq);
+              T* out = static_cast<T*>(A.out) + t * A.o_ts + int64_t(hq) * A.o_hs +
+                       c * kStageCols + e;
+              const uint32_t w = Bits<T>::pack(v0 * stage.inv[r], v1 * stage.inv[r]);
+              if (A.out_vec) {
+                *reinterpret_cast<uint32_t*>(out) = w;
+              } else {
+                const uint16_t h0 = uint16_t(w), h1 = uint16_t(w >> 16);
+                out[0] = *reinterpret_cast<const T*>(&h0);
+                out[1] = *reinterpret_cast<const T*>(&h1);
+              }
+            } else {
+              *reinterpret_cast<float2*>(A.part_o + (pr + r) * D + c * kStageCols + e) =
+                  make_float2(v0, v1);
+            }
+          }
+        }
+        if (stop) break;
+      }
+      if (live && copy == 0) {
+        int64_t trow;
+        int hq;
+        place(rr, &trow, &hq);
+        if (s.whole)
+          A.lse[trow * A.Hq + hq] =
+              bad ? nan : (top == -INFINITY ? 0.f : top * kAttnLn2) + logf(total);
+        else
+          A.part_ml[pr + rr] = make_float2(bad ? nan : top, total);
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&S.ofree));
+      if (lane == 0) {
+        mbar_arrive(smem_addr(&S.ofree));
+        mbar_arrive(smem_addr(&S.qempty[unit % C::kQBufs]));
+      }
       if (tid == 0 && !s.whole && s.first == 0) {
         AttnSplit& u = A.split[blockIdx.x];
         u.last = attn_owner(A, P, s.unit_end - 1);
