@@ -145,13 +145,14 @@ struct AttnPlan {
   int code, code_b;  // a data error of the whole batch, and its request
 };
 
-template <int TN, int MR, bool WEIGHTS>
+// A request's share of the line; PAD: what each of its units adds to its tiles.
+template <int TN, int MR, bool WEIGHTS, int PAD = 0>
 __device__ __forceinline__ int64_t attn_tiles(const AttnArgs& A, const AttnReq& r) {
-  return WEIGHTS ? int64_t(r.ntiles) : int64_t(A.Hkv / A.hg) * r.mtiles * r.ntiles;
+  return WEIGHTS ? int64_t(r.ntiles) : int64_t(A.Hkv / A.hg) * r.mtiles * (r.ntiles + PAD);
 }
 
 // All threads of the block call this.  CTA 0 records the requests' errors.
-template <int TN, int MR, bool WEIGHTS, int THREADS>
+template <int TN, int MR, bool WEIGHTS, int THREADS, int PAD = 0>
 __device__ AttnPlan attn_plan(const AttnArgs& A) {
   __shared__ int64_t s_tiles[THREADS / 32 + 1];
   __shared__ int s_rows[THREADS / 32 + 1];
@@ -174,7 +175,7 @@ __device__ AttnPlan attn_plan(const AttnArgs& A) {
     const AttnReq r = attn_request<TN, MR, WEIGHTS>(A, b);
     if (A.k_per_req[b] != r.k) atomicMin(&s_badk, b);
     if (blockIdx.x == 0) A.status[b] = r.code;
-    tiles += attn_tiles<TN, MR, WEIGHTS>(A, r);
+    tiles += attn_tiles<TN, MR, WEIGHTS, PAD>(A, r);
     rows += r.k + 1;
   }
   int64_t it = tiles;
@@ -215,7 +216,7 @@ __device__ AttnPlan attn_plan(const AttnArgs& A) {
   if (P.start < P.end && P.start >= base && P.start < base + tiles) {
     for (int b = b0; b < b1; ++b) {
       const AttnReq r = attn_request<TN, MR, WEIGHTS>(A, b);
-      const int64_t t = attn_tiles<TN, MR, WEIGHTS>(A, r);
+      const int64_t t = attn_tiles<TN, MR, WEIGHTS, PAD>(A, r);
       if (P.start < base + t) {
         s_b = b;
         s_toff = toff;

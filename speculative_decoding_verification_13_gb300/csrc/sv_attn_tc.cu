@@ -60,14 +60,20 @@ constexpr int kSegs = 8;          // parts announced ahead of the warp that is f
 constexpr float kRescaleLog2 = 8.0f;
 
 // Copies' sums meet in shared memory: maximum and sum of each row of M, what
-// its row is divided by, and twice 16 columns of O.
-constexpr int kStageCols = 16, kStageRow = kStageCols + 1;  // floats, one for the banks
+// its row is divided by, and as many columns of the live rows' O as fit.
+constexpr int kStageFloats = kTcMr * 33;
 struct Stage {
   float2 ml[kTcMr];
   float inv[kTcMr];
-  float o[2][kTcMr * kStageRow];
+  float o[kStageFloats];
 };
 constexpr size_t kStageBytes = (sizeof(Stage) + 127) / 128 * 128;
+
+// What a unit costs beside its tiles, in tiles: the line that is cut over the
+// CTAs counts it (64 requests of 1 to 16000 positions without it: the CTA with
+// the most short ones took twice as long as the others).
+template <int D>
+constexpr int kUnitTiles = D == 64 ? 3 : 2;
 
 template <int D>
 struct Shape {
@@ -99,7 +105,7 @@ struct TcShared {
   uint64_t announced[kSegs];
   uint64_t full[11], empty[11];
   uint64_t qfull[2], qempty[2], sfull[kBufs], pfull[kBufs], pvdone[kBufs], ofree;
-  uint64_t looked[2], ends, drain;  // softmax warps among themselves
+  uint64_t looked[2], drain;  // softmax warps among themselves
   uint32_t tmem;
   int abort;
   int first_bad;
@@ -132,7 +138,7 @@ struct Buf {
   }
 };
 
-template <int TN>
+template <int TN, int PAD>
 struct Walk {
   int64_t pos, end, base;
   int b, t_off;
@@ -143,18 +149,28 @@ struct Walk {
   }
   __device__ __forceinline__ bool next(const AttnArgs& A, Seg& s) {
     if (pos >= end) return false;
-    int64_t nt = attn_tiles<TN, kTcMr, false>(A, R);
-    while (pos >= base + nt) {
-      base += nt;
-      t_off += R.k + 1;
-      R = attn_request<TN, kTcMr, false>(A, ++b);
-      nt = attn_tiles<TN, kTcMr, false>(A, R);
+    int64_t nt, local;
+    int unit;
+    for (;;) {
+      nt = attn_tiles<TN, kTcMr, false, PAD>(A, R);
+      while (pos >= base + nt) {
+        base += nt;
+        t_off += R.k + 1;
+        R = attn_request<TN, kTcMr, false>(A, ++b);
+        nt = attn_tiles<TN, kTcMr, false, PAD>(A, R);
+      }
+      local = pos - base;
+      const int span = R.ntiles + PAD, at = int(local % span);
+      unit = int(local / span);
+      if (at >= PAD) {
+        s.first = at - PAD;
+        break;
+      }
+      pos += PAD - at;   // a unit's tiles come behind what it costs itself
+      if (pos >= end) return false;
     }
-    const int64_t local = pos - base;
-    const int unit = int(local / R.ntiles);
     s.b = b;
     s.t_off = t_off;
-    s.first = int(local % R.ntiles);
     const int64_t left = end - pos;
     s.count = int(left < R.ntiles - s.first ? left : R.ntiles - s.first);
     s.h = unit / R.mtiles * A.hg + int(blockIdx.x) % A.hg;
@@ -275,6 +291,20 @@ __device__ __forceinline__ bool tc_sync(uint64_t* bar, uint32_t parity, TcShared
   return tc_wait_warp(bar, parity, S);
 }
 
+// Hardware barrier of the softmax warps, and the same with one truth value for
+// all of them.  None may stay away: they leave their loop only together.
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_any(bool x) {
+  int any;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %1, 0;\n"
+      "barrier.cta.red.or.pred q, 2, 128, p;\nselp.b32 %0, 1, 0, q;\n}\n"
+      : "=r"(any)
+      : "r"(int(x))
+      : "memory");
+  return any != 0;
+}
+
 // The part that warp comes to next; false at the end, or when the CTA gave up.
 __device__ __forceinline__ bool next_seg(TcShared& S, int unit, Seg& s) {
   if (!tc_wait_warp(&S.announced[unit % kSegs], (unit / kSegs) & 1, S)) return false;
@@ -314,7 +344,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int i = 0; i < kSegs; ++i) mbar_init(smem_addr(&S.announced[i]), 1);
     mbar_init(smem_addr(&S.looked[0]), 4);
     mbar_init(smem_addr(&S.looked[1]), 4);
-    mbar_init(smem_addr(&S.ends), 4);
     mbar_init(smem_addr(&S.drain), 1);
     fence_mbar_init();
     S.abort = 0;
@@ -327,7 +356,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                  "r"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  const AttnPlan P = attn_plan<TN, kTcMr, false, kTcThreads>(A);
+  const AttnPlan P = attn_plan<TN, kTcMr, false, kTcThreads, kUnitTiles<D>>(A);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -451,7 +480,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr int kChunks = D / 8, kStep = 32 / kChunks;
     const int ch = lane % kChunks;
     const T* q = static_cast<const T*>(A.q);
-    Walk<TN> walk(A, P);
+    Walk<TN, kUnitTiles<D>> walk(A, P);
     for (int unit = 0;; ++unit) {
       Seg s;
       s.count = 0;
@@ -540,7 +569,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int unit_pv = -1;
     bool ok = kind > 0;
     while (ok) {
-      const int next = issue_s();
+      // S of the next tile goes ahead of this tile's second product, but not
+      // across units: the next unit's first keys may be far away yet
+      const bool ahead = left > 0;
+      int next = ahead ? issue_s() : 0;
       if (next < 0) break;
       const uint32_t slot = v_slot.at;
       if (kind == 2) {
@@ -562,6 +594,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mma_commit(lead, &S.empty[slot]);
       v_slot.step();
       pb.step();
+      if (!ahead) next = issue_s();
       kind = next;
       ok = next > 0;
     }
@@ -576,11 +609,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t lanes = tmem + (uint32_t(warp * 32) << 16);
     Seg s;
     int g = 0;
-    uint32_t looked = 0, collected = 0, ends = 0;
+    uint32_t looked = 0, collected = 0;
     Slot<C::kSlots> v_slot{1, 0};
     Buf bf, done;                // of this tile, and of the one before (its product with V)
-    bool stop = false;
-    for (int unit = 0; !stop && next_seg(S, unit, s); ++unit) {
+    for (int unit = 0;; ++unit) {
+      bool stop = !next_seg(S, unit, s);
+      if (softmax_any(stop)) break;
       const int apart = kTcMr / s.copies;
       const int copy = tid / apart, rr = tid % apart;   // warps lie in one copy
       const bool active = warp * 32 % apart < s.rows;
@@ -778,9 +812,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc_fence_before();
         }
       }
-      if (stop) break;
       // ------------------------------------------------- the unit's rows
-      if (!tc_wait_warp(&S.pvdone[done.at], done.phase, S)) break;
+      if (!stop) stop = !tc_wait_warp(&S.pvdone[done.at], done.phase, S);
+      if (softmax_any(stop)) break;
       tc_fence_after();
       const bool bad = *reinterpret_cast<volatile int*>(&S.bad[unit % kSegs]) != 0;
       const float nan = __int_as_float(0x7fc00000);
@@ -832,14 +866,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
       } else {
-        // The copies' sums and outputs add up at their common maximum, 16
-        // columns of O at a time; all threads then write what is live of them.
+        // The copies' sums and outputs add up at their common maximum, as many
+        // columns of O at a time as fit; all threads then write them.
         Stage& stage = *reinterpret_cast<Stage*>(
             smem_p + (C::kOwnStage ? C::kQBufs * C::kQBytes + C::kSlots * kSlotBytes
                                    : unit % C::kQBufs * C::kQBytes));
         stage.ml[tid] = make_float2(m, l);
-        if (!tc_sync(&S.ends, ends, S)) break;
-        ends ^= 1;
+        softmax_sync();
         for (int c = 0; c < s.copies; ++c) top = fmaxf(top, stage.ml[rr + c * apart].x);
         total = 0.f;
         for (int c = 0; c < s.copies; ++c) {
@@ -848,27 +881,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         const float f = m > -INFINITY ? exp2f(m - top) : 0.f;
         if (copy == 0) stage.inv[rr] = bad ? nan : total == 0.f ? 0.f : 1.f / total;
+        int cols = D;
+        while (s.rows * s.copies * (cols + 1) > kStageFloats) cols >>= 1;
+        const int half = cols / 2, shift = 31 - __clz(half);
 #pragma unroll 1
-        for (int c = 0; c < D / kStageCols; ++c) {
-          float* buf = stage.o[c & 1];
+        for (int c0 = 0; c0 < D; c0 += cols) {
           if (active) {
-            uint32_t o[16];
-            tmem_ld16(lanes + C::kOCol + c * kStageCols, o);
-            tmem_ld_wait();
+            float* to = stage.o + (copy * s.rows + rr) * (cols + 1);
+#pragma unroll 1
+            for (int c = 0; c < cols; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(lanes + C::kOCol + c0 + c, o);
+              tmem_ld_wait();
+              if (live) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              buf[tid * kStageRow + e] = __uint_as_float(o[e]) * f;
+                for (int e = 0; e < 16; ++e) to[c + e] = __uint_as_float(o[e]) * f;
+              }
+            }
           }
-          if (!tc_sync(&S.ends, ends, S)) {
-            stop = true;
-            break;
-          }
-          ends ^= 1;
-          for (int i = tid; i < s.rows * (kStageCols / 2); i += 128) {
-            const int r = i / (kStageCols / 2), e = i % (kStageCols / 2) * 2;
+          softmax_sync();
+          for (int i = tid; i < s.rows * half; i += 128) {
+            const int r = i >> shift, e = (i & (half - 1)) * 2;
             float v0 = 0.f, v1 = 0.f;
             for (int k = 0; k < s.copies; ++k) {
-              const float* from = buf + (k * apart + r) * kStageRow + e;
+              const float* from = stage.o + (k * s.rows + r) * (cols + 1) + e;
               v0 += from[0];
               v1 += from[1];
             }
@@ -876,8 +912,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               int64_t t;
               int hq;
               place(r, &t, &hq);
-              T* out = static_cast<T*>(A.out) + t * A.o_ts + int64_t(hq) * A.o_hs +
-                       c * kStageCols + e;
+              T* out = static_cast<T*>(A.out) + t * A.o_ts + int64_t(hq) * A.o_hs + c0 + e;
               const uint32_t w = Bits<T>::pack(v0 * stage.inv[r], v1 * stage.inv[r]);
               if (A.out_vec) {
                 *reinterpret_cast<uint32_t*>(out) = w;
@@ -887,12 +922,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 out[1] = *reinterpret_cast<const T*>(&h1);
               }
             } else {
-              *reinterpret_cast<float2*>(A.part_o + (pr + r) * D + c * kStageCols + e) =
-                  make_float2(v0, v1);
+              *reinterpret_cast<float2*>(A.part_o + (pr + r) * D + c0 + e) = make_float2(v0, v1);
             }
           }
+          softmax_sync();
         }
-        if (stop) break;
       }
       if (live && copy == 0) {
         int64_t trow;
