@@ -9,9 +9,9 @@
 // share of the HBM.
 //
 // One CTA per SM, over its piece of the line of tiles (sv_attn.cuh):
-//   warp 7     finds the CTA's units, announces them and loads their Q, one ahead
+//   warp 8     finds the CTA's units, announces them and loads their Q, one ahead
 //              where two fit.
-//   warps 4-5  load, tile by tile, K (warp 4) and V (warp 5) into a ring of slots, in the
+//   warps 4, 5 load, tile by tile, K and V into rings of slots, in the
 //              128-byte swizzled layout that the tensor cores read (K along the
 //              head: K-major; V along the head: MN-major).  The copy engine
 //              moves what a page has of the tile in boxes of 128 bytes by the
@@ -25,8 +25,10 @@
 //              for every copy in flight, 229 us; rows gathered by the copy
 //              engine, four an instruction, of which it takes one in about 50
 //              cycles, 264 us.
-//   warp 6     issues the products (one lane).  S has three accumulators, so that
-//              S of the next tiles does not wait for the product of this one.
+//   warps 6, 7 issue the products, one S and one O.  S has three accumulators, so
+//              that S of the next tiles does not wait for the product of this
+//              one.  (One warp for both: a tile of 128 positions of heads of 64
+//              took 1760 cycles, of which its 12 products 620.)
 //   warps 0-3  softmax, one row a thread (the lanes of TMEM): scores from TMEM,
 //              running maximum, P rounded to the type (half a step of it, the
 //              one rounding of a weight; sums stay in 32 bits) back to TMEM over
@@ -52,10 +54,10 @@
 namespace sv {
 namespace {
 
-constexpr int kTcThreads = 256;   // 4 softmax, 2 load, 1 product, 1 query warp
+constexpr int kTcThreads = 288;   // 4 softmax warps, then one each of the following
 constexpr int kTcMr = 128;
 constexpr int kBufs = 3;          // S accumulators, each then the P of its tile
-constexpr int kLoadWarp = 4, kMmaWarp = 6, kQueryWarp = 7;
+constexpr int kLoadWarp = 4, kScoreWarp = 6, kValueWarp = 7, kQueryWarp = 8;
 constexpr int kSegs = 8;          // parts announced ahead of the warp that is furthest back
 constexpr float kRescaleLog2 = 8.0f;
 
@@ -82,6 +84,9 @@ struct Shape {
   static constexpr int kQBytes = kTcMr * D * 2;
   static constexpr int kQBufs = D == 256 ? 1 : 2;
   static constexpr int kSlots = D == 64 ? 10 : 5;  // what shared memory holds
+  // of K; the rest, three at least (the softmax warps look at V of a tile whose
+  // slot was filled before at most three tiles ago), are of V
+  static constexpr int kKSlots = kSlots / 2;
   static constexpr uint32_t kOCol = kBufs * TN;     // TMEM columns: the S accumulators, then O
   // where copies of rows are added up: a query buffer, or a place of its own
   static constexpr bool kOwnStage = kQBytes < int(kStageBytes);
@@ -105,7 +110,7 @@ struct TcShared {
   uint64_t announced[kSegs];
   uint64_t full[11], empty[11];
   uint64_t qfull[2], qempty[2], sfull[kBufs], pfull[kBufs], pvdone[kBufs], ofree;
-  uint64_t looked[2], drain;  // softmax warps among themselves
+  uint64_t looked[2], drain[2];  // softmax warps among themselves; products after a failure
   uint32_t tmem;
   int abort;
   int first_bad;
@@ -114,14 +119,16 @@ struct TcShared {
   int dirty[kBufs];  // per S buffer: 1 + the tile whose V holds a non-finite value
 };
 
-// A place in the ring and the phase of its barriers, one tile (K and V) a step.
-template <int N>
-struct Slot {
-  uint32_t at, phase;
+// A place in a ring of slots and the phase of its barriers.  K and V have rings
+// of their own: with one for both, a load warp could meet a barrier two phases
+// behind, whose parity is that of the phase it waits for.
+struct Ring {
+  uint32_t at, phase, base, end;
+  __device__ __forceinline__ Ring(uint32_t first, uint32_t n, uint32_t phase_)
+      : at(first), phase(phase_), base(first), end(first + n) {}
   __device__ __forceinline__ void step() {
-    at += 2;
-    if (at >= N) {
-      at -= N;
+    if (++at == end) {
+      at = base;
       phase ^= 1;
     }
   }
@@ -283,6 +290,22 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, TcShared
 __device__ __forceinline__ bool tc_wait_warp(uint64_t* bar, uint32_t parity, TcShared& S) {
   return __all_sync(0xffffffffu, tc_wait(bar, parity, S));
 }
+// Two barriers at once: their polls overlap (a poll that succeeds still takes
+// about 100 cycles between two products).
+__device__ __forceinline__ bool tc_wait_two(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
+                                            TcShared& S) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p, q;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n"
+      "and.pred p, p, q;\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_addr(a)), "r"(pa), "r"(smem_addr(b)), "r"(pb)
+      : "memory");
+  if (__all_sync(0xffffffffu, ok != 0)) return true;
+  return tc_wait_warp(a, pa, S) && tc_wait_warp(b, pb, S);
+}
 // Barrier of the four warps that count on `bar`, bounded like every other wait
 // (a warp that gave up would leave a hardware barrier waiting for ever).
 __device__ __forceinline__ bool tc_sync(uint64_t* bar, uint32_t parity, TcShared& S) {
@@ -344,13 +367,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int i = 0; i < kSegs; ++i) mbar_init(smem_addr(&S.announced[i]), 1);
     mbar_init(smem_addr(&S.looked[0]), 4);
     mbar_init(smem_addr(&S.looked[1]), 4);
-    mbar_init(smem_addr(&S.drain), 1);
+    mbar_init(smem_addr(&S.drain[0]), 1);
+    mbar_init(smem_addr(&S.drain[1]), 1);
     fence_mbar_init();
     S.abort = 0;
     S.first_bad = INT32_MAX;
     A.split[blockIdx.x].valid = 0;
   }
-  if (warp == kMmaWarp) {
+  if (warp == kValueWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(&S.tmem)),
                  "r"(kTmemCols));
@@ -364,7 +388,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (P.code) fail_all<T>(A);
   const bool go = P.code == 0 && P.start < P.end;
 
-  if (go && warp >= kLoadWarp && warp < kMmaWarp) {
+  if (go && warp >= kLoadWarp && warp < kScoreWarp) {
     // ----------------------------------------------------------------- loads
     const int kv = warp - kLoadWarp;              // 0: K, 1: V
     constexpr int kParts = D / 64;                // 128-byte parts of a row
@@ -374,7 +398,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // keys that no other unit of the call reads leave the L2 first
     const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
     Seg s;
-    Slot<C::kSlots> at{uint32_t(kv), 1};  // empty barriers: the first round passes at once
+    Ring at(kv ? C::kKSlots : 0, kv ? C::kSlots - C::kKSlots : C::kKSlots,
+            1);  // empty barriers: the first round passes at once
     bool stop = false;
     for (int unit = 0; !stop && next_seg(S, unit, s); ++unit) {
       const int hi = s.R.code ? 0 : s.R.hi;
@@ -517,16 +542,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&S.qfull[qb]));
     }
-  } else if (go && warp == kMmaWarp) {
+  } else if (go && (warp == kScoreWarp || warp == kValueWarp)) {
     // -------------------------------------------------------------- products
+    // Two warps, so that one's waits do not hold up the other's products: every
+    // order between them goes by barriers.
     constexpr uint32_t kBase = (1u << 4) | (Bits<T>::kFmt << 7) | (Bits<T>::kFmt << 10) |
                                (uint32_t(kTcMr >> 4) << 24);
     constexpr uint32_t kIdescS = kBase | (uint32_t(TN >> 3) << 17);
     constexpr uint32_t kIdescO = kBase | (uint32_t(D >> 3) << 17) | (1u << 16);
     const uint32_t lead = lane == 0;
-    Slot<C::kSlots> k_slot{0, 0}, v_slot{1, 0};
-    int left = 0, unit = -1;     // tiles of the unit whose S is issued next, the unit
-    Buf sb, pb;                  // buffers of the next S and of the next P
+    const bool scores = warp == kScoreWarp;
+    Ring slot(scores ? 0 : C::kKSlots, scores ? C::kKSlots : C::kSlots - C::kKSlots, 0);
+    Buf buf;
     // The fence that orders the lanes' copies before the products' reads takes
     // as long as the products in flight: only slots that were filled by them.
     auto slot_copied = [&](uint32_t i) {
@@ -535,73 +562,58 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // descriptors of the first Q buffer and slot; others lie a constant away
     const uint64_t q_desc = sw128_desc(smem0), k_desc = sw128_desc(ring0);
     const uint64_t v_desc = sw128_mn_desc(ring0, TN * 128);
-    auto issue_s = [&]() -> int {  // 0: no tile left, 1: issued, 2: the first of its unit, -1: gave up
-      int kind = 1;
-      if (left == 0) {
-        ++unit;
-        Seg s;
-        if (!next_seg(S, unit, s)) return 0;
-        left = s.count;
-        kind = 2;
-        if (!tc_wait_warp(&S.qfull[unit % C::kQBufs], (unit / C::kQBufs) & 1, S)) return -1;
-      }
-      // the buffer's last P has been read (the first round passes at once)
-      if (!tc_wait_warp(&S.pvdone[sb.at], sb.phase ^ 1, S)) return -1;
-      const uint32_t slot = k_slot.at;
-      if (!tc_wait_warp(&S.full[slot], k_slot.phase, S)) return -1;
-      if (slot_copied(slot)) fence_async_proxy();
-      tc_fence_after();
-      const uint64_t q = q_desc + uint32_t((unit % C::kQBufs) * (C::kQBytes >> 4));
-      const uint64_t k = k_desc + slot * (kSlotBytes >> 4);
-      const uint32_t d = tmem + sb.at * TN;
+    bool ok = true;
+    for (int unit = 0; ok; ++unit) {
+      ok = tc_wait_warp(&S.announced[unit % kSegs], (unit / kSegs) & 1, S);
+      const int count = ok ? S.seg[unit % kSegs].count : 0;
+      if (count == 0) break;
+      if (scores) {
+        const int qb = unit % C::kQBufs;
+        ok = tc_wait_warp(&S.qfull[qb], (unit / C::kQBufs) & 1, S);
+        const uint64_t q = q_desc + uint32_t(qb * (C::kQBytes >> 4));
+        for (int t = 0; ok && t < count; ++t) {
+          // keys there, and the buffer's last P read (the first round passes at once)
+          ok = tc_wait_two(&S.full[slot.at], slot.phase, &S.pvdone[buf.at], buf.phase ^ 1, S);
+          if (!ok) break;
+          if (slot_copied(slot.at)) fence_async_proxy();
+          tc_fence_after();
+          const uint64_t k = k_desc + slot.at * (kSlotBytes >> 4);
+          const uint32_t d = tmem + buf.at * TN;
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c)
-        mma_ss(lead, d, q + (((c >> 2) * (kTcMr * 128) + (c & 3) * 32) >> 4),
-               k + (((c >> 2) * (TN * 128) + (c & 3) * 32) >> 4), kIdescS, c != 0);
-      mma_commit(lead, &S.sfull[sb.at]);
-      mma_commit(lead, &S.empty[slot]);
-      --left;
-      k_slot.step();
-      sb.step();
-      return kind;
-    };
-    int kind = issue_s();
-    int unit_pv = -1;
-    bool ok = kind > 0;
-    while (ok) {
-      // S of the next tile goes ahead of this tile's second product, but not
-      // across units: the next unit's first keys may be far away yet
-      const bool ahead = left > 0;
-      int next = ahead ? issue_s() : 0;
-      if (next < 0) break;
-      const uint32_t slot = v_slot.at;
-      if (kind == 2) {
-        ++unit_pv;
+          for (int c = 0; c < D / 16; ++c)
+            mma_ss(lead, d, q + (((c >> 2) * (kTcMr * 128) + (c & 3) * 32) >> 4),
+                   k + (((c >> 2) * (TN * 128) + (c & 3) * 32) >> 4), kIdescS, c != 0);
+          mma_commit(lead, &S.sfull[buf.at]);
+          mma_commit(lead, &S.empty[slot.at]);
+          slot.step();
+          buf.step();
+        }
+      } else {
         // O still holds the unit before until its rows have been read
-        if (unit_pv > 0 && !tc_wait_warp(&S.ofree, (unit_pv - 1) & 1, S)) break;
-      }
-      if (!tc_wait_warp(&S.full[slot], v_slot.phase, S)) break;
-      if (!tc_wait_warp(&S.pfull[pb.at], pb.phase, S)) break;
-      if (slot_copied(slot)) fence_async_proxy();
-      tc_fence_after();
-      const uint64_t v = v_desc + slot * (kSlotBytes >> 4);
-      const uint32_t p = tmem + pb.at * TN;
+        if (unit > 0) ok = tc_wait_warp(&S.ofree, (unit - 1) & 1, S);
+        for (int t = 0; ok && t < count; ++t) {
+          ok = tc_wait_two(&S.full[slot.at], slot.phase, &S.pfull[buf.at], buf.phase, S);
+          if (!ok) break;
+          if (slot_copied(slot.at)) fence_async_proxy();
+          tc_fence_after();
+          const uint64_t v = v_desc + slot.at * (kSlotBytes >> 4);
+          const uint32_t p = tmem + buf.at * TN;
 #pragma unroll
-      for (int c = 0; c < TN / 16; ++c)
-        mma_ts(lead, tmem + C::kOCol, p + c * 8, v + c * (2048 >> 4), kIdescO,
-               (c != 0) || kind != 2);
-      mma_commit(lead, &S.pvdone[pb.at]);
-      mma_commit(lead, &S.empty[slot]);
-      v_slot.step();
-      pb.step();
-      if (!ahead) next = issue_s();
-      kind = next;
-      ok = next > 0;
+          for (int c = 0; c < TN / 16; ++c)
+            mma_ts(lead, tmem + C::kOCol, p + c * 8, v + c * (2048 >> 4), kIdescO,
+                   (c != 0) || t > 0);
+          mma_commit(lead, &S.pvdone[buf.at]);
+          mma_commit(lead, &S.empty[slot.at]);
+          slot.step();
+          buf.step();
+        }
+      }
     }
     if (*reinterpret_cast<volatile int*>(&S.abort)) {
       // every product issued must finish before TMEM is freed
-      mma_commit(lead, &S.drain);
-      mbar_wait_for(smem_addr(&S.drain), 0);
+      uint64_t* drain = &S.drain[scores ? 0 : 1];
+      mma_commit(lead, drain);
+      mbar_wait_for(smem_addr(drain), 0);
       __syncwarp();
     }
   } else if (go && warp < kLoadWarp) {
@@ -610,7 +622,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     Seg s;
     int g = 0;
     uint32_t looked = 0, collected = 0;
-    Slot<C::kSlots> v_slot{1, 0};
+    Ring v_slot(C::kKSlots, C::kSlots - C::kKSlots, 0);
     Buf bf, done;                // of this tile, and of the one before (its product with V)
     for (int unit = 0;; ++unit) {
       bool stop = !next_seg(S, unit, s);
@@ -703,24 +715,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             fence_async_proxy();
           }
         }
-        // N columns of the tile, the warp's copy's share
-        auto weigh = [&](auto width) -> bool {
-          constexpr int N = decltype(width)::value;
+        // The warp's copy's share of the columns, N at a time (two rounds where
+        // it has all of 128: the first round's scores are read again after the
+        // maximum over both)
+        auto weigh = [&](auto width, auto rounds) -> bool {
+          constexpr int N = decltype(width)::value, ROUNDS = decltype(rounds)::value;
           const int c0 = copy * N;
           float x[N];
+          auto fetch = [&](int round) {
 #pragma unroll
-          for (int c = 0; c < N / 32; ++c)
-            tmem_ld32(scol + c0 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[c * 32]));
-          tmem_ld_wait();
-          if (edge) {
+            for (int c = 0; c < N / 32; ++c)
+              tmem_ld32(scol + c0 + round * N + c * 32,
+                        *reinterpret_cast<uint32_t(*)[32]>(&x[c * 32]));
+            tmem_ld_wait();
+            if (edge) {
+              const int p = p0 + c0 + round * N;
 #pragma unroll
-            for (int c = 0; c < N; ++c)
-              x[c] = p0 + c0 + c >= row_lo && p0 + c0 + c < row_hi ? x[c] : -INFINITY;
+              for (int c = 0; c < N; ++c)
+                x[c] = p + c >= row_lo && p + c < row_hi ? x[c] : -INFINITY;
+            }
+          };
+          float high = -INFINITY;
+#pragma unroll
+          for (int round = 0; round < ROUNDS; ++round) {
+            fetch(round);
+#pragma unroll
+            for (int c = 0; c < N; ++c) high = fmaxf(high, x[c]);
           }
-          float top = x[0];
-#pragma unroll
-          for (int c = 1; c < N; ++c) top = fmaxf(top, x[c]);
-          const float grown = fmaxf(m, top * A.scale2);   // scale2 > 0
+          const float grown = fmaxf(m, high * A.scale2);   // scale2 > 0
           const bool rescale = live && grown > m + kRescaleLog2;
           if (__any_sync(0xffffffffu, rescale)) {
             // all rows of the warp move to their present maximum
@@ -729,14 +751,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               if (!tc_wait_warp(&S.pvdone[done.at], done.phase, S)) return false;
               tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(lanes + C::kOCol + c * 32, o);
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld16(lanes + C::kOCol + c * 16, o);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
+                for (int e = 0; e < 16; ++e)
                   o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st32(lanes + C::kOCol + c * 32, o);
+                tmem_st16(lanes + C::kOCol + c * 16, o);
               }
             }
             l *= f;
@@ -745,39 +767,61 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const float sh = m == -INFINITY ? 0.f : m;
           const uint64_t sc2 = pk2(A.scale2, A.scale2), sh2 = pk2(-sh, -sh);
           uint64_t sum = pk2(0.f, 0.f);
-          uint32_t pw[N / 2];
+          // the last round's scores are still there; P of a round lies over
+          // scores that are read by then (of this or an earlier round)
+          uint32_t held[ROUNDS > 1 ? N / 2 : 1];
 #pragma unroll
-          for (int c = 0; c < N; c += 2) {
-            float e0, e1;
-            upk2(fma2(pk2(x[c], x[c + 1]), sc2, sh2), e0, e1);
-            e0 = ex2_approx(e0);
-            e1 = ex2_approx(e1);
-            sum = add2(sum, pk2(e0, e1));
-            pw[c / 2] = Bits<T>::pack(e0, e1);
+          for (int round = ROUNDS - 1; round >= 0; --round) {
+            if (round != ROUNDS - 1) fetch(round);
+            uint32_t pw[N / 2];
+#pragma unroll
+            for (int c = 0; c < N; c += 2) {
+              float e0, e1;
+              upk2(fma2(pk2(x[c], x[c + 1]), sc2, sh2), e0, e1);
+              e0 = ex2_approx(e0);
+              e1 = ex2_approx(e1);
+              sum = add2(sum, pk2(e0, e1));
+              pw[c / 2] = Bits<T>::pack(e0, e1);
+            }
+            if (ROUNDS > 1 && round == 1) {
+#pragma unroll
+              for (int c = 0; c < N / 2; ++c) held[c] = pw[c];
+            } else {
+              // the other copies' columns are theirs: zeros here
+              uint32_t zero[16];
+#pragma unroll
+              for (int c = 0; c < 16; ++c) zero[c] = 0;
+#pragma unroll
+              for (int i = 0; i < TN / N / ROUNDS; ++i)
+#pragma unroll
+                for (int c = 0; c < N / 32; ++c) {
+                  const uint32_t to = scol + i * (N / 2) + c * 16;
+                  if (i == copy) tmem_st16(to, *reinterpret_cast<uint32_t(*)[16]>(&pw[c * 16]));
+                  else tmem_st16(to, zero);
+                }
+              if constexpr (ROUNDS > 1) {
+#pragma unroll
+                for (int c = 0; c < N / 32; ++c)
+                  tmem_st16(scol + N / 2 + c * 16,
+                            *reinterpret_cast<uint32_t(*)[16]>(&held[c * 16]));
+              }
+            }
           }
           float s0, s1;
           upk2(sum, s0, s1);
           l += s0 + s1;
-          // the other copies' columns are theirs: zeros here
-          uint32_t zero[16];
-#pragma unroll
-          for (int c = 0; c < 16; ++c) zero[c] = 0;
-#pragma unroll
-          for (int i = 0; i < TN / N; ++i)
-#pragma unroll
-            for (int c = 0; c < N / 32; ++c) {
-              const uint32_t to = scol + i * (N / 2) + c * 16;
-              if (i == copy) tmem_st16(to, *reinterpret_cast<uint32_t(*)[16]>(&pw[c * 16]));
-              else tmem_st16(to, zero);
-            }
           tmem_st_wait();
           return true;
         };
         if (active) {
           bool ok;
-          if (s.copies == 1) ok = weigh(std::integral_constant<int, TN>());
-          else if (s.copies == 2) ok = weigh(std::integral_constant<int, TN / 2>());
-          else ok = weigh(std::integral_constant<int, TN == 128 ? 32 : TN / 2>());
+          using One = std::integral_constant<int, 1>;
+          if (s.copies == 1)
+            ok = weigh(std::integral_constant<int, 64>(), std::integral_constant<int, TN / 64>());
+          else if (s.copies == 2)
+            ok = weigh(std::integral_constant<int, TN / 2>(), One());
+          else
+            ok = weigh(std::integral_constant<int, 32>(), One());
           if (!ok) {
             stop = true;
             break;
@@ -960,7 +1004,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   if (tid == 0)
     A.status[A.B + blockIdx.x] = S.abort ? -SV_ERR_TIMEOUT : S.first_bad;
-  if (warp == kMmaWarp) {
+  if (warp == kValueWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(kTmemCols));
