@@ -74,10 +74,12 @@ bool misaligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p
 size_t elem_size(int dtype) { return dtype == SV_BF16 || dtype == SV_F16 ? 2 : 4; }
 
 int sm_count() {
+  static std::atomic<int> known[kMaxDevices];
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < kMaxDevices && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < kMaxDevices) known[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
 

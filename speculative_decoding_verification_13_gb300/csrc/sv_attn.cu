@@ -388,9 +388,10 @@ cudaError_t launch_join(Kern kernel, const AttnArgs& A, cudaStream_t s) {
 template <class T>
 cudaError_t run_attn(const AttnArgs& A, bool weights, cudaStream_t s) {
   const size_t smem = weights ? smem_weights<T>(A.D) : smem_attn<T>(A.D);
-  const void* f = weights ? reinterpret_cast<const void*>(attn_weights_kernel<T>)
-                          : reinterpret_cast<const void*>(attn_kernel<T>);
-  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  // the most that any head size takes
+  static std::atomic<uint64_t> done_w{0}, done_a{0};
+  cudaError_t e = weights ? allow_smem(attn_weights_kernel<T>, smem_weights<T>(kMaxD), done_w)
+                          : allow_smem(attn_kernel<T>, smem_attn<T>(kMaxD), done_a);
   if (e != cudaSuccess) return e;
   if (weights) {
     attn_weights_kernel<T><<<A.ctas, kAtThreads, smem, s>>>(A);

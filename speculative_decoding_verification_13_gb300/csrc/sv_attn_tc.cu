@@ -1031,9 +1031,8 @@ bool rows_map(CUtensorMap* map, const AttnArgs& A, bool bf16) {
 
 template <class T, int D>
 cudaError_t run(const AttnArgs& A, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(
-      attn_tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Shape<D>::kSmem));
-  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> configured{0};
+  if (cudaError_t e = allow_smem(attn_tc_kernel<T, D>, Shape<D>::kSmem, configured)) return e;
   CUtensorMap map;
   AttnArgs B = A;
   // rows of a page that lie in one tile, whole groups of 8 of the swizzled layout

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/specverify.h"
 
 namespace sv {
@@ -249,6 +251,20 @@ struct AttnArgs;
 size_t attn_workspace_bytes(int32_t B, int32_t D, int sms, bool weights);
 cudaError_t launch_attn(AttnArgs A, int dtype, bool weights, void* workspace, int sms,
                         cudaStream_t s);
+
+// A kernel's limit of dynamic shared memory, raised once per device.  `done` is
+// a static of the caller's, one bit a device; a device past the 64th asks again.
+template <class Kern>
+inline cudaError_t allow_smem(Kern kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Launch of a kernel that may start while the previous kernel on the stream
 // finishes (programmatic dependent launch): it must execute pdl_wait() before

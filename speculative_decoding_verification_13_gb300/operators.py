@@ -18,8 +18,7 @@ import math
 
 import torch
 
-from . import (SV_BF16, SV_F32, SV_OK, SpecVerifyError, _KvCache, _Logits, _check, _ptr, get_error,
-               load_library)
+from . import SV_BF16, SV_F32, SV_OK, SpecVerifyError, _KvCache, _Logits, _check, load_library
 
 SV_F16 = 2
 SV_LOGPROBS_TOP_MAX = 32
@@ -66,20 +65,18 @@ def _library():
 
 # ----------------------------------------------------------- streams, workspaces
 _workspaces = {}   # (kind, device, stream) -> workspace: calls of one stream are in order
-_last = {}         # (kind, device) -> (workspace, stream) of the last call
+_last = {}         # (kind, device) -> (workspace, stream handle, stream) of the last call
 _sizes = {}        # workspace sizes already asked for
 
 
 def _stream_of(stream, dev):
-    return torch.cuda.current_stream(dev) if stream is None else stream
+    """The handle of ``stream``, or of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
 
 
-def _scratch(kind, dev, stream, size):
-    """A workspace for a call on ``stream``: one per stream, or one of its own
-    while a graph is being captured (the graph may be replayed next to the
-    stream's other calls)."""
-    size_key = (kind, dev.index, size)
-    need = _sizes.get(size_key)
+def _workspace_size(kind, dev, size):
+    key = (kind, dev.index, size)
+    need = _sizes.get(key)
     if need is None:
         with torch.cuda.device(dev):
             need = int(getattr(_library(), f"spec_{kind}_workspace_size")(*size))
@@ -87,27 +84,45 @@ def _scratch(kind, dev, stream, size):
             raise SpecVerifyError(1, f"spec_{kind}_workspace_size")
         if len(_sizes) > 4096:
             _sizes.clear()
-        _sizes[size_key] = need
-    key = (kind, dev.index, stream.cuda_stream)
-    ws = None if torch.cuda.is_current_stream_capturing() else _workspaces.get(key)
+        _sizes[key] = need
+    return need
+
+
+def _scratch(kind, dev, stream, handle, size):
+    """A workspace for a call on the stream: one per stream, or one of its own
+    while a graph is being captured (the graph may be replayed next to the
+    stream's other calls)."""
+    need = _workspace_size(kind, dev, size)
+    key = (kind, dev.index, handle)
+    capturing = torch.cuda.is_current_stream_capturing()
+    ws = None if capturing else _workspaces.get(key)
     if ws is None or ws.numel() < need:
-        with torch.cuda.stream(stream):
+        if stream is None:
             ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-        if not torch.cuda.is_current_stream_capturing():
+        else:
+            with torch.cuda.stream(stream):
+                ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        if not capturing:
             _workspaces[key] = ws
-    _last[kind, dev.index] = ws, stream
+    _last[kind, dev.index] = ws, handle, stream
     return ws
 
 
 def _error(kind, stream, device):
     d = torch.device(device or "cuda")
     index = d.index if d.index is not None else torch.cuda.current_device()
-    ws, last = _last[kind, index]
-    return get_error(ws, last if stream is None else stream)
+    ws, handle, _ = _last[kind, index]
+    code, req, row = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int64()
+    rc = _library().spec_verify_get_error(ws.data_ptr(), handle if stream is None else
+                                          stream.cuda_stream, ctypes.byref(code),
+                                          ctypes.byref(req), ctypes.byref(row))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_verify_get_error")
+    return code.value, req.value, row.value
 
 
 def _call(name, dev, *args):
-    f = getattr(_library(), name)
+    f = getattr(_lib or _library(), name)
     if torch.cuda.current_device() == dev.index:
         rc = f(*args)
     else:
@@ -119,89 +134,110 @@ def _call(name, dev, *args):
 
 # --------------------------------------------------------------------- checks
 def _vector(t, name, dtype, n, dev, optional=False):
+    """A contiguous vector of n elements or more; returns its address."""
     if t is None:
         if optional:
-            return
+            return None
         raise ValueError(f"{name} is required")
-    _check(t, name, dtype)
-    if t.device != dev:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != dev or \
+            t.dim() != 1 or not t.is_contiguous():
+        _check(t, name, dtype)
         raise ValueError(f"{name} is on {t.device}, not on {dev}")
     if t.numel() < n:
         raise ValueError(f"{name} holds {t.numel()} elements, {n} are needed")
+    return t.data_ptr()
 
 
 def _matrix(t, name, dtype, shape, dev):
-    """A contiguous tensor of this shape."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev:
+    """A contiguous tensor of this shape; returns its address."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != dev:
         raise TypeError(f"{name} must be a {dtype} tensor on {dev}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}")
+    return t.data_ptr()
 
 
 def _rows2d(t, name, dtype, rows, dev):
-    """A float matrix with contiguous rows; returns its row stride."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev or t.dim() != 2:
+    """A float matrix with contiguous rows; returns its address, row stride and columns."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != dev or t.dim() != 2:
         raise TypeError(f"{name} must be a 2-D {dtype} tensor on {dev}")
-    if t.shape[0] < rows or (t.shape[1] > 1 and t.stride(1) != 1):
+    n, cols = t.shape
+    stride, one = t.stride()
+    if n < rows or (cols > 1 and one != 1):
         raise ValueError(f"{name} must have {rows} contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.data_ptr(), stride if n > 1 else cols, cols
 
 
 def _cache_desc(cache, name="cache"):
+    """The cache's descriptor and shape."""
     if not isinstance(cache, torch.Tensor) or not cache.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if cache.dim() != 5 or not cache.is_contiguous() or cache.shape[2] != 2:
+    if cache.dim() != 5 or not cache.is_contiguous():
         raise ValueError(f"{name} must be contiguous [num_pages, n_layers, 2, page_size, E]")
-    if cache.element_size() not in (2, 4):
+    shape = cache.shape
+    pages, layers, two, S, E = shape
+    if two != 2:
+        raise ValueError(f"{name} must be contiguous [num_pages, n_layers, 2, page_size, E]")
+    es = cache.element_size()
+    if es not in (2, 4):
         raise TypeError(f"{name} must have a 2- or 4-byte dtype")
-    return _KvCache(cache.data_ptr() if cache.numel() else None, cache.shape[0], cache.shape[1],
-                    cache.shape[3], cache.shape[4], cache.element_size())
+    return _KvCache(cache.data_ptr() or None, pages, layers, S, E, es), shape
 
 
 def _table(t, name, B, dev):
+    """A block table; returns its address and columns."""
     if t is None:
         raise ValueError(f"{name} is required")
-    _check(t, name, torch.int32, ndim=2)
-    if t.device != dev or not t.is_contiguous() or t.shape[0] != B:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != 2 or \
+            t.device != dev or not t.is_contiguous():
+        _check(t, name, torch.int32, ndim=2)
         raise ValueError(f"{name} must be contiguous with {B} rows on {dev}")
+    rows, cols = t.shape
+    if rows != B:
+        raise ValueError(f"{name} must be contiguous with {B} rows on {dev}")
+    return t.data_ptr(), cols
 
 
 def _attention_args(q, cache, layer, kv_len, block_table, k_per_req, spec, scale, window):
     """The checks that both attention calls share; returns their leading arguments."""
-    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3 or q.dtype not in _DTYPES:
-        raise TypeError("q must be a 3-D float32, bfloat16 or float16 CUDA tensor")
-    desc = _cache_desc(cache)
-    dev = q.device
-    if cache.dtype != q.dtype or cache.device != dev:
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
+        raise TypeError("q must be a 3-D CUDA tensor")
+    dtype, dev = q.dtype, q.device
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"q must be float32, bfloat16 or float16, got {dtype}")
+    desc, shape = _cache_desc(cache)
+    if cache.dtype is not dtype or cache.device != dev:
         raise TypeError("q and cache must share dtype and device")
     rows, Hq, D = q.shape
-    E = cache.shape[4]
+    _, layers, _, _, E = shape
     if D < 1 or E % D or Hq < 1 or Hq % (E // D):
         raise ValueError(f"{Hq} heads of {D} do not fit a cache entry of {E} elements")
-    if D > 1 and q.stride(2) != 1:
+    ts, hs, one = q.stride()
+    if D > 1 and one != 1:
         raise ValueError("the heads of q must be contiguous")
-    if not 0 <= layer < cache.shape[1]:
-        raise ValueError(f"layer {layer} of {cache.shape[1]}")
+    if not 0 <= layer < layers:
+        raise ValueError(f"layer {layer} of {layers}")
     if window < 0:
         raise ValueError("window must be 0 (off) or positive")
-    B = int(k_per_req.shape[0])
-    _vector(k_per_req, "k_per_req", torch.int32, B, dev)
-    _vector(kv_len, "kv_len", torch.int32, B, dev)
-    _table(block_table, "block_table", B, dev)
-    slots = 0
+    B = k_per_req.shape[0]
+    k_ptr = _vector(k_per_req, "k_per_req", torch.int32, B, dev)
+    n_ptr = _vector(kv_len, "kv_len", torch.int32, B, dev)
+    t_ptr, cols = _table(block_table, "block_table", B, dev)
+    slots, s_ptr = 0, None
     if spec is not None:
         if not isinstance(spec, torch.Tensor) or spec.dim() != 5 or spec.shape[1] < 1:
             raise ValueError("spec must be [B, slots, n_layers, 2, E]")
-        slots = spec.shape[1]
-        if spec.dtype != q.dtype or spec.device != dev:
+        if spec.dtype is not dtype or spec.device != dev:
             raise TypeError("spec must share q's dtype and device")
-        if tuple(spec.shape) != (B, slots, cache.shape[1], 2, E) or not spec.is_contiguous():
+        slots = spec.shape[1]
+        if spec.shape != (B, slots, layers, 2, E) or not spec.is_contiguous():
             raise ValueError("spec must be contiguous [B, slots, n_layers, 2, E] matching the cache")
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    return dev, B, rows, Hq, D, (
-        ctypes.byref(desc), _DTYPES[q.dtype], int(layer), E // D, _ptr(q), q.stride(0),
-        q.stride(1), Hq, rows, _ptr(spec), slots, _ptr(k_per_req), _ptr(kv_len),
-        _ptr(block_table), block_table.shape[1], scale, int(window))
+        s_ptr = spec.data_ptr()
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    return dev, dtype, B, rows, Hq, D, (
+        ctypes.byref(desc), code, layer, E // D, q.data_ptr(), ts, hs, Hq, rows, s_ptr, slots,
+        k_ptr, n_ptr, t_ptr, cols, scale, window)
 
 
 # ------------------------------------------------------------------ operators
@@ -221,20 +257,20 @@ def attention(q, cache, layer, kv_len, block_table, k_per_req, spec=None, *, sca
 
     Returns ``(out [rows, q_heads, D], lse [rows, q_heads] float32)``; a token
     that sees nothing has out 0 and lse -inf."""
-    dev, B, rows, Hq, D, args = _attention_args(q, cache, layer, kv_len, block_table, k_per_req,
-                                                spec, scale, window)
+    dev, dtype, B, rows, Hq, D, args = _attention_args(q, cache, layer, kv_len, block_table,
+                                                       k_per_req, spec, scale, window)
     if out is None:
-        out = torch.empty((rows, Hq, D), dtype=q.dtype, device=dev)
+        out = torch.empty((rows, Hq, D), dtype=dtype, device=dev)
     else:
-        _matrix(out, "out", q.dtype, (rows, Hq, D), dev)
+        _matrix(out, "out", dtype, (rows, Hq, D), dev)
     if out_lse is None:
         out_lse = torch.empty((rows, Hq), dtype=torch.float32, device=dev)
     else:
         _matrix(out_lse, "out_lse", torch.float32, (rows, Hq), dev)
-    s = _stream_of(stream, dev)
-    ws = _scratch("attention", dev, s, (B, D))
-    _call("spec_attention", dev, *args, _ptr(out), _ptr(out_lse), s.cuda_stream, B, _ptr(ws),
-          ws.numel())
+    handle = _stream_of(stream, dev)
+    ws = _scratch("attention", dev, stream, handle, (B, D))
+    _call("spec_attention", dev, *args, out.data_ptr(), out_lse.data_ptr(), handle, B,
+          ws.data_ptr(), ws.numel())
     return out, out_lse
 
 
@@ -248,20 +284,20 @@ def attention_weights(q, cache, layer, kv_len, block_table, k_per_req, lse, scor
     rejected drafts leave no trace.  Positions 0 .. kv_len - 1 and, with
     ``spec``, those that the commit will append are written to ``out_score``
     (default: ``score`` itself).  Returns ``out_score``."""
-    dev, B, rows, Hq, D, args = _attention_args(q, cache, layer, kv_len, block_table, k_per_req,
-                                                spec, scale, window)
-    _matrix(lse, "lse", torch.float32, (rows, Hq), dev)
-    _vector(accept_len, "accept_len", torch.int32, B, dev, optional=True)
-    stride = _rows2d(score, "score", torch.float32, B, dev)
+    dev, _, B, rows, Hq, _, args = _attention_args(q, cache, layer, kv_len, block_table,
+                                                   k_per_req, spec, scale, window)
+    l_ptr = _matrix(lse, "lse", torch.float32, (rows, Hq), dev)
+    a_ptr = _vector(accept_len, "accept_len", torch.int32, B, dev, optional=True)
+    s_ptr, stride, cols = _rows2d(score, "score", torch.float32, B, dev)
     if out_score is None:
         out_score = score
-    out_stride = _rows2d(out_score, "out_score", torch.float32, B, dev)
-    if out_score.shape[1] != score.shape[1]:
+    o_ptr, out_stride, out_cols = _rows2d(out_score, "out_score", torch.float32, B, dev)
+    if out_cols != cols:
         raise ValueError("score and out_score must have the same columns")
-    s = _stream_of(stream, dev)
-    ws = _scratch("attention_weights", dev, s, (B,))
-    _call("spec_attention_weights", dev, *args, _ptr(lse), _ptr(accept_len), _ptr(score), stride,
-          _ptr(out_score), out_stride, score.shape[1], s.cuda_stream, B, _ptr(ws), ws.numel())
+    handle = _stream_of(stream, dev)
+    ws = _scratch("attention_weights", dev, stream, handle, (B,))
+    _call("spec_attention_weights", dev, *args, l_ptr, a_ptr, s_ptr, stride, o_ptr, out_stride,
+          cols, handle, B, ws.data_ptr(), ws.numel())
     return out_score
 
 
@@ -280,54 +316,55 @@ def kv_evict(cache, score, kv_len, block_table, budget, sinks=0, recent=0, *, ou
     ``out_score`` and ``out_len`` default to score and kv_len, in place.
 
     Returns ``(out_len [B] int32, kept [B, budget] int32 or None)``."""
-    desc = _cache_desc(cache)
+    desc, shape = _cache_desc(cache)
     dev = cache.device
-    B = int(kv_len.shape[0])
-    _vector(kv_len, "kv_len", torch.int32, B, dev)
-    _table(block_table, "block_table", B, dev)
-    budget, sinks, recent = int(budget), int(sinks), int(recent)
+    B = kv_len.shape[0]
+    n_ptr = _vector(kv_len, "kv_len", torch.int32, B, dev)
+    t_ptr, cols = _table(block_table, "block_table", B, dev)
     if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget:
         raise ValueError("budget must be positive and hold sinks and recent")
-    stride = _rows2d(score, "score", torch.float32, B, dev)
+    s_ptr, stride, score_cols = _rows2d(score, "score", torch.float32, B, dev)
     if out_score is None:
         out_score = score
-    out_stride = _rows2d(out_score, "out_score", torch.float32, B, dev)
+    os_ptr, out_stride, out_cols = _rows2d(out_score, "out_score", torch.float32, B, dev)
     if out_len is None:
         out_len = kv_len
-    _vector(out_len, "out_len", torch.int32, B, dev)
-    out_desc, out_cols = None, 0
+    m_ptr = _vector(out_len, "out_len", torch.int32, B, dev)
+    out_desc, ot_ptr, ot_cols = None, None, 0
     if out_table is not None:
-        _table(out_table, "out_table", B, dev)
+        ot_ptr, ot_cols = _table(out_table, "out_table", B, dev)
         dst = cache if out_cache is None else out_cache
-        out_desc = _cache_desc(dst, "out_cache")
-        if dst.dtype != cache.dtype or dst.device != dev or dst.shape[1:] != cache.shape[1:]:
+        out_desc, out_shape = _cache_desc(dst, "out_cache")
+        if dst.dtype is not cache.dtype or dst.device != dev or out_shape[1:] != shape[1:]:
             raise ValueError("out_cache must match the cache in all but its pages")
-        out_cols = out_table.shape[1]
+        out_desc = ctypes.byref(out_desc)
     elif out_cache is not None:
         raise ValueError("out_cache needs out_table")
     if out_kept is None and with_kept:
         out_kept = torch.empty((B, budget), dtype=torch.int32, device=dev)
-    if out_kept is not None:
-        _matrix(out_kept, "out_kept", torch.int32, (B, budget), dev)
-    s = _stream_of(stream, dev)
-    ws = _scratch("kv_evict", dev, s, (B, budget))
-    _call("spec_kv_evict", dev, ctypes.byref(desc), _ptr(block_table), block_table.shape[1],
-          ctypes.byref(out_desc) if out_desc is not None else None, _ptr(out_table), out_cols,
-          _ptr(score), stride, score.shape[1], _ptr(out_score), out_stride, out_score.shape[1],
-          _ptr(kv_len), _ptr(out_len), budget, sinks, recent, _ptr(out_kept), s.cuda_stream, B,
-          _ptr(ws), ws.numel())
+    k_ptr = None if out_kept is None else _matrix(out_kept, "out_kept", torch.int32, (B, budget),
+                                                  dev)
+    handle = _stream_of(stream, dev)
+    ws = _scratch("kv_evict", dev, stream, handle, (B, budget))
+    _call("spec_kv_evict", dev, ctypes.byref(desc), t_ptr, cols, out_desc, ot_ptr, ot_cols, s_ptr,
+          stride, score_cols, os_ptr, out_stride, out_cols, n_ptr, m_ptr, budget, sinks, recent,
+          k_ptr, handle, B, ws.data_ptr(), ws.numel())
     return out_len, out_kept
 
 
 def _rows_desc(x):
+    """The descriptor, device, rows and columns of a logit matrix."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() != 2:
         raise TypeError("logits must be a 2-D CUDA tensor")
-    if x.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"logits must be float32 or bfloat16, got {x.dtype}")
-    if x.shape[1] > 1 and x.stride(1) != 1:
+    dtype = x.dtype
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
+        raise TypeError(f"logits must be float32 or bfloat16, got {dtype}")
+    R, V = x.shape
+    stride, one = x.stride()
+    if V > 1 and one != 1:
         raise ValueError("logit rows must be contiguous")
-    return _Logits(x.data_ptr() if x.numel() else None, _DTYPES[x.dtype], x.shape[1], x.shape[0],
-                   x.stride(0) if x.shape[0] > 1 else x.shape[1])
+    return _Logits(x.data_ptr() or None, _DTYPES[dtype], V, R, stride if R > 1 else V), x.device, \
+        R, V
 
 
 def logprobs(logits, tokens, temperature=None, n_top=0, *, stream=None):
@@ -340,25 +377,23 @@ def logprobs(logits, tokens, temperature=None, n_top=0, *, stream=None):
     max, logsum [rows] float32 and top_tokens, top_logprobs [rows, n_top] (None
     without n_top; ties go to the lowest index; -1 and -inf where a row has
     fewer tokens of nonzero probability)."""
-    x = _rows_desc(logits)
-    dev, R = logits.device, logits.shape[0]
-    _vector(tokens, "tokens", torch.int32, R, dev, optional=True)
-    _vector(temperature, "temperature", torch.float32, R, dev, optional=True)
-    n_top = int(n_top)
+    x, dev, R, _ = _rows_desc(logits)
+    t_ptr = _vector(tokens, "tokens", torch.int32, R, dev, optional=True)
+    T_ptr = _vector(temperature, "temperature", torch.float32, R, dev, optional=True)
     if not 0 <= n_top <= SV_LOGPROBS_TOP_MAX:
         raise ValueError(f"n_top must be in [0, {SV_LOGPROBS_TOP_MAX}]")
     f = torch.empty((4, R), dtype=torch.float32, device=dev)
-    tok = top = None
+    tok = top = tok_ptr = top_ptr = None
     if n_top:
         tok = torch.empty((R, n_top), dtype=torch.int32, device=dev)
         top = torch.empty((R, n_top), dtype=torch.float32, device=dev)
-    s = _stream_of(stream, dev)
-    ws = _scratch("logprobs", dev, s, (R,))
+        tok_ptr, top_ptr = tok.data_ptr(), top.data_ptr()
+    handle = _stream_of(stream, dev)
+    ws = _scratch("logprobs", dev, stream, handle, (R,))
     at = f.data_ptr()
-    _call("spec_logprobs", dev, ctypes.byref(x), _ptr(tokens), _ptr(temperature), n_top, at,
-          at + 4 * R, at + 8 * R, at + 12 * R, _ptr(tok), _ptr(top), s.cuda_stream, _ptr(ws),
-          ws.numel())
-    return LogProbs(f[0], f[1], f[2], f[3], tok, top)
+    _call("spec_logprobs", dev, ctypes.byref(x), t_ptr, T_ptr, n_top, at, at + 4 * R, at + 8 * R,
+          at + 12 * R, tok_ptr, top_ptr, handle, ws.data_ptr(), ws.numel())
+    return LogProbs(*f.unbind(0), tok, top)
 
 
 def logprobs_grad(logits, tokens, max, logsum, entropy, grad_logprob, grad_entropy=None,
@@ -369,24 +404,21 @@ def logprobs_grad(logits, tokens, max, logsum, entropy, grad_logprob, grad_entro
 
     Returns ``out`` [rows, V] of the logits' dtype; it may be the logits
     themselves.  Rows with token -1 get 0."""
-    x = _rows_desc(logits)
-    dev, (R, V) = logits.device, logits.shape
-    _vector(tokens, "tokens", torch.int32, R, dev)
-    _vector(max, "max", torch.float32, R, dev)
-    _vector(logsum, "logsum", torch.float32, R, dev)
-    _vector(entropy, "entropy", torch.float32, R, dev, optional=grad_entropy is None)
-    _vector(grad_logprob, "grad_logprob", torch.float32, R, dev, optional=True)
-    _vector(grad_entropy, "grad_entropy", torch.float32, R, dev, optional=True)
-    _vector(temperature, "temperature", torch.float32, R, dev, optional=True)
+    x, dev, R, V = _rows_desc(logits)
+    t_ptr = _vector(tokens, "tokens", torch.int32, R, dev)
+    m_ptr = _vector(max, "max", torch.float32, R, dev)
+    l_ptr = _vector(logsum, "logsum", torch.float32, R, dev)
+    h_ptr = _vector(entropy, "entropy", torch.float32, R, dev, optional=grad_entropy is None)
+    gl_ptr = _vector(grad_logprob, "grad_logprob", torch.float32, R, dev, optional=True)
+    gh_ptr = _vector(grad_entropy, "grad_entropy", torch.float32, R, dev, optional=True)
+    T_ptr = _vector(temperature, "temperature", torch.float32, R, dev, optional=True)
     if out is None:
         out = torch.empty((R, V), dtype=logits.dtype, device=dev)
-    out_stride = _rows2d(out, "out", logits.dtype, R, dev)
-    if tuple(out.shape) != (R, V):
+    o_ptr, out_stride, out_cols = _rows2d(out, "out", logits.dtype, R, dev)
+    if out_cols != V or out.shape[0] != R:
         raise ValueError(f"out must be {(R, V)}")
-    s = _stream_of(stream, dev)
-    _call("spec_logprobs_grad", dev, ctypes.byref(x), _ptr(tokens), _ptr(temperature), _ptr(max),
-          _ptr(logsum), _ptr(entropy), _ptr(grad_logprob), _ptr(grad_entropy), _ptr(out),
-          out_stride, s.cuda_stream)
+    _call("spec_logprobs_grad", dev, ctypes.byref(x), t_ptr, T_ptr, m_ptr, l_ptr, h_ptr, gl_ptr,
+          gh_ptr, o_ptr, out_stride, _stream_of(stream, dev))
     return out
 
 
