@@ -406,11 +406,12 @@ cudaError_t run_attn(const AttnArgs& A, bool weights, cudaStream_t s) {
 constexpr int kCtasPerSm = 2;  // shared memory of the widest heads
 constexpr int kTcRows = 128;   // rows a unit of the tensor-core kernel
 
-// Heads and types that the tensor-core kernel takes.  The largest score is
-// found before the scaling, so the scale has to be positive; its entries are numbered in 32 bits.
-bool on_tensor_cores(const AttnArgs& A, int dtype) {
-  return dtype != SV_F32 && (A.D == 64 || A.D == 128 || A.D == 256) && A.scale2 > 0.0f &&
-         (A.num_pages > 0 || A.spec) &&
+// Heads and types that the tensor-core kernels take; they number the cache's
+// entries in 32 bits.  Attention finds the largest score before the scaling, so
+// the scale has to be positive there.
+bool on_tensor_cores(const AttnArgs& A, int dtype, bool weights) {
+  return dtype != SV_F32 && (A.D == 64 || A.D == 128 || A.D == 256) &&
+         (weights || A.scale2 > 0.0f) && (A.num_pages > 0 || A.spec) &&
          A.num_pages * (A.page_bytes / A.entry_bytes) <= INT32_MAX;
 }
 
@@ -443,9 +444,9 @@ size_t attn_workspace_bytes(int32_t B, int32_t D, int sms, bool weights) {
 
 cudaError_t launch_attn(AttnArgs A, int dtype, bool weights, void* workspace, int sms,
                         cudaStream_t s) {
-  const bool tc = !weights && on_tensor_cores(A, dtype);
+  const bool tc = on_tensor_cores(A, dtype, weights);
   A.ctas = tc ? sms : sms * kCtasPerSm;
-  A.hg = tc ? std::gcd(A.ctas, A.Hkv) : 1;
+  A.hg = tc && !weights ? std::gcd(A.ctas, A.Hkv) : 1;
   const AttnLayout L = attn_layout(A.B, A.D, A.ctas, tc ? kTcRows : kMr);
   char* w = static_cast<char*>(workspace);
   A.hdr = reinterpret_cast<WsHeader*>(w);
@@ -461,6 +462,7 @@ cudaError_t launch_attn(AttnArgs A, int dtype, bool weights, void* workspace, in
     A.page_rows = int32_t(A.page_bytes / A.entry_bytes);
     A.q_vec = aligned(A.q) && A.q_ts % 8 == 0 && A.q_hs % 8 == 0;
     A.out_vec = aligned(A.out);
+    if (weights) return launch_attn_weights_tc(A, dtype, s);
     const cudaError_t e = launch_attn_tc(A, dtype, s);
     if (e != cudaSuccess) return e;
     return dtype == SV_BF16 ? launch_join(attn_join_kernel<__nv_bfloat16, kTcRows>, A, s)

@@ -283,7 +283,8 @@ __device__ void fail_all(const AttnArgs& A) {
 
 #endif  // __CUDACC__
 
-// The tensor-core kernel's share of a call (MR = 128, one CTA per SM).
+// The tensor-core kernels' share of a call (MR = 128, one CTA per SM).
 cudaError_t launch_attn_tc(const AttnArgs& A, int dtype, cudaStream_t s);
+cudaError_t launch_attn_weights_tc(const AttnArgs& A, int dtype, cudaStream_t s);
 
 }  // namespace sv

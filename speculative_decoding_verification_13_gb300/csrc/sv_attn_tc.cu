@@ -48,8 +48,7 @@
 // products land, and TMEM is freed.
 #include <type_traits>
 
-#include "sv_attn.cuh"
-#include "sv_tcgen05.cuh"
+#include "sv_attn_tc.cuh"
 
 namespace sv {
 namespace {
@@ -119,21 +118,6 @@ struct TcShared {
   int dirty[kBufs];  // per S buffer: 1 + the tile whose V holds a non-finite value
 };
 
-// A place in a ring of slots and the phase of its barriers.  K and V have rings
-// of their own: with one for both, a load warp could meet a barrier two phases
-// behind, whose parity is that of the phase it waits for.
-struct Ring {
-  uint32_t at, phase, base, end;
-  __device__ __forceinline__ Ring(uint32_t first, uint32_t n, uint32_t phase_)
-      : at(first), phase(phase_), base(first), end(first + n) {}
-  __device__ __forceinline__ void step() {
-    if (++at == end) {
-      at = base;
-      phase ^= 1;
-    }
-  }
-};
-
 // One of the S buffers and the phase of its barriers, one tile a step.
 struct Buf {
   uint32_t at = 0, phase = 0;
@@ -192,29 +176,6 @@ struct Walk {
   }
 };
 
-template <class T> struct Bits;
-template <> struct Bits<__nv_bfloat16> {
-  static constexpr uint32_t kFmt = 1, kExp = 0x7f807f80u, kOne = 0x00800080u, kExp1 = 0x7f80u,
-                            kMan1 = 0x007fu;
-  __device__ static uint32_t pack(float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-};
-template <> struct Bits<__half> {
-  static constexpr uint32_t kFmt = 0, kExp = 0x7c007c00u, kOne = 0x04000400u, kExp1 = 0x7c00u,
-                            kMan1 = 0x03ffu;
-  __device__ static uint32_t pack(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-};
-// any of the two 16-bit values of w infinite or NaN
-template <class T>
-__device__ __forceinline__ bool any_nonfinite(uint32_t w) {
-  return (((w & Bits<T>::kExp) + Bits<T>::kOne) & 0x80008000u) != 0;
-}
-
 // Descriptor of an MN-major 16-bit tile with 128-byte swizzling: rows (of K)
 // of 128 bytes, 8-row groups 1024 bytes apart, blocks of 64 elements of MN
 // `block` bytes apart.
@@ -223,96 +184,6 @@ __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t addr, uint32_t block)
          (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
-// The products and their commits are issued by one lane of a warp that runs
-// them as a whole: predicated instructions, no branch, so that descriptors stay
-// in the warp's uniform registers (one lane in a branch of its own had to move
-// every operand there: about 100 cycles a product).
-__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b,
-                                       uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n.reg .pred p, e;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 e, %5, 0;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b,
-                                       uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n.reg .pred p, e;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 e, %5, 0;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
-      : "memory");
-}
-__device__ __forceinline__ void mma_commit(uint32_t lead, uint64_t* bar) {
-  asm volatile(
-      "{\n.reg .pred e;\nsetp.ne.b32 e, %1, 0;\n"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
-          smem_addr(bar)),
-      "r"(lead)
-      : "memory");
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-// This lane's arrival on a barrier, made when its copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                         uint32_t bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
-      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
-      : "memory");
-}
-__device__ __forceinline__ uint64_t l2_evict_normal_policy() {
-  uint64_t pol;
-  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
-  return pol;
-}
-
-// Bounded wait; false, with the CTA's abort flag set, on expiry.  The clock of
-// the bound is read only after a number of polls: a wait here is short, and
-// reading the global timer would be most of it.
-__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, TcShared& S) {
-  const uint32_t at = smem_addr(bar);
-  for (int i = 0; i < 128; ++i)
-    if (mbar_try_wait(at, parity)) return true;
-  if (mbar_wait_for(at, parity, kWaitNs, &S.abort)) return true;
-  *reinterpret_cast<volatile int*>(&S.abort) = 1;
-  return false;
-}
-// The same for a whole warp, one answer for all its lanes.
-__device__ __forceinline__ bool tc_wait_warp(uint64_t* bar, uint32_t parity, TcShared& S) {
-  return __all_sync(0xffffffffu, tc_wait(bar, parity, S));
-}
-// Two barriers at once: their polls overlap (a poll that succeeds still takes
-// about 100 cycles between two products).
-__device__ __forceinline__ bool tc_wait_two(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
-                                            TcShared& S) {
-  uint32_t ok;
-  asm volatile(
-      "{\n.reg .pred p, q;\n"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n"
-      "and.pred p, p, q;\nselp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_addr(a)), "r"(pa), "r"(smem_addr(b)), "r"(pb)
-      : "memory");
-  if (__all_sync(0xffffffffu, ok != 0)) return true;
-  return tc_wait_warp(a, pa, S) && tc_wait_warp(b, pb, S);
-}
-// Barrier of the four warps that count on `bar`, bounded like every other wait
-// (a warp that gave up would leave a hardware barrier waiting for ever).
-__device__ __forceinline__ bool tc_sync(uint64_t* bar, uint32_t parity, TcShared& S) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(bar));
-  return tc_wait_warp(bar, parity, S);
-}
 
 // Hardware barrier of the softmax warps, and the same with one truth value for
 // all of them.  None may stay away: they leave their loop only together.
@@ -391,10 +262,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (go && warp >= kLoadWarp && warp < kScoreWarp) {
     // ----------------------------------------------------------------- loads
     const int kv = warp - kLoadWarp;              // 0: K, 1: V
-    constexpr int kParts = D / 64;                // 128-byte parts of a row
-    const int part = lane % kParts, box0 = lane / kParts * A.box_rows;  // this lane's box
-    const bool boxes = A.box_rows > 0 && box0 < TN;
-    constexpr int kChunks = D / 8;                // 16-byte chunks of a row
     // keys that no other unit of the call reads leave the L2 first
     const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
     Seg s;
@@ -406,96 +273,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int cached = min(s.R.n, hi);
       const int p0 = (s.R.tile0 + s.first) * TN;
       const int32_t* table = A.table + int64_t(s.b) * A.max_pages;
-      auto column = [&](int p) { return A.s_shift >= 0 ? p >> A.s_shift : p / A.S; };
       auto missing = [&](int page) {
         if (page >= 0 && page < A.num_pages) return false;
         S.bad[unit % kSegs] = 1;
         atomicMin(&S.first_bad, s.b);
         return true;
       };
-      // A tile comes in boxes, or row by row; the pages of its box, or of its
-      // rows (row lane + 32 i of the tile), are read one tile ahead, so that
-      // nothing waits for the block table.
-      constexpr int kOwn = TN / 32;
-      int page[kOwn];
-      auto boxed = [&](int t) { return A.box_rows > 0 && p0 + (t + 1) * TN <= cached; };
-      auto next_page = [&](int t) {
-        if (boxed(t)) {
-          if (boxes) page[0] = __ldg(table + column(p0 + t * TN + box0));
-        } else {
-#pragma unroll
-          for (int i = 0; i < kOwn; ++i) {
-            const int p = p0 + t * TN + lane + 32 * i;
-            if (p < cached) page[i] = __ldg(table + column(p));
-          }
-        }
-      };
-      next_page(0);
+      // pages are read one tile ahead, so that nothing waits for the block table
+      TilePages<TN> next = tile_pages<D, TN>(A, table, cached, p0);
       for (int t = 0; t < s.count; ++t) {
-        const int pt = p0 + t * TN;
-        int pg[kOwn];
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) pg[i] = page[i];
-        if (t + 1 < s.count) next_page(t + 1);
-        const uint32_t slot = at.at;
-        if (!tc_wait_warp(&S.empty[slot], at.phase, S)) {
+        const TilePages<TN> pages = next;
+        if (t + 1 < s.count) next = tile_pages<D, TN>(A, table, cached, p0 + (t + 1) * TN);
+        if (!tc_wait_warp(&S.empty[at.at], at.phase, S)) {
           stop = true;
           break;
         }
-        const uint32_t dst = ring0 + slot * kSlotBytes, bar = smem_addr(&S.full[slot]);
-        if (boxed(t)) {
-          if (lane == 0) {
-            S.copied[slot] = 0;
-            mbar_arrive_expect_tx(bar, kSlotBytes);
-          } else {
-            mbar_arrive(bar);
-          }
-          __syncwarp();
-          if (boxes) {
-            const int p = pt + box0;
-            // a missing page: a box outside the matrix is all zeros
-            const int row = missing(pg[0])
-                                ? -A.box_rows
-                                : pg[0] * A.page_rows + kv * A.S + (p - column(p) * A.S);
-            box_load(dst + part * (TN * 128) + box0 * 128, &rows_map, s.h * D + part * 64, row,
-                     bar, s.R.mtiles > 1 ? again : once);
-          }
-        } else {
-          // addresses of the lane's own rows; each round's lanes then fetch
-          // theirs from the lane that has it
-          uint64_t own[kOwn];
-#pragma unroll
-          for (int i = 0; i < kOwn; ++i) {
-            const int p = pt + lane + 32 * i;
-            const char* a = nullptr;   // stays null for a row that is filled with zeros
-            if (p >= cached) {
-              if (p < hi)
-                a = A.spec + int64_t(s.b) * A.spec_req + int64_t(p - s.R.n) * A.spec_tok +
-                    kv * A.entry_bytes;
-            } else if (!missing(pg[i])) {
-              a = A.cache + pg[i] * A.page_bytes + kv * A.v_off +
-                  (p - column(p) * A.S) * A.entry_bytes;
-            }
-            own[i] = a ? reinterpret_cast<uint64_t>(a + int64_t(s.h) * D * 2) : 0;
-          }
-          const int ch = lane % kChunks;
-          constexpr int kStep = 32 / kChunks;   // rows per round
-#pragma unroll
-          for (int i = 0; i < kOwn; ++i)
-#pragma unroll 4
-            for (int j = 0; j < 32; j += kStep) {
-              const int from = j + lane / kChunks, r = 32 * i + from;
-              const uint64_t a =
-                  (uint64_t(__shfl_sync(0xffffffffu, uint32_t(own[i] >> 32), from)) << 32) |
-                  __shfl_sync(0xffffffffu, uint32_t(own[i]), from);
-              cp_async16(dst + (ch >> 3) * (TN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                         a ? reinterpret_cast<const char*>(a) + ch * 16
-                           : reinterpret_cast<const char*>(A.k_per_req),
-                         a ? 16u : 0u);
-            }
-          if (lane == 0) S.copied[slot] = 1;
-          cp_async_arrive(bar);
-        }
+        load_tile<D, TN>(A, rows_map, pages, s.b, s.R.n, cached, hi, p0 + t * TN, s.h, kv,
+                         ring0 + at.at * kSlotBytes, &S.full[at.at], &S.copied[at.at],
+                         s.R.mtiles > 1 ? again : once, missing);
         at.step();
       }
     }
@@ -1011,38 +806,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-// The cache from the layer's first entry on as a matrix of entries of E
-// elements, moved in boxes of 128 bytes by box_rows entries.
-bool rows_map(CUtensorMap* map, const AttnArgs& A, bool bf16) {
-  const EncodeTiledFn fn = tensor_map_encoder();
-  if (!fn) return false;
-  const uint64_t elems = uint64_t(A.entry_bytes) / 2;
-  const cuuint64_t dims[2] = {elems, cuuint64_t(A.num_pages > 0 ? A.num_pages : 1) *
-                                         cuuint64_t(A.page_rows) - cuuint64_t(A.layer_row)};
-  const cuuint64_t strides[1] = {cuuint64_t(A.entry_bytes)};
-  const cuuint32_t box[2] = {64, cuuint32_t(A.box_rows > 0 ? A.box_rows : 8)}, step[2] = {1, 1};
-  // an empty pool has no page that a row could come from: any address will do
-  const void* base = A.num_pages > 0 ? static_cast<const void*>(A.cache) : A.spec;
-  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-            const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <class T, int D>
 cudaError_t run(const AttnArgs& A, cudaStream_t s) {
   static std::atomic<uint64_t> configured{0};
   if (cudaError_t e = allow_smem(attn_tc_kernel<T, D>, Shape<D>::kSmem, configured)) return e;
   CUtensorMap map;
   AttnArgs B = A;
-  // rows of a page that lie in one tile, whole groups of 8 of the swizzled layout
-  int rows = A.S, rest = Shape<D>::TN;
-  while (rest) {
-    const int r = rows % rest;
-    rows = rest;
-    rest = r;
-  }
-  B.box_rows = rows % 8 == 0 ? rows : 0;
+  B.box_rows = box_rows(A.S, Shape<D>::TN, D);
   if (!rows_map(&map, B, Bits<T>::kFmt != 0)) return cudaErrorInvalidValue;
   attn_tc_kernel<T, D><<<A.ctas, kTcThreads, Shape<D>::kSmem, s>>>(map, B);
   return cudaGetLastError();
