@@ -12,10 +12,11 @@
 // One CTA per SM over an even piece of all requests' tiles of 128 positions;
 // per tile a step for every head and 64 rows of it:
 //   warp 4     loads K of a head and tile into a ring (as attention loads it);
-//   warp 5     loads the steps' Q, as the N of the product, with each row's lse
-//              and the position of its token; it also finds the parts of the
-//              piece and announces them;
-//   warp 6     issues the products into four accumulators in TMEM;
+//   warps 6-8  load the steps' Q, the N of the product, in turn, with each row's
+//              lse and the position of its token; the first also finds the parts
+//              of the piece and announces them.  (One warp, an address per copy:
+//              32 requests with up to 15 drafts took 299 us.)
+//   warp 5     issues the products into four accumulators in TMEM;
 //   warps 0-3  one position a thread: exp(s - lse) summed over the rows.
 // Every wait is bounded, as in attention.
 #include "sv_attn_tc.cuh"
@@ -23,13 +24,12 @@
 namespace sv {
 namespace {
 
-constexpr int kWtThreads = 224;
+constexpr int kWtThreads = 288;
 constexpr int kWtTile = 128;      // positions
 constexpr int kWtRows = 64;       // rows per step
 constexpr int kAccs = 4;
-constexpr int kKeyWarp = 4, kRowWarp = 5, kProductWarp = 6;
+constexpr int kKeyWarp = 4, kProductWarp = 5, kRowWarp = 6;  // three row warps
 constexpr int kParts = 4;         // parts announced ahead
-constexpr int kPartReaders = 6;   // warps that take them
 
 template <int D>
 struct WtShape {
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     }
     for (int i = 0; i < kParts; ++i) {
       mbar_init(smem_addr(&S.announced[i]), 1);
-      mbar_init(smem_addr(&S.taken[i]), kPartReaders);
+      mbar_init(smem_addr(&S.taken[i]), 5 + C::kQBufs);  // all warps but the first row warp
     }
     mbar_init(smem_addr(&S.drain), 1);
     fence_mbar_init();
@@ -147,80 +147,102 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (go && warp == kRowWarp) {
+  } else if (go && warp >= kRowWarp && warp < kRowWarp + C::kQBufs) {
     // --------------------------------------------------- parts, and their rows
     constexpr int kChunks = D / 8, kStep = 32 / kChunks;
+    const int mine = warp - kRowWarp;   // this warp's buffer: every kQBufs-th step
     const int ch = lane % kChunks;
     const T* q = static_cast<const T*>(A.q);
+    unsigned char* buf = smem_p + kQ0 + mine * C::kQBytes;
+    const uint32_t buf_at = smem0 + kQ0 + mine * C::kQBytes;
     int64_t pos = P.start, base = P.base;
     int b = P.b, t_off = P.t_off;
     AttnReq R = attn_request<kWtTile, kWtTile, true>(A, b);
-    Ring qb(0, C::kQBufs, 1);
+    uint32_t phase = 1;
+    int step = 0;                       // of the piece, modulo kQBufs
     bool stop = false;
     for (int i = 0; !stop; ++i) {
       Part w;
       w.count = 0;
-      if (pos < P.end) {
-        while (pos >= base + R.ntiles) {
-          base += R.ntiles;
-          t_off += R.k + 1;
-          R = attn_request<kWtTile, kWtTile, true>(A, ++b);
+      if (mine > 0) {
+        if (!next_part(S, i, w)) break;
+      } else {
+        if (pos < P.end) {
+          while (pos >= base + R.ntiles) {
+            base += R.ntiles;
+            t_off += R.k + 1;
+            R = attn_request<kWtTile, kWtTile, true>(A, ++b);
+          }
+          w.b = b;
+          w.t_off = t_off;
+          w.tile = R.tile0 + int(pos - base);
+          const int64_t left = P.end - pos, rest = base + R.ntiles - pos;
+          w.count = int(left < rest ? left : rest);
+          w.R = R;
+          pos += w.count;
         }
-        w.b = b;
-        w.t_off = t_off;
-        w.tile = R.tile0 + int(pos - base);
-        const int64_t left = P.end - pos, rest = base + R.ntiles - pos;
-        w.count = int(left < rest ? left : rest);
-        w.R = R;
-        pos += w.count;
+        if (!tc_wait_warp(&S.taken[i % kParts], ((i / kParts) & 1) ^ 1, S)) break;
+        if (lane == 0) {
+          S.part[i % kParts] = w;
+          mbar_arrive(smem_addr(&S.announced[i % kParts]));
+        }
+        if (w.count == 0) break;
       }
-      if (!tc_wait_warp(&S.taken[i % kParts], ((i / kParts) & 1) ^ 1, S)) break;
-      if (lane == 0) {
-        S.part[i % kParts] = w;
-        mbar_arrive(smem_addr(&S.announced[i % kParts]));
-      }
-      if (w.count == 0) break;
       const int nrows = w.R.take * A.G;
       for (int t = 0; t < w.count && !stop; ++t) {
         const int steps = row_steps(A, w.R, (w.tile + t) * kWtTile);
         for (int h = 0; h < A.Hkv && !stop; ++h)
           for (int c = 0; c < steps; ++c) {
-            if (!tc_wait_warp(&S.qempty[qb.at], qb.phase, S)) {
+            const bool other = step != mine;
+            step = step + 1 == C::kQBufs ? 0 : step + 1;
+            if (other) continue;
+            if (!tc_wait_warp(&S.qempty[mine], phase, S)) {
               stop = true;
               break;
             }
+            phase ^= 1;
             const int row0 = c * kWtRows, rows = min(kWtRows, nrows - row0);
             const int padded = (rows + 15) & ~15;
-            for (int r = lane / kChunks; r < padded; r += kStep) {
-              const uint32_t at = kQ0 + qb.at * C::kQBytes + (ch >> 3) * (kWtRows * 128) + r * 128 +
-                                  (((ch & 7) ^ (r & 7)) << 4);
-              const int row = row0 + r;
-              const T* src = q;
-              if (r < rows)
-                src = q + int64_t(w.t_off + row / A.G) * A.q_ts +
-                      int64_t(h * A.G + row % A.G) * A.q_hs + ch * 8;
-              if (A.q_vec) {
-                cp_async16(smem0 + at, src, r < rows ? 16u : 0u);
-              } else {
-                T* dst = reinterpret_cast<T*>(smem_p + at);
-                for (int x = 0; x < 8; ++x) dst[x] = r < rows ? src[x] : from_float<T>(0.f);
-              }
-            }
-            for (int r = lane; r < padded; r += 32) {
-              const int row = row0 + r;
+            // rows lane and lane + 32: their addresses, lse and tokens' positions
+            uint64_t own[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int r = lane + 32 * x, row = row0 + r;
+              const int tok = row / A.G, hq = h * A.G + row % A.G;
+              own[x] = 0;
               float v = INFINITY;
               if (r < rows) {
-                v = A.lse[int64_t(w.t_off + row / A.G) * A.Hq + h * A.G + row % A.G] * kAttnLog2e;
+                own[x] = reinterpret_cast<uint64_t>(q + int64_t(w.t_off + tok) * A.q_ts +
+                                                    int64_t(hq) * A.q_hs);
+                v = A.lse[int64_t(w.t_off + tok) * A.Hq + hq] * kAttnLog2e;
                 if (v == -INFINITY) v = INFINITY;   // a row that saw nothing weighs nothing
               }
-              S.lse[qb.at][r] = v;
-              S.at[qb.at][r] = w.R.at0 + row / A.G;
+              S.lse[mine][r] = v;
+              S.at[mine][r] = w.R.at0 + tok;
             }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll 4
+              for (int j = 0; j < 32; j += kStep) {
+                if (32 * x + j >= padded) break;
+                const int from = j + lane / kChunks, r = 32 * x + from;
+                const uint64_t a =
+                    (uint64_t(__shfl_sync(0xffffffffu, uint32_t(own[x] >> 32), from)) << 32) |
+                    __shfl_sync(0xffffffffu, uint32_t(own[x]), from);
+                const T* src = a ? reinterpret_cast<const T*>(a) + ch * 8 : q;
+                const uint32_t off =
+                    (ch >> 3) * (kWtRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+                if (A.q_vec) {
+                  cp_async16(buf_at + off, src, a ? 16u : 0u);
+                } else {
+                  T* dst = reinterpret_cast<T*>(buf + off);
+                  for (int e = 0; e < 8; ++e) dst[e] = a ? src[e] : from_float<T>(0.f);
+                }
+              }
             asm volatile("cp.async.wait_all;" ::: "memory");
             fence_async_proxy();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&S.qfull[qb.at]));
-            qb.step();
+            if (lane == 0) mbar_arrive(smem_addr(&S.qfull[mine]));
           }
       }
     }
