@@ -280,17 +280,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         return true;
       };
       // pages are read one tile ahead, so that nothing waits for the block table
-      TilePages<TN> next = tile_pages<D, TN>(A, table, cached, p0);
+      TilePages<TN, 1> next = tile_pages<D, TN>(A, table, cached, p0);
       for (int t = 0; t < s.count; ++t) {
-        const TilePages<TN> pages = next;
+        const TilePages<TN, 1> pages = next;
         if (t + 1 < s.count) next = tile_pages<D, TN>(A, table, cached, p0 + (t + 1) * TN);
         if (!tc_wait_warp(&S.empty[at.at], at.phase, S)) {
           stop = true;
           break;
         }
-        load_tile<D, TN>(A, rows_map, pages, s.b, s.R.n, cached, hi, p0 + t * TN, s.h, kv,
+        load_tile<D, TN, 1>(A, rows_map, pages, s.b, s.R.n, cached, hi, p0 + t * TN, s.h, kv,
                          ring0 + at.at * kSlotBytes, &S.full[at.at], &S.copied[at.at],
-                         s.R.mtiles > 1 ? again : once, missing);
+                         s.R.mtiles > 1 ? again : once, 0, missing);
         at.step();
       }
     }
@@ -812,7 +812,7 @@ cudaError_t run(const AttnArgs& A, cudaStream_t s) {
   if (cudaError_t e = allow_smem(attn_tc_kernel<T, D>, Shape<D>::kSmem, configured)) return e;
   CUtensorMap map;
   AttnArgs B = A;
-  B.box_rows = box_rows(A.S, Shape<D>::TN, D);
+  B.box_rows = box_rows(A.S, Shape<D>::TN, D, 32);
   if (!rows_map(&map, B, Bits<T>::kFmt != 0)) return cudaErrorInvalidValue;
   attn_tc_kernel<T, D><<<A.ctas, kTcThreads, Shape<D>::kSmem, s>>>(map, B);
   return cudaGetLastError();

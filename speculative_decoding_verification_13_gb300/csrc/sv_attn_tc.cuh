@@ -144,10 +144,11 @@ __device__ __forceinline__ bool tc_sync(uint64_t* bar, uint32_t parity, Sh& S) {
 
 
 // The pages of one tile: of this lane's box (the first), or of its rows lane +
-// 32 i where the tile does not come in boxes.
-template <int TN>
+// 32 i where the tile does not come in boxes.  SHARES warps may load a tile
+// together, each every SHARES-th box or its share of the rows.
+template <int TN, int SHARES>
 struct TilePages {
-  int page[TN / 32];
+  int page[TN / 32 / SHARES];
 };
 
 __device__ __forceinline__ int page_column(const AttnArgs& A, int p) {
@@ -161,46 +162,50 @@ __device__ __forceinline__ bool tile_boxed(const AttnArgs& A, int cached, int p0
   return A.box_rows > 0 && p0 + TN <= cached;
 }
 
-template <int D, int TN>
-__device__ __forceinline__ TilePages<TN> tile_pages(const AttnArgs& A, const int32_t* table,
-                                                    int cached, int p0) {
+template <int D, int TN, int SHARES = 1>
+__device__ __forceinline__ TilePages<TN, SHARES> tile_pages(const AttnArgs& A,
+                                                            const int32_t* table, int cached,
+                                                            int p0, int share = 0) {
   const int lane = threadIdx.x & 31;
-  TilePages<TN> t;
+  TilePages<TN, SHARES> t;
   if (tile_boxed<TN>(A, cached, p0)) {
-    const int box0 = lane / (D / 64) * A.box_rows;
+    const int box0 = (lane * SHARES + share) / (D / 64) * A.box_rows;
     t.page[0] = box0 < TN ? __ldg(table + page_column(A, p0 + box0)) : 0;
   } else {
 #pragma unroll
-    for (int i = 0; i < TN / 32; ++i) {
-      const int p = p0 + lane + 32 * i;
+    for (int i = 0; i < TN / 32 / SHARES; ++i) {
+      const int p = p0 + share * (TN / SHARES) + lane + 32 * i;
       t.page[i] = p < cached ? __ldg(table + page_column(A, p)) : 0;
     }
   }
   return t;
 }
 
-// A warp loads K (kv 0) or V (kv 1) of head h and positions p0 .. p0 + TN - 1 of
-// request b into the slot at dst: [D / 64][TN][64] of 16 bits, 128-byte
-// swizzled.  `full` counts 32 arrivals; `copied` tells how the tile came.
-// missing(page) is true, and notes it, for a page that is not in the pool.
-template <int D, int TN, class F>
+// A warp loads its share of K (kv 0) or V (kv 1) of head h and positions p0 ..
+// p0 + TN - 1 of request b into the slot at dst: [D / 64][TN][64] of 16 bits,
+// 128-byte swizzled.  `full` counts 32 arrivals a share; `copied` tells how the
+// tile came.  missing(page) is true, and notes it, for a page that is not in the
+// pool.
+template <int D, int TN, int SHARES, class F>
 __device__ __forceinline__ void load_tile(const AttnArgs& A, const CUtensorMap& map,
-                                          const TilePages<TN>& pages, int b, int n, int cached,
-                                          int hi, int p0, int h, int kv, uint32_t dst,
-                                          uint64_t* full, int* copied, uint64_t policy,
+                                          const TilePages<TN, SHARES>& pages, int b, int n,
+                                          int cached, int hi, int p0, int h, int kv, uint32_t dst,
+                                          uint64_t* full, int* copied, uint64_t policy, int share,
                                           F missing) {
   const int lane = threadIdx.x & 31;
   const uint32_t bar = smem_addr(full);
   if (tile_boxed<TN>(A, cached, p0)) {
+    constexpr int kParts = D / 64;   // 128-byte parts of a row
     if (lane == 0) {
+      const int boxes = (TN / A.box_rows * kParts - share + SHARES - 1) / SHARES;
       *copied = 0;
-      mbar_arrive_expect_tx(bar, TN * D * 2);
+      mbar_arrive_expect_tx(bar, uint32_t(boxes * A.box_rows * 128));
     } else {
       mbar_arrive(bar);
     }
     __syncwarp();
-    constexpr int kParts = D / 64;   // 128-byte parts of a row
-    const int part = lane % kParts, box0 = lane / kParts * A.box_rows;  // this lane's box
+    const int box = lane * SHARES + share;   // this lane's box
+    const int part = box % kParts, box0 = box / kParts * A.box_rows;
     if (box0 < TN) {
       const int p = p0 + box0, pg = pages.page[0];
       // a missing page: a box outside the matrix is all zeros
@@ -213,10 +218,12 @@ __device__ __forceinline__ void load_tile(const AttnArgs& A, const CUtensorMap& 
   }
   // addresses of the lane's own rows; each round's lanes then fetch theirs from
   // the lane that has it
-  uint64_t own[TN / 32];
+  constexpr int kOwn = TN / 32 / SHARES;
+  const int first = share * (TN / SHARES);
+  uint64_t own[kOwn];
 #pragma unroll
-  for (int i = 0; i < TN / 32; ++i) {
-    const int p = p0 + lane + 32 * i;
+  for (int i = 0; i < kOwn; ++i) {
+    const int p = p0 + first + lane + 32 * i;
     const char* a = nullptr;   // stays null for a row that is filled with zeros
     if (p >= cached) {
       if (p < hi)
@@ -230,10 +237,10 @@ __device__ __forceinline__ void load_tile(const AttnArgs& A, const CUtensorMap& 
   constexpr int kChunks = D / 8, kStep = 32 / kChunks;   // 16-byte chunks of a row, rows a round
   const int ch = lane % kChunks;
 #pragma unroll
-  for (int i = 0; i < TN / 32; ++i)
+  for (int i = 0; i < kOwn; ++i)
 #pragma unroll 4
     for (int j = 0; j < 32; j += kStep) {
-      const int from = j + lane / kChunks, r = 32 * i + from;
+      const int from = j + lane / kChunks, r = first + 32 * i + from;
       const uint64_t a = (uint64_t(__shfl_sync(0xffffffffu, uint32_t(own[i] >> 32), from)) << 32) |
                          __shfl_sync(0xffffffffu, uint32_t(own[i]), from);
       cp_async16(dst + (ch >> 3) * (TN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
@@ -246,15 +253,16 @@ __device__ __forceinline__ void load_tile(const AttnArgs& A, const CUtensorMap& 
 }
 
 // Rows of a page that lie in one tile of `tile` positions, 0 unless they are
-// whole groups of 8 of the swizzled layout and a warp's lanes can take a box each.
-inline int box_rows(int page_size, int tile, int head_dim) {
+// whole groups of 8 of the swizzled layout and the loading lanes can take a box
+// each.
+inline int box_rows(int page_size, int tile, int head_dim, int lanes) {
   int rows = page_size, rest = tile;
   while (rest) {
     const int r = rows % rest;
     rows = rest;
     rest = r;
   }
-  return rows % 8 == 0 && tile / rows * (head_dim / 64) <= 32 ? rows : 0;
+  return rows % 8 == 0 && tile / rows * (head_dim / 64) <= lanes ? rows : 0;
 }
 
 // The cache from the layer's first entry on as a matrix of entries of E

@@ -11,12 +11,13 @@
 //
 // One CTA per SM over an even piece of all requests' tiles of 128 positions;
 // per tile a step for every head and 64 rows of it:
-//   warp 4     loads K of a head and tile into a ring (as attention loads it);
-//   warps 6-8  load the steps' Q, the N of the product, in turn, with each row's
+//   warps 4, 5 load K of a head and tile into a ring, half a tile each (as attention
+//              loads it);
+//   warps 7-9  load the steps' Q, the N of the product, in turn, with each row's
 //              lse and the position of its token; the first also finds the parts
 //              of the piece and announces them.  (One warp, an address per copy:
 //              32 requests with up to 15 drafts took 299 us.)
-//   warp 5     issues the products into four accumulators in TMEM;
+//   warp 6     issues the products into four accumulators in TMEM;
 //   warps 0-3  one position a thread: exp(s - lse) summed over the rows.
 // Every wait is bounded, as in attention.
 #include "sv_attn_tc.cuh"
@@ -24,11 +25,11 @@
 namespace sv {
 namespace {
 
-constexpr int kWtThreads = 288;
+constexpr int kWtThreads = 320;
 constexpr int kWtTile = 128;      // positions
 constexpr int kWtRows = 64;       // rows per step
 constexpr int kAccs = 4;
-constexpr int kKeyWarp = 4, kProductWarp = 5, kRowWarp = 6;  // three row warps
+constexpr int kKeyWarp = 4, kProductWarp = 6, kRowWarp = 7;  // two key, three row warps
 constexpr int kParts = 4;         // parts announced ahead
 
 template <int D>
@@ -84,7 +85,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(smem_addr(&S.full[i]), 32);
+      mbar_init(smem_addr(&S.full[i]), 64);
       mbar_init(smem_addr(&S.empty[i]), 1);
     }
     for (int i = 0; i < C::kQBufs; ++i) {
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     }
     for (int i = 0; i < kParts; ++i) {
       mbar_init(smem_addr(&S.announced[i]), 1);
-      mbar_init(smem_addr(&S.taken[i]), 5 + C::kQBufs);  // all warps but the first row warp
+      mbar_init(smem_addr(&S.taken[i]), 6 + C::kQBufs);  // all warps but the first row warp
     }
     mbar_init(smem_addr(&S.drain), 1);
     fence_mbar_init();
@@ -117,8 +118,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   const uint32_t tmem = S.tmem;
   const bool go = P.code == 0 && P.start < P.end;
 
-  if (go && warp == kKeyWarp) {
+  if (go && warp >= kKeyWarp && warp < kProductWarp) {
     // ------------------------------------------------------------------ keys
+    const int share = warp - kKeyWarp;
     const uint64_t policy = l2_evict_first_policy();
     Part w;
     Ring at(0, C::kSlots, 1);
@@ -128,20 +130,21 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       const int32_t* table = A.table + int64_t(w.b) * A.max_pages;
       // a missing page is noted where its scores would be written
       auto missing = [&](int page) { return page < 0 || page >= A.num_pages; };
-      TilePages<kWtTile> next = tile_pages<D, kWtTile>(A, table, cached, w.tile * kWtTile);
+      TilePages<kWtTile, 2> next =
+          tile_pages<D, kWtTile, 2>(A, table, cached, w.tile * kWtTile, share);
       for (int t = 0; t < w.count && !stop; ++t) {
         const int p0 = (w.tile + t) * kWtTile;
-        const TilePages<kWtTile> pages = next;
-        if (t + 1 < w.count) next = tile_pages<D, kWtTile>(A, table, cached, p0 + kWtTile);
+        const TilePages<kWtTile, 2> pages = next;
+        if (t + 1 < w.count) next = tile_pages<D, kWtTile, 2>(A, table, cached, p0 + kWtTile, share);
         if (row_steps(A, w.R, p0) == 0) continue;
         for (int h = 0; h < A.Hkv; ++h) {
           if (!tc_wait_warp(&S.empty[at.at], at.phase, S)) {
             stop = true;
             break;
           }
-          load_tile<D, kWtTile>(A, keys_map, pages, w.b, w.R.n, cached, w.R.hi, p0, h, 0,
-                                smem0 + at.at * C::kSlotBytes, &S.full[at.at], &S.copied[at.at],
-                                policy, missing);
+          load_tile<D, kWtTile, 2>(A, keys_map, pages, w.b, w.R.n, cached, w.R.hi, p0, h, 0,
+                                   smem0 + at.at * C::kSlotBytes, &S.full[at.at],
+                                   &S.copied[at.at], policy, share, missing);
           at.step();
         }
       }
@@ -376,7 +379,7 @@ cudaError_t run(const AttnArgs& A, cudaStream_t s) {
   if (cudaError_t e = allow_smem(weights_tc_kernel<T, D>, WtShape<D>::kSmem, configured)) return e;
   CUtensorMap map;
   AttnArgs B = A;
-  B.box_rows = box_rows(A.S, kWtTile, D);
+  B.box_rows = box_rows(A.S, kWtTile, D, 64);
   if (!rows_map(&map, B, Bits<T>::kFmt != 0)) return cudaErrorInvalidValue;
   weights_tc_kernel<T, D><<<A.ctas, kWtThreads, WtShape<D>::kSmem, s>>>(map, B);
   return cudaGetLastError();
