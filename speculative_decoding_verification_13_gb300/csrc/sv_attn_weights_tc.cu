@@ -50,12 +50,16 @@ struct Part {                     // consecutive tiles of one request; count 0: 
 struct WtShared {
   Part part[kParts];
   uint64_t announced[kParts], taken[kParts];
-  uint64_t full[8], empty[8], qfull[3], qempty[3], sfull[kAccs], sempty[kAccs], drain;
+  uint64_t full[8], empty[8], qfull[3], qempty[3], lfull[6], lempty[6], sfull[kAccs],
+      sempty[kAccs], drain;
   uint32_t tmem;
   int abort, first_bad;
   int copied[8];
-  alignas(16) float lse[3][kWtRows];  // in the log2 domain, +inf for a row that does not count
-  alignas(16) int at[3][kWtRows];     // positions of the rows' tokens
+  // of the rows of a step: lse in the log2 domain, +inf for a row that does not
+  // count, and their tokens' positions.  Two for each Q buffer: the sums are
+  // still at them when the product is done with Q
+  alignas(16) float lse[6][kWtRows];
+  alignas(16) int at[6][kWtRows];
 };
 
 // Steps per head of a part; none for a tile in front of every row's window.
@@ -90,7 +94,11 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     }
     for (int i = 0; i < C::kQBufs; ++i) {
       mbar_init(smem_addr(&S.qfull[i]), 1);
-      mbar_init(smem_addr(&S.qempty[i]), 5);   // the product and the four summing warps
+      mbar_init(smem_addr(&S.qempty[i]), 1);
+    }
+    for (int i = 0; i < 2 * C::kQBufs; ++i) {
+      mbar_init(smem_addr(&S.lfull[i]), 1);
+      mbar_init(smem_addr(&S.lempty[i]), 4);
     }
     for (int i = 0; i < kAccs; ++i) {
       mbar_init(smem_addr(&S.sfull[i]), 1);
@@ -161,7 +169,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     int64_t pos = P.start, base = P.base;
     int b = P.b, t_off = P.t_off;
     AttnReq R = attn_request<kWtTile, kWtTile, true>(A, b);
-    uint32_t phase = 1;
+    uint32_t phase = 1, lphase = 1;
+    int turn = 0;
     int step = 0;                       // of the piece, modulo kQBufs
     bool stop = false;
     for (int i = 0; !stop; ++i) {
@@ -199,11 +208,13 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             const bool other = step != mine;
             step = step + 1 == C::kQBufs ? 0 : step + 1;
             if (other) continue;
-            if (!tc_wait_warp(&S.qempty[mine], phase, S)) {
+            const int lb = mine + turn * C::kQBufs;   // this step's lse buffer
+            if (!tc_wait_warp(&S.lempty[lb], lphase, S)) {
               stop = true;
               break;
             }
-            phase ^= 1;
+            turn ^= 1;
+            lphase ^= turn ^ 1;
             const int row0 = c * kWtRows, rows = min(kWtRows, nrows - row0);
             const int padded = (rows + 15) & ~15;
             // rows lane and lane + 32: their addresses, lse and tokens' positions
@@ -220,9 +231,16 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 v = A.lse[int64_t(w.t_off + tok) * A.Hq + hq] * kAttnLog2e;
                 if (v == -INFINITY) v = INFINITY;   // a row that saw nothing weighs nothing
               }
-              S.lse[mine][r] = v;
-              S.at[mine][r] = w.R.at0 + tok;
+              S.lse[lb][r] = v;
+              S.at[lb][r] = w.R.at0 + tok;
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&S.lfull[lb]));
+            if (!tc_wait_warp(&S.qempty[mine], phase, S)) {
+              stop = true;
+              break;
+            }
+            phase ^= 1;
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll 4
@@ -300,7 +318,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     // ------------------------------------------------------------------ sums
     const uint32_t lanes = tmem + (uint32_t(warp * 32) << 16);
     Part w;
-    Ring qb(0, C::kQBufs, 0), acc(0, kAccs, 0);
+    Ring acc(0, kAccs, 0), lb(0, 2 * C::kQBufs, 0);
     bool ok = true;
     for (int i = 0; ok && next_part(S, i, w); ++i) {
       const int nrows = w.R.take * A.G;
@@ -313,7 +331,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         float sum = 0.f;
         for (int h = 0; ok && h < A.Hkv; ++h)
           for (int c = 0; c < steps; ++c) {
-            ok = tc_wait_two(&S.sfull[acc.at], acc.phase, &S.qfull[qb.at], qb.phase, S);
+            ok = tc_wait_two(&S.sfull[acc.at], acc.phase, &S.lfull[lb.at], lb.phase, S);
             if (!ok) break;
             tc_fence_after();
             const int n = (min(kWtRows, nrows - c * kWtRows) + 15) & ~15;
@@ -325,14 +343,14 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 #pragma unroll
               for (int x = 0; x < 4; ++x)
                 *reinterpret_cast<float4*>(&z[4 * x]) =
-                    *reinterpret_cast<const float4*>(&S.lse[qb.at][x0 + 4 * x]);
+                    *reinterpret_cast<const float4*>(&S.lse[lb.at][x0 + 4 * x]);
               tmem_ld_wait();
 #pragma unroll
               for (int x = 0; x < 16; ++x) z[x] = fmaf(__uint_as_float(s[x]), A.scale2, -z[x]);
               if (edge) {
 #pragma unroll
                 for (int x = 0; x < 16; ++x) {
-                  const int at = S.at[qb.at][x0 + x];
+                  const int at = S.at[lb.at][x0 + x];
                   if (p <= at && (A.window <= 0 || p > at - A.window)) sum += ex2_approx(z[x]);
                 }
               } else {
@@ -346,9 +364,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             __syncwarp();
             if (lane == 0) {
               mbar_arrive(smem_addr(&S.sempty[acc.at]));
-              mbar_arrive(smem_addr(&S.qempty[qb.at]));
+              mbar_arrive(smem_addr(&S.lempty[lb.at]));
             }
-            qb.step();
+            lb.step();
             acc.step();
           }
         if (ok && p < w.R.hi) {
