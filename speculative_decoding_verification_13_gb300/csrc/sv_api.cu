@@ -580,8 +580,10 @@ int spec_logprobs(const sv_logits* logits, const int32_t* tokens, const float* t
       workspace_bytes < logprobs_workspace_bytes(logits->rows))
     return SV_ERR_WORKSPACE;
   if (logits->rows == 0) return SV_OK;
+  const int sms = sm_count();
+  if (sms == 0) return SV_ERR_CUDA;
   return launch_logprobs(*logits, tokens, temperature, n_top, out_logprob, out_entropy, out_max,
-                         out_logsum, out_top_tokens, out_top_logprobs, workspace,
+                         out_logsum, out_top_tokens, out_top_logprobs, workspace, sms,
                          static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? SV_OK
              : SV_ERR_CUDA;

@@ -7,21 +7,26 @@
 // and for a loss with gradients g_l of log p_t and g_h of H:
 //   dL/dx_y = (1/T) (g_l (1[y = t] - p_y) - g_h p_y (log p_y + H)).
 //
-// Forward: one CTA per row, one pass over it (HBM-bound).  Every thread keeps
-// a running maximum m, sum s and weighted sum t = sum e^y y, rescaled when its
-// maximum grows; a group of four 16-byte vectors is loaded ahead and its
-// maximum decides whether to rescale.  (x - m) is taken before the scaling, so
-// that a row of the type's lowest value is a uniform row.
+// Forward: one pass over a row by one CTA, or by a cluster of up to 8 where
+// there are few rows (HBM-bound).  Every thread keeps a running maximum m, sum s
+// and weighted sum t = sum e^y y, rescaled when its maximum grows; the row
+// comes through a ring of 16 KB copies, and the maximum of a thread's four
+// 16-byte vectors of a round decides whether to rescale.  What bounds the pass beside HBM is the issue of instructions, so
+// two elements share an instruction wherever the type allows: y = x c - m c (in
+// log2 units) is one packed fma, the rounding of m c being taken out of the sums
+// at the end.  That form has no room for -inf (0 times -inf) and none for
+// products that overflow: a group whose t is not a number is done again with
+// (x - m) taken first and exponents bounded, and so is a row of very large
+// logits; a row of the type's lowest value is then a uniform row.
+// 4096 rows of 151936 in bf16: element by element 266 us.
 //
 // Alternatives without keeping candidates during the pass: each thread
-// remembers the maximum of each quarter of its elements (a cell).  Every one
-// of the 8 warps holds ceil(n / 8) cells at or above its ceil(n/8)-th largest
-// lane maximum, so the smallest of those 8 values bounds the n-th largest
-// element from below; only cells that reach it are read again (about a
-// twentieth of the row on random logits, most of it from L2), and the
-// elements that reach it are ranked by (logit, index).  Rows where more than
-// kCandCap elements reach the bound (long ties) are scanned once more by the
-// warps, each keeping its 32 best in order.
+// remembers the maximum of each quarter of its elements (a cell).  The n-th
+// largest of the 256 threads' maxima bounds the n-th largest element from
+// below; only cells that reach it are read again (n of 1024 and few more), and
+// the elements that reach it are ranked by (logit, index).  Parts where more
+// than kCandCap elements reach the bound (long ties) are scanned once more by
+// the warps, each keeping its 32 best in order.
 #include <cuda_bf16.h>
 
 #include "sv_internal.cuh"
@@ -31,8 +36,11 @@ namespace {
 
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpUnroll = 4;    // vectors in flight per thread
+constexpr int kLpUnroll = 4;    // vectors of a thread per round
+constexpr int kLpTile = kLpThreads * kLpUnroll * 16;   // bytes of a round: 16 KB
+constexpr int kLpStages = 4;    // rounds in flight per CTA; three CTAs fit an SM
 constexpr int kLpSegs = 4;      // cells per thread
+constexpr int kLpCluster = 8;   // CTAs per row, at most
 constexpr int kCandCap = 512;   // elements that may reach the bound
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -42,6 +50,7 @@ struct LpArgs {
   const void* x;
   int64_t rows, stride;
   int32_t V, n_top;
+  int32_t cluster;            // CTAs per row
   const int32_t* tokens;      // may be null
   const float* temperature;   // may be null
   float *logprob, *entropy, *mx, *logsum;
@@ -133,23 +142,38 @@ __device__ __forceinline__ float scale_log2(const float* temperature, int64_t r)
   return kLog2e / T;
 }
 
+// Running maximum and sums of one thread.  `exact`: sums refer to m itself and
+// (x - m) comes first; otherwise they refer to mc, the float nearest to m c.
 struct Running {
-  float m = -INFINITY, s = 0.f, t = 0.f;
+  float m = -INFINITY, mc = 0.f, s = 0.f, t = 0.f;
+  bool exact = false;
   // the maximum grows to at least g (NaN stays)
   __device__ __forceinline__ void raise(float g, float c2) {
     if (!(g <= m)) {
-      const float mn = fmax_nan(m, g);
+      const float mn = fmax_nan(m, g), mcn = mn * c2;
+      if (!exact && !(fabsf(mcn) < 16384.f)) to_exact(c2);
       if (m > -INFINITY) {
-        const float d = fmaxf((m - mn) * c2, kFloor2);
+        const float d = fmaxf(exact ? (m - mn) * c2 : mc - mcn, kFloor2);
         const float f = ex2_approx(d);
         t = f * fmaf(s, d, t);
         s *= f;
       }
       m = mn;
+      mc = exact ? 0.f : mcn;
     }
   }
-  __device__ __forceinline__ float shift() const { return m > -INFINITY ? m : 0.f; }
-  __device__ __forceinline__ void add(float x, float sh, float c2) {
+  __device__ __forceinline__ void to_exact(float c2) {
+    if (!exact && m > -INFINITY) {
+      const float d = -fmaf(m, c2, -mc);   // mc - m c, below 2^-10
+      const float f = exp2f(d);
+      t = f * fmaf(s, d, t);
+      s *= f;
+    }
+    exact = true;
+    mc = 0.f;
+  }
+  __device__ __forceinline__ void add(float x, float c2) {
+    const float sh = m > -INFINITY ? m : 0.f;
     const float y = fmaxf((x - sh) * c2, kFloor2);
     const float e = ex2_approx(y);
     s += e;
@@ -186,19 +210,156 @@ __device__ __forceinline__ uint64_t warp_merge_desc(uint64_t a, uint64_t b) {
   return v;
 }
 
+// The number of the reading threads for which x holds.
+__device__ __forceinline__ int lp_count(bool x) {
+  int n;
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %1, 0;\n"
+      "barrier.cta.red.popc.aligned.u32 %0, 1, %2, p;\n}\n"
+      : "=r"(n)
+      : "r"(int(x)), "n"(kLpThreads)
+      : "memory");
+  return n;
+}
+
+// The n_top best elements of a CTA's part of a row, in order, as composite keys
+// at the front of s_cand; returns their number.
+// Barrier of the eight warps that read the row.
+__device__ __forceinline__ void lp_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kLpThreads) : "memory");
+}
+
+template <class T>
+__device__ int best_of_part(const LpArgs& A, const RowCut& cut, const uint4* vec, int first,
+                            int niter, int edge, float xe, int ie, const float (&cmax)[kLpSegs],
+                            uint32_t bound16, int* s_ncell, int* s_ncand, uint16_t* s_cell,
+                            uint64_t* s_cand) {
+  using E = Elem<T>;
+  constexpr int VE = E::VE;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // the bound as a value, at least the lowest finite float
+  const float bound =
+      fmaxf(composite_value(uint64_t(bound16) << 48), -3.402823466e38f);
+  auto offer = [&](float x, int i) {
+    if (x >= bound) {
+      const int at = atomicAdd(s_ncand, 1);
+      if (at < kCandCap) s_cand[at] = composite_key(x, uint32_t(i));
+    }
+  };
+  if (tid < edge) offer(xe, ie);
+#pragma unroll
+  for (int q = 0; q < kLpSegs; ++q)
+    if (cmax[q] >= bound) s_cell[atomicAdd(s_ncell, 1)] = uint16_t(q * kLpThreads + tid);
+  lp_sync();
+  // a warp per cell, its lanes over the cell's vectors
+  const int cells = *s_ncell;
+  for (int i = warp; i < cells; i += kLpWarps) {
+    const int cell = s_cell[i], q = cell / kLpThreads;
+    const int j1 = (first + niter * (q + 1) / kLpSegs) * kLpUnroll;
+    for (int j = (first + niter * q / kLpSegs) * kLpUnroll + lane; j < j1; j += 32) {
+      const int vi = j * kLpThreads + cell % kLpThreads;
+      if (vi >= cut.nvec) continue;
+      const uint4 v = vec[vi];
+      if (!(E::vmax(v) >= bound)) continue;
+      float x[VE];
+      E::unpack(v, x);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) offer(x[e], cut.head + vi * VE + e);
+    }
+  }
+  lp_sync();
+  int n = *s_ncand;
+  if (n > kCandCap) {
+    // long ties at the bound: every warp keeps the 32 best of its share in order
+    lp_sync();
+    uint64_t list = 0;
+    auto visit = [&](uint64_t key) {
+      const uint64_t last = (uint64_t(__shfl_sync(0xffffffffu, uint32_t(list >> 32), 31)) << 32) |
+                            __shfl_sync(0xffffffffu, uint32_t(list), 31);
+      if (key <= last) key = 0;
+      if (__any_sync(0xffffffffu, key != 0))
+        list = warp_merge_desc(list, warp_sort_desc(key));
+    };
+    const int v1 = min(cut.nvec, (first + niter) * kLpThreads * kLpUnroll);
+    for (int i0 = first * kLpThreads * kLpUnroll + warp * 32; i0 < v1; i0 += kLpThreads) {
+      const int i = i0 + lane;
+      const uint4 v = i < v1
+                          ? vec[i]
+                          : make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
+      float x[VE];
+      E::unpack(v, x);
+#pragma unroll
+      for (int e = 0; e < VE; ++e)
+        visit(x[e] >= bound ? composite_key(x[e], uint32_t(cut.head + i * VE + e)) : 0);
+    }
+    if (warp == 0)  // head and tail hold at most 14 elements: warp 0's lanes have them
+      visit(tid < edge && xe >= bound ? composite_key(xe, uint32_t(ie)) : 0);
+    s_cand[tid] = list;
+    n = kLpThreads;
+    lp_sync();
+  }
+  // rank by counting: keys are distinct (0 stands for none)
+  uint64_t mine[kCandCap / kLpThreads];
+  int at[kCandCap / kLpThreads];
+#pragma unroll
+  for (int j = 0; j < kCandCap / kLpThreads; ++j) {
+    const int c = tid + j * kLpThreads;
+    mine[j] = c < n ? s_cand[c] : 0;
+    at[j] = A.n_top;
+    if (mine[j]) {
+      at[j] = 0;
+      for (int k = 0; k < n; ++k) at[j] += s_cand[k] > mine[j];
+    }
+  }
+  if (tid == 0) *s_ncell = 0;
+  lp_sync();
+#pragma unroll
+  for (int j = 0; j < kCandCap / kLpThreads; ++j)
+    if (at[j] < A.n_top) {
+      s_cand[at[j]] = mine[j];
+      atomicAdd(s_ncell, 1);
+    }
+  lp_sync();
+  return *s_ncell;
+}
+
+// What a CTA of a cluster finds of its part of a row.
+struct LpPart {
+  float m;
+  double s, t;
+  int expired;
+};
+
+// The address of the cluster's CTA `rank` that holds what p holds here.
+template <class P>
+__device__ __forceinline__ P* cluster_map(P* p, uint32_t rank) {
+  P* q;
+  asm("mapa.u64 %0, %1, %2;" : "=l"(q) : "l"(p), "r"(rank));
+  return q;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" :::
+               "memory");
+}
+
 template <class T, bool TOP>
-__global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LpArgs A) {
+__global__ void __launch_bounds__(kLpThreads + 32, 3) logprobs_kernel(const LpArgs A) {
   using E = Elem<T>;
   constexpr int VE = E::VE;
   __shared__ float s_m[kLpWarps];
   __shared__ double s_s[kLpWarps], s_t[kLpWarps];
-  __shared__ uint32_t s_bound[kLpWarps];
   __shared__ int s_ncell, s_ncand;
   __shared__ uint16_t s_cell[TOP ? kLpThreads * kLpSegs : 1];
   __shared__ uint64_t s_cand[TOP ? kCandCap : 1];
+  __shared__ LpPart s_part[kLpCluster];            // rank 0: the cluster's sums
+  __shared__ uint64_t s_top[TOP ? kLpCluster * SV_LOGPROBS_TOP_MAX : 1];  // and best keys
+  __shared__ uint64_t s_full[kLpStages], s_empty[kLpStages];
+  __shared__ int s_abort;
+  extern __shared__ __align__(128) unsigned char lp_ring[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t r = blockIdx.x;
-  if (r == 0 && tid == 0) {
+  const int C = A.cluster, rank = int(blockIdx.x) % C;
+  const int64_t r = blockIdx.x / C;
+  if (blockIdx.x == 0 && tid == 0) {
     A.hdr->err_code = kStatusList;
     A.hdr->err_row = A.rows;
     A.hdr->err_req = 0;  // entries are rows
@@ -212,6 +373,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LpArgs A) {
   if (tok < -1 || tok >= A.V) code = SV_ERR_DATA_TOKEN;
   const float nan = __int_as_float(0x7fc00000);
   if (code || tok == -1) {  // a row without a token: nothing of it is read
+    if (rank != 0) return;
     if (tid == 0) {
       A.status[r] = code;
       if (A.logprob) A.logprob[r] = nan;
@@ -225,51 +387,139 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LpArgs A) {
     }
     return;
   }
-  float xt = 0.f;
-  if (tid == 0) xt = E::load(row + tok);
-
   const RowCut cut = cut_row(row, A.V);
   const uint4* vec = reinterpret_cast<const uint4*>(row + cut.head);
-  const int niter = (cut.nvec + kLpThreads * kLpUnroll - 1) / (kLpThreads * kLpUnroll);
+  const int rounds = (cut.nvec + kLpThreads * kLpUnroll - 1) / (kLpThreads * kLpUnroll);
+  // this CTA's rounds
+  const int first = int(int64_t(rounds) * rank / C);
+  const int niter = int(int64_t(rounds) * (rank + 1) / C) - first;
+  if (tid == 0) {
+    for (int i = 0; i < kLpStages; ++i) {
+      mbar_init(smem_addr(&s_full[i]), 1);
+      mbar_init(smem_addr(&s_empty[i]), kLpWarps);
+    }
+    fence_mbar_init();
+    s_abort = 0;
+  }
+  __syncthreads();
+  if (warp == kLpWarps) {
+    // the row's rounds, 16 KB a copy, kLpStages ahead
+    if (lane == 0) {
+      const uint64_t policy = l2_evict_first_policy();
+      int k = 0;
+      for (; k < niter; ++k) {
+        const int s = k % kLpStages;
+        if (!mbar_wait_for(smem_addr(&s_empty[s]), ((k / kLpStages) & 1) ^ 1, kWaitNs, &s_abort))
+          break;
+        const int v0 = (first + k) * (kLpTile / 16);
+        const uint32_t bytes = uint32_t(min(kLpTile / 16, cut.nvec - v0)) * 16;
+        mbar_arrive_expect_tx(smem_addr(&s_full[s]), bytes);
+        bulk_load_hint(smem_addr(lp_ring) + s * kLpTile, vec + v0, bytes, smem_addr(&s_full[s]),
+                       policy);
+      }
+      if (k < niter) {  // gave up: let the copies land before the CTA may end
+        *reinterpret_cast<volatile int*>(&s_abort) = 1;
+        for (int j = max(0, k - kLpStages); j < k; ++j)
+          mbar_wait_for(smem_addr(&s_full[j % kLpStages]), (j / kLpStages) & 1);
+      }
+    }
+    return;
+  }
+  float xt = 0.f;
+  if (tid == 0 && rank == 0) xt = E::load(row + tok);
   Running st;
   float cmax[kLpSegs];
+  const uint64_t cc = pk2(c2, c2);
 #pragma unroll
   for (int q = 0; q < kLpSegs; ++q) {
     float cm = -INFINITY;
-    const int it1 = niter * (q + 1) / kLpSegs;
-    for (int it = niter * q / kLpSegs; it < it1; ++it) {
-      uint4 v[kLpUnroll];
-#pragma unroll
-      for (int u = 0; u < kLpUnroll; ++u) {
-        const int i = (it * kLpUnroll + u) * kLpThreads + tid;
-        v[u] = i < cut.nvec ? __ldcs(vec + i)
-                            : make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
+    const int it1 = first + niter * (q + 1) / kLpSegs;
+    for (int it = first + niter * q / kLpSegs; it < it1; ++it) {
+      const int k = it - first, stage = k % kLpStages;
+      bool there = true;
+      if (!mbar_wait_for(smem_addr(&s_full[stage]), (k / kLpStages) & 1, kWaitNs, &s_abort)) {
+        *reinterpret_cast<volatile int*>(&s_abort) = 1;   // the row fails below
+        there = false;
       }
-      float g = E::vmax(v[0]);
+      const uint4* tile =
+          reinterpret_cast<const uint4*>(lp_ring + stage * kLpTile) + tid;
+      const int left = cut.nvec - it * (kLpTile / 16);   // vectors from this round on
+      if (there && left >= kLpTile / 16) {
+        uint4 v[kLpUnroll];
 #pragma unroll
-      for (int u = 1; u < kLpUnroll; ++u) g = fmax_nan(g, E::vmax(v[u]));
-      if (TOP) cm = fmaxf(cm, g);
-      st.raise(g, c2);
-      const float sh = st.shift();
+        for (int u = 0; u < kLpUnroll; ++u) v[u] = tile[u * kLpThreads];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&s_empty[stage]));
+        float g = E::vmax(v[0]);
 #pragma unroll
-      for (int u = 0; u < kLpUnroll; ++u) {
-        float x[VE];
-        E::unpack(v[u], x);
+        for (int u = 1; u < kLpUnroll; ++u) g = fmax_nan(g, E::vmax(v[u]));
+        if (TOP) cm = fmaxf(cm, g);
+        st.raise(g, c2);
+        if (!st.exact) {
+          const uint64_t sh = pk2(-st.mc, -st.mc);
+          uint64_t s2 = pk2(st.s, 0.f), t2 = pk2(st.t, 0.f);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) st.add(x[e], sh, c2);
+          for (int u = 0; u < kLpUnroll; ++u) {
+            float x[VE];
+            E::unpack(v[u], x);
+#pragma unroll
+            for (int e = 0; e < VE; e += 2) {
+              const uint64_t y = fma2(pk2(x[e], x[e + 1]), cc, sh);
+              float y0, y1;
+              upk2(y, y0, y1);
+              const uint64_t w = pk2(ex2_approx(y0), ex2_approx(y1));
+              s2 = add2(s2, w);
+              t2 = fma2(w, y, t2);
+            }
+          }
+          float s0, s1, t0, t1;
+          upk2(s2, s0, s1);
+          upk2(t2, t0, t1);
+          const float t = t0 + t1;
+          if (t == t) {
+            st.s = s0 + s1;
+            st.t = t;
+            continue;
+          }
+          st.to_exact(c2);   // an element of probability 0, or a product out of range
+        }
+#pragma unroll 1
+        for (int u = 0; u < kLpUnroll; ++u) {
+          float x[VE];
+          E::unpack(u == 0 ? v[0] : u == 1 ? v[1] : u == 2 ? v[2] : v[3], x);
+#pragma unroll
+          for (int e = 0; e < VE; ++e) st.add(x[e], c2);
+        }
+      } else {
+        // the row's last round, vector by vector
+        st.to_exact(c2);
+#pragma unroll 1
+        for (int u = 0; there && u * kLpThreads + tid < left; ++u) {
+          float x[VE];
+          const uint4 v = tile[u * kLpThreads];
+          const float g = E::vmax(v);
+          if (TOP) cm = fmaxf(cm, g);
+          st.raise(g, c2);
+          E::unpack(v, x);
+#pragma unroll
+          for (int e = 0; e < VE; ++e) st.add(x[e], c2);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&s_empty[stage]));
       }
     }
     cmax[q] = cm;
   }
-  // head and tail: one element per thread
-  const int edge = cut.head + cut.tail;
+  st.to_exact(c2);
+  // head and tail: one element per thread, of the first CTA
+  const int edge = rank == 0 ? cut.head + cut.tail : 0;
   float xe = -INFINITY;
   int ie = 0;
   if (tid < edge) {
     ie = tid < cut.head ? tid : A.V - edge + tid;
     xe = E::load(row + ie);
     st.raise(xe, c2);
-    st.add(xe, st.shift(), c2);
+    st.add(xe, c2);
   }
 
   // ------------------------------------------------ the row's m, S and sum
@@ -277,22 +527,22 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LpArgs A) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) s_m[warp] = m;
+  uint32_t bound16 = 0;
   if (TOP) {
-    // this warp's share of the bound: its ceil(n / 8)-th largest lane maximum
+    // The bound: the n-th largest of the 256 threads' maxima (so many elements
+    // at least are at or above it), found bit by bit in the upper 16 bits of
+    // their ordered images.
     float lm = cmax[0];
 #pragma unroll
     for (int q = 1; q < kLpSegs; ++q) lm = fmaxf(lm, cmax[q]);
-    uint32_t key = uint32_t(composite_key(lm, 0) >> 32);
-    uint32_t b = 0;
-    for (int k = 0; k < (A.n_top + kLpWarps - 1) / kLpWarps; ++k) {
-      b = __reduce_max_sync(0xffffffffu, key);
-      const uint32_t who = __ballot_sync(0xffffffffu, key == b);
-      if (lane == __ffs(who) - 1) key = 0;
+    const uint32_t key = uint32_t(composite_key(lm, 0) >> 48);
+    for (int bit = 15; bit >= 0; --bit) {
+      const uint32_t with = bound16 | (1u << bit);
+      if (lp_count(key >= with) >= A.n_top) bound16 = with;
     }
-    if (lane == 0) s_bound[warp] = b;
     if (tid == 0) s_ncell = s_ncand = 0;
   }
-  __syncthreads();
+  lp_sync();
   m = s_m[0];
 #pragma unroll
   for (int w = 1; w < kLpWarps; ++w) m = fmax_nan(m, s_m[w]);
@@ -311,116 +561,87 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LpArgs A) {
       s_t[warp] = t;
     }
   }
-  __syncthreads();
+  lp_sync();
   double S = 0.0, W = 0.0;
 #pragma unroll
   for (int w = 0; w < kLpWarps; ++w) {
     S += s_s[w];
     W += s_t[w];
   }
-  const bool bad = !(m > -INFINITY && m < INFINITY);
   const float temp = temperature_of(A.temperature, r);
+
+  // ------------------------------------------------------- the alternatives
+  int n = 0;   // candidates in s_cand
+  if constexpr (TOP) {
+    n = best_of_part<T>(A, cut, vec, first, niter, edge, xe, ie, cmax, bound16, &s_ncell, &s_ncand,
+                        s_cell, s_cand);
+  }
+  if (C > 1) {
+    // sums and best keys of the cluster's CTAs meet in the first one's memory
+    if (tid == 0) {
+      LpPart* to = cluster_map(&s_part[rank], 0);
+      to->m = m;
+      to->s = S;
+      to->t = W;
+      to->expired = *reinterpret_cast<volatile int*>(&s_abort);
+    }
+    if constexpr (TOP) {
+      uint64_t* to = cluster_map(&s_top[rank * SV_LOGPROBS_TOP_MAX], 0);
+      if (tid < SV_LOGPROBS_TOP_MAX) to[tid] = tid < n ? s_cand[tid] : 0;
+    }
+    cluster_sync();
+    if (rank != 0) return;
+    m = s_part[0].m;
+    for (int k = 1; k < C; ++k) m = fmax_nan(m, s_part[k].m);
+    S = W = 0.0;
+    for (int k = 0; k < C; ++k) {
+      const LpPart p = s_part[k];
+      if (p.expired) *reinterpret_cast<volatile int*>(&s_abort) = 1;
+      if (!(p.m > -INFINITY)) continue;   // a part without a finite logit
+      const double d = (double(p.m) - double(m)) * double(c2);
+      const double f = exp2(d);
+      S += f * p.s;
+      W += f > 0.0 ? f * (p.t + p.s * d) : 0.0;
+    }
+    if constexpr (TOP) {
+      lp_sync();
+      n = C * SV_LOGPROBS_TOP_MAX;
+      if (tid < n) s_cand[tid] = s_top[tid];
+      lp_sync();
+    }
+  }
+  const bool expired = *reinterpret_cast<volatile int*>(&s_abort) != 0;
+  const bool bad = expired || !(m > -INFINITY && m < INFINITY);
   const float logsum = bad ? nan : logf(float(S));
   if (tid == 0) {
-    A.status[r] = bad ? SV_ERR_DATA_LOGIT : 0;
+    A.status[r] = expired ? SV_ERR_TIMEOUT : bad ? SV_ERR_DATA_LOGIT : 0;
     if (A.logprob)
       A.logprob[r] = bad || !A.tokens ? nan : token_logprob(xt, m, temp, logsum);
     if (A.entropy) A.entropy[r] = bad ? nan : logsum - kLn2 * float(W / S);
     if (A.mx) A.mx[r] = bad ? nan : m;
     if (A.logsum) A.logsum[r] = logsum;
   }
-  if (!TOP) return;
-  if (bad) {
+  if constexpr (TOP) {
     if (tid < A.n_top) {
       A.top_tok[r * A.n_top + tid] = -1;
-      A.top_lp[r * A.n_top + tid] = nan;
+      A.top_lp[r * A.n_top + tid] = bad ? nan : -INFINITY;   // what is missing stays so
     }
-    return;
-  }
-
-  // ------------------------------------------------------- the alternatives
-  // the bound as a value: the smallest of the warps', at least the lowest finite float
-  uint32_t bk = s_bound[0];
-#pragma unroll
-  for (int w = 1; w < kLpWarps; ++w) bk = min(bk, s_bound[w]);
-  const float bound = fmaxf(composite_value(uint64_t(bk) << 32), -3.402823466e38f);
-  auto offer = [&](float x, int i) {
-    if (x >= bound) {
-      const int at = atomicAdd(&s_ncand, 1);
-      if (at < kCandCap) s_cand[at] = composite_key(x, uint32_t(i));
+    lp_sync();
+    if (bad) return;
+    for (int c = tid; c < n; c += kLpThreads) {
+      const uint64_t key = s_cand[c];
+      if (!key) continue;
+      // in order already where one CTA had the row
+      int rank_of = c;
+      if (C > 1) {
+        rank_of = 0;
+        for (int k = 0; k < n; ++k) rank_of += s_cand[k] > key;
+      }
+      if (rank_of < A.n_top) {
+        A.top_tok[r * A.n_top + rank_of] = composite_index(key);
+        A.top_lp[r * A.n_top + rank_of] = token_logprob(composite_value(key), m, temp, logsum);
+      }
     }
-  };
-  if (tid < edge) offer(xe, ie);
-#pragma unroll
-  for (int q = 0; q < kLpSegs; ++q)
-    if (cmax[q] >= bound) s_cell[atomicAdd(&s_ncell, 1)] = uint16_t(q * kLpThreads + tid);
-  __syncthreads();
-  const int per = (niter / kLpSegs + 1) * kLpUnroll;  // vectors per cell, at most
-  const int total = s_ncell * per;
-  for (int i = tid; i < total; i += kLpThreads) {
-    const int cell = s_cell[i / per], j = i % per;
-    const int q = cell / kLpThreads;
-    const int it = niter * q / kLpSegs + j / kLpUnroll;
-    if (it >= niter * (q + 1) / kLpSegs) continue;
-    const int vi = (it * kLpUnroll + j % kLpUnroll) * kLpThreads + cell % kLpThreads;
-    if (vi >= cut.nvec) continue;
-    const uint4 v = vec[vi];
-    if (!(E::vmax(v) >= bound)) continue;
-    float x[VE];
-    E::unpack(v, x);
-#pragma unroll
-    for (int e = 0; e < VE; ++e) offer(x[e], cut.head + vi * VE + e);
-  }
-  __syncthreads();
-  int n = s_ncand;
-  if (n > kCandCap) {
-    // long ties at the bound: every warp keeps the 32 best of its share in order
-    __syncthreads();
-    uint64_t list = 0;
-    auto visit = [&](uint64_t key) {
-      const uint64_t last = (uint64_t(__shfl_sync(0xffffffffu, uint32_t(list >> 32), 31)) << 32) |
-                            __shfl_sync(0xffffffffu, uint32_t(list), 31);
-      if (key <= last) key = 0;
-      if (__any_sync(0xffffffffu, key != 0))
-        list = warp_merge_desc(list, warp_sort_desc(key));
-    };
-    for (int i0 = warp * 32; i0 < cut.nvec; i0 += kLpThreads) {
-      const int i = i0 + lane;
-      const uint4 v = i < cut.nvec
-                          ? vec[i]
-                          : make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
-      float x[VE];
-      E::unpack(v, x);
-#pragma unroll
-      for (int e = 0; e < VE; ++e)
-        visit(x[e] >= bound ? composite_key(x[e], uint32_t(cut.head + i * VE + e)) : 0);
-    }
-    if (warp == 0)  // head and tail hold at most 14 elements: warp 0's lanes have them
-      visit(tid < edge && xe >= bound ? composite_key(xe, uint32_t(ie)) : 0);
-    s_cand[tid] = list;
-    n = kLpThreads;
-    __syncthreads();
-  }
-  // rank by counting: keys are distinct (0 stands for none)
-  for (int c = tid; c < n; c += kLpThreads) {
-    const uint64_t key = s_cand[c];
-    if (!key) continue;
-    int rank = 0;
-    for (int k = 0; k < n; ++k) rank += s_cand[k] > key;
-    if (rank < A.n_top) {
-      A.top_tok[r * A.n_top + rank] = composite_index(key);
-      A.top_lp[r * A.n_top + rank] = token_logprob(composite_value(key), m, temp, logsum);
-    }
-  }
-  // fewer finite logits than alternatives asked for
-  if (tid == 0) s_ncell = 0;
-  __syncthreads();
-  for (int c = tid; c < n; c += kLpThreads)
-    if (s_cand[c]) atomicAdd(&s_ncell, 1);
-  __syncthreads();
-  if (tid < A.n_top && tid >= s_ncell) {
-    A.top_tok[r * A.n_top + tid] = -1;
-    A.top_lp[r * A.n_top + tid] = -INFINITY;
   }
 }
 
@@ -500,6 +721,14 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const LpGra
   }
 }
 
+template <class T, bool TOP>
+cudaError_t launch_rows(const cudaLaunchConfig_t& cfg, const LpArgs& A) {
+  static std::atomic<uint64_t> configured{0};
+  if (cudaError_t e = allow_smem(logprobs_kernel<T, TOP>, cfg.dynamicSmemBytes, configured))
+    return e;
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, TOP>, A);
+}
+
 }  // namespace
 
 size_t logprobs_workspace_bytes(int64_t rows) {
@@ -508,7 +737,8 @@ size_t logprobs_workspace_bytes(int64_t rows) {
 
 cudaError_t launch_logprobs(const sv_logits& x, const int32_t* tokens, const float* temperature,
                             int n_top, float* logprob, float* entropy, float* mx, float* logsum,
-                            int32_t* top_tok, float* top_lp, void* workspace, cudaStream_t s) {
+                            int32_t* top_tok, float* top_lp, void* workspace, int sms,
+                            cudaStream_t s) {
   LpArgs A;
   A.x = x.data;
   A.rows = x.rows;
@@ -525,15 +755,28 @@ cudaError_t launch_logprobs(const sv_logits& x, const int32_t* tokens, const flo
   A.top_lp = top_lp;
   A.hdr = static_cast<WsHeader*>(workspace);
   A.status = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + align256(sizeof(WsHeader)));
-  const unsigned grid = unsigned(x.rows);
-  if (x.dtype == SV_BF16) {
-    if (n_top > 0) logprobs_kernel<__nv_bfloat16, true><<<grid, kLpThreads, 0, s>>>(A);
-    else logprobs_kernel<__nv_bfloat16, false><<<grid, kLpThreads, 0, s>>>(A);
-  } else {
-    if (n_top > 0) logprobs_kernel<float, true><<<grid, kLpThreads, 0, s>>>(A);
-    else logprobs_kernel<float, false><<<grid, kLpThreads, 0, s>>>(A);
-  }
-  return cudaGetLastError();
+  // CTAs per row: a power of two, at least a round each, while the grid stays
+  // within one CTA per SM (8 rows of 32000 in fp32: one CTA a row 14 us)
+  const int rounds = x.vocab / (kLpThreads * kLpUnroll * (x.dtype == SV_BF16 ? 8 : 4));
+  A.cluster = 1;
+  while (A.cluster < kLpCluster && A.cluster * 2 <= rounds && x.rows * A.cluster * 2 <= sms)
+    A.cluster *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(x.rows * A.cluster));
+  cfg.blockDim = dim3(kLpThreads + 32);
+  cfg.dynamicSmemBytes = size_t(kLpStages) * kLpTile;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(A.cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = A.cluster > 1 ? 1 : 0;
+  if (x.dtype == SV_BF16)
+    return n_top > 0 ? launch_rows<__nv_bfloat16, true>(cfg, A)
+                     : launch_rows<__nv_bfloat16, false>(cfg, A);
+  return n_top > 0 ? launch_rows<float, true>(cfg, A) : launch_rows<float, false>(cfg, A);
 }
 
 int64_t logprobs_grad_blocks(const sv_logits& x) {
