@@ -21,12 +21,13 @@
 // 4096 rows of 151936 in bf16: element by element 266 us.
 //
 // Alternatives without keeping candidates during the pass: each thread
-// remembers the maximum of each quarter of its elements (a cell).  The n-th
-// largest of the 256 threads' maxima bounds the n-th largest element from
-// below; only cells that reach it are read again (n of 1024 and few more), and
-// the elements that reach it are ranked by (logit, index).  Parts where more
-// than kCandCap elements reach the bound (long ties) are scanned once more by
-// the warps, each keeping its 32 best in order.
+// remembers the maximum of each sixteenth of its elements (a cell).  The 8
+// largest thread maxima of every warp are 64 elements of the row, so the n-th
+// largest of them bounds the row's n-th largest from below; only cells that
+// reach it are read again (little more than n of 4096 on random logits), and the
+// elements that reach it are ranked by (logit, index).  Parts where more cells
+// or elements than there is room for reach the bound (long ties) are scanned
+// once more by the warps, each keeping its 32 best in order.
 #include <cuda_bf16.h>
 
 #include "sv_internal.cuh"
@@ -39,9 +40,11 @@ constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpUnroll = 4;    // vectors of a thread per round
 constexpr int kLpTile = kLpThreads * kLpUnroll * 16;   // bytes of a round: 16 KB
 constexpr int kLpStages = 4;    // rounds in flight per CTA; three CTAs fit an SM
-constexpr int kLpSegs = 4;      // cells per thread
+constexpr int kLpSegs = 8;      // cells per thread, at most
+constexpr int kLpBest = 8;      // maxima of a warp that the bound is taken from
+constexpr int kCellCap = 512;   // cells that may reach the bound
 constexpr int kLpCluster = 8;   // CTAs per row, at most
-constexpr int kCandCap = 512;   // elements that may reach the bound
+constexpr int kCandCap = 256;   // elements that may reach the bound
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFloor2 = -1000.0f;  // exponents below 2^-1000 are zero either way
@@ -210,16 +213,56 @@ __device__ __forceinline__ uint64_t warp_merge_desc(uint64_t a, uint64_t b) {
   return v;
 }
 
-// The number of the reading threads for which x holds.
-__device__ __forceinline__ int lp_count(bool x) {
-  int n;
-  asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %1, 0;\n"
-      "barrier.cta.red.popc.aligned.u32 %0, 1, %2, p;\n}\n"
-      : "=r"(n)
-      : "r"(int(x)), "n"(kLpThreads)
-      : "memory");
-  return n;
+// What a CTA of a cluster finds of its part of a row.
+struct LpPart {
+  float m;
+  double s, t;
+  int expired;
+};
+
+template <bool TOP>
+struct LpShared {
+  uint64_t full[kLpStages], empty[kLpStages];
+  double s[kLpWarps], t[kLpWarps];
+  float m[kLpWarps];
+  uint32_t best[TOP ? kLpWarps * kLpBest : 1];
+  int abort, ncell, ncand;
+  LpPart part[kLpCluster];                                  // rank 0: the cluster's sums
+  uint64_t top[TOP ? kLpCluster * SV_LOGPROBS_TOP_MAX : 1]; // and best keys
+  uint64_t cand[TOP ? kCandCap : 1];
+  uint16_t cmax[TOP ? kLpSegs : 1][kLpThreads];   // cells' maxima: upper 16 bits of their images
+  uint16_t cell[TOP ? kCellCap : 1];
+};
+
+// A CTA's part of one row.
+template <class T>
+struct RowPart {
+  int64_t r;
+  const T* row;
+  const uint4* vec;
+  RowCut cut;
+  float c2;
+  int first, niter;   // its rounds
+  int tok, code;
+  bool skip;          // a row without a token, or with a bad one: nothing of it is read
+};
+template <class T>
+__device__ __forceinline__ RowPart<T> row_part(const LpArgs& A, int64_t r, int rank) {
+  RowPart<T> P;
+  P.r = r;
+  P.row = static_cast<const T*>(A.x) + r * A.stride;
+  P.tok = A.tokens ? A.tokens[r] : 0;
+  P.c2 = scale_log2(A.temperature, r);
+  P.code = 0;
+  if (!(P.c2 == P.c2)) P.code = SV_ERR_DATA_TEMPERATURE;
+  if (P.tok < -1 || P.tok >= A.V) P.code = SV_ERR_DATA_TOKEN;
+  P.skip = P.code || P.tok == -1;
+  P.cut = cut_row(P.row, A.V);
+  P.vec = reinterpret_cast<const uint4*>(P.row + P.cut.head);
+  const int rounds = (P.cut.nvec + kLpTile / 16 - 1) / (kLpTile / 16);
+  P.first = int(int64_t(rounds) * rank / A.cluster);
+  P.niter = int(int64_t(rounds) * (rank + 1) / A.cluster) - P.first;
+  return P;
 }
 
 // The n_top best elements of a CTA's part of a row, in order, as composite keys
@@ -230,10 +273,9 @@ __device__ __forceinline__ void lp_sync() {
 }
 
 template <class T>
-__device__ int best_of_part(const LpArgs& A, const RowCut& cut, const uint4* vec, int first,
-                            int niter, int edge, float xe, int ie, const float (&cmax)[kLpSegs],
-                            uint32_t bound16, int* s_ncell, int* s_ncand, uint16_t* s_cell,
-                            uint64_t* s_cand) {
+__device__ int best_of_part(const LpArgs& A, LpShared<true>& S, const RowCut& cut,
+                            const uint4* vec, int first, int niter, int len, int edge, float xe,
+                            int ie, uint32_t bound16) {
   using E = Elem<T>;
   constexpr int VE = E::VE;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -242,22 +284,25 @@ __device__ int best_of_part(const LpArgs& A, const RowCut& cut, const uint4* vec
       fmaxf(composite_value(uint64_t(bound16) << 48), -3.402823466e38f);
   auto offer = [&](float x, int i) {
     if (x >= bound) {
-      const int at = atomicAdd(s_ncand, 1);
-      if (at < kCandCap) s_cand[at] = composite_key(x, uint32_t(i));
+      const int at = atomicAdd(&S.ncand, 1);
+      if (at < kCandCap) S.cand[at] = composite_key(x, uint32_t(i));
     }
   };
   if (tid < edge) offer(xe, ie);
-#pragma unroll
-  for (int q = 0; q < kLpSegs; ++q)
-    if (cmax[q] >= bound) s_cell[atomicAdd(s_ncell, 1)] = uint16_t(q * kLpThreads + tid);
+  for (int q = 0; q * len < niter; ++q)
+    if (S.cmax[q][tid] >= bound16) {
+      const int at = atomicAdd(&S.ncell, 1);
+      if (at < kCellCap) S.cell[at] = uint16_t(q * kLpThreads + tid);
+    }
   lp_sync();
-  // a warp per cell, its lanes over the cell's vectors
-  const int cells = *s_ncell;
-  for (int i = warp; i < cells; i += kLpWarps) {
-    const int cell = s_cell[i], q = cell / kLpThreads;
-    const int j1 = (first + niter * (q + 1) / kLpSegs) * kLpUnroll;
-    for (int j = (first + niter * q / kLpSegs) * kLpUnroll + lane; j < j1; j += 32) {
-      const int vi = j * kLpThreads + cell % kLpThreads;
+  // all vectors of those cells at once, over all threads
+  const int cells = S.ncell;
+  if (cells <= kCellCap) {
+    const int per = len * kLpUnroll;   // vectors per cell, at most
+    for (int i = tid; i < cells * per; i += kLpThreads) {
+      const int cell = S.cell[i / per], j = cell / kLpThreads * per + i % per;
+      if (j >= niter * kLpUnroll) continue;
+      const int vi = (first * kLpUnroll + j) * kLpThreads + cell % kLpThreads;
       if (vi >= cut.nvec) continue;
       const uint4 v = vec[vi];
       if (!(E::vmax(v) >= bound)) continue;
@@ -268,8 +313,8 @@ __device__ int best_of_part(const LpArgs& A, const RowCut& cut, const uint4* vec
     }
   }
   lp_sync();
-  int n = *s_ncand;
-  if (n > kCandCap) {
+  int n = S.ncand;
+  if (n > kCandCap || cells > kCellCap) {
     // long ties at the bound: every warp keeps the 32 best of its share in order
     lp_sync();
     uint64_t list = 0;
@@ -294,7 +339,7 @@ __device__ int best_of_part(const LpArgs& A, const RowCut& cut, const uint4* vec
     }
     if (warp == 0)  // head and tail hold at most 14 elements: warp 0's lanes have them
       visit(tid < edge && xe >= bound ? composite_key(xe, uint32_t(ie)) : 0);
-    s_cand[tid] = list;
+    S.cand[tid] = list;
     n = kLpThreads;
     lp_sync();
   }
@@ -304,31 +349,24 @@ __device__ int best_of_part(const LpArgs& A, const RowCut& cut, const uint4* vec
 #pragma unroll
   for (int j = 0; j < kCandCap / kLpThreads; ++j) {
     const int c = tid + j * kLpThreads;
-    mine[j] = c < n ? s_cand[c] : 0;
+    mine[j] = c < n ? S.cand[c] : 0;
     at[j] = A.n_top;
     if (mine[j]) {
       at[j] = 0;
-      for (int k = 0; k < n; ++k) at[j] += s_cand[k] > mine[j];
+      for (int k = 0; k < n; ++k) at[j] += S.cand[k] > mine[j];
     }
   }
-  if (tid == 0) *s_ncell = 0;
+  if (tid == 0) S.ncell = 0;
   lp_sync();
 #pragma unroll
   for (int j = 0; j < kCandCap / kLpThreads; ++j)
     if (at[j] < A.n_top) {
-      s_cand[at[j]] = mine[j];
-      atomicAdd(s_ncell, 1);
+      S.cand[at[j]] = mine[j];
+      atomicAdd(&S.ncell, 1);
     }
   lp_sync();
-  return *s_ncell;
+  return S.ncell;
 }
-
-// What a CTA of a cluster finds of its part of a row.
-struct LpPart {
-  float m;
-  double s, t;
-  int expired;
-};
 
 // The address of the cluster's CTA `rank` that holds what p holds here.
 template <class P>
@@ -342,103 +380,35 @@ __device__ __forceinline__ void cluster_sync() {
                "memory");
 }
 
+// The eight reading warps' work on one row (their CTA's part of it).
 template <class T, bool TOP>
-__global__ void __launch_bounds__(kLpThreads + 32, 3) logprobs_kernel(const LpArgs A) {
+__device__ void consume_row(const LpArgs& A, LpShared<TOP>& S, const unsigned char* lp_ring,
+                            const RowPart<T>& P, int rank) {
   using E = Elem<T>;
   constexpr int VE = E::VE;
-  __shared__ float s_m[kLpWarps];
-  __shared__ double s_s[kLpWarps], s_t[kLpWarps];
-  __shared__ int s_ncell, s_ncand;
-  __shared__ uint16_t s_cell[TOP ? kLpThreads * kLpSegs : 1];
-  __shared__ uint64_t s_cand[TOP ? kCandCap : 1];
-  __shared__ LpPart s_part[kLpCluster];            // rank 0: the cluster's sums
-  __shared__ uint64_t s_top[TOP ? kLpCluster * SV_LOGPROBS_TOP_MAX : 1];  // and best keys
-  __shared__ uint64_t s_full[kLpStages], s_empty[kLpStages];
-  __shared__ int s_abort;
-  extern __shared__ __align__(128) unsigned char lp_ring[];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int C = A.cluster, rank = int(blockIdx.x) % C;
-  const int64_t r = blockIdx.x / C;
-  if (blockIdx.x == 0 && tid == 0) {
-    A.hdr->err_code = kStatusList;
-    A.hdr->err_row = A.rows;
-    A.hdr->err_req = 0;  // entries are rows
-    A.hdr->n_active = 0;
-  }
-  const T* row = static_cast<const T*>(A.x) + r * A.stride;
-  const int tok = A.tokens ? A.tokens[r] : 0;
-  const float c2 = scale_log2(A.temperature, r);
-  int code = 0;
-  if (!(c2 == c2)) code = SV_ERR_DATA_TEMPERATURE;
-  if (tok < -1 || tok >= A.V) code = SV_ERR_DATA_TOKEN;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, C = A.cluster;
   const float nan = __int_as_float(0x7fc00000);
-  if (code || tok == -1) {  // a row without a token: nothing of it is read
-    if (rank != 0) return;
-    if (tid == 0) {
-      A.status[r] = code;
-      if (A.logprob) A.logprob[r] = nan;
-      if (A.entropy) A.entropy[r] = nan;
-      if (A.mx) A.mx[r] = nan;
-      if (A.logsum) A.logsum[r] = nan;
-    }
-    if (TOP && tid < A.n_top) {
-      A.top_tok[r * A.n_top + tid] = -1;
-      A.top_lp[r * A.n_top + tid] = nan;
-    }
-    return;
-  }
-  const RowCut cut = cut_row(row, A.V);
-  const uint4* vec = reinterpret_cast<const uint4*>(row + cut.head);
-  const int rounds = (cut.nvec + kLpThreads * kLpUnroll - 1) / (kLpThreads * kLpUnroll);
-  // this CTA's rounds
-  const int first = int(int64_t(rounds) * rank / C);
-  const int niter = int(int64_t(rounds) * (rank + 1) / C) - first;
-  if (tid == 0) {
-    for (int i = 0; i < kLpStages; ++i) {
-      mbar_init(smem_addr(&s_full[i]), 1);
-      mbar_init(smem_addr(&s_empty[i]), kLpWarps);
-    }
-    fence_mbar_init();
-    s_abort = 0;
-  }
-  __syncthreads();
-  if (warp == kLpWarps) {
-    // the row's rounds, 16 KB a copy, kLpStages ahead
-    if (lane == 0) {
-      const uint64_t policy = l2_evict_first_policy();
-      int k = 0;
-      for (; k < niter; ++k) {
-        const int s = k % kLpStages;
-        if (!mbar_wait_for(smem_addr(&s_empty[s]), ((k / kLpStages) & 1) ^ 1, kWaitNs, &s_abort))
-          break;
-        const int v0 = (first + k) * (kLpTile / 16);
-        const uint32_t bytes = uint32_t(min(kLpTile / 16, cut.nvec - v0)) * 16;
-        mbar_arrive_expect_tx(smem_addr(&s_full[s]), bytes);
-        bulk_load_hint(smem_addr(lp_ring) + s * kLpTile, vec + v0, bytes, smem_addr(&s_full[s]),
-                       policy);
-      }
-      if (k < niter) {  // gave up: let the copies land before the CTA may end
-        *reinterpret_cast<volatile int*>(&s_abort) = 1;
-        for (int j = max(0, k - kLpStages); j < k; ++j)
-          mbar_wait_for(smem_addr(&s_full[j % kLpStages]), (j / kLpStages) & 1);
-      }
-    }
-    return;
-  }
+  const int64_t r = P.r;
+  const T* row = P.row;
+  const RowCut cut = P.cut;
+  const uint4* vec = P.vec;
+  const float c2 = P.c2;
+  const int first = P.first, niter = P.niter, tok = P.tok;
   float xt = 0.f;
   if (tid == 0 && rank == 0) xt = E::load(row + tok);
   Running st;
-  float cmax[kLpSegs];
+  float lm = -INFINITY;   // the thread's maximum
+  const int len = (niter + kLpSegs - 1) / kLpSegs;   // rounds per cell
+  const int end = first + niter;
   const uint64_t cc = pk2(c2, c2);
-#pragma unroll
-  for (int q = 0; q < kLpSegs; ++q) {
+  for (int q = 0, it = first; it < end; ++q) {
     float cm = -INFINITY;
-    const int it1 = first + niter * (q + 1) / kLpSegs;
-    for (int it = first + niter * q / kLpSegs; it < it1; ++it) {
+    const int it1 = min(end, it + len);
+    for (; it < it1; ++it) {
       const int k = it - first, stage = k % kLpStages;
       bool there = true;
-      if (!mbar_wait_for(smem_addr(&s_full[stage]), (k / kLpStages) & 1, kWaitNs, &s_abort)) {
-        *reinterpret_cast<volatile int*>(&s_abort) = 1;   // the row fails below
+      if (!mbar_wait_for(smem_addr(&S.full[stage]), (k / kLpStages) & 1, kWaitNs, &S.abort)) {
+        *reinterpret_cast<volatile int*>(&S.abort) = 1;   // the row fails below
         there = false;
       }
       const uint4* tile =
@@ -449,7 +419,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, 3) logprobs_kernel(const LpAr
 #pragma unroll
         for (int u = 0; u < kLpUnroll; ++u) v[u] = tile[u * kLpThreads];
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&s_empty[stage]));
+        if (lane == 0) mbar_arrive(smem_addr(&S.empty[stage]));
         float g = E::vmax(v[0]);
 #pragma unroll
         for (int u = 1; u < kLpUnroll; ++u) g = fmax_nan(g, E::vmax(v[u]));
@@ -505,10 +475,13 @@ __global__ void __launch_bounds__(kLpThreads + 32, 3) logprobs_kernel(const LpAr
           for (int e = 0; e < VE; ++e) st.add(x[e], c2);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&s_empty[stage]));
+        if (lane == 0) mbar_arrive(smem_addr(&S.empty[stage]));
       }
     }
-    cmax[q] = cm;
+    if (TOP) {
+      S.cmax[q][tid] = uint16_t(composite_key(cm, 0) >> 48);
+      lm = fmaxf(lm, cm);
+    }
   }
   st.to_exact(c2);
   // head and tail: one element per thread, of the first CTA
@@ -526,26 +499,35 @@ __global__ void __launch_bounds__(kLpThreads + 32, 3) logprobs_kernel(const LpAr
   float m = st.m;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) s_m[warp] = m;
+  if (lane == 0) S.m[warp] = m;
   uint32_t bound16 = 0;
   if (TOP) {
-    // The bound: the n-th largest of the 256 threads' maxima (so many elements
-    // at least are at or above it), found bit by bit in the upper 16 bits of
-    // their ordered images.
-    float lm = cmax[0];
-#pragma unroll
-    for (int q = 1; q < kLpSegs; ++q) lm = fmaxf(lm, cmax[q]);
-    const uint32_t key = uint32_t(composite_key(lm, 0) >> 48);
-    for (int bit = 15; bit >= 0; --bit) {
-      const uint32_t with = bound16 | (1u << bit);
-      if (lp_count(key >= with) >= A.n_top) bound16 = with;
+    // the warp's largest thread maxima, as the upper 16 bits of their ordered images
+    uint32_t key = uint32_t(composite_key(lm, 0) >> 48);
+    for (int k = 0; k < kLpBest; ++k) {
+      const uint32_t best = __reduce_max_sync(0xffffffffu, key);
+      const uint32_t who = __ballot_sync(0xffffffffu, key == best);
+      if (lane == __ffs(who) - 1) key = 0;
+      if (lane == 0) S.best[warp * kLpBest + k] = best;
     }
-    if (tid == 0) s_ncell = s_ncand = 0;
+    if (tid == 0) S.ncell = S.ncand = 0;
   }
   lp_sync();
-  m = s_m[0];
+  if (TOP) {
+    // the bound: the n-th largest of those 64 (every warp finds it for itself)
+    static_assert(kLpWarps * kLpBest == 64, "two a lane");
+    const uint32_t a = S.best[lane], b = S.best[lane + 32];
+    int ra = 0, rb = 0;   // ranks, ties in order of place
+    for (int k = 0; k < 64; ++k) {
+      const uint32_t o = S.best[k];
+      ra += o > a || (o == a && k < lane);
+      rb += o > b || (o == b && k < lane + 32);
+    }
+    bound16 = __reduce_max_sync(0xffffffffu, ra == A.n_top - 1 ? a : rb == A.n_top - 1 ? b : 0u);
+  }
+  m = S.m[0];
 #pragma unroll
-  for (int w = 1; w < kLpWarps; ++w) m = fmax_nan(m, s_m[w]);
+  for (int w = 1; w < kLpWarps; ++w) m = fmax_nan(m, S.m[w]);
   {
     // a maximum that is NaN or infinite makes the row's sums meaningless: it fails below
     const float d = st.m > -INFINITY ? fmaxf((st.m - m) * c2, kFloor2) : 0.f;
@@ -557,67 +539,66 @@ __global__ void __launch_bounds__(kLpThreads + 32, 3) logprobs_kernel(const LpAr
       t += __shfl_xor_sync(0xffffffffu, t, o);
     }
     if (lane == 0) {
-      s_s[warp] = s;
-      s_t[warp] = t;
+      S.s[warp] = s;
+      S.t[warp] = t;
     }
   }
   lp_sync();
-  double S = 0.0, W = 0.0;
+  double sum = 0.0, W = 0.0;
 #pragma unroll
   for (int w = 0; w < kLpWarps; ++w) {
-    S += s_s[w];
-    W += s_t[w];
+    sum += S.s[w];
+    W += S.t[w];
   }
   const float temp = temperature_of(A.temperature, r);
 
   // ------------------------------------------------------- the alternatives
-  int n = 0;   // candidates in s_cand
+  int n = 0;   // candidates in S.cand
   if constexpr (TOP) {
-    n = best_of_part<T>(A, cut, vec, first, niter, edge, xe, ie, cmax, bound16, &s_ncell, &s_ncand,
-                        s_cell, s_cand);
+    n = best_of_part<T>(A, S, cut, vec, first, niter, len, edge, xe, ie, bound16);
   }
   if (C > 1) {
     // sums and best keys of the cluster's CTAs meet in the first one's memory
     if (tid == 0) {
-      LpPart* to = cluster_map(&s_part[rank], 0);
+      LpPart* to = cluster_map(&S.part[rank], 0);
       to->m = m;
-      to->s = S;
+      to->s = sum;
       to->t = W;
-      to->expired = *reinterpret_cast<volatile int*>(&s_abort);
+      to->expired = *reinterpret_cast<volatile int*>(&S.abort);
     }
     if constexpr (TOP) {
-      uint64_t* to = cluster_map(&s_top[rank * SV_LOGPROBS_TOP_MAX], 0);
-      if (tid < SV_LOGPROBS_TOP_MAX) to[tid] = tid < n ? s_cand[tid] : 0;
+      uint64_t* to = cluster_map(&S.top[rank * SV_LOGPROBS_TOP_MAX], 0);
+      if (tid < SV_LOGPROBS_TOP_MAX) to[tid] = tid < n ? S.cand[tid] : 0;
     }
     cluster_sync();
     if (rank != 0) return;
-    m = s_part[0].m;
-    for (int k = 1; k < C; ++k) m = fmax_nan(m, s_part[k].m);
-    S = W = 0.0;
+    m = S.part[0].m;
+    for (int k = 1; k < C; ++k) m = fmax_nan(m, S.part[k].m);
+    sum = W = 0.0;
     for (int k = 0; k < C; ++k) {
-      const LpPart p = s_part[k];
-      if (p.expired) *reinterpret_cast<volatile int*>(&s_abort) = 1;
+      const LpPart p = S.part[k];
+      if (p.expired) *reinterpret_cast<volatile int*>(&S.abort) = 1;
       if (!(p.m > -INFINITY)) continue;   // a part without a finite logit
       const double d = (double(p.m) - double(m)) * double(c2);
       const double f = exp2(d);
-      S += f * p.s;
+      sum += f * p.s;
       W += f > 0.0 ? f * (p.t + p.s * d) : 0.0;
     }
     if constexpr (TOP) {
       lp_sync();
       n = C * SV_LOGPROBS_TOP_MAX;
-      if (tid < n) s_cand[tid] = s_top[tid];
+      if (tid < n) S.cand[tid] = S.top[tid];
       lp_sync();
     }
   }
-  const bool expired = *reinterpret_cast<volatile int*>(&s_abort) != 0;
+  const bool expired = *reinterpret_cast<volatile int*>(&S.abort) != 0;
   const bool bad = expired || !(m > -INFINITY && m < INFINITY);
-  const float logsum = bad ? nan : logf(float(S));
+  const float logsum = bad ? nan : logf(float(sum));
   if (tid == 0) {
     A.status[r] = expired ? SV_ERR_TIMEOUT : bad ? SV_ERR_DATA_LOGIT : 0;
     if (A.logprob)
       A.logprob[r] = bad || !A.tokens ? nan : token_logprob(xt, m, temp, logsum);
-    if (A.entropy) A.entropy[r] = bad ? nan : logsum - kLn2 * float(W / S);
+    if (A.entropy) A.entropy[r] = bad ? nan : logsum - kLn2 * float(W / sum);
     if (A.mx) A.mx[r] = bad ? nan : m;
     if (A.logsum) A.logsum[r] = logsum;
   }
@@ -629,19 +610,83 @@ __global__ void __launch_bounds__(kLpThreads + 32, 3) logprobs_kernel(const LpAr
     lp_sync();
     if (bad) return;
     for (int c = tid; c < n; c += kLpThreads) {
-      const uint64_t key = s_cand[c];
+      const uint64_t key = S.cand[c];
       if (!key) continue;
       // in order already where one CTA had the row
       int rank_of = c;
       if (C > 1) {
         rank_of = 0;
-        for (int k = 0; k < n; ++k) rank_of += s_cand[k] > key;
+        for (int k = 0; k < n; ++k) rank_of += S.cand[k] > key;
       }
       if (rank_of < A.n_top) {
         A.top_tok[r * A.n_top + rank_of] = composite_index(key);
         A.top_lp[r * A.n_top + rank_of] = token_logprob(composite_value(key), m, temp, logsum);
       }
     }
+  }
+}
+
+template <class T, bool TOP>
+__global__ void __launch_bounds__(kLpThreads + 32, 3) logprobs_kernel(const LpArgs A) {
+  __shared__ LpShared<TOP> S;
+  extern __shared__ __align__(128) unsigned char lp_ring[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int C = A.cluster, rank = int(blockIdx.x) % C;
+  if (tid == 0) {
+    for (int i = 0; i < kLpStages; ++i) {
+      mbar_init(smem_addr(&S.full[i]), 1);
+      mbar_init(smem_addr(&S.empty[i]), kLpWarps);
+    }
+    fence_mbar_init();
+    S.abort = 0;
+    if (blockIdx.x == 0) {
+      A.hdr->err_code = kStatusList;
+      A.hdr->err_row = A.rows;
+      A.hdr->err_req = 0;  // entries are rows
+      A.hdr->n_active = 0;
+    }
+  }
+  __syncthreads();
+  if (C > 1) cluster_sync();   // every CTA of the cluster is there before its memory is written
+  const RowPart<T> P = row_part<T>(A, blockIdx.x / C, rank);
+  if (warp == kLpWarps) {
+    // the row's rounds, 16 KB a copy, kLpStages ahead
+    if (lane != 0 || P.skip) return;
+    const uint64_t policy = l2_evict_first_policy();
+    int k = 0;
+    for (; k < P.niter; ++k) {
+      const int s = k % kLpStages;
+      if (!mbar_wait_for(smem_addr(&S.empty[s]), ((k / kLpStages) & 1) ^ 1, kWaitNs, &S.abort))
+        break;
+      const int v0 = (P.first + k) * (kLpTile / 16);
+      const uint32_t bytes = uint32_t(min(kLpTile / 16, P.cut.nvec - v0)) * 16;
+      mbar_arrive_expect_tx(smem_addr(&S.full[s]), bytes);
+      bulk_load_hint(smem_addr(lp_ring) + s * kLpTile, P.vec + v0, bytes, smem_addr(&S.full[s]),
+                     policy);
+    }
+    if (k < P.niter) {  // gave up: let the copies land before the CTA may end
+      *reinterpret_cast<volatile int*>(&S.abort) = 1;
+      for (int j = max(0, k - kLpStages); j < k; ++j)
+        mbar_wait_for(smem_addr(&S.full[j % kLpStages]), (j / kLpStages) & 1);
+    }
+    return;
+  }
+  if (!P.skip) {
+    consume_row<T, TOP>(A, S, lp_ring, P, rank);
+    return;
+  }
+  if (rank != 0) return;
+  const float nan = __int_as_float(0x7fc00000);
+  if (tid == 0) {
+    A.status[P.r] = P.code;
+    if (A.logprob) A.logprob[P.r] = nan;
+    if (A.entropy) A.entropy[P.r] = nan;
+    if (A.mx) A.mx[P.r] = nan;
+    if (A.logsum) A.logsum[P.r] = nan;
+  }
+  if (TOP && tid < A.n_top) {
+    A.top_tok[P.r * A.n_top + tid] = -1;
+    A.top_lp[P.r * A.n_top + tid] = nan;
   }
 }
 
