@@ -10,7 +10,7 @@
 // Forward: one pass over a row by one CTA, or by a cluster of up to 8 where
 // there are few rows (HBM-bound).  Every thread keeps a running maximum m, sum s
 // and weighted sum t = sum e^y y, rescaled when its maximum grows; the row
-// comes through a ring of 16 KB copies, and the maximum of a thread's four
+// comes through a ring of 32 KB copies, and the maximum of a thread's eight
 // 16-byte vectors of a round decides whether to rescale.  What bounds the pass beside HBM is the issue of instructions, so
 // two elements share an instruction wherever the type allows: y = x c - m c (in
 // log2 units) is one packed fma, the rounding of m c being taken out of the sums
@@ -21,9 +21,9 @@
 // 4096 rows of 151936 in bf16: element by element 266 us.
 //
 // Alternatives without keeping candidates during the pass: each thread
-// remembers the maximum of each sixteenth of its elements (a cell).  The 8
-// largest thread maxima of every warp are 64 elements of the row, so the n-th
-// largest of them bounds the row's n-th largest from below; only cells that
+// remembers the maximum of each sixteenth of its elements (a cell).  The 4
+// (8 where n > 16) largest thread maxima of every warp are elements of the row,
+// so the n-th largest of them bounds the row's n-th largest from below; only cells that
 // reach it are read again (little more than n of 4096 on random logits), and the
 // elements that reach it are ranked by (logit, index).  Parts where more cells
 // or elements than there is room for reach the bound (long ties) are scanned
@@ -37,9 +37,9 @@ namespace {
 
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpUnroll = 4;    // vectors of a thread per round
-constexpr int kLpTile = kLpThreads * kLpUnroll * 16;   // bytes of a round: 16 KB
-constexpr int kLpStages = 4;    // rounds in flight per CTA; three CTAs fit an SM
+constexpr int kLpUnroll = 8;    // vectors of a thread per round
+constexpr int kLpTile = kLpThreads * kLpUnroll * 16;   // bytes of a round: 32 KB
+constexpr int kLpStages = 2;    // rounds in flight per CTA; three CTAs fit an SM
 constexpr int kLpSegs = 8;      // cells per thread, at most
 constexpr int kLpBest = 8;      // maxima of a warp that the bound is taken from
 constexpr int kCellCap = 512;   // cells that may reach the bound
@@ -225,7 +225,7 @@ struct LpShared {
   uint64_t full[kLpStages], empty[kLpStages];
   double s[kLpWarps], t[kLpWarps];
   float m[kLpWarps];
-  uint32_t best[TOP ? kLpWarps * kLpBest : 1];
+  alignas(16) uint32_t best[TOP ? kLpWarps * kLpBest : 4];
   int abort, ncell, ncand;
   LpPart part[kLpCluster];                                  // rank 0: the cluster's sums
   uint64_t top[TOP ? kLpCluster * SV_LOGPROBS_TOP_MAX : 1]; // and best keys
@@ -401,6 +401,16 @@ __device__ void consume_row(const LpArgs& A, LpShared<TOP>& S, const unsigned ch
   const int len = (niter + kLpSegs - 1) / kLpSegs;   // rounds per cell
   const int end = first + niter;
   const uint64_t cc = pk2(c2, c2);
+  auto exact_vector = [&](const uint4& w) {
+    float x[VE];
+    E::unpack(w, x);
+#pragma unroll 1
+    for (int e = 0; e < VE; e += 4) {
+      const bool high = e != 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) st.add(high ? x[(i + 4) % VE] : x[i], c2);
+    }
+  };
   for (int q = 0, it = first; it < end; ++q) {
     float cm = -INFINITY;
     const int it1 = min(end, it + len);
@@ -453,26 +463,18 @@ __device__ void consume_row(const LpArgs& A, LpShared<TOP>& S, const unsigned ch
           }
           st.to_exact(c2);   // an element of probability 0, or a product out of range
         }
-#pragma unroll 1
-        for (int u = 0; u < kLpUnroll; ++u) {
-          float x[VE];
-          E::unpack(u == 0 ? v[0] : u == 1 ? v[1] : u == 2 ? v[2] : v[3], x);
 #pragma unroll
-          for (int e = 0; e < VE; ++e) st.add(x[e], c2);
-        }
+        for (int u = 0; u < kLpUnroll; ++u) exact_vector(v[u]);
       } else {
         // the row's last round, vector by vector
         st.to_exact(c2);
 #pragma unroll 1
         for (int u = 0; there && u * kLpThreads + tid < left; ++u) {
-          float x[VE];
           const uint4 v = tile[u * kLpThreads];
           const float g = E::vmax(v);
           if (TOP) cm = fmaxf(cm, g);
           st.raise(g, c2);
-          E::unpack(v, x);
-#pragma unroll
-          for (int e = 0; e < VE; ++e) st.add(x[e], c2);
+          exact_vector(v);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&S.empty[stage]));
@@ -505,25 +507,38 @@ __device__ void consume_row(const LpArgs& A, LpShared<TOP>& S, const unsigned ch
     // the warp's largest thread maxima, as the upper 16 bits of their ordered images
     uint32_t key = uint32_t(composite_key(lm, 0) >> 48);
     for (int k = 0; k < kLpBest; ++k) {
+      if (k >= 4 && A.n_top <= 16) break;   // 32 of them do
       const uint32_t best = __reduce_max_sync(0xffffffffu, key);
       const uint32_t who = __ballot_sync(0xffffffffu, key == best);
       if (lane == __ffs(who) - 1) key = 0;
-      if (lane == 0) S.best[warp * kLpBest + k] = best;
+      if (lane == 0) S.best[k * kLpWarps + warp] = best;
     }
     if (tid == 0) S.ncell = S.ncand = 0;
   }
   lp_sync();
   if (TOP) {
-    // the bound: the n-th largest of those 64 (every warp finds it for itself)
+    // the bound: the n-th largest of those (every warp finds it for itself), the
+    // least of the values that fewer than n are above
     static_assert(kLpWarps * kLpBest == 64, "two a lane");
-    const uint32_t a = S.best[lane], b = S.best[lane + 32];
-    int ra = 0, rb = 0;   // ranks, ties in order of place
-    for (int k = 0; k < 64; ++k) {
-      const uint32_t o = S.best[k];
-      ra += o > a || (o == a && k < lane);
-      rb += o > b || (o == b && k < lane + 32);
+    const uint32_t a = S.best[lane], b = A.n_top <= 16 ? 0u : S.best[lane + 32];
+    int ra = 0, rb = 0;
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(&S.best[k]);
+      ra += (o.x > a) + (o.y > a) + (o.z > a) + (o.w > a);
+      rb += (o.x > b) + (o.y > b) + (o.z > b) + (o.w > b);
     }
-    bound16 = __reduce_max_sync(0xffffffffu, ra == A.n_top - 1 ? a : rb == A.n_top - 1 ? b : 0u);
+    if (A.n_top > 16) {
+#pragma unroll
+      for (int k = 32; k < 64; k += 4) {
+        const uint4 o = *reinterpret_cast<const uint4*>(&S.best[k]);
+        ra += (o.x > a) + (o.y > a) + (o.z > a) + (o.w > a);
+        rb += (o.x > b) + (o.y > b) + (o.z > b) + (o.w > b);
+      }
+    }
+    uint32_t low = ra < A.n_top ? a : 0xffffffffu;
+    if (A.n_top > 16 && rb < A.n_top) low = min(low, b);
+    bound16 = __reduce_min_sync(0xffffffffu, low);
   }
   m = S.m[0];
 #pragma unroll
@@ -650,7 +665,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, 3) logprobs_kernel(const LpAr
   if (C > 1) cluster_sync();   // every CTA of the cluster is there before its memory is written
   const RowPart<T> P = row_part<T>(A, blockIdx.x / C, rank);
   if (warp == kLpWarps) {
-    // the row's rounds, 16 KB a copy, kLpStages ahead
+    // the row's rounds, 32 KB a copy, kLpStages ahead
     if (lane != 0 || P.skip) return;
     const uint64_t policy = l2_evict_first_policy();
     int k = 0;
