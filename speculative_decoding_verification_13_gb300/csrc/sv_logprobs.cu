@@ -22,7 +22,7 @@
 //
 // Alternatives without keeping candidates during the pass: each thread
 // remembers the maximum of each sixteenth of its elements (a cell).  The 4
-// (8 where n > 16) largest thread maxima of every warp are elements of the row,
+// (8 where n > 24) largest thread maxima of every warp are elements of the row,
 // so the n-th largest of them bounds the row's n-th largest from below; only cells that
 // reach it are read again (little more than n of 4096 on random logits), and the
 // elements that reach it are ranked by (logit, index).  Parts where more cells
@@ -507,7 +507,7 @@ __device__ void consume_row(const LpArgs& A, LpShared<TOP>& S, const unsigned ch
     // the warp's largest thread maxima, as the upper 16 bits of their ordered images
     uint32_t key = uint32_t(composite_key(lm, 0) >> 48);
     for (int k = 0; k < kLpBest; ++k) {
-      if (k >= 4 && A.n_top <= 16) break;   // 32 of them do
+      if (k >= 4 && A.n_top <= 24) break;   // 32 of them do
       const uint32_t best = __reduce_max_sync(0xffffffffu, key);
       const uint32_t who = __ballot_sync(0xffffffffu, key == best);
       if (lane == __ffs(who) - 1) key = 0;
@@ -520,7 +520,7 @@ __device__ void consume_row(const LpArgs& A, LpShared<TOP>& S, const unsigned ch
     // the bound: the n-th largest of those (every warp finds it for itself), the
     // least of the values that fewer than n are above
     static_assert(kLpWarps * kLpBest == 64, "two a lane");
-    const uint32_t a = S.best[lane], b = A.n_top <= 16 ? 0u : S.best[lane + 32];
+    const uint32_t a = S.best[lane], b = A.n_top <= 24 ? 0u : S.best[lane + 32];
     int ra = 0, rb = 0;
 #pragma unroll
     for (int k = 0; k < 32; k += 4) {
@@ -528,7 +528,7 @@ __device__ void consume_row(const LpArgs& A, LpShared<TOP>& S, const unsigned ch
       ra += (o.x > a) + (o.y > a) + (o.z > a) + (o.w > a);
       rb += (o.x > b) + (o.y > b) + (o.z > b) + (o.w > b);
     }
-    if (A.n_top > 16) {
+    if (A.n_top > 24) {
 #pragma unroll
       for (int k = 32; k < 64; k += 4) {
         const uint4 o = *reinterpret_cast<const uint4*>(&S.best[k]);
@@ -537,7 +537,7 @@ __device__ void consume_row(const LpArgs& A, LpShared<TOP>& S, const unsigned ch
       }
     }
     uint32_t low = ra < A.n_top ? a : 0xffffffffu;
-    if (A.n_top > 16 && rb < A.n_top) low = min(low, b);
+    if (A.n_top > 24 && rb < A.n_top) low = min(low, b);
     bound16 = __reduce_min_sync(0xffffffffu, low);
   }
   m = S.m[0];
