@@ -382,7 +382,7 @@ def logprobs(logits, tokens, temperature=None, n_top=0, *, stream=None):
     T_ptr = _vector(temperature, "temperature", torch.float32, R, dev, optional=True)
     if not 0 <= n_top <= SV_LOGPROBS_TOP_MAX:
         raise ValueError(f"n_top must be in [0, {SV_LOGPROBS_TOP_MAX}]")
-    f = torch.empty((4, R), dtype=torch.float32, device=dev)
+    lp, ent, mx, ls = [torch.empty((R,), dtype=torch.float32, device=dev) for _ in range(4)]
     tok = top = tok_ptr = top_ptr = None
     if n_top:
         tok = torch.empty((R, n_top), dtype=torch.int32, device=dev)
@@ -390,10 +390,10 @@ def logprobs(logits, tokens, temperature=None, n_top=0, *, stream=None):
         tok_ptr, top_ptr = tok.data_ptr(), top.data_ptr()
     handle = _stream_of(stream, dev)
     ws = _scratch("logprobs", dev, stream, handle, (R,))
-    at = f.data_ptr()
-    _call("spec_logprobs", dev, ctypes.byref(x), t_ptr, T_ptr, n_top, at, at + 4 * R, at + 8 * R,
-          at + 12 * R, tok_ptr, top_ptr, handle, ws.data_ptr(), ws.numel())
-    return LogProbs(*f.unbind(0), tok, top)
+    _call("spec_logprobs", dev, ctypes.byref(x), t_ptr, T_ptr, n_top, lp.data_ptr(),
+          ent.data_ptr(), mx.data_ptr(), ls.data_ptr(), tok_ptr, top_ptr, handle, ws.data_ptr(),
+          ws.numel())
+    return LogProbs(lp, ent, mx, ls, tok, top)
 
 
 def logprobs_grad(logits, tokens, max, logsum, entropy, grad_logprob, grad_entropy=None,
