@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const AttnArgs A) {
 // Joins the partials of the unit that CTA blockIdx.x began and later ones
 // continued: a warp per row, the partials in order of position.
 constexpr int kJoinThreads = 128;
-constexpr int kJoinSplit = 8;   // blocks per unit
+constexpr int kJoinSplit = 16;  // blocks per unit
 
 template <class T, int MR>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs A) {
@@ -269,10 +269,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
     float acc[kMaxD / 32], l = 0.f;
 #pragma unroll
     for (int c = 0; c < kMaxD / 32; ++c) acc[c] = 0.f;
+#pragma unroll 4
     for (int s = 0; s < nseg; ++s) {
       const float2 ml = A.part_ml[slot(s)];
-      const float f = exp2f(ml.x - sh);
-      if (ml.x == -INFINITY) continue;  // this part saw nothing
+      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - sh);  // 0: this part saw nothing
       l = fmaf(ml.y, f, l);
       const float* po = A.part_o + slot(s) * A.D;
 #pragma unroll

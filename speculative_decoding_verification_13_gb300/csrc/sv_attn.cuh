@@ -214,7 +214,12 @@ __device__ AttnPlan attn_plan(const AttnArgs& A) {
   int64_t base = wt + it - tiles;
   int toff = wr + ir - rows;
   if (P.start < P.end && P.start >= base && P.start < base + tiles) {
-    for (int b = b0; b < b1; ++b) {
+    if (per == 1) {
+      s_b = b0;
+      s_toff = toff;
+      s_base = base;
+    }
+    for (int b = b0; per > 1 && b < b1; ++b) {
       const AttnReq r = attn_request<TN, MR, WEIGHTS>(A, b);
       const int64_t t = attn_tiles<TN, MR, WEIGHTS, PAD>(A, r);
       if (P.start < base + t) {

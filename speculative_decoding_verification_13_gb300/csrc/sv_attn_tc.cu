@@ -65,6 +65,7 @@ constexpr float kRescaleLog2 = 8.0f;
 constexpr int kStageFloats = kTcMr * 33;
 struct Stage {
   float2 ml[kTcMr];
+  int64_t out[kTcMr];   // where the row's output begins
   float inv[kTcMr];
   float o[kStageFloats];
 };
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             l *= f;
             m = grown;
           }
-          const float sh = m == -INFINITY ? 0.f : m;
+          const float sh = (m == -INFINITY ? 0.f : m) - Bits<T>::kLift;
           const uint64_t sc2 = pk2(A.scale2, A.scale2), sh2 = pk2(-sh, -sh);
           uint64_t sum = pk2(0.f, 0.f);
           // the last round's scores are still there; P of a round lies over
@@ -716,10 +717,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         total = 0.f;
         for (int c = 0; c < s.copies; ++c) {
           const float2 x = stage.ml[rr + c * apart];
-          if (x.x > -INFINITY || x.y != x.y) total = fmaf(x.y, exp2f(x.x - top), total);
+          if (x.x > -INFINITY || x.y != x.y) total = fmaf(x.y, ex2_approx(x.x - top), total);
         }
-        const float f = m > -INFINITY ? exp2f(m - top) : 0.f;
-        if (copy == 0) stage.inv[rr] = bad ? nan : total == 0.f ? 0.f : 1.f / total;
+        const float f = m > -INFINITY ? ex2_approx(m - top) : 0.f;
+        if (live && copy == 0) {
+          int64_t t;
+          int hq;
+          place(rr, &t, &hq);
+          stage.out[rr] = t * A.o_ts + int64_t(hq) * A.o_hs;
+          stage.inv[rr] = bad ? nan : total == 0.f ? 0.f : 1.f / total;
+        }
         int cols = D;
         while (s.rows * s.copies * (cols + 1) > kStageFloats) cols >>= 1;
         const int half = cols / 2, shift = 31 - __clz(half);
@@ -748,10 +755,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               v1 += from[1];
             }
             if (s.whole) {
-              int64_t t;
-              int hq;
-              place(r, &t, &hq);
-              T* out = static_cast<T*>(A.out) + t * A.o_ts + int64_t(hq) * A.o_hs + c0 + e;
+              T* out = static_cast<T*>(A.out) + stage.out[r] + c0 + e;
               const uint32_t w = Bits<T>::pack(v0 * stage.inv[r], v1 * stage.inv[r]);
               if (A.out_vec) {
                 *reinterpret_cast<uint32_t*>(out) = w;
@@ -771,11 +775,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         int64_t trow;
         int hq;
         place(rr, &trow, &hq);
+        const float ref = top - Bits<T>::kLift;   // what O and the sum refer to
         if (s.whole)
           A.lse[trow * A.Hq + hq] =
-              bad ? nan : (top == -INFINITY ? 0.f : top * kAttnLn2) + logf(total);
+              bad ? nan : (ref == -INFINITY ? 0.f : ref * kAttnLn2) + logf(total);
         else
-          A.part_ml[pr + rr] = make_float2(bad ? nan : top, total);
+          A.part_ml[pr + rr] = make_float2(bad ? nan : ref, total);
       }
       tc_fence_before();
       __syncwarp();

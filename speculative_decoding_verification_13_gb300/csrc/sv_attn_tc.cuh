@@ -23,8 +23,13 @@ struct Ring {
   }
 };
 
+// A type's bits, and kLift: weights are held 2^kLift times as large.  The
+// smallest normal number of fp16 is 2^-14, so that weights of long contexts
+// would lose bits; with the lift and at most 2^8 above the stored maximum they
+// stay below its largest, 65504, and are normal down to 2^-21 of the maximum.
 template <class T> struct Bits;
 template <> struct Bits<__nv_bfloat16> {
+  static constexpr float kLift = 0.f;
   static constexpr uint32_t kFmt = 1, kExp = 0x7f807f80u, kOne = 0x00800080u, kExp1 = 0x7f80u,
                             kMan1 = 0x007fu;
   __device__ static uint32_t pack(float lo, float hi) {
@@ -33,6 +38,7 @@ template <> struct Bits<__nv_bfloat16> {
   }
 };
 template <> struct Bits<__half> {
+  static constexpr float kLift = 7.f;
   static constexpr uint32_t kFmt = 0, kExp = 0x7c007c00u, kOne = 0x04000400u, kExp1 = 0x7c00u,
                             kMan1 = 0x03ffu;
   __device__ static uint32_t pack(float lo, float hi) {

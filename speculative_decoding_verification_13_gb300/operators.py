@@ -88,6 +88,14 @@ def _workspace_size(kind, dev, size):
     return need
 
 
+def _empty(shape, dtype, dev, stream):
+    """An output of a call on ``stream``, of that stream's memory."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _scratch(kind, dev, stream, handle, size):
     """A workspace for a call on the stream: one per stream, or one of its own
     while a graph is being captured (the graph may be replayed next to the
@@ -97,11 +105,7 @@ def _scratch(kind, dev, stream, handle, size):
     capturing = torch.cuda.is_current_stream_capturing()
     ws = None if capturing else _workspaces.get(key)
     if ws is None or ws.numel() < need:
-        if stream is None:
-            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-        else:
-            with torch.cuda.stream(stream):
-                ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        ws = _empty(max(need, 256), torch.uint8, dev, stream)
         if not capturing:
             _workspaces[key] = ws
     _last[kind, dev.index] = ws, handle, stream
@@ -260,11 +264,11 @@ def attention(q, cache, layer, kv_len, block_table, k_per_req, spec=None, *, sca
     dev, dtype, B, rows, Hq, D, args = _attention_args(q, cache, layer, kv_len, block_table,
                                                        k_per_req, spec, scale, window)
     if out is None:
-        out = torch.empty((rows, Hq, D), dtype=dtype, device=dev)
+        out = _empty((rows, Hq, D), dtype, dev, stream)
     else:
         _matrix(out, "out", dtype, (rows, Hq, D), dev)
     if out_lse is None:
-        out_lse = torch.empty((rows, Hq), dtype=torch.float32, device=dev)
+        out_lse = _empty((rows, Hq), torch.float32, dev, stream)
     else:
         _matrix(out_lse, "out_lse", torch.float32, (rows, Hq), dev)
     handle = _stream_of(stream, dev)
@@ -341,7 +345,7 @@ def kv_evict(cache, score, kv_len, block_table, budget, sinks=0, recent=0, *, ou
     elif out_cache is not None:
         raise ValueError("out_cache needs out_table")
     if out_kept is None and with_kept:
-        out_kept = torch.empty((B, budget), dtype=torch.int32, device=dev)
+        out_kept = _empty((B, budget), torch.int32, dev, stream)
     k_ptr = None if out_kept is None else _matrix(out_kept, "out_kept", torch.int32, (B, budget),
                                                   dev)
     handle = _stream_of(stream, dev)
@@ -382,11 +386,11 @@ def logprobs(logits, tokens, temperature=None, n_top=0, *, stream=None):
     T_ptr = _vector(temperature, "temperature", torch.float32, R, dev, optional=True)
     if not 0 <= n_top <= SV_LOGPROBS_TOP_MAX:
         raise ValueError(f"n_top must be in [0, {SV_LOGPROBS_TOP_MAX}]")
-    lp, ent, mx, ls = [torch.empty((R,), dtype=torch.float32, device=dev) for _ in range(4)]
+    lp, ent, mx, ls = [_empty((R,), torch.float32, dev, stream) for _ in range(4)]
     tok = top = tok_ptr = top_ptr = None
     if n_top:
-        tok = torch.empty((R, n_top), dtype=torch.int32, device=dev)
-        top = torch.empty((R, n_top), dtype=torch.float32, device=dev)
+        tok = _empty((R, n_top), torch.int32, dev, stream)
+        top = _empty((R, n_top), torch.float32, dev, stream)
         tok_ptr, top_ptr = tok.data_ptr(), top.data_ptr()
     handle = _stream_of(stream, dev)
     ws = _scratch("logprobs", dev, stream, handle, (R,))
@@ -413,7 +417,7 @@ def logprobs_grad(logits, tokens, max, logsum, entropy, grad_logprob, grad_entro
     gh_ptr = _vector(grad_entropy, "grad_entropy", torch.float32, R, dev, optional=True)
     T_ptr = _vector(temperature, "temperature", torch.float32, R, dev, optional=True)
     if out is None:
-        out = torch.empty((R, V), dtype=logits.dtype, device=dev)
+        out = _empty((R, V), logits.dtype, dev, stream)
     o_ptr, out_stride, out_cols = _rows2d(out, "out", logits.dtype, R, dev)
     if out_cols != V or out.shape[0] != R:
         raise ValueError(f"out must be {(R, V)}")

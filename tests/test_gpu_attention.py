@@ -155,6 +155,29 @@ def test_long_context_is_split_and_joined():
                 score_error(c, size) + 20020 * 2.0 ** -24 + 2.0 ** -23 * abs(want)
 
 
+def test_many_small_weights_in_half_precision():
+    # one position holds most of the weight, 20000 hold 2^-20 of it each: below the
+    # normal range of fp16 but for the scaling of the weights
+    n, D = 20000, 64
+    cache = torch.zeros(n // 16 + 1, 1, 2, 16, D, dtype=F16)
+    flat = cache.permute(0, 3, 1, 2, 4)
+    flat[..., 0, 0] = -13.8984375
+    flat[..., 1, :] = 1.0
+    flat[3, 5, 0, 0, 0] = 0.0
+    flat[3, 5, 0, 1, :] = 0.0
+    q = torch.zeros(1, 2, D, dtype=F16)
+    q[..., 0] = 8.0
+    i32 = torch.int32
+    table = torch.arange(n // 16 + 1, dtype=i32)[None]
+    out, lse = sv.attention(q.to(DEV), cache.to(DEV), 0, torch.tensor([n], dtype=i32, device=DEV),
+                            table.to(DEV), torch.zeros(1, dtype=i32, device=DEV))
+    total = 1 + (n - 1) * math.exp(-13.8984375)
+    want = 1 - 1 / total
+    # half a step for the weights, one for the result, n additions
+    assert (out.double() - want).abs().max() <= want * (2 * 2.0 ** -11 + n * 2.0 ** -24 + 2.0 ** -20)
+    assert (lse.double() - math.log(total)).abs().max() <= n * 2.0 ** -24 + 2.0 ** -20
+
+
 def test_results_do_not_change_from_run_to_run():
     c = Case(9, [3000, 17, 700, 0], [7, 0, 3, 1], 4, 4, 128, 16, B16)
     args, sp = c.gpu()
