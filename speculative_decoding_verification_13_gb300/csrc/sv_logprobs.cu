@@ -31,6 +31,7 @@
 #include <cuda_bf16.h>
 
 #include "sv_internal.cuh"
+#include "sv_tcgen05.cuh"
 
 namespace sv {
 namespace {
@@ -265,13 +266,25 @@ __device__ __forceinline__ RowPart<T> row_part(const LpArgs& A, int64_t r, int r
   return P;
 }
 
-// The n_top best elements of a CTA's part of a row, in order, as composite keys
-// at the front of s_cand; returns their number.
-// Barrier of the eight warps that read the row.
-__device__ __forceinline__ void lp_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kLpThreads) : "memory");
+// A warp gives a slot of the ring back.  Its reads go by way of registers and the
+// next copy into the slot does not, so that an arrival alone does not keep them
+// in order: without the fence, and with the arrival straight behind the loads, a
+// few rows in 4096 had some of their sums from the round after.
+__device__ __forceinline__ void give_back(uint64_t* empty) {
+  fence_async_proxy();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(empty));
 }
 
+// Barrier of the eight warps that read the row.  Lanes may come to it apart (the
+// form for whole warps would then count a part of a warp as all of it).
+__device__ __forceinline__ void lp_sync() {
+  __syncwarp();
+  asm volatile("barrier.cta.sync 1, %0;" ::"n"(kLpThreads) : "memory");
+}
+
+// The n_top best elements of a CTA's part of a row, in order, as composite keys
+// at the front of s_cand; returns their number.
 template <class T>
 __device__ int best_of_part(const LpArgs& A, LpShared<true>& S, const RowCut& cut,
                             const uint4* vec, int first, int niter, int len, int edge, float xe,
@@ -376,8 +389,8 @@ __device__ __forceinline__ P* cluster_map(P* p, uint32_t rank) {
   return q;
 }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" :::
-               "memory");
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // The eight reading warps' work on one row (their CTA's part of it).
@@ -421,18 +434,16 @@ __device__ void consume_row(const LpArgs& A, LpShared<TOP>& S, const unsigned ch
         *reinterpret_cast<volatile int*>(&S.abort) = 1;   // the row fails below
         there = false;
       }
-      const uint4* tile =
-          reinterpret_cast<const uint4*>(lp_ring + stage * kLpTile) + tid;
+      const uint4* tile = reinterpret_cast<const uint4*>(lp_ring + stage * kLpTile) + tid;
       const int left = cut.nvec - it * (kLpTile / 16);   // vectors from this round on
       if (there && left >= kLpTile / 16) {
         uint4 v[kLpUnroll];
 #pragma unroll
         for (int u = 0; u < kLpUnroll; ++u) v[u] = tile[u * kLpThreads];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&S.empty[stage]));
         float g = E::vmax(v[0]);
 #pragma unroll
         for (int u = 1; u < kLpUnroll; ++u) g = fmax_nan(g, E::vmax(v[u]));
+        give_back(&S.empty[stage]);
         if (TOP) cm = fmaxf(cm, g);
         st.raise(g, c2);
         if (!st.exact) {
@@ -476,8 +487,7 @@ __device__ void consume_row(const LpArgs& A, LpShared<TOP>& S, const unsigned ch
           st.raise(g, c2);
           exact_vector(v);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&S.empty[stage]));
+        give_back(&S.empty[stage]);
       }
     }
     if (TOP) {

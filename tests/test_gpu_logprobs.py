@@ -128,6 +128,29 @@ def test_masks_ties_and_extremes(dtype, V):
     run(x, tok, torch.full((9,), 0.25), 32)
 
 
+@pytest.mark.parametrize("R,V,dtype,n_top", [(4096, 98304, B16, 20), (3000, 50001, F32, 32)])
+def test_many_waves_of_rows_repeat_bit_for_bit(R, V, dtype, n_top):
+    """Far more rows than run at a time: rows that start while others end.  A call
+    repeats to the bit, and every row's sum holds."""
+    g = torch.Generator(device=DEV).manual_seed(R)
+    x = (torch.randn(R, V, device=DEV, generator=g) * 2.5).to(dtype)
+    tok = torch.randint(0, V, (R,), device=DEV, generator=g, dtype=torch.int32)
+    first = sv.logprobs(x, tok, None, n_top)
+    for _ in range(7):
+        r = sv.logprobs(x, tok, None, n_top)
+        for name in ("logprob", "entropy", "max", "logsum", "top_tokens", "top_logprobs"):
+            assert torch.equal(getattr(r, name), getattr(first, name)), name
+    for i in range(0, R, 256):
+        d = x[i:i + 256].double()
+        m = d.max(1, keepdim=True).values
+        y = m - d
+        e = torch.exp(-y)
+        ls = torch.log(e.sum(1))
+        M = (e * y).sum(1) / e.sum(1)
+        tol = 4 * E * M + 2.0 ** -21 + (V / 256 + 64) * E + 2 * E * ls
+        assert ((first.logsum[i:i + 256].double() - ls).abs() <= tol).all()
+
+
 def test_zero_signs_tie():
     x = torch.full((1, 700), -5.0)
     x[0, 100::2] = 0.0
