@@ -188,9 +188,13 @@ __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t addr, uint32_t block)
 
 // Hardware barrier of the softmax warps, and the same with one truth value for
 // all of them.  None may stay away: they leave their loop only together.
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
+__device__ __forceinline__ void softmax_sync() {
+  __syncwarp();
+  asm volatile("barrier.cta.sync 2, 128;" ::: "memory");
+}
 __device__ __forceinline__ bool softmax_any(bool x) {
   int any;
+  __syncwarp();
   asm volatile(
       "{\n.reg .pred p, q;\nsetp.ne.b32 p, %1, 0;\n"
       "barrier.cta.red.or.pred q, 2, 128, p;\nselp.b32 %0, 1, 0, q;\n}\n"
