@@ -410,7 +410,7 @@ constexpr int kTcRows = 128;   // rows a unit of the tensor-core kernel
 // entries in 32 bits.  Attention finds the largest score before the scaling, so
 // the scale has to be positive there.
 bool on_tensor_cores(const AttnArgs& A, int dtype, bool weights) {
-  return dtype != SV_F32 && (A.D == 64 || A.D == 128 || A.D == 256) &&
+  return dtype != SV_F32 && A.D >= 64 && A.D % 16 == 0 &&
          (weights || A.scale2 > 0.0f) && (A.num_pages > 0 || A.spec) &&
          A.num_pages * (A.page_bytes / A.entry_bytes) <= INT32_MAX;
 }

@@ -211,7 +211,7 @@ __device__ __forceinline__ bool next_seg(TcShared& S, int unit, Seg& s) {
   return s.count > 0;
 }
 
-template <class T, int D>
+template <class T, int D, bool PART>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const AttnArgs A) {
   using C = Shape<D>;
@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   unsigned char* smem_p = tc_smem_raw + (smem0 - smem_addr(tc_smem_raw));
   const uint32_t ring0 = smem0 + C::kQBufs * C::kQBytes;
   constexpr int kSlotBytes = C::kSlotBytes;
+  const int dim = head_width<D, PART>(A);
 
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
@@ -285,17 +286,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         return true;
       };
       // pages are read one tile ahead, so that nothing waits for the block table
-      TilePages<TN, 1> next = tile_pages<D, TN>(A, table, cached, p0);
+      TilePages<TN, 1> next = tile_pages<D, PART, TN>(A, table, cached, p0);
       for (int t = 0; t < s.count; ++t) {
         const TilePages<TN, 1> pages = next;
-        if (t + 1 < s.count) next = tile_pages<D, TN>(A, table, cached, p0 + (t + 1) * TN);
+        if (t + 1 < s.count) next = tile_pages<D, PART, TN>(A, table, cached, p0 + (t + 1) * TN);
         if (!tc_wait_warp(&S.empty[at.at], at.phase, S)) {
           stop = true;
           break;
         }
-        load_tile<D, TN, 1>(A, rows_map, pages, s.b, s.R.n, cached, hi, p0 + t * TN, s.h, kv,
-                         ring0 + at.at * kSlotBytes, &S.full[at.at], &S.copied[at.at],
-                         s.R.mtiles > 1 ? again : once, 0, missing);
+        load_tile<D, PART, TN, 1>(A, rows_map, pages, s.b, s.R.n, cached, hi, p0 + t * TN, s.h, kv,
+                                  ring0 + at.at * kSlotBytes, &S.full[at.at],
+                                  &S.copied[at.at], s.R.mtiles > 1 ? again : once, 0, missing);
         at.step();
       }
     }
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // them 128 / copies rows apart; rows between them stay as they are (what
       // a row of S or O holds reaches no other row).
       const int apart = kTcMr / s.copies;
-      for (int i = lane / kChunks; i < s.rows * s.copies; i += kStep) {
+      for (int i = lane / kChunks; i < s.rows * s.copies && ch * 8 < dim; i += kStep) {
         const int rr = i / s.copies, r = rr + i % s.copies * apart, row = s.row0 + rr;
         const T* src = q + int64_t(s.t_off + row / A.G) * A.q_ts +
                        int64_t(s.h * A.G + row % A.G) * A.q_hs + ch * 8;
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr uint32_t kBase = (1u << 4) | (Bits<T>::kFmt << 7) | (Bits<T>::kFmt << 10) |
                                (uint32_t(kTcMr >> 4) << 24);
     constexpr uint32_t kIdescS = kBase | (uint32_t(TN >> 3) << 17);
-    constexpr uint32_t kIdescO = kBase | (uint32_t(D >> 3) << 17) | (1u << 16);
+    const uint32_t idesc_o = kBase | (uint32_t(dim >> 3) << 17) | (1u << 16);
     const uint32_t lead = lane == 0;
     const bool scores = warp == kScoreWarp;
     Ring slot(scores ? 0 : C::kKSlots, scores ? C::kKSlots : C::kSlots - C::kKSlots, 0);
@@ -380,9 +381,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const uint64_t k = k_desc + slot.at * (kSlotBytes >> 4);
           const uint32_t d = tmem + buf.at * TN;
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c)
+          for (int c = 0; c < D / 16; ++c) {
+            if (PART && c * 16 >= dim) break;
             mma_ss(lead, d, q + (((c >> 2) * (kTcMr * 128) + (c & 3) * 32) >> 4),
                    k + (((c >> 2) * (TN * 128) + (c & 3) * 32) >> 4), kIdescS, c != 0);
+          }
           mma_commit(lead, &S.sfull[buf.at]);
           mma_commit(lead, &S.empty[slot.at]);
           slot.step();
@@ -400,7 +403,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const uint32_t p = tmem + buf.at * TN;
 #pragma unroll
           for (int c = 0; c < TN / 16; ++c)
-            mma_ts(lead, tmem + C::kOCol, p + c * 8, v + c * (2048 >> 4), kIdescO,
+            mma_ts(lead, tmem + C::kOCol, p + c * 8, v + c * (2048 >> 4), idesc_o,
                    (c != 0) || t > 0);
           mma_commit(lead, &S.pvdone[buf.at]);
           mma_commit(lead, &S.empty[slot.at]);
@@ -518,8 +521,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // The warp's copy's share of the columns, N at a time (two rounds where
         // it has all of 128: the first round's scores are read again after the
         // maximum over both)
-        auto weigh = [&](auto width, auto rounds) -> bool {
-          constexpr int N = decltype(width)::value, ROUNDS = decltype(rounds)::value;
+        auto weigh = [&](auto columns, auto rounds) -> bool {
+          constexpr int N = decltype(columns)::value, ROUNDS = decltype(rounds)::value;
           const int c0 = copy * N;
           float x[N];
           auto fetch = [&](int round) {
@@ -551,7 +554,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               if (!tc_wait_warp(&S.pvdone[done.at], done.phase, S)) return false;
               tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < D / 16; ++c) {
+              for (int c = 0; c < dim / 16; ++c) {
                 uint32_t o[16];
                 tmem_ld16(lanes + C::kOCol + c * 16, o);
                 tmem_ld_wait();
@@ -677,7 +680,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         place(rr, &trow, &hq);
         if (active) {
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = 0; c * 32 < dim; ++c) {
             uint32_t o[32];
             tmem_ld32(lanes + C::kOCol + c * 32, o);
             tmem_ld_wait();
@@ -691,21 +694,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                      __uint_as_float(o[2 * e + 1]) * inv);
               if (A.out_vec) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                for (int e = 0; e < 4; ++e) {
+                  if (PART && c * 32 + e * 8 >= dim) break;
                   *reinterpret_cast<uint4*>(out + e * 8) =
                       make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                }
               } else {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
+                  if (PART && c * 32 + e >= dim) break;
                   const uint16_t h = uint16_t(w[e / 2] >> (16 * (e & 1)));
                   out[e] = *reinterpret_cast<const T*>(&h);
                 }
               }
             } else {
-              uint4* po = reinterpret_cast<uint4*>(A.part_o + (pr + rr) * D + c * 32);
+              uint4* po = reinterpret_cast<uint4*>(A.part_o + (pr + rr) * dim + c * 32);
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
+              for (int e = 0; e < 8; ++e) {
+                if (PART && c * 32 + e * 4 >= dim) break;
                 po[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              }
             }
           }
         }
@@ -735,7 +743,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         while (s.rows * s.copies * (cols + 1) > kStageFloats) cols >>= 1;
         const int half = cols / 2, shift = 31 - __clz(half);
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += cols) {
+        for (int c0 = 0; c0 < dim; c0 += cols) {
           if (active) {
             float* to = stage.o + (copy * s.rows + rr) * (cols + 1);
 #pragma unroll 1
@@ -752,6 +760,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           softmax_sync();
           for (int i = tid; i < s.rows * half; i += 128) {
             const int r = i >> shift, e = (i & (half - 1)) * 2;
+            if (PART && c0 + e >= dim) continue;
             float v0 = 0.f, v1 = 0.f;
             for (int k = 0; k < s.copies; ++k) {
               const float* from = stage.o + (k * s.rows + r) * (cols + 1) + e;
@@ -769,7 +778,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 out[1] = *reinterpret_cast<const T*>(&h1);
               }
             } else {
-              *reinterpret_cast<float2*>(A.part_o + (pr + r) * D + c0 + e) = make_float2(v0, v1);
+              *reinterpret_cast<float2*>(A.part_o + (pr + r) * dim + c0 + e) = make_float2(v0, v1);
             }
           }
           softmax_sync();
@@ -815,25 +824,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-template <class T, int D>
+template <class T, int D, bool PART>
 cudaError_t run(const AttnArgs& A, cudaStream_t s) {
   static std::atomic<uint64_t> configured{0};
-  if (cudaError_t e = allow_smem(attn_tc_kernel<T, D>, Shape<D>::kSmem, configured)) return e;
+  if (cudaError_t e = allow_smem(attn_tc_kernel<T, D, PART>, Shape<D>::kSmem, configured)) return e;
   CUtensorMap map;
   AttnArgs B = A;
   B.box_rows = box_rows(A.S, Shape<D>::TN, D, 32);
   if (!rows_map(&map, B, Bits<T>::kFmt != 0)) return cudaErrorInvalidValue;
-  attn_tc_kernel<T, D><<<A.ctas, kTcThreads, Shape<D>::kSmem, s>>>(map, B);
+  attn_tc_kernel<T, D, PART><<<A.ctas, kTcThreads, Shape<D>::kSmem, s>>>(map, B);
   return cudaGetLastError();
 }
 
 template <class T>
 cudaError_t run_dim(const AttnArgs& A, cudaStream_t s) {
-  switch (A.D) {
-    case 64: return run<T, 64>(A, s);
-    case 128: return run<T, 128>(A, s);
-    default: return run<T, 256>(A, s);
-  }
+  if (A.D == 64) return run<T, 64, false>(A, s);
+  if (A.D <= 128) return A.D == 128 ? run<T, 128, false>(A, s) : run<T, 128, true>(A, s);
+  return A.D == 256 ? run<T, 256, false>(A, s) : run<T, 256, true>(A, s);
 }
 
 }  // namespace

@@ -149,6 +149,20 @@ __device__ __forceinline__ bool tc_sync(uint64_t* bar, uint32_t parity, Sh& S) {
 }
 
 
+// Heads of any multiple of 16 from 64 on are taken at D, the next of 64, 128 and
+// 256: PART says that the head is narrower than D.  What lies behind it in a slot
+// (entries of the next head, or nothing) is in no product: scores end at the
+// head's last 16 elements, and products with V have its columns only.
+template <int D, bool PART>
+__device__ __forceinline__ int head_width(const AttnArgs& A) {
+  return PART ? A.D : D;
+}
+// 128-byte parts of a row
+template <int D, bool PART>
+__device__ __forceinline__ int row_parts(const AttnArgs& A) {
+  return PART && D > 128 ? (A.D + 63) / 64 : D / 64;
+}
+
 // The pages of one tile: of this lane's box (the first), or of its rows lane +
 // 32 i where the tile does not come in boxes.  SHARES warps may load a tile
 // together, each every SHARES-th box or its share of the rows.
@@ -168,14 +182,14 @@ __device__ __forceinline__ bool tile_boxed(const AttnArgs& A, int cached, int p0
   return A.box_rows > 0 && p0 + TN <= cached;
 }
 
-template <int D, int TN, int SHARES = 1>
+template <int D, bool PART, int TN, int SHARES = 1>
 __device__ __forceinline__ TilePages<TN, SHARES> tile_pages(const AttnArgs& A,
                                                             const int32_t* table, int cached,
                                                             int p0, int share = 0) {
   const int lane = threadIdx.x & 31;
   TilePages<TN, SHARES> t;
   if (tile_boxed<TN>(A, cached, p0)) {
-    const int box0 = (lane * SHARES + share) / (D / 64) * A.box_rows;
+    const int box0 = (lane * SHARES + share) / row_parts<D, PART>(A) * A.box_rows;
     t.page[0] = box0 < TN ? __ldg(table + page_column(A, p0 + box0)) : 0;
   } else {
 #pragma unroll
@@ -192,7 +206,7 @@ __device__ __forceinline__ TilePages<TN, SHARES> tile_pages(const AttnArgs& A,
 // 128-byte swizzled.  `full` counts 32 arrivals a share; `copied` tells how the
 // tile came.  missing(page) is true, and notes it, for a page that is not in the
 // pool.
-template <int D, int TN, int SHARES, class F>
+template <int D, bool PART, int TN, int SHARES, class F>
 __device__ __forceinline__ void load_tile(const AttnArgs& A, const CUtensorMap& map,
                                           const TilePages<TN, SHARES>& pages, int b, int n,
                                           int cached, int hi, int p0, int h, int kv, uint32_t dst,
@@ -200,10 +214,11 @@ __device__ __forceinline__ void load_tile(const AttnArgs& A, const CUtensorMap& 
                                           F missing) {
   const int lane = threadIdx.x & 31;
   const uint32_t bar = smem_addr(full);
+  const int dim = head_width<D, PART>(A);
   if (tile_boxed<TN>(A, cached, p0)) {
-    constexpr int kParts = D / 64;   // 128-byte parts of a row
+    const int parts = row_parts<D, PART>(A);
     if (lane == 0) {
-      const int boxes = (TN / A.box_rows * kParts - share + SHARES - 1) / SHARES;
+      const int boxes = (TN / A.box_rows * parts - share + SHARES - 1) / SHARES;
       *copied = 0;
       mbar_arrive_expect_tx(bar, uint32_t(boxes * A.box_rows * 128));
     } else {
@@ -211,14 +226,14 @@ __device__ __forceinline__ void load_tile(const AttnArgs& A, const CUtensorMap& 
     }
     __syncwarp();
     const int box = lane * SHARES + share;   // this lane's box
-    const int part = box % kParts, box0 = box / kParts * A.box_rows;
+    const int part = box % parts, box0 = box / parts * A.box_rows;
     if (box0 < TN) {
       const int p = p0 + box0, pg = pages.page[0];
       // a missing page: a box outside the matrix is all zeros
       const int row = missing(pg)
                           ? -A.box_rows
                           : pg * A.page_rows + kv * A.S + (p - page_column(A, p) * A.S);
-      box_load(dst + part * (TN * 128) + box0 * 128, &map, h * D + part * 64, row, bar, policy);
+      box_load(dst + part * (TN * 128) + box0 * 128, &map, h * dim + part * 64, row, bar, policy);
     }
     return;
   }
@@ -238,7 +253,7 @@ __device__ __forceinline__ void load_tile(const AttnArgs& A, const CUtensorMap& 
       a = A.cache + pages.page[i] * A.page_bytes + kv * A.v_off +
           (p - page_column(A, p) * A.S) * A.entry_bytes;
     }
-    own[i] = a ? reinterpret_cast<uint64_t>(a + int64_t(h) * D * 2) : 0;
+    own[i] = a ? reinterpret_cast<uint64_t>(a + int64_t(h) * dim * 2) : 0;
   }
   constexpr int kChunks = D / 8, kStep = 32 / kChunks;   // 16-byte chunks of a row, rows a round
   const int ch = lane % kChunks;
@@ -249,6 +264,7 @@ __device__ __forceinline__ void load_tile(const AttnArgs& A, const CUtensorMap& 
       const int from = j + lane / kChunks, r = first + 32 * i + from;
       const uint64_t a = (uint64_t(__shfl_sync(0xffffffffu, uint32_t(own[i] >> 32), from)) << 32) |
                          __shfl_sync(0xffffffffu, uint32_t(own[i]), from);
+      if (PART && ch * 8 >= dim) continue;
       cp_async16(dst + (ch >> 3) * (TN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
                  a ? reinterpret_cast<const char*>(a) + ch * 16
                    : reinterpret_cast<const char*>(A.k_per_req),

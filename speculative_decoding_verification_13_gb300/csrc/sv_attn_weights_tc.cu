@@ -76,7 +76,7 @@ __device__ __forceinline__ bool next_part(WtShared& S, int i, Part& p) {
   return p.count > 0;
 }
 
-template <class T, int D>
+template <class T, int D, bool PART>
 __global__ void __launch_bounds__(kWtThreads, 1)
     weights_tc_kernel(const __grid_constant__ CUtensorMap keys_map, const AttnArgs A) {
   using C = WtShape<D>;
@@ -139,18 +139,18 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       // a missing page is noted where its scores would be written
       auto missing = [&](int page) { return page < 0 || page >= A.num_pages; };
       TilePages<kWtTile, 2> next =
-          tile_pages<D, kWtTile, 2>(A, table, cached, w.tile * kWtTile, share);
+          tile_pages<D, PART, kWtTile, 2>(A, table, cached, w.tile * kWtTile, share);
       for (int t = 0; t < w.count && !stop; ++t) {
         const int p0 = (w.tile + t) * kWtTile;
         const TilePages<kWtTile, 2> pages = next;
-        if (t + 1 < w.count) next = tile_pages<D, kWtTile, 2>(A, table, cached, p0 + kWtTile, share);
+        if (t + 1 < w.count) next = tile_pages<D, PART, kWtTile, 2>(A, table, cached, p0 + kWtTile, share);
         if (row_steps(A, w.R, p0) == 0) continue;
         for (int h = 0; h < A.Hkv; ++h) {
           if (!tc_wait_warp(&S.empty[at.at], at.phase, S)) {
             stop = true;
             break;
           }
-          load_tile<D, kWtTile, 2>(A, keys_map, pages, w.b, w.R.n, cached, w.R.hi, p0, h, 0,
+          load_tile<D, PART, kWtTile, 2>(A, keys_map, pages, w.b, w.R.n, cached, w.R.hi, p0, h, 0,
                                    smem0 + at.at * C::kSlotBytes, &S.full[at.at],
                                    &S.copied[at.at], policy, share, missing);
           at.step();
@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 const uint64_t a =
                     (uint64_t(__shfl_sync(0xffffffffu, uint32_t(own[x] >> 32), from)) << 32) |
                     __shfl_sync(0xffffffffu, uint32_t(own[x]), from);
+                if (PART && ch * 8 >= A.D) continue;
                 const T* src = a ? reinterpret_cast<const T*>(a) + ch * 8 : q;
                 const uint32_t off =
                     (ch >> 3) * (kWtRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
@@ -294,10 +295,12 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             const uint32_t idesc = kBase | (n >> 3 << 17);
             const uint64_t q = q_desc + qb.at * (C::kQBytes >> 4);
 #pragma unroll
-            for (int x = 0; x < D / 16; ++x)
+            for (int x = 0; x < D / 16; ++x) {
+              if (PART && x * 16 >= A.D) break;
               mma_ss(lead, tmem + acc.at * kWtRows,
                      k + (((x >> 2) * (kWtTile * 128) + (x & 3) * 32) >> 4),
                      q + (((x >> 2) * (kWtRows * 128) + (x & 3) * 32) >> 4), idesc, x != 0);
+            }
             mma_commit(lead, &S.sfull[acc.at]);
             mma_commit(lead, &S.qempty[qb.at]);
             qb.step();
@@ -391,25 +394,23 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   }
 }
 
-template <class T, int D>
+template <class T, int D, bool PART>
 cudaError_t run(const AttnArgs& A, cudaStream_t s) {
   static std::atomic<uint64_t> configured{0};
-  if (cudaError_t e = allow_smem(weights_tc_kernel<T, D>, WtShape<D>::kSmem, configured)) return e;
+  if (cudaError_t e = allow_smem(weights_tc_kernel<T, D, PART>, WtShape<D>::kSmem, configured)) return e;
   CUtensorMap map;
   AttnArgs B = A;
   B.box_rows = box_rows(A.S, kWtTile, D, 64);
   if (!rows_map(&map, B, Bits<T>::kFmt != 0)) return cudaErrorInvalidValue;
-  weights_tc_kernel<T, D><<<A.ctas, kWtThreads, WtShape<D>::kSmem, s>>>(map, B);
+  weights_tc_kernel<T, D, PART><<<A.ctas, kWtThreads, WtShape<D>::kSmem, s>>>(map, B);
   return cudaGetLastError();
 }
 
 template <class T>
 cudaError_t run_dim(const AttnArgs& A, cudaStream_t s) {
-  switch (A.D) {
-    case 64: return run<T, 64>(A, s);
-    case 128: return run<T, 128>(A, s);
-    default: return run<T, 256>(A, s);
-  }
+  if (A.D == 64) return run<T, 64, false>(A, s);
+  if (A.D <= 128) return A.D == 128 ? run<T, 128, false>(A, s) : run<T, 128, true>(A, s);
+  return A.D == 256 ? run<T, 256, false>(A, s) : run<T, 256, true>(A, s);
 }
 
 }  // namespace

@@ -95,6 +95,13 @@ CASES = [
     ([200, 90, 0], [5, 15, 2], 2, 4, 128, 16, B16, True, 1),
     ([200, 90, 500], [5, 15, 0], 2, 4, 128, 16, B16, True, 70),
     ([200, 90, 3], [5, 15, 0], 2, 2, 64, 16, F32, False, 33),
+    ([300, 131, 2], [5, 0, 15], 3, 4, 80, 16, F16, True, 0),         # between 64, 128 and 256
+    ([400, 128, 70], [0, 32, 3], 2, 7, 96, 32, B16, True, 90),
+    ([290, 129], [7, 1], 3, 2, 112, 7, B16, False, 0),
+    ([300, 64, 9], [3, 0, 32], 3, 4, 144, 64, B16, True, 0),
+    ([257, 90], [15, 2], 2, 8, 192, 16, F16, True, 65),
+    ([200, 33], [0, 4], 1, 1, 240, 8, B16, True, 0),
+    ([130, 90], [2, 0], 2, 2, 72, 16, F16, True, 0),                 # no multiple of 16
 ]
 
 
@@ -223,6 +230,37 @@ def test_a_later_token_of_the_drafts_does_not_reach_an_earlier_one():
         c.q = q
         assert not np.isfinite(o[3, :, 5]).any() and np.isfinite(o[3, :, 6]).all()
         assert np.isnan(o[4:]).all() and torch.isnan(lse[4:]).all()
+
+
+@pytest.mark.parametrize("D", [80, 208])
+def test_another_head_s_values_do_not_reach_a_narrow_head(D):
+    # whole boxes of 128 bytes reach into the next head's entries
+    c = Case(16, [640, 200], [3, 0], 2, 4, D, 16, B16)
+    want = c.oracle()
+    c.cache[..., D:] = math.nan
+    c.spec[..., D:] = math.inf
+    args, sp = c.gpu()
+    out, lse = sv.attention(*args, sp)
+    first = lambda x: x[:, :4]
+    c.q = c.q[:, :4]
+    check(c, first(out), first(lse), [first(x) for x in want])
+    assert torch.isnan(lse[:, 4:]).all()
+    score = torch.zeros(2, 700, device=DEV)
+    got = sv.attention_weights(*args, torch.zeros_like(lse), score, sp,
+                               out_score=torch.zeros_like(score))
+    assert torch.isnan(got[0, :640]).all()
+
+
+@pytest.mark.parametrize("dtype,D", [(B16, 80), (F16, 160)])
+def test_narrow_heads_split_over_blocks_and_unaligned(dtype, D):
+    c = Case(17, [3001, 50], [2, 1], 2, 3, D, 16, dtype)
+    rows = c.q.shape[0]
+    q = torch.zeros(6, rows, D + 1, dtype=dtype, device=DEV)[..., 1:].transpose(0, 1)
+    q.copy_(c.q)
+    args, sp = c.gpu(q)
+    flat = torch.zeros(rows * 6 * D + 1, dtype=dtype, device=DEV)
+    out, lse = sv.attention(*args, sp, out=flat[1:].view(rows, 6, D))
+    check(c, out, lse, c.oracle())
 
 
 def test_data_errors_fail_their_request_only():
