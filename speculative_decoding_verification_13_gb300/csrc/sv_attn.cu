@@ -246,52 +246,116 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const AttnArgs A) {
 }
 
 // Joins the partials of the unit that CTA blockIdx.x began and later ones
-// continued: a warp per row, the partials in order of position.
+// continued, in order of position.  A warp has a row; where a unit lies in many
+// parts, a long context with few rows, the block's warps have a share of one row's
+// parts each.  Every lane finds the factor of a part, and the loads of eight
+// parts are under way at once: the time is that of a few dependent loads.  36000
+// positions, 4 heads of 256 in 38 parts each: JOINTIME us, one part after the other
+// by one warp took 64.
 constexpr int kJoinThreads = 128;
+constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinSplit = 16;  // blocks per unit
+constexpr int kJoinShare = 8;   // parts from which on the warps share a row
+constexpr int kJoinAhead = 8;
 
 template <class T, int MR>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs A) {
+  constexpr int kVecs = kMaxD / 4 / 32;   // 16-byte vectors a lane
+  __shared__ float4 s_acc[kJoinWarps][kMaxD / 4];
+  __shared__ float s_l[kJoinWarps];
   pdl_wait();
   const int c0 = blockIdx.x;
   const AttnSplit u = A.split[c0];
   if (!u.valid) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int nseg = (u.last - c0) / A.hg + 1;
-  for (int r = blockIdx.y * (kJoinThreads / 32) + warp; r < u.rows;
-       r += kJoinSplit * (kJoinThreads / 32)) {
+  const int nseg = (u.last - c0) / A.hg + 1, nvec = A.D / 4;
+  const bool share = nseg > kJoinShare;
+  const int first = share ? nseg * warp / kJoinWarps : 0;
+  const int end = share ? nseg * (warp + 1) / kJoinWarps : nseg;
+  for (int r = share ? blockIdx.y : blockIdx.y * kJoinWarps + warp; r < u.rows;
+       r += share ? kJoinSplit : kJoinSplit * kJoinWarps) {
     auto slot = [&](int s) { return (int64_t(c0 + s * A.hg) * 2 + (s == 0 ? 1 : 0)) * MR + r; };
     float m = -INFINITY;
     for (int s = lane; s < nseg; s += 32) m = fmax_nan(m, A.part_ml[slot(s)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float sh = m == -INFINITY ? 0.f : m;
-    float acc[kMaxD / 32], l = 0.f;
+    float4 acc[kVecs];
+    float l = 0.f;
 #pragma unroll
-    for (int c = 0; c < kMaxD / 32; ++c) acc[c] = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < nseg; ++s) {
-      const float2 ml = A.part_ml[slot(s)];
-      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - sh);  // 0: this part saw nothing
-      l = fmaf(ml.y, f, l);
-      const float* po = A.part_o + slot(s) * A.D;
-#pragma unroll
-      for (int c = 0; c < kMaxD / 32; ++c) {
-        if (c * 32 >= A.D) break;
-        if (c * 32 + lane < A.D) acc[c] = fmaf(po[c * 32 + lane], f, acc[c]);
+    for (int c = 0; c < kVecs; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = first; s0 < end; s0 += 32) {
+      const int parts = min(32, end - s0);
+      float f = 0.f;   // 0: this part saw nothing
+      if (lane < parts) {
+        const float2 ml = A.part_ml[slot(s0 + lane)];
+        f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - sh);
+        l = fmaf(ml.y, f, l);
       }
+      for (int j0 = 0; j0 < parts; j0 += kJoinAhead) {
+        float4 v[kJoinAhead][kVecs];
+#pragma unroll
+        for (int j = 0; j < kJoinAhead; ++j) {
+          const float4* po =
+              reinterpret_cast<const float4*>(A.part_o + slot(s0 + min(j0 + j, parts - 1)) * A.D);
+#pragma unroll
+          for (int c = 0; c < kVecs; ++c)
+            v[j][c] = c * 32 + lane < nvec ? po[c * 32 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int j = 0; j < kJoinAhead; ++j) {
+          const float fj = __shfl_sync(0xffffffffu, f, j0 + j);
+          if (j0 + j >= parts) break;
+#pragma unroll
+          for (int c = 0; c < kVecs; ++c) {
+            acc[c].x = fmaf(v[j][c].x, fj, acc[c].x);
+            acc[c].y = fmaf(v[j][c].y, fj, acc[c].y);
+            acc[c].z = fmaf(v[j][c].z, fj, acc[c].z);
+            acc[c].w = fmaf(v[j][c].w, fj, acc[c].w);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (share) {   // the shares in order
+#pragma unroll
+      for (int c = 0; c < kVecs; ++c) s_acc[warp][c * 32 + lane] = acc[c];
+      if (lane == 0) s_l[warp] = l;
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (int w = 1; w < kJoinWarps; ++w) {
+          l += s_l[w];
+#pragma unroll
+          for (int c = 0; c < kVecs; ++c) {
+            const float4 x = s_acc[w][c * 32 + lane];
+            acc[c].x += x.x;
+            acc[c].y += x.y;
+            acc[c].z += x.z;
+            acc[c].w += x.w;
+          }
+        }
+      }
+      __syncthreads();
+      if (warp != 0) continue;
     }
     const int row = u.row0 + r;
     const int64_t t = u.t_off + row / A.G;
     const int hq = u.h * A.G + row % A.G;
     T* o = static_cast<T*>(A.out) + t * A.o_ts + int64_t(hq) * A.o_hs;
-    const float nan = __int_as_float(0x7fc00000);
     const bool bad = !(m == m);
+    const float inv = bad ? __int_as_float(0x7fc00000) : l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-    for (int c = 0; c < kMaxD / 32; ++c)
-      if (c * 32 + lane < A.D)
-        o[c * 32 + lane] = from_float<T>(bad ? nan : l == 0.f ? 0.f : acc[c] / l);
-    if (lane == 0) A.lse[t * A.Hq + hq] = bad ? nan : sh * kAttnLn2 + logf(l);
+    for (int c = 0; c < kVecs; ++c) {
+      if (c * 32 + lane >= nvec) break;
+      T* to = o + (c * 32 + lane) * 4;
+      to[0] = from_float<T>(acc[c].x * inv);
+      to[1] = from_float<T>(acc[c].y * inv);
+      to[2] = from_float<T>(acc[c].z * inv);
+      to[3] = from_float<T>(acc[c].w * inv);
+    }
+    if (lane == 0) A.lse[t * A.Hq + hq] = bad ? __int_as_float(0x7fc00000) : sh * kAttnLn2 + logf(l);
   }
 }
 

@@ -209,8 +209,14 @@ __device__ AttnPlan attn_plan(const AttnArgs& A) {
   const int pieces = A.ctas / A.hg;
   P.ctas = int(total < pieces ? total : int64_t(pieces));
   const int c = blockIdx.x / A.hg;
-  P.start = c < P.ctas ? total * c / P.ctas : total;
-  P.end = c < P.ctas ? total * (c + 1) / P.ctas : total;
+  // total c / ctas, with short divisions where they do
+  P.start = P.end = total;
+  if (c < P.ctas) {
+    const int64_t each = total <= INT32_MAX ? int32_t(total) / P.ctas : total / P.ctas;
+    const int rest = int(total - each * P.ctas);
+    P.start = each * c + rest * c / P.ctas;
+    P.end = each * (c + 1) + rest * (c + 1) / P.ctas;
+  }
   int64_t base = wt + it - tiles;
   int toff = wr + ir - rows;
   if (P.start < P.end && P.start >= base && P.start < base + tiles) {
@@ -256,7 +262,9 @@ __device__ AttnPlan attn_plan(const AttnArgs& A) {
 
 // The CTA of this one's heads that owns tile x of the line.
 __device__ __forceinline__ int attn_owner(const AttnArgs& A, const AttnPlan& P, int64_t x) {
-  return int(((x + 1) * P.ctas - 1) / P.total) * A.hg + int(blockIdx.x) % A.hg;
+  const int64_t y = (x + 1) * P.ctas - 1;
+  const int piece = y <= INT32_MAX ? int32_t(y) / int32_t(P.total) : int(y / P.total);
+  return piece * A.hg + int(blockIdx.x) % A.hg;
 }
 
 // Address of key p of request b (head 0, K), null where its page is missing.

@@ -324,21 +324,43 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // Rows of a row-major swizzled tile per 64 elements of the head, copies of
       // them 128 / copies rows apart; rows between them stay as they are (what
       // a row of S or O holds reaches no other row).
-      const int apart = kTcMr / s.copies;
-      for (int i = lane / kChunks; i < s.rows * s.copies && ch * 8 < dim; i += kStep) {
-        const int rr = i / s.copies, r = rr + i % s.copies * apart, row = s.row0 + rr;
-        const T* src = q + int64_t(s.t_off + row / A.G) * A.q_ts +
-                       int64_t(s.h * A.G + row % A.G) * A.q_hs + ch * 8;
-        const uint32_t at = uint32_t(qb * C::kQBytes + (ch >> 3) * (kTcMr * 128) + r * 128 +
-                                     (((ch & 7) ^ (r & 7)) << 4));
-        if (A.q_vec) {
-          cp_async16(smem0 + at, src, 16);
-        } else {
-          T* dst = reinterpret_cast<T*>(smem_p + at);
-          for (int x = 0; x < 8; ++x) dst[x] = src[x];
+      // The lanes find the rows' addresses together, and fetch them from one another;
+      // eight loads are under way at once.  No branches (one takes as long as ten
+      // other instructions of a lone warp): lanes without a row repeat the last one.
+      const int apart = kTcMr / s.copies, last = s.rows - 1;
+      auto fill = [&](auto vec) {
+        constexpr int kAhead = 8;
+        for (int r0 = 0; r0 < s.rows; r0 += 32) {
+          const int mine = s.row0 + min(r0 + lane, last);
+          const uint64_t own = reinterpret_cast<uint64_t>(
+              q + int64_t(s.t_off + mine / A.G) * A.q_ts + int64_t(s.h * A.G + mine % A.G) * A.q_hs);
+#pragma unroll 1
+          for (int j0 = 0; j0 < min(32, s.rows - r0); j0 += kAhead * kStep) {
+            uint4 v[kAhead];
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) {
+              const int from = j0 + x * kStep + lane / kChunks;
+              const uint64_t at =
+                  (uint64_t(__shfl_sync(0xffffffffu, uint32_t(own >> 32), from)) << 32) |
+                  __shfl_sync(0xffffffffu, uint32_t(own), from);
+              v[x] = load_chunk<decltype(vec)::value>(reinterpret_cast<const T*>(at) +
+                                                      (PART && ch * 8 >= dim ? 0 : ch * 8));
+            }
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) {
+              const int r = min(r0 + j0 + x * kStep + lane / kChunks, last);
+              unsigned char* to = smem_p + qb * C::kQBytes + (ch >> 3) * (kTcMr * 128) + r * 128;
+              // copies lie 32, 64 or 128 rows apart: the same place in the swizzle
+              const int place = ((ch & 7) ^ (r & 7)) << 4;
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                if (c < s.copies) *reinterpret_cast<uint4*>(to + c * apart * 128 + place) = v[x];
+            }
+          }
         }
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
+      };
+      if (A.q_vec) fill(std::true_type());
+      else fill(std::false_type());
       fence_async_proxy();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&S.qfull[qb]));
