@@ -241,26 +241,33 @@ __global__ void __launch_bounds__(kWtThreads, 1)
               break;
             }
             phase ^= 1;
+            // without branches, which take a lone warp as long as ten other instructions
+            auto fill = [&](auto vec) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll 4
-              for (int j = 0; j < 32; j += kStep) {
-                if (32 * x + j >= padded) break;
-                const int from = j + lane / kChunks, r = 32 * x + from;
-                const uint64_t a =
-                    (uint64_t(__shfl_sync(0xffffffffu, uint32_t(own[x] >> 32), from)) << 32) |
-                    __shfl_sync(0xffffffffu, uint32_t(own[x]), from);
-                if (PART && ch * 8 >= A.D) continue;
-                const T* src = a ? reinterpret_cast<const T*>(a) + ch * 8 : q;
-                const uint32_t off =
-                    (ch >> 3) * (kWtRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-                if (A.q_vec) {
-                  cp_async16(buf_at + off, src, a ? 16u : 0u);
-                } else {
-                  T* dst = reinterpret_cast<T*>(buf + off);
-                  for (int e = 0; e < 8; ++e) dst[e] = a ? src[e] : from_float<T>(0.f);
-                }
-              }
+              for (int x = 0; x < 2; ++x)
+#pragma unroll 1
+                for (int j0 = 0; j0 < min(32, padded - 32 * x); j0 += 8 * kStep)
+#pragma unroll
+                  for (int j = 0; j < 8 * kStep; j += kStep) {
+                    const int from = j0 + j + lane / kChunks, r = 32 * x + from;
+                    const uint64_t a =
+                        (uint64_t(__shfl_sync(0xffffffffu, uint32_t(own[x] >> 32), from)) << 32) |
+                        __shfl_sync(0xffffffffu, uint32_t(own[x]), from);
+                    const T* src = a ? reinterpret_cast<const T*>(a) +
+                                           (PART && ch * 8 >= A.D ? 0 : ch * 8)
+                                     : q;
+                    const uint32_t off =
+                        (ch >> 3) * (kWtRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+                    if (decltype(vec)::value) {
+                      cp_async16(buf_at + off, src, a ? 16u : 0u);
+                    } else {
+                      T* dst = reinterpret_cast<T*>(buf + off);
+                      for (int e = 0; e < 8; ++e) dst[e] = a ? src[e] : from_float<T>(0.f);
+                    }
+                  }
+            };
+            if (A.q_vec) fill(std::true_type());
+            else fill(std::false_type());
             asm volatile("cp.async.wait_all;" ::: "memory");
             fence_async_proxy();
             __syncwarp();
