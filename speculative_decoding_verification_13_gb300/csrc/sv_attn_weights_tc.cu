@@ -1,5 +1,5 @@
 // Accumulated attention weights on the fifth-generation tensor cores, for bf16
-// and fp16 and heads of 64, 128 and 256.
+// and fp16 and heads of 64 to 256, multiples of 16.
 //
 //   score[b][p] += sum over heads h and counted rows r of exp(s - lse[r])
 //
@@ -15,11 +15,16 @@
 //              loads it);
 //   warps 7-9  load the steps' Q, the N of the product, in turn, with each row's
 //              lse and the position of its token; the first also finds the parts
-//              of the piece and announces them.  (One warp, an address per copy:
-//              32 requests with up to 15 drafts took 299 us.)
+//              of the piece and announces them.
 //   warp 6     issues the products into four accumulators in TMEM;
 //   warps 0-3  one position a thread: exp(s - lse) summed over the rows.
 // Every wait is bounded, as in attention.
+//
+// Measured, bf16, 8 KV heads of 128 with 4 query heads each, pages of 16: 32
+// requests of 2001 to 8190 positions with up to 15 drafts 61 us (4.9 TB/s; one row
+// warp with an address per copy 299, three with branches in their loops 70); 24
+// of 500 to 9001, one token, 35 us (4.2 TB/s, of which about 8 us until the first
+// product).
 #include "sv_attn_tc.cuh"
 
 namespace sv {

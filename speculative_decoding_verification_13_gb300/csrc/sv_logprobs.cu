@@ -11,14 +11,16 @@
 // there are few rows (HBM-bound).  Every thread keeps a running maximum m, sum s
 // and weighted sum t = sum e^y y, rescaled when its maximum grows; the row
 // comes through a ring of 32 KB copies, and the maximum of a thread's eight
-// 16-byte vectors of a round decides whether to rescale.  What bounds the pass beside HBM is the issue of instructions, so
-// two elements share an instruction wherever the type allows: y = x c - m c (in
+// 16-byte vectors of a round decides whether to rescale.  What bounds the pass
+// beside HBM is the issue of instructions, so two elements share an instruction
+// wherever the type allows: y = x c - m c (in
 // log2 units) is one packed fma, the rounding of m c being taken out of the sums
 // at the end.  That form has no room for -inf (0 times -inf) and none for
 // products that overflow: a group whose t is not a number is done again with
 // (x - m) taken first and exponents bounded, and so is a row of very large
 // logits; a row of the type's lowest value is then a uniform row.
-// 4096 rows of 151936 in bf16: element by element 266 us.
+// 4096 rows of 151936 in bf16: 233 us with twenty alternatives (5.3 TB/s),
+// 205 us without; element by element 266 us.
 //
 // Alternatives without keeping candidates during the pass: each thread
 // remembers the maximum of each sixteenth of its elements (a cell).  The 4
