@@ -16,10 +16,12 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libspecverify.so")
-SOURCES = ["sv_api.cu", "sv_setup.cu", "sv_rowpass.cu", "sv_finalize.cu", "sv_draw.cu", "sv_noalloc.cu", "sv_kv.cu", "sv_lmhead.cu", "sv_adapt.cu", "sv_greedy.cu",
-           "sv_attn.cu", "sv_attn_tc.cu", "sv_attn_weights_tc.cu",
-           "sv_evict.cu", "sv_logprobs.cu"]
-HEADERS = ["sv_internal.cuh", "sv_select.cuh", "sv_bigrow.cuh", "sv_weights.cuh", "sv_attn.cuh", "sv_tcgen05.cuh", "sv_attn_tc.cuh"]
+SOURCES = ["sv_api.cu", "sv_setup.cu", "sv_rowpass.cu", "sv_finalize.cu", "sv_draw.cu",
+           "sv_noalloc.cu", "sv_kv.cu", "sv_lmhead.cu", "sv_adapt.cu", "sv_greedy.cu",
+           "sv_attn.cu", "sv_attn_tc.cu", "sv_attn_weights_tc.cu", "sv_evict.cu",
+           "sv_logprobs.cu"]
+HEADERS = ["sv_internal.cuh", "sv_select.cuh", "sv_bigrow.cuh", "sv_weights.cuh", "sv_attn.cuh",
+           "sv_tcgen05.cuh", "sv_attn_tc.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
               "--expt-relaxed-constexpr"]
