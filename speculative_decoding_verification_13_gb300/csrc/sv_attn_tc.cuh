@@ -268,6 +268,7 @@ __device__ __forceinline__ void load_tile(const AttnArgs& A, const CUtensorMap& 
   }
   constexpr int kChunks = D / 8, kStep = 32 / kChunks;   // 16-byte chunks of a row, rows a round
   const int ch = lane % kChunks;
+  const char* none = A.spec ? A.spec : A.cache;   // not read, but on 16 bytes
 #pragma unroll
   for (int i = 0; i < kOwn; ++i)
 #pragma unroll 4
@@ -277,9 +278,7 @@ __device__ __forceinline__ void load_tile(const AttnArgs& A, const CUtensorMap& 
                          __shfl_sync(0xffffffffu, uint32_t(own[i]), from);
       if (PART && ch * 8 >= dim) continue;
       cp_async16(dst + (ch >> 3) * (TN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                 a ? reinterpret_cast<const char*>(a) + ch * 16
-                   : reinterpret_cast<const char*>(A.k_per_req),
-                 a ? 16u : 0u);
+                 a ? reinterpret_cast<const char*>(a) + ch * 16 : none, a ? 16u : 0u);
     }
   if (lane == 0) *copied = 1;
   cp_async_arrive(bar);

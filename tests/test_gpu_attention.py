@@ -263,6 +263,31 @@ def test_narrow_heads_split_over_blocks_and_unaligned(dtype, D):
     check(c, out, lse, c.oracle())
 
 
+@pytest.mark.parametrize("S", [8, 16, 64, 128, 24, 5])
+@pytest.mark.parametrize("dtype,D", [(B16, 128), (F16, 64), (B16, 256), (F16, 80)])
+def test_last_tiles_of_every_kind(S, dtype, D):
+    # ends of the cache at, before and behind the edges of tiles, pages and boxes;
+    # lengths and drafts off the 16-byte grid
+    n = [127, 128, 129, 120, 64, 65, 8, 7, 255, 136, 0]
+    k = [0, 3, 0, 15, 1, 7, 2, 0, 1, 8, 5]
+    c = Case(S + D, n, k, 2, 2, D, S, dtype, layers=1)
+    args, sp = c.gpu()
+    wide = torch.zeros(2, len(n) + 1, dtype=torch.int32, device=DEV)
+    wide[0, 1:], wide[1, 1:] = args[3], args[5]
+    args = args[:3] + (wide[0, 1:], args[4], wide[1, 1:])
+    out, lse = sv.attention(*args, sp)
+    want = c.oracle()
+    check(c, out, lse, want)
+    score = torch.zeros(len(n), 300)
+    truth = torch.as_tensor(want[1], dtype=torch.float32)
+    ref = oa.weights(c.q, c.cache, c.layer, n, c.table, k, truth, score, c.spec)
+    got = sv.attention_weights(*args, truth.to(DEV), score.to(DEV), sp)
+    f = np.isfinite(want[1])
+    rel = 2 * score_error(c, float(want[3][f].max())) + 2.0 ** -22 * np.abs(want[1][f]).max()
+    tol = (rel + (16 * 4 + 4) * 2.0 ** -24) * ref + 1e-30
+    assert (np.abs(got.double().cpu().numpy() - ref) <= tol).all()
+
+
 def test_data_errors_fail_their_request_only():
     c = Case(8, [40, 100, 30, 20], [1, 2, 0, 3], 2, 2, 128, 16, B16)
     want = c.oracle()
