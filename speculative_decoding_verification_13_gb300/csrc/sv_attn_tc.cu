@@ -53,7 +53,7 @@
 // products land, and TMEM is freed.
 //
 // Measured, bf16, 8 KV heads of 128 with 4 query heads each, pages of 16: 64
-// requests of 1 to 16000 positions, one token, 88 us with the join (4.7 TB/s); 32
+// requests of 1 to 16000 positions, one token, 82 us with the join (5.1 TB/s); 32
 // of 2001 to 8190 with up to 15 drafts 115 us (5.3 TB/s); one of 900 positions 18
 // us, all of it latency.  fp16, 16 heads of 64, 3 requests of 100001 to 131071
 // positions and 7 drafts, pages of 64: 225 to 229 us (6.6 TB/s).  What the first two lose to the HBM's rate is the
@@ -84,10 +84,11 @@ struct Stage {
 constexpr size_t kStageBytes = (sizeof(Stage) + 127) / 128 * 128;
 
 // What a unit costs beside its tiles, in tiles: the line that is cut over the
-// CTAs counts it (64 requests of 1 to 16000 positions without it: the CTA with
-// the most short ones took twice as long as the others).
+// CTAs counts it.  64 requests of 1 to 16000 positions: without it the CTA with the
+// most short ones took twice as long as the others; with 2 tiles 158000 cycles
+// against 127000 (88 us), a unit costing about 3.5 of 2200; with 4 82 us, as with 6.
 template <int D>
-constexpr int kUnitTiles = D == 64 ? 3 : 2;
+constexpr int kUnitTiles = D == 64 ? 3 : 4;
 
 template <int D>
 struct Shape {
@@ -781,13 +782,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (active) {
             float* to = stage.o + (copy * s.rows + rr) * (cols + 1);
 #pragma unroll 1
-            for (int c = 0; c < cols; c += 16) {
-              uint32_t o[16];
-              tmem_ld16(lanes + C::kOCol + c0 + c, o);
+            for (int c = 0; c < cols; c += 32) {   // 32 columns fit whatever the rows
+              uint32_t o[32];
+              tmem_ld32(lanes + C::kOCol + c0 + c, o);
               tmem_ld_wait();
               if (live) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) to[c + e] = __uint_as_float(o[e]) * f;
+                for (int e = 0; e < 32; ++e) to[c + e] = __uint_as_float(o[e]) * f;
               }
             }
           }
