@@ -20,16 +20,17 @@
 // Measured, bf16, 36 layers of 2 x 1024 elements, pages of 16, 4 requests of 3001
 // to 9003 positions cut to 2000, in place: 394 us, of which the move 6.0 TB/s.  One
 // of 1041 positions cut to 512, 4 layers: 16 us, most of it the select's chain of
-// four histograms.  Two of 7111 to 30965 cut to 11: 43 us, with one position a
-// thread and round 50, with the first digit's equal counts of a warp added up by a
-// match first 49.
+// four histograms.  Positions a thread and round of the select: 1, 2, 4 and
+// 8 take it 9.9, 8.7, 10.5 and 13.4 us at 1041 positions, 20, 18, 19 and 21 at
+// 9003, the call 50, 47 and 43 us (1, 2, 4) at 30965.  Adding up a warp's equal
+// first digits by a match before the histogram cost 6 us there.
 #include "sv_internal.cuh"
 
 namespace sv {
 namespace {
 
 constexpr int kSelThreads = 1024;
-constexpr int kSelEach = 4;     // positions of a thread per round
+constexpr int kSelEach = 2;     // positions of a thread per round
 constexpr int kMoveThreads = 256;
 constexpr int kMoveBatch = 8;
 
