@@ -129,6 +129,7 @@ struct TcShared {
   int first_bad;
   int bad[kSegs];    // the part needs a missing page
   int copied[11];    // per slot: filled by the lanes' copies, not by the copy engine
+  uint32_t signs[2][8];  // per column: +inf, -inf among the part's values
   int dirty[kBufs];  // per S buffer: 1 + the tile whose V holds a non-finite value
 };
 
@@ -198,6 +199,13 @@ __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t addr, uint32_t block)
          (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
+
+// Bit 0: a value is +inf, bit 1: it is -inf; both: NaN.
+template <class T>
+__device__ __forceinline__ uint32_t value_signs(uint32_t x) {
+  if ((x & Bits<T>::kExp1) != Bits<T>::kExp1) return 0;
+  return (x & Bits<T>::kMan1) ? 3u : (x & 0x8000u) ? 2u : 1u;
+}
 
 // Hardware barrier of the softmax warps, and the same with one truth value for
 // all of them.  None may stay away: they leave their loop only together.
@@ -708,116 +716,180 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         *t = int64_t(s.t_off) + x / A.G;
         *hq = s.h * A.G + x % A.G;
       };
-      if (s.copies == 1) {
-        const float inv = bad ? nan : total == 0.f ? 0.f : 1.f / total;
-        int64_t trow;
-        int hq;
-        place(rr, &trow, &hq);
-        if (active) {
-#pragma unroll 1
-          for (int c = 0; c * 32 < dim; ++c) {
-            uint32_t o[32];
-            tmem_ld32(lanes + C::kOCol + c * 32, o);
-            tmem_ld_wait();
-            if (!live) continue;
-            if (s.whole) {
-              T* out = static_cast<T*>(A.out) + trow * A.o_ts + int64_t(hq) * A.o_hs + c * 32;
-              uint32_t w[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                w[e] = Bits<T>::pack(__uint_as_float(o[2 * e]) * inv,
-                                     __uint_as_float(o[2 * e + 1]) * inv);
-              if (A.out_vec) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  if (PART && c * 32 + e * 8 >= dim) break;
-                  *reinterpret_cast<uint4*>(out + e * 8) =
-                      make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-                }
-              } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  if (PART && c * 32 + e >= dim) break;
-                  const uint16_t h = uint16_t(w[e / 2] >> (16 * (e & 1)));
-                  out[e] = *reinterpret_cast<const T*>(&h);
-                }
-              }
-            } else {
-              uint4* po = reinterpret_cast<uint4*>(A.part_o + (pr + rr) * dim + c * 32);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                if (PART && c * 32 + e * 4 >= dim) break;
-                po[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-              }
-            }
-          }
+      // Weights that are 0 in M's other copies, or too small for the type, times an
+      // infinite value give NaN where the formula gives the infinity.  So where a
+      // row of proper weights has NaN, the part's values are looked through once
+      // more, and what their signs say takes its place.  Tiles [in0, in1) are seen
+      // by every row; what the others hold is looked up row by row.  Looking for
+      // NaN costs 1 % with 15 drafts (115.4 -> 116.9 us).
+      const int part0 = s.R.tile0 + s.first, part1 = part0 + s.count;
+      const int in0 = max(part0, (all_lo + TN - 1) / TN);
+      const int in1 = max(in0, min(part1, all_hi / TN));
+      auto value_of = [&](int p) -> const uint16_t* {
+        int64_t v_off;
+        const char* k = attn_key(A, s.b, s.R.n, p, &v_off);
+        return k ? reinterpret_cast<const uint16_t*>(k + v_off) + int64_t(s.h) * dim : nullptr;
+      };
+      auto settle = [&](float v, int r, int d) {
+        if (!isnan(v)) return v;
+        uint32_t seen = ((S.signs[0][d >> 5] >> (d & 31)) & 1) |
+                        (((S.signs[1][d >> 5] >> (d & 31)) & 1) << 1);
+        const int row_at = s.R.at0 + (s.row0 + r) / A.G;
+        const int lo = max(part0 * TN, A.window > 0 ? max(0, row_at - A.window + 1) : 0);
+        const int hi = min(part1 * TN, min(row_at + 1, s.R.hi));
+        for (int p = lo; p < hi; ++p) {
+          if (p == in0 * TN) p = in1 * TN;
+          const uint16_t* x = p < hi ? value_of(p) : nullptr;
+          if (x) seen |= value_signs<T>(x[d]);
         }
-      } else {
-        // The copies' sums and outputs add up at their common maximum, as many
-        // columns of O at a time as fit; all threads then write them.
-        Stage& stage = *reinterpret_cast<Stage*>(
-            smem_p + (C::kOwnStage ? C::kQBufs * C::kQBytes + C::kSlots * kSlotBytes
-                                   : unit % C::kQBufs * C::kQBytes));
-        stage.ml[tid] = make_float2(m, l);
-        softmax_sync();
-        for (int c = 0; c < s.copies; ++c) top = fmaxf(top, stage.ml[rr + c * apart].x);
-        total = 0.f;
-        for (int c = 0; c < s.copies; ++c) {
-          const float2 x = stage.ml[rr + c * apart];
-          if (x.x > -INFINITY || x.y != x.y) total = fmaf(x.y, ex2_approx(x.x - top), total);
-        }
-        const float f = m > -INFINITY ? ex2_approx(m - top) : 0.f;
-        if (live && copy == 0) {
-          int64_t t;
+        return seen == 1 ? INFINITY : seen == 2 ? -INFINITY : v;
+      };
+      bool staged = s.copies > 1, settled = false;
+      for (;;) {
+        bool odd = false;   // a value of this thread's that is no number
+        if (!staged) {
+          const float inv = bad ? nan : total == 0.f ? 0.f : 1.f / total;
+          int64_t trow;
           int hq;
-          place(rr, &t, &hq);
-          stage.out[rr] = t * A.o_ts + int64_t(hq) * A.o_hs;
-          stage.inv[rr] = bad ? nan : total == 0.f ? 0.f : 1.f / total;
-        }
-        int cols = D;
-        while (s.rows * s.copies * (cols + 1) > kStageFloats) cols >>= 1;
-        const int half = cols / 2, shift = 31 - __clz(half);
-#pragma unroll 1
-        for (int c0 = 0; c0 < dim; c0 += cols) {
+          place(rr, &trow, &hq);
           if (active) {
-            float* to = stage.o + (copy * s.rows + rr) * (cols + 1);
 #pragma unroll 1
-            for (int c = 0; c < cols; c += 32) {   // 32 columns fit whatever the rows
+            for (int c = 0; c * 32 < dim; ++c) {
               uint32_t o[32];
-              tmem_ld32(lanes + C::kOCol + c0 + c, o);
+              tmem_ld32(lanes + C::kOCol + c * 32, o);
               tmem_ld_wait();
-              if (live) {
+              if (!live) continue;
+              bool any = false;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) to[c + e] = __uint_as_float(o[e]) * f;
-              }
-            }
-          }
-          softmax_sync();
-          for (int i = tid; i < s.rows * half; i += 128) {
-            const int r = i >> shift, e = (i & (half - 1)) * 2;
-            if (PART && c0 + e >= dim) continue;
-            float v0 = 0.f, v1 = 0.f;
-            for (int k = 0; k < s.copies; ++k) {
-              const float* from = stage.o + (k * s.rows + r) * (cols + 1) + e;
-              v0 += from[0];
-              v1 += from[1];
-            }
-            if (s.whole) {
-              T* out = static_cast<T*>(A.out) + stage.out[r] + c0 + e;
-              const uint32_t w = Bits<T>::pack(v0 * stage.inv[r], v1 * stage.inv[r]);
-              if (A.out_vec) {
-                *reinterpret_cast<uint32_t*>(out) = w;
+              for (int e = 0; e < 32; ++e)
+                any |= !(PART && c * 32 + e >= dim) && isnan(__uint_as_float(o[e]));
+              odd |= any && inv == inv;
+              if (s.whole) {
+                T* out = static_cast<T*>(A.out) + trow * A.o_ts + int64_t(hq) * A.o_hs + c * 32;
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  w[e] = Bits<T>::pack(__uint_as_float(o[2 * e]) * inv,
+                                       __uint_as_float(o[2 * e + 1]) * inv);
+                if (A.out_vec) {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    if (PART && c * 32 + e * 8 >= dim) break;
+                    *reinterpret_cast<uint4*>(out + e * 8) =
+                        make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                  }
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) {
+                    if (PART && c * 32 + e >= dim) break;
+                    const uint16_t h = uint16_t(w[e / 2] >> (16 * (e & 1)));
+                    out[e] = *reinterpret_cast<const T*>(&h);
+                  }
+                }
               } else {
-                const uint16_t h0 = uint16_t(w), h1 = uint16_t(w >> 16);
-                out[0] = *reinterpret_cast<const T*>(&h0);
-                out[1] = *reinterpret_cast<const T*>(&h1);
+                uint4* po = reinterpret_cast<uint4*>(A.part_o + (pr + rr) * dim + c * 32);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  if (PART && c * 32 + e * 4 >= dim) break;
+                  po[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                }
               }
-            } else {
-              *reinterpret_cast<float2*>(A.part_o + (pr + r) * dim + c0 + e) = make_float2(v0, v1);
             }
           }
+        } else {
+          // The copies' sums and outputs add up at their common maximum, as many
+          // columns of O at a time as fit; all threads then write them.
+          Stage& stage = *reinterpret_cast<Stage*>(
+              smem_p + (C::kOwnStage ? C::kQBufs * C::kQBytes + C::kSlots * kSlotBytes
+                                     : unit % C::kQBufs * C::kQBytes));
+          stage.ml[tid] = make_float2(m, l);
           softmax_sync();
+          for (int c = 0; c < s.copies; ++c) top = fmaxf(top, stage.ml[rr + c * apart].x);
+          total = 0.f;
+          for (int c = 0; c < s.copies; ++c) {
+            const float2 x = stage.ml[rr + c * apart];
+            if (x.x > -INFINITY || x.y != x.y) total = fmaf(x.y, ex2_approx(x.x - top), total);
+          }
+          const float f = m > -INFINITY ? ex2_approx(m - top) : 0.f;
+          if (live && copy == 0) {
+            int64_t t;
+            int hq;
+            place(rr, &t, &hq);
+            stage.out[rr] = t * A.o_ts + int64_t(hq) * A.o_hs;
+            stage.inv[rr] = bad ? nan : total == 0.f ? 0.f : 1.f / total;
+          }
+          int cols = D;
+          while (s.rows * s.copies * (cols + 1) > kStageFloats) cols >>= 1;
+          const int half = cols / 2, shift = 31 - __clz(half);
+#pragma unroll 1
+          for (int c0 = 0; c0 < dim; c0 += cols) {
+            if (active) {
+              float* to = stage.o + (copy * s.rows + rr) * (cols + 1);
+#pragma unroll 1
+              for (int c = 0; c < cols; c += 32) {   // 32 columns fit whatever the rows
+                uint32_t o[32];
+                tmem_ld32(lanes + C::kOCol + c0 + c, o);
+                tmem_ld_wait();
+                if (live) {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) to[c + e] = __uint_as_float(o[e]) * f;
+                }
+              }
+            }
+            softmax_sync();
+            for (int i = tid; i < s.rows * half; i += 128) {
+              const int r = i >> shift, e = (i & (half - 1)) * 2;
+              if (PART && c0 + e >= dim) continue;
+              float v0 = 0.f, v1 = 0.f;
+              for (int k = 0; k < s.copies; ++k) {
+                const float* from = stage.o + (k * s.rows + r) * (cols + 1) + e;
+                v0 += from[0];
+                v1 += from[1];
+              }
+              if ((isnan(v0) || isnan(v1)) && stage.inv[r] == stage.inv[r]) {
+                if (settled) {
+                  v0 = settle(v0, r, c0 + e);
+                  v1 = settle(v1, r, c0 + e + 1);
+                }
+                odd = true;
+              }
+              if (s.whole) {
+                T* out = static_cast<T*>(A.out) + stage.out[r] + c0 + e;
+                const uint32_t w = Bits<T>::pack(v0 * stage.inv[r], v1 * stage.inv[r]);
+                if (A.out_vec) {
+                  *reinterpret_cast<uint32_t*>(out) = w;
+                } else {
+                  const uint16_t h0 = uint16_t(w), h1 = uint16_t(w >> 16);
+                  out[0] = *reinterpret_cast<const T*>(&h0);
+                  out[1] = *reinterpret_cast<const T*>(&h1);
+                }
+              } else {
+                *reinterpret_cast<float2*>(A.part_o + (pr + r) * dim + c0 + e) =
+                    make_float2(v0, v1);
+              }
+            }
+            if (c0 + cols < dim) softmax_sync();   // the last columns: the barrier below
+          }
         }
+        if (settled || !softmax_any(odd)) break;
+        // signs of the infinite and NaN values that every row sees
+        if (tid < 2 * D / 32) S.signs[tid / (D / 32)][tid % (D / 32)] = 0;
+        softmax_sync();
+        for (int p = in0 * TN + tid; p < in1 * TN; p += 128) {
+          const uint4* v = reinterpret_cast<const uint4*>(value_of(p));
+          for (int c = 0; v && c < dim / 8; ++c) {
+            const uint4 x = v[c];
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t seen = value_signs<T>(w[i / 2] >> (16 * (i & 1)));
+              const int d = c * 8 + i;
+              if (seen & 1) atomicOr(&S.signs[0][d >> 5], 1u << (d & 31));
+              if (seen & 2) atomicOr(&S.signs[1][d >> 5], 1u << (d & 31));
+            }
+          }
+        }
+        softmax_sync();
+        staged = settled = true;
       }
       if (live && copy == 0) {
         int64_t trow;

@@ -47,3 +47,65 @@ def test_a_key_of_weight_zero_leaves_the_score(dtype, k, G, sign):
     tol = (rel + ((k + 1) * 2 * G + 4) * 2.0 ** -24) * ref + 1e-30
     assert np.isfinite(got).all()
     assert (np.abs(got - ref) <= tol).all()
+
+
+def expect(c, out, lse, window=0):
+    """Checks against the oracle; what is not finite there has to be the same here."""
+    with np.errstate(invalid="ignore"):
+        o, l, mag, size = c.oracle(window=window)
+    got = out.double().cpu().numpy()
+    assert np.isfinite(l).all()
+    fine = np.isfinite(o)
+    assert not fine.all()
+    assert np.array_equal(got[~fine], o[~fine], equal_nan=True)
+    assert np.isfinite(got[fine]).all()
+    clean = torch.where(torch.as_tensor(fine), out.cpu(), torch.zeros((), dtype=out.dtype))
+    check(c, clean, lse, [np.where(fine, o, 0), l, np.where(fine, mag, 0), size])
+
+
+def put(c, b, p, d, v):
+    c.cache[c.table[b, p // c.cache.shape[3]], c.layer, 1, p % c.cache.shape[3], d] = v
+
+
+# rows a head: 4 lie four times in the product, 52 twice, 128 and 132 once or in two tiles
+@pytest.mark.parametrize("k,G", [(0, 4), (12, 4), (31, 4), (32, 4)])
+@pytest.mark.parametrize("dtype,D,S", [(B16, 128, 16), (F16, 64, 5), (B16, 256, 64), (F16, 80, 16),
+                                       (F32, 64, 16)])
+def test_infinite_values_in_inner_tiles(dtype, D, S, k, G):
+    c = Case(22, [700, 40], [k, 0], 2, G, D, S, dtype)
+    put(c, 0, 130, 3, math.inf)
+    put(c, 0, 200, 5, -math.inf)
+    put(c, 0, 310, 7, math.nan)
+    put(c, 0, 150, 9, math.inf)        # both signs, and one sign in several places
+    put(c, 0, 420, 9, -math.inf)
+    for p in (7, 260, 300, 500):
+        put(c, 0, p, D - 1, -math.inf)
+        put(c, 0, p, D + 4, math.inf)  # the other head
+    args, sp = c.gpu()
+    expect(c, *sv.attention(*args, sp))
+
+
+@pytest.mark.parametrize("dtype,D", [(B16, 128), (F16, 64)])
+@pytest.mark.parametrize("k", [0, 15])
+def test_infinite_values_of_a_long_request(dtype, D, k):
+    # the request lies in parts over many blocks
+    c = Case(23, [9001], [k], 1, 2, D, 16, dtype, layers=1, junk=False)
+    put(c, 0, 4000, 1, math.inf)
+    put(c, 0, 8999, 2, -math.inf)
+    put(c, 0, 77, 3, math.inf)
+    put(c, 0, 6000, 3, math.inf)
+    put(c, 0, 20, 4, math.nan)
+    args, sp = c.gpu()
+    expect(c, *sv.attention(*args, sp))
+
+
+def test_an_infinite_value_of_little_weight_in_half_precision():
+    # a weight of e^-25, below the smallest number of fp16
+    c = Case(24, [600], [0], 1, 4, 64, 16, F16, layers=1)
+    c.cache[..., 0, :, 0] = 0
+    c.q[..., 0] = 8
+    c.q[..., 1:] *= 0.1
+    put(c, 0, 200, 6, math.inf)
+    c.cache[c.table[0, 200 // 16], 0, 0, 200 % 16, 0] = -25
+    args, sp = c.gpu()
+    expect(c, *sv.attention(*args, sp))
