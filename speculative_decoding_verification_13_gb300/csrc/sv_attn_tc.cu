@@ -526,7 +526,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) plus[i] = minus[i] = 0;
             const uint32_t* vw = reinterpret_cast<const uint32_t*>(v);
-            for (int c = 0; live && copy == 0 && c < TN; ++c) {
+            // each copy has the signs of its own columns: one without weight has none
+            for (int c = copy * (TN / s.copies); live && c < (copy + 1) * (TN / s.copies); ++c) {
               if (p0 + c < row_lo || p0 + c >= row_hi) continue;
 #pragma unroll
               for (int i = 0; i < D / 32; ++i)

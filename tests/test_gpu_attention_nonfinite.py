@@ -109,3 +109,16 @@ def test_an_infinite_value_of_little_weight_in_half_precision():
     c.cache[c.table[0, 200 // 16], 0, 0, 200 % 16, 0] = -25
     args, sp = c.gpu()
     expect(c, *sv.attention(*args, sp))
+
+
+@pytest.mark.parametrize("dtype,D", [(B16, 128), (F16, 64), (B16, 256), (F32, 64)])
+@pytest.mark.parametrize("k,G", [(0, 4), (9, 4)])
+def test_infinite_values_that_only_the_last_columns_of_a_tile_see(dtype, D, k, G):
+    # a window that leaves the first columns of the only tile to nobody
+    c = Case(25, [100, 127], [k, 0], 2, G, D, 16, dtype)
+    put(c, 0, 97, 3, math.inf)
+    put(c, 0, 96, 4, -math.inf)
+    put(c, 1, 120, 5, math.nan)
+    put(c, 1, 40, 6, math.inf)         # in front of the window: seen by none
+    args, sp = c.gpu()
+    expect(c, *sv.attention(*args, sp, window=15), window=15)
