@@ -53,12 +53,13 @@ class Loop:
         self.spec = torch.zeros(B, k + 1, layers, 2, E, dtype=dtype, device=device)
 
     def draft(self):
-        """k drafts a request, one after the other, and the drafter's logits."""
+        """k drafts a request, one after the other, and the logits they are drawn from, in
+        the type that verification takes: it compares with the distribution of the draw."""
         u = torch.rand(self.B, self.k, device=self.dev, generator=self.g)
         one = torch.ones_like(self.k_per_req)
         tokens, logits, last = [], [], self.last
         for i in range(self.k):
-            x = self.embed[last.long()].float() @ self.drafter
+            x = (self.embed[last.long()].float() @ self.drafter).to(self.dtype)
             last = sv.draft_sample(x, one, self.temperature, u[:, i].contiguous())[0]
             tokens.append(last.clone())
             logits.append(x)
@@ -86,7 +87,7 @@ class Loop:
         drafts, draft_logits = self.draft()
         logits, kept = self.target(torch.cat([self.last[:, None], drafts], 1))
         uniforms = torch.rand(logits.shape[0], device=self.dev, generator=self.g)
-        accept, tokens = sv.verify(logits, draft_logits.reshape(-1, self.vocab).to(self.dtype),
+        accept, tokens = sv.verify(logits, draft_logits.reshape(-1, self.vocab),
                                    drafts.reshape(-1), self.k_per_req, self.temperature, uniforms)
         scored = sv.logprobs(logits, tokens, n_top=4)   # -1 past the last emitted: skipped
         for i, (q, lse) in enumerate(kept):

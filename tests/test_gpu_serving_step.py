@@ -52,3 +52,29 @@ def test_a_gradient_step_raises_the_emitted_tokens():
         ok = tokens >= 0
         again = sv.logprobs(loop.learnt_from @ loop.drafter, tokens)
         assert again.logprob[ok].sum() > learnt.logprob[ok].sum()
+
+
+def test_drafts_come_from_the_logits_that_verification_gets(monkeypatch):
+    # acceptance compares the target with the distribution the drafts were drawn from
+    import serving_step
+    import speculative_decoding_verification_13_gb300 as sv
+    loop = serving_step.Loop(seed=2)
+    drawn, verified = [], []
+    sample, verify = sv.draft_sample, sv.verify
+
+    def sample_and_note(logits, *a, **kw):
+        drawn.append(logits.float().clone())
+        return sample(logits, *a, **kw)
+
+    def verify_and_note(target, draft, *a, **kw):
+        verified.append(draft.float().clone())
+        return verify(target, draft, *a, **kw)
+
+    monkeypatch.setattr(sv, "draft_sample", sample_and_note)
+    monkeypatch.setattr(sv, "verify", verify_and_note)
+    for _ in range(3):
+        loop.step(rate=0.3)
+        seen = torch.stack(drawn, 1).reshape(-1, loop.vocab)
+        assert torch.equal(seen, verified[-1])
+        drawn.clear()
+    assert verified[-1].abs().max() > 0
