@@ -15,6 +15,7 @@ from __future__ import annotations
 import collections
 import ctypes
 import math
+import threading
 
 import torch
 
@@ -64,6 +65,10 @@ def _library():
 
 
 # ----------------------------------------------------------- streams, workspaces
+# A call's kernels talk through its workspace, which is its stream's: from the
+# choice of the workspace to the last launch there is one call at a time, whatever
+# thread it comes from (the interpreter's own lock is given away in the C call).
+_lock = threading.Lock()
 _workspaces = {}   # (kind, device, stream) -> workspace: calls of one stream are in order
 _last = {}         # (kind, device) -> (workspace, stream handle, stream) of the last call
 _sizes = {}        # workspace sizes already asked for
@@ -115,11 +120,12 @@ def _scratch(kind, dev, stream, handle, size):
 def _error(kind, stream, device):
     d = torch.device(device or "cuda")
     index = d.index if d.index is not None else torch.cuda.current_device()
-    ws, handle, _ = _last[kind, index]
     code, req, row = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int64()
-    rc = _library().spec_verify_get_error(ws.data_ptr(), handle if stream is None else
-                                          stream.cuda_stream, ctypes.byref(code),
-                                          ctypes.byref(req), ctypes.byref(row))
+    with _lock:
+        ws, handle, _ = _last[kind, index]
+        rc = _library().spec_verify_get_error(ws.data_ptr(), handle if stream is None else
+                                              stream.cuda_stream, ctypes.byref(code),
+                                              ctypes.byref(req), ctypes.byref(row))
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_verify_get_error")
     return code.value, req.value, row.value
@@ -134,6 +140,14 @@ def _call(name, dev, *args):
             rc = f(*args)
     if rc != SV_OK:
         raise SpecVerifyError(rc, name)
+
+
+def _launch(kind, dev, stream, size, args, batch=()):
+    """spec_<kind> on the stream, with its workspace."""
+    handle = _stream_of(stream, dev)
+    with _lock:
+        ws = _scratch(kind, dev, stream, handle, size)
+        _call("spec_" + kind, dev, *args, handle, *batch, ws.data_ptr(), ws.numel())
 
 
 # --------------------------------------------------------------------- checks
@@ -271,10 +285,7 @@ def attention(q, cache, layer, kv_len, block_table, k_per_req, spec=None, *, sca
         out_lse = _empty((rows, Hq), torch.float32, dev, stream)
     else:
         _matrix(out_lse, "out_lse", torch.float32, (rows, Hq), dev)
-    handle = _stream_of(stream, dev)
-    ws = _scratch("attention", dev, stream, handle, (B, D))
-    _call("spec_attention", dev, *args, out.data_ptr(), out_lse.data_ptr(), handle, B,
-          ws.data_ptr(), ws.numel())
+    _launch("attention", dev, stream, (B, D), (*args, out.data_ptr(), out_lse.data_ptr()), (B,))
     return out, out_lse
 
 
@@ -298,10 +309,8 @@ def attention_weights(q, cache, layer, kv_len, block_table, k_per_req, lse, scor
     o_ptr, out_stride, out_cols = _rows2d(out_score, "out_score", torch.float32, B, dev)
     if out_cols != cols:
         raise ValueError("score and out_score must have the same columns")
-    handle = _stream_of(stream, dev)
-    ws = _scratch("attention_weights", dev, stream, handle, (B,))
-    _call("spec_attention_weights", dev, *args, l_ptr, a_ptr, s_ptr, stride, o_ptr, out_stride,
-          cols, handle, B, ws.data_ptr(), ws.numel())
+    _launch("attention_weights", dev, stream, (B,),
+            (*args, l_ptr, a_ptr, s_ptr, stride, o_ptr, out_stride, cols), (B,))
     return out_score
 
 
@@ -348,11 +357,9 @@ def kv_evict(cache, score, kv_len, block_table, budget, sinks=0, recent=0, *, ou
         out_kept = _empty((B, budget), torch.int32, dev, stream)
     k_ptr = None if out_kept is None else _matrix(out_kept, "out_kept", torch.int32, (B, budget),
                                                   dev)
-    handle = _stream_of(stream, dev)
-    ws = _scratch("kv_evict", dev, stream, handle, (B, budget))
-    _call("spec_kv_evict", dev, ctypes.byref(desc), t_ptr, cols, out_desc, ot_ptr, ot_cols, s_ptr,
-          stride, score_cols, os_ptr, out_stride, out_cols, n_ptr, m_ptr, budget, sinks, recent,
-          k_ptr, handle, B, ws.data_ptr(), ws.numel())
+    _launch("kv_evict", dev, stream, (B, budget),
+            (ctypes.byref(desc), t_ptr, cols, out_desc, ot_ptr, ot_cols, s_ptr, stride, score_cols,
+             os_ptr, out_stride, out_cols, n_ptr, m_ptr, budget, sinks, recent, k_ptr), (B,))
     return out_len, out_kept
 
 
@@ -392,11 +399,9 @@ def logprobs(logits, tokens, temperature=None, n_top=0, *, stream=None):
         tok = _empty((R, n_top), torch.int32, dev, stream)
         top = _empty((R, n_top), torch.float32, dev, stream)
         tok_ptr, top_ptr = tok.data_ptr(), top.data_ptr()
-    handle = _stream_of(stream, dev)
-    ws = _scratch("logprobs", dev, stream, handle, (R,))
-    _call("spec_logprobs", dev, ctypes.byref(x), t_ptr, T_ptr, n_top, lp.data_ptr(),
-          ent.data_ptr(), mx.data_ptr(), ls.data_ptr(), tok_ptr, top_ptr, handle, ws.data_ptr(),
-          ws.numel())
+    _launch("logprobs", dev, stream, (R,),
+            (ctypes.byref(x), t_ptr, T_ptr, n_top, lp.data_ptr(), ent.data_ptr(), mx.data_ptr(),
+             ls.data_ptr(), tok_ptr, top_ptr))
     return LogProbs(lp, ent, mx, ls, tok, top)
 
 
