@@ -404,7 +404,9 @@ int spec_adapt_k(const int32_t* accept_len, const int32_t* k_used, double* succ,
  * row of a request that needs a page missing from its block table
  * (SV_ERR_DATA_PAGE).  Results do not depend on the batch's order in time:
  * sums have a fixed order on a given device.  Same ownership, stream and
- * error conventions as spec_verify. */
+ * error conventions as spec_verify; a call of this and the following entries
+ * with batch (rows) 0 launches nothing and leaves the workspace as it is, so
+ * that there is no error of it to read. */
 size_t spec_attention_workspace_size(int32_t batch, int32_t head_dim);
 
 int spec_attention(const sv_kv_cache* cache, int32_t dtype, int32_t layer, int32_t kv_heads,

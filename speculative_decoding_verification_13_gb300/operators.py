@@ -70,7 +70,8 @@ def _library():
 # thread it comes from (the interpreter's own lock is given away in the C call).
 _lock = threading.Lock()
 _workspaces = {}   # (kind, device, stream) -> workspace: calls of one stream are in order
-_last = {}         # (kind, device) -> (workspace, stream handle, stream) of the last call
+_last = {}         # (kind, device) -> (workspace, stream handle) of the last call; the
+                   # workspace is None for a call with nothing to do, which wrote none
 _sizes = {}        # workspace sizes already asked for
 
 
@@ -113,7 +114,6 @@ def _scratch(kind, dev, stream, handle, size):
         ws = _empty(max(need, 256), torch.uint8, dev, stream)
         if not capturing:
             _workspaces[key] = ws
-    _last[kind, dev.index] = ws, handle, stream
     return ws
 
 
@@ -122,7 +122,9 @@ def _error(kind, stream, device):
     index = d.index if d.index is not None else torch.cuda.current_device()
     code, req, row = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int64()
     with _lock:
-        ws, handle, _ = _last[kind, index]
+        ws, handle = _last[kind, index]
+        if ws is None:
+            return 0, -1, -1
         rc = _library().spec_verify_get_error(ws.data_ptr(), handle if stream is None else
                                               stream.cuda_stream, ctypes.byref(code),
                                               ctypes.byref(req), ctypes.byref(row))
@@ -148,6 +150,8 @@ def _launch(kind, dev, stream, size, args, batch=()):
     with _lock:
         ws = _scratch(kind, dev, stream, handle, size)
         _call("spec_" + kind, dev, *args, handle, *batch, ws.data_ptr(), ws.numel())
+        # size[0] counts the requests or rows
+        _last[kind, dev.index] = ws if size[0] else None, handle
 
 
 # --------------------------------------------------------------------- checks
