@@ -399,8 +399,8 @@ int spec_adapt_k(const int32_t* accept_len, const int32_t* k_used, double* succ,
  *              aligned (its size depends on the current device's SM count)
  * A k outside [0, SV_MAX_K] or sum (k + 1) != rows fails the whole batch
  * (SV_ERR_DATA_K / SV_ERR_DATA_ROWS, every output NaN).  A request whose
- * kv_len is negative or above max_pages * page_size (SV_ERR_DATA_LENGTH) or
- * with more than spec_slots tokens (SV_ERR_DATA_K) gets NaN rows; so does a
+ * kv_len is negative or above max_pages * page_size, or of more than 2^31 - 256
+ * positions with its tokens (SV_ERR_DATA_LENGTH), or with more than spec_slots tokens (SV_ERR_DATA_K) gets NaN rows; so does a
  * row of a request that needs a page missing from its block table
  * (SV_ERR_DATA_PAGE).  Results do not depend on the batch's order in time:
  * sums have a fixed order on a given device.  Same ownership, stream and

@@ -130,7 +130,7 @@ int attn_args(const sv_kv_cache* cache, int32_t dtype, int32_t layer, int32_t kv
   A.Hkv = kv_heads;
   A.G = q_heads / kv_heads;
   A.D = D;
-  A.window = window;
+  A.window = window < kMaxPositions ? window : 0;  // a wider one hides nothing
   A.Rt = rows;
   A.scale2 = scale * 1.4426950408889634f;
   *out = A;

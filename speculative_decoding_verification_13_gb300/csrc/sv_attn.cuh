@@ -26,6 +26,10 @@
 
 namespace sv {
 
+// Positions of a request, at most: a tile's end, and a window's start for a token
+// up to 32 positions before the first, stay within 32 bits.
+constexpr int32_t kMaxPositions = INT32_MAX - 255;
+
 struct AttnSplit {  // a unit begun by this CTA and continued by later ones
   int32_t valid, last;            // last: the CTA that ends it
   int32_t t_off, h, row0, rows;   // its rows row0 .. row0 + rows - 1 of the request
@@ -107,7 +111,7 @@ __device__ __forceinline__ AttnReq attn_request(const AttnArgs& A, int b) {
   r.code = 0;
   const int k = min(max(r.k, 0), SV_MAX_K);
   if (r.k != k) r.code = SV_ERR_DATA_K;
-  else if (r.n < 0 || int64_t(r.n) + k + 1 > INT32_MAX ||
+  else if (r.n < 0 || int64_t(r.n) + k + 1 > kMaxPositions ||
            int64_t(r.n) > int64_t(A.max_pages) * A.S)
     r.code = SV_ERR_DATA_LENGTH;
   else if (A.spec && k + 1 > A.slots) r.code = SV_ERR_DATA_K;

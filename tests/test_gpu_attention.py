@@ -395,3 +395,21 @@ def test_binding_refusals():
         sv.attention(q, cache, layer, n, table, k, sp, out=torch.empty_like(q)[:1])
     with pytest.raises(ValueError):
         sv.attention_weights(*args, torch.zeros(3, 4, device=DEV), torch.zeros(1, 64, device=DEV))
+
+
+@pytest.mark.parametrize("dtype,D", [(B16, 128), (F16, 64), (F32, 64)])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 256, 2 ** 31 - 257, 1 << 30])
+def test_the_widest_windows_hide_nothing(dtype, D, window):
+    # tokens in front of the first position among them: their window starts at about
+    # -2^31, which has to stay in 32 bits
+    n, k = [2, 0, 40, 300], [32, 3, 32, 1]
+    c = Case(18, n, k, 2, 2, D, 16, dtype, spec=False)
+    args, _ = c.gpu()
+    out, lse = sv.attention(*args, window=window)
+    assert sv.attention_error()[0] == 0
+    check(c, out, lse, c.oracle())
+    zero = torch.zeros(4, 310, device=DEV)
+    got = [sv.attention_weights(*args, lse, zero, window=w, out_score=torch.zeros_like(zero))
+           for w in (0, window)]
+    assert sv.attention_weights_error()[0] == 0
+    assert torch.equal(*got)
