@@ -69,6 +69,8 @@ int prepare_device(int vocab, DeviceState* out) {
   return SV_OK;
 }
 
+std::atomic<int32_t> g_expire_wait{0};
+
 bool misaligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
 
 size_t elem_size(int dtype) { return dtype == SV_BF16 || dtype == SV_F16 ? 2 : 4; }
@@ -133,6 +135,7 @@ int attn_args(const sv_kv_cache* cache, int32_t dtype, int32_t layer, int32_t kv
   A.window = window < kMaxPositions ? window : 0;  // a wider one hides nothing
   A.Rt = rows;
   A.scale2 = scale * 1.4426950408889634f;
+  A.test_expire = g_expire_wait.load(std::memory_order_relaxed);
   *out = A;
   return SV_OK;
 }
@@ -425,6 +428,8 @@ int spec_verify_greedy_from_argmax(const int32_t* target_argmax, const int32_t* 
              ? SV_OK
              : SV_ERR_CUDA;
 }
+
+void spec_test_expire_wait(int32_t n) { g_expire_wait.store(n, std::memory_order_relaxed); }
 
 size_t spec_attention_workspace_size(int32_t batch, int32_t head_dim) {
   const int sms = sm_count();

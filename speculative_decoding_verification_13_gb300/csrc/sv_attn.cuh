@@ -68,6 +68,7 @@ struct AttnArgs {
   int32_t box_rows;               // entries per box of the copy engine, 0: no boxes
   int32_t page_rows, layer_row;   // entries per page, entries before the layer's first
   int32_t q_vec, out_vec;         // 16-byte aligned heads
+  int32_t test_expire;            // 1 + the block whose wait runs out, 0 in normal use
 };
 
 #ifdef __CUDACC__

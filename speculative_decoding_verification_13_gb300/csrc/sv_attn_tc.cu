@@ -50,7 +50,8 @@
 // they are replaced by 0 in the tile, and added to the row's O afterwards.
 //
 // Every wait is bounded; on expiry the CTA's status records it, its copies and
-// products land, and TMEM is freed.
+// products land (the warps that issue them wait for the last of them before they
+// end, in every call), and TMEM is freed.
 //
 // Measured, bf16, 8 KV heads of 128 with 4 query heads each, pages of 16: 64
 // requests of 1 to 16000 positions, one token, 82 us with the join (5.1 TB/s); 32
@@ -123,7 +124,8 @@ struct TcShared {
   uint64_t announced[kSegs];
   uint64_t full[11], empty[11];
   uint64_t qfull[2], qempty[2], sfull[kBufs], pfull[kBufs], pvdone[kBufs], ofree;
-  uint64_t looked[2], drain[2];  // softmax warps among themselves; products after a failure
+  uint64_t looked[2], drain[2];  // softmax warps among themselves; the end of the products
+  uint64_t never;                // nothing arrives on it: the test of an expired wait
   uint32_t tmem;
   int abort;
   int first_bad;
@@ -267,6 +269,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_init(smem_addr(&S.looked[1]), 4);
     mbar_init(smem_addr(&S.drain[0]), 1);
     mbar_init(smem_addr(&S.drain[1]), 1);
+    mbar_init(smem_addr(&S.never), 1);
     fence_mbar_init();
     S.abort = 0;
     S.first_bad = INT32_MAX;
@@ -295,6 +298,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     Ring at(kv ? C::kKSlots : 0, kv ? C::kSlots - C::kKSlots : C::kKSlots,
             1);  // empty barriers: the first round passes at once
     bool stop = false;
+    int filled = 0;
     for (int unit = 0; !stop && next_seg(S, unit, s); ++unit) {
       const int hi = s.R.code ? 0 : s.R.hi;
       const int cached = min(s.R.n, hi);
@@ -319,9 +323,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                   ring0 + at.at * kSlotBytes, &S.full[at.at],
                                   &S.copied[at.at], s.R.mtiles > 1 ? again : once, 0, missing);
         at.step();
+        ++filled;
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    ring_land(at, filled, S.full);
   } else if (go && warp == kQueryWarp) {
     // --------------------------------------------- parts, and their queries
     constexpr int kChunks = D / 8, kStep = 32 / kChunks;
@@ -455,13 +461,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
     }
-    if (*reinterpret_cast<volatile int*>(&S.abort)) {
-      // every product issued must finish before TMEM is freed
-      uint64_t* drain = &S.drain[scores ? 0 : 1];
-      mma_commit(lead, drain);
-      mbar_wait_for(smem_addr(drain), 0);
-      __syncwarp();
-    }
+    // every product issued must finish before TMEM is freed, whoever gives up when
+    uint64_t* drain = &S.drain[scores ? 0 : 1];
+    mma_commit(lead, drain);
+    mbar_wait_for(smem_addr(drain), 0);
+    __syncwarp();
   } else if (go && warp < kLoadWarp) {
     // --------------------------------------------------------------- softmax
     const uint32_t lanes = tmem + (uint32_t(warp * 32) << 16);
@@ -472,6 +476,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     Buf bf, done;                // of this tile, and of the one before (its product with V)
     for (int unit = 0;; ++unit) {
       bool stop = !next_seg(S, unit, s);
+      if (unit == 0 && A.test_expire == int(blockIdx.x) + 1 &&
+          !mbar_wait_for(smem_addr(&S.never), 0, kTestWaitNs)) {
+        *reinterpret_cast<volatile int*>(&S.abort) = 1;
+        stop = true;
+      }
       if (softmax_any(stop)) break;
       const int apart = kTcMr / s.copies;
       const int copy = tid / apart, rr = tid % apart;   // warps lie in one copy

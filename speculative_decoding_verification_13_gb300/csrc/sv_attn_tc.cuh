@@ -23,6 +23,23 @@ struct Ring {
   }
 };
 
+// A load warp that is done, or has given up, waits until the copies into its
+// ring's last slots have landed (bounded): the shared memory that they are to
+// fill is the block's only until it ends.  `at`: where the next tile would go,
+// its phase that of the slot's empty barrier; a slot's tile before ended the full
+// barrier's phase of the opposite parity.
+__device__ __forceinline__ void ring_land(Ring at, int filled, uint64_t* full) {
+  for (int i = min(filled, int(at.end - at.base)); i > 0; --i) {
+    if (at.at == at.base) {
+      at.at = at.end;
+      at.phase ^= 1;
+    }
+    --at.at;
+    mbar_wait_for(smem_addr(&full[at.at]), at.phase ^ 1);
+  }
+  __syncwarp();
+}
+
 // A type's bits, and kLift: weights are held 2^kLift times as large.  The
 // smallest normal number of fp16 is 2^-14, so that weights of long contexts
 // would lose bits; with the lift and at most 2^8 above the stored maximum they

@@ -1,0 +1,58 @@
+"""An expired wait in the operators' kernels, in the form that faults nothing:
+with the test switch set, one wait of one block, on a barrier nothing arrives on,
+runs out after its short limit.  The call reports SV_ERR_TIMEOUT, its copies
+land, and the next calls are as before."""
+
+import time
+
+import pytest
+import torch
+
+import speculative_decoding_verification_13_gb300 as sv
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+SV_ERR_TIMEOUT = 24
+
+
+@pytest.fixture
+def expire():
+    lib = sv.load_library()
+    yield lib.spec_test_expire_wait
+    lib.spec_test_expire_wait(0)
+
+
+def batch(D, dtype, seed=3):
+    """Long and short requests: parts of one over many blocks, several in a block."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    n, k, S, Hk = [20000, 5, 300, 0, 4000], [3, 0, 15, 1, 7], 16, 2
+    pages = [-(-x // S) for x in n]
+    table = torch.full((5, max(pages)), -1, dtype=torch.int32)
+    at = 0
+    for b, c in enumerate(pages):
+        table[b, :c] = torch.arange(at, at + c)
+        at += c
+    cache = torch.randn(at, 1, 2, S, Hk * D, device=DEV, generator=g).to(dtype)
+    spec = torch.randn(5, 16, 1, 2, Hk * D, device=DEV, generator=g).to(dtype)
+    q = torch.randn(sum(k) + 5, Hk * 4, D, device=DEV, generator=g).to(dtype)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    return (q, cache, 0, torch.tensor(n, **i32), table.to(DEV), torch.tensor(k, **i32)), spec
+
+
+@pytest.mark.parametrize("D,dtype", [(128, torch.bfloat16), (64, torch.float16),
+                                     (256, torch.bfloat16)])
+@pytest.mark.parametrize("block", [0, 1, 77, 151])
+def test_attention_reports_an_expired_wait_and_recovers(expire, D, dtype, block):
+    args, spec = batch(D, dtype)
+    want = sv.attention(*args, spec)
+    assert sv.attention_error()[0] == 0
+    t0 = time.perf_counter()
+    expire(block + 1)
+    sv.attention(*args, spec)
+    assert sv.attention_error() == (SV_ERR_TIMEOUT, -1, -1)
+    assert time.perf_counter() - t0 < 5
+    expire(0)
+    for _ in range(3):
+        again = sv.attention(*args, spec)
+        assert sv.attention_error()[0] == 0
+        assert torch.equal(want[0], again[0]) and torch.equal(want[1], again[1])
