@@ -50,8 +50,7 @@
 // they are replaced by 0 in the tile, and added to the row's O afterwards.
 //
 // Every wait is bounded; on expiry the CTA's status records it, its copies and
-// products land (the warps that issue them wait for the last of them before they
-// end, in every call), and TMEM is freed.
+// products land, TMEM is freed, and the rows of the CTA's parts become NaN.
 //
 // Measured, bf16, 8 KV heads of 128 with 4 query heads each, pages of 16: 64
 // requests of 1 to 16000 positions, one token, 82 us with the join (5.1 TB/s); 32
@@ -124,11 +123,15 @@ struct TcShared {
   uint64_t announced[kSegs];
   uint64_t full[11], empty[11];
   uint64_t qfull[2], qempty[2], sfull[kBufs], pfull[kBufs], pvdone[kBufs], ofree;
-  uint64_t looked[2], drain[2];  // softmax warps among themselves; the end of the products
+  uint64_t looked[2], drain[2];  // softmax warps among themselves; products after a failure
   uint64_t never;                // nothing arrives on it: the test of an expired wait
   uint32_t tmem;
   int abort;
   int first_bad;
+  struct {
+    uint32_t at, phase;
+    int filled;
+  } loaded[2];       // the rings of K and V as their warps left them
   int bad[kSegs];    // the part needs a missing page
   int copied[11];    // per slot: filled by the lanes' copies, not by the copy engine
   uint32_t signs[2][8];  // per column: +inf, -inf among the part's values
@@ -234,9 +237,64 @@ __device__ __forceinline__ bool next_seg(TcShared& S, int unit, Seg& s) {
   return s.count > 0;
 }
 
+// The unit that the CTA begins with s ends in a later one: the join's record of it.
+__device__ __forceinline__ void begin_split(const AttnArgs& A, const AttnPlan& P, const Seg& s) {
+  AttnSplit& u = A.split[blockIdx.x];
+  u.last = attn_owner(A, P, s.unit_end - 1);
+  u.t_off = s.t_off;
+  u.h = s.h;
+  u.row0 = s.row0;
+  u.rows = s.rows;
+  u.valid = 1;
+}
+
+// All threads, after a wait of the CTA expired and every warp has left its loop.
+// Copies and products that were issued finish, whichever warp gave up and when.
+// Then every row of the CTA's parts becomes NaN, whether it was written or not, and
+// so does what the join makes of them with other CTAs' parts.  A function of its
+// own, which finds the CTA's piece again: in the kernel's body it cost the loops
+// their registers (long contexts 230 -> 247 us).
+template <class T, int D>
+__device__ __noinline__ void give_up(const AttnArgs& A, TcShared& S) {
+  using C = Shape<D>;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp == kLoadWarp || warp == kLoadWarp + 1) {
+    const int kv = warp - kLoadWarp;
+    Ring at(kv ? C::kKSlots : 0, kv ? C::kSlots - C::kKSlots : C::kKSlots, S.loaded[kv].phase);
+    at.at = S.loaded[kv].at;
+    ring_land(at, S.loaded[kv].filled, S.full);
+  } else if (warp == kScoreWarp || warp == kValueWarp) {
+    uint64_t* drain = &S.drain[warp - kScoreWarp];
+    mma_commit(lane == 0, drain);
+    mbar_wait_for(smem_addr(drain), 0);
+    __syncwarp();
+  }
+  __syncthreads();
+  const float nan = __int_as_float(0x7fc00000);
+  const AttnPlan P = attn_plan<C::TN, kTcMr, false, kTcThreads, kUnitTiles<D>>(A);
+  Walk<C::TN, kUnitTiles<D>> walk(A, P);
+  Seg s;
+  while (walk.next(A, s)) {
+    const int slot = s.first == 0 ? 1 : 0;
+    for (int r = warp; r < s.rows; r += kTcThreads / 32) {
+      const int x = s.row0 + r, hq = s.h * A.G + x % A.G;
+      const int64_t t = int64_t(s.t_off) + x / A.G;
+      if (s.whole) {
+        T* out = static_cast<T*>(A.out) + t * A.o_ts + int64_t(hq) * A.o_hs;
+        for (int d = lane; d < A.D; d += 32) out[d] = from_float<T>(nan);
+        if (lane == 0) A.lse[t * A.Hq + hq] = nan;
+      } else if (lane == 0) {
+        A.part_ml[(int64_t(blockIdx.x) * 2 + slot) * kTcMr + r] = make_float2(nan, 0.f);
+      }
+    }
+    if (tid == 0 && !s.whole && s.first == 0) begin_split(A, P, s);
+  }
+}
+
 template <class T, int D, bool PART>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    attn_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const AttnArgs A) {
+    attn_tc_kernel(const __grid_constant__ CUtensorMap rows_map,
+                   const __grid_constant__ AttnArgs A) {
   using C = Shape<D>;
   constexpr int TN = C::TN;
   extern __shared__ unsigned char tc_smem_raw[];
@@ -312,7 +370,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       };
       // pages are read one tile ahead, so that nothing waits for the block table
       TilePages<TN, 1> next = tile_pages<D, PART, TN>(A, table, cached, p0);
-      for (int t = 0; t < s.count; ++t) {
+      int t = 0;
+      for (; t < s.count; ++t) {
         const TilePages<TN, 1> pages = next;
         if (t + 1 < s.count) next = tile_pages<D, PART, TN>(A, table, cached, p0 + (t + 1) * TN);
         if (!tc_wait_warp(&S.empty[at.at], at.phase, S)) {
@@ -323,11 +382,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                   ring0 + at.at * kSlotBytes, &S.full[at.at],
                                   &S.copied[at.at], s.R.mtiles > 1 ? again : once, 0, missing);
         at.step();
-        ++filled;
       }
+      filled += t;
+    }
+    if (lane == 0) {
+      S.loaded[kv].at = at.at;
+      S.loaded[kv].phase = at.phase;
+      S.loaded[kv].filled = filled;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    ring_land(at, filled, S.full);
   } else if (go && warp == kQueryWarp) {
     // --------------------------------------------- parts, and their queries
     constexpr int kChunks = D / 8, kStep = 32 / kChunks;
@@ -461,11 +524,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
     }
-    // every product issued must finish before TMEM is freed, whoever gives up when
-    uint64_t* drain = &S.drain[scores ? 0 : 1];
-    mma_commit(lead, drain);
-    mbar_wait_for(smem_addr(drain), 0);
-    __syncwarp();
   } else if (go && warp < kLoadWarp) {
     // --------------------------------------------------------------- softmax
     const uint32_t lanes = tmem + (uint32_t(warp * 32) << 16);
@@ -476,7 +534,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     Buf bf, done;                // of this tile, and of the one before (its product with V)
     for (int unit = 0;; ++unit) {
       bool stop = !next_seg(S, unit, s);
-      if (unit == 0 && A.test_expire == int(blockIdx.x) + 1 &&
+      if (unit == 0 && A.test_expire == int(blockIdx.x) + 1 && !stop &&
           !mbar_wait_for(smem_addr(&S.never), 0, kTestWaitNs)) {
         *reinterpret_cast<volatile int*>(&S.abort) = 1;
         stop = true;
@@ -918,20 +976,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_arrive(smem_addr(&S.ofree));
         mbar_arrive(smem_addr(&S.qempty[unit % C::kQBufs]));
       }
-      if (tid == 0 && !s.whole && s.first == 0) {
-        AttnSplit& u = A.split[blockIdx.x];
-        u.last = attn_owner(A, P, s.unit_end - 1);
-        u.t_off = s.t_off;
-        u.h = s.h;
-        u.row0 = s.row0;
-        u.rows = s.rows;
-        u.valid = 1;
-      }
+      if (tid == 0 && !s.whole && s.first == 0) begin_split(A, P, s);
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (S.abort) give_up<T, D>(A, S);
   if (tid == 0)
     A.status[A.B + blockIdx.x] = S.abort ? -SV_ERR_TIMEOUT : S.first_bad;
   if (warp == kValueWarp) {

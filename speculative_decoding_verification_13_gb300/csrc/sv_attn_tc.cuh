@@ -23,11 +23,11 @@ struct Ring {
   }
 };
 
-// A load warp that is done, or has given up, waits until the copies into its
-// ring's last slots have landed (bounded): the shared memory that they are to
-// fill is the block's only until it ends.  `at`: where the next tile would go,
-// its phase that of the slot's empty barrier; a slot's tile before ended the full
-// barrier's phase of the opposite parity.
+// After a wait expired: waits (bounded) until the copies into the ring's last
+// slots have landed, since the shared memory that they are to fill is the block's
+// only until it ends.  `at`: where the next tile would have gone, its phase that of
+// the slot's empty barrier; a slot's tile before ended the full barrier's phase of
+// the opposite parity.
 __device__ __forceinline__ void ring_land(Ring at, int filled, uint64_t* full) {
   for (int i = min(filled, int(at.end - at.base)); i > 0; --i) {
     if (at.at == at.base) {

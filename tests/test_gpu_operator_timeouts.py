@@ -25,7 +25,7 @@ def expire():
 def batch(D, dtype, seed=3):
     """Long and short requests: parts of one over many blocks, several in a block."""
     g = torch.Generator(device=DEV).manual_seed(seed)
-    n, k, S, Hk = [20000, 5, 300, 0, 4000], [3, 0, 15, 1, 7], 16, 2
+    n, k, S, Hk = [60000, 5, 300, 0, 14000], [3, 0, 15, 1, 7], 16, 2
     pages = [-(-x // S) for x in n]
     table = torch.full((5, max(pages)), -1, dtype=torch.int32)
     at = 0
@@ -56,3 +56,21 @@ def test_attention_reports_an_expired_wait_and_recovers(expire, D, dtype, block)
         again = sv.attention(*args, spec)
         assert sv.attention_error()[0] == 0
         assert torch.equal(want[0], again[0]) and torch.equal(want[1], again[1])
+
+
+@pytest.mark.parametrize("D,dtype", [(128, torch.bfloat16), (64, torch.float16),
+                                     (256, torch.bfloat16)])
+@pytest.mark.parametrize("block", [0, 1, 40, 77, 151])
+def test_no_row_of_an_expired_call_holds_anything_but_its_result_or_nan(expire, D, dtype, block):
+    args, spec = batch(D, dtype)
+    want, want_lse = sv.attention(*args, spec)
+    # other outputs and parts in the buffers
+    sv.attention(-args[0], *args[1:], spec)
+    out, lse = torch.full_like(want, 7), torch.full_like(want_lse, 7)
+    expire(block + 1)
+    sv.attention(*args, spec, out=out, out_lse=lse)
+    assert sv.attention_error()[0] == SV_ERR_TIMEOUT
+    failed = torch.isnan(lse)
+    assert failed.any() and not failed.all()
+    assert torch.isnan(out[failed]).all()
+    assert torch.equal(out[~failed], want[~failed]) and torch.equal(lse[~failed], want_lse[~failed])
