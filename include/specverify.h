@@ -433,7 +433,8 @@ int spec_attention(const sv_kv_cache* cache, int32_t dtype, int32_t layer, int32
  * positions past score_cols or its block table (SV_ERR_DATA_LENGTH) or more
  * than spec_slots tokens (SV_ERR_DATA_K) is left untouched; positions on a
  * missing page are not written (SV_ERR_DATA_PAGE).  A batch error writes
- * nothing.  Each score has one writer and a fixed order of its sum. */
+ * nothing; positions that an expired wait left out (SV_ERR_TIMEOUT) stay as they
+ * are.  Each score has one writer and a fixed order of its sum. */
 size_t spec_attention_weights_workspace_size(int32_t batch);
 
 int spec_attention_weights(const sv_kv_cache* cache, int32_t dtype, int32_t layer,
@@ -515,10 +516,10 @@ int spec_logprobs_grad(const sv_logits* logits, const int32_t* tokens, const flo
                        const float* g_logprob, const float* g_entropy, void* out,
                        int64_t out_stride, void* stream);
 
-/* Test of the timeout path of spec_attention on the tensor cores (process-wide,
- * 0 in normal use): while it is n > 0, block n - 1 of every call that has
- * work lets one bounded wait, on a barrier nothing arrives on, run out after 1 ms.
- * The call then reports SV_ERR_TIMEOUT. */
+/* Test of the timeout path of spec_attention and spec_attention_weights on the
+ * tensor cores (process-wide, 0 in normal use): while it is n > 0, block n - 1 of
+ * every call that has work lets one bounded wait, on a barrier nothing arrives on,
+ * run out after 1 ms.  The call then reports SV_ERR_TIMEOUT. */
 void spec_test_expire_wait(int32_t n);
 
 /* Human-readable text of a status code. */

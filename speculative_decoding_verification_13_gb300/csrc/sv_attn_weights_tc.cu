@@ -18,7 +18,8 @@
 //              of the piece and announces them.
 //   warp 6     issues the products into four accumulators in TMEM;
 //   warps 0-3  one position a thread: exp(s - lse) summed over the rows.
-// Every wait is bounded, as in attention.
+// Every wait is bounded, as in attention; scores that an expired one left out
+// stay as they are.
 //
 // Measured, bf16, 8 KV heads of 128 with 4 query heads each, pages of 16: 32
 // requests of 2001 to 8190 positions with up to 15 drafts 61 us (4.9 TB/s; one row
@@ -56,7 +57,11 @@ struct WtShared {
   Part part[kParts];
   uint64_t announced[kParts], taken[kParts];
   uint64_t full[8], empty[8], qfull[3], qempty[3], lfull[6], lempty[6], sfull[kAccs],
-      sempty[kAccs], drain;
+      sempty[kAccs], drain, never;   // never: nothing arrives, the test of an expired wait
+  struct {
+    uint32_t at, phase;
+    int filled;
+  } loaded[2];                    // the ring of K as each of its warps left it
   uint32_t tmem;
   int abort, first_bad;
   int copied[8];
@@ -79,6 +84,25 @@ __device__ __forceinline__ bool next_part(WtShared& S, int i, Part& p) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&S.taken[i % kParts]));
   return p.count > 0;
+}
+
+// All threads, after a wait of the CTA expired and every warp has left its loop:
+// copies and products that were issued finish, whichever warp gave up and when.
+// Of a slot that only one of its two warps filled the wait runs out.
+template <int D>
+__device__ __noinline__ void give_up(WtShared& S) {
+  const int warp = threadIdx.x >> 5;
+  if (warp == kKeyWarp || warp == kKeyWarp + 1) {
+    const int share = warp - kKeyWarp;
+    Ring at(0, WtShape<D>::kSlots, S.loaded[share].phase);
+    at.at = S.loaded[share].at;
+    ring_land(at, S.loaded[share].filled, S.full);
+  } else if (warp == kProductWarp) {
+    mma_commit((threadIdx.x & 31) == 0, &S.drain);
+    mbar_wait_for(smem_addr(&S.drain), 0);
+    __syncwarp();
+  }
+  __syncthreads();
 }
 
 template <class T, int D, bool PART>
@@ -114,6 +138,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       mbar_init(smem_addr(&S.taken[i]), 6 + C::kQBufs);  // all warps but the first row warp
     }
     mbar_init(smem_addr(&S.drain), 1);
+    mbar_init(smem_addr(&S.never), 1);
     fence_mbar_init();
     S.abort = 0;
     S.first_bad = INT32_MAX;
@@ -138,6 +163,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     Part w;
     Ring at(0, C::kSlots, 1);
     bool stop = false;
+    int filled = 0;
     for (int i = 0; !stop && next_part(S, i, w); ++i) {
       const int cached = min(w.R.n, w.R.hi);
       const int32_t* table = A.table + int64_t(w.b) * A.max_pages;
@@ -159,8 +185,14 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                                    smem0 + at.at * C::kSlotBytes, &S.full[at.at],
                                    &S.copied[at.at], policy, share, missing);
           at.step();
+          ++filled;
         }
       }
+    }
+    if (lane == 0) {
+      S.loaded[share].at = at.at;
+      S.loaded[share].phase = at.phase;
+      S.loaded[share].filled = filled;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (go && warp >= kRowWarp && warp < kRowWarp + C::kQBufs) {
@@ -325,12 +357,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         }
       }
     }
-    if (*reinterpret_cast<volatile int*>(&S.abort)) {
-      // every product issued must finish before TMEM is freed
-      mma_commit(lead, &S.drain);
-      mbar_wait_for(smem_addr(&S.drain), 0);
-      __syncwarp();
-    }
   } else if (go && warp < kKeyWarp) {
     // ------------------------------------------------------------------ sums
     const uint32_t lanes = tmem + (uint32_t(warp * 32) << 16);
@@ -338,6 +364,11 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     Ring acc(0, kAccs, 0), lb(0, 2 * C::kQBufs, 0);
     bool ok = true;
     for (int i = 0; ok && next_part(S, i, w); ++i) {
+      if (i == 0 && A.test_expire == int(blockIdx.x) + 1 &&
+          !mbar_wait_for(smem_addr(&S.never), 0, kTestWaitNs)) {
+        *reinterpret_cast<volatile int*>(&S.abort) = 1;
+        break;
+      }
       const int nrows = w.R.take * A.G;
       for (int t = 0; ok && t < w.count; ++t) {
         const int p0 = (w.tile + t) * kWtTile, p = p0 + tid;
@@ -400,6 +431,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (S.abort) give_up<D>(S);
   if (tid == 0) A.status[A.B + blockIdx.x] = S.abort ? -SV_ERR_TIMEOUT : S.first_bad;
   if (warp == kProductWarp) {
     tc_fence_after();

@@ -74,3 +74,28 @@ def test_no_row_of_an_expired_call_holds_anything_but_its_result_or_nan(expire, 
     assert failed.any() and not failed.all()
     assert torch.isnan(out[failed]).all()
     assert torch.equal(out[~failed], want[~failed]) and torch.equal(lse[~failed], want_lse[~failed])
+
+
+@pytest.mark.parametrize("D,dtype", [(128, torch.bfloat16), (64, torch.float16),
+                                     (256, torch.bfloat16)])
+@pytest.mark.parametrize("block", [0, 1, 40, 151])
+def test_weights_report_an_expired_wait_and_recover(expire, D, dtype, block):
+    args, spec = batch(D, dtype)
+    lse = sv.attention(*args, spec)[1]
+    score = torch.rand(5, 60100, device=DEV)
+    call = lambda: sv.attention_weights(*args, lse, score, spec,
+                                        out_score=torch.full_like(score, 7))
+    want = call()
+    assert sv.attention_weights_error()[0] == 0
+    t0 = time.perf_counter()
+    expire(block + 1)
+    got = call()
+    assert sv.attention_weights_error() == (SV_ERR_TIMEOUT, -1, -1)
+    assert time.perf_counter() - t0 < 5
+    left = (got == 7) & (want != 7)     # positions that the block did not come to
+    assert left.any() and not left.all()
+    assert torch.equal(got[~left], want[~left])
+    expire(0)
+    for _ in range(3):
+        assert torch.equal(call(), want)
+        assert sv.attention_weights_error()[0] == 0
