@@ -516,10 +516,11 @@ int spec_logprobs_grad(const sv_logits* logits, const int32_t* tokens, const flo
                        const float* g_logprob, const float* g_entropy, void* out,
                        int64_t out_stride, void* stream);
 
-/* Test of the timeout path of spec_attention and spec_attention_weights on the
- * tensor cores (process-wide, 0 in normal use): while it is n > 0, block n - 1 of
- * every call that has work lets one bounded wait, on a barrier nothing arrives on,
- * run out after 1 ms.  The call then reports SV_ERR_TIMEOUT. */
+/* Test of the timeout path of spec_logprobs, and of spec_attention and
+ * spec_attention_weights on the tensor cores (process-wide, 0 in normal use): while
+ * it is n > 0, block n - 1 of every call, if it has work, lets one bounded wait, on
+ * a barrier nothing arrives on, run out after 1 ms.  The call then reports
+ * SV_ERR_TIMEOUT. */
 void spec_test_expire_wait(int32_t n);
 
 /* Human-readable text of a status code. */

@@ -589,6 +589,7 @@ int spec_logprobs(const sv_logits* logits, const int32_t* tokens, const float* t
   if (sms == 0) return SV_ERR_CUDA;
   return launch_logprobs(*logits, tokens, temperature, n_top, out_logprob, out_entropy, out_max,
                          out_logsum, out_top_tokens, out_top_logprobs, workspace, sms,
+                         g_expire_wait.load(std::memory_order_relaxed),
                          static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? SV_OK
              : SV_ERR_CUDA;

@@ -234,7 +234,7 @@ size_t logprobs_workspace_bytes(int64_t rows);
 cudaError_t launch_logprobs(const sv_logits& x, const int32_t* tokens, const float* temperature,
                             int n_top, float* logprob, float* entropy, float* mx, float* logsum,
                             int32_t* top_tok, float* top_lp, void* workspace, int sms,
-                            cudaStream_t s);
+                            int test_expire, cudaStream_t s);
 int64_t logprobs_grad_blocks(const sv_logits& x);
 cudaError_t launch_logprobs_grad(const sv_logits& x, const int32_t* tokens,
                                  const float* temperature, const float* mx, const float* logsum,

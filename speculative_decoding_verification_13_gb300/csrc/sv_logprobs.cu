@@ -64,6 +64,7 @@ struct LpArgs {
   float* top_lp;
   int32_t* status;            // [rows]
   WsHeader* hdr;
+  int32_t test_expire;        // 1 + the block whose wait runs out, 0 in normal use
 };
 
 template <class T> struct Elem;
@@ -226,6 +227,7 @@ struct LpPart {
 template <bool TOP>
 struct LpShared {
   uint64_t full[kLpStages], empty[kLpStages];
+  uint64_t never;   // nothing arrives on it: the test of an expired wait
   double s[kLpWarps], t[kLpWarps];
   float m[kLpWarps];
   alignas(16) uint32_t best[TOP ? kLpWarps * kLpBest : 4];
@@ -416,6 +418,8 @@ __device__ void consume_row(const LpArgs& A, LpShared<TOP>& S, const unsigned ch
   const int len = (niter + kLpSegs - 1) / kLpSegs;   // rounds per cell
   const int end = first + niter;
   const uint64_t cc = pk2(c2, c2);
+  const bool late = A.test_expire == int(blockIdx.x) + 1 && warp == 0 &&
+                    !mbar_wait_for(smem_addr(&S.never), 0, kTestWaitNs);
   auto exact_vector = [&](const uint4& w) {
     float x[VE];
     E::unpack(w, x);
@@ -432,10 +436,12 @@ __device__ void consume_row(const LpArgs& A, LpShared<TOP>& S, const unsigned ch
     for (; it < it1; ++it) {
       const int k = it - first, stage = k % kLpStages;
       bool there = true;
-      if (!mbar_wait_for(smem_addr(&S.full[stage]), (k / kLpStages) & 1, kWaitNs, &S.abort)) {
+      if (late ||
+          !mbar_wait_for(smem_addr(&S.full[stage]), (k / kLpStages) & 1, kWaitNs, &S.abort)) {
         *reinterpret_cast<volatile int*>(&S.abort) = 1;   // the row fails below
         there = false;
       }
+      there = __all_sync(0xffffffffu, there);
       const uint4* tile = reinterpret_cast<const uint4*>(lp_ring + stage * kLpTile) + tid;
       const int left = cut.nvec - it * (kLpTile / 16);   // vectors from this round on
       if (there && left >= kLpTile / 16) {
@@ -489,7 +495,8 @@ __device__ void consume_row(const LpArgs& A, LpShared<TOP>& S, const unsigned ch
           st.raise(g, c2);
           exact_vector(v);
         }
-        give_back(&S.empty[stage]);
+        // a slot whose copy has not landed is not free, and the copy warp gives up
+        if (there) give_back(&S.empty[stage]);
       }
     }
     if (TOP) {
@@ -664,6 +671,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, 3) logprobs_kernel(const LpAr
       mbar_init(smem_addr(&S.full[i]), 1);
       mbar_init(smem_addr(&S.empty[i]), kLpWarps);
     }
+    mbar_init(smem_addr(&S.never), 1);
     fence_mbar_init();
     S.abort = 0;
     if (blockIdx.x == 0) {
@@ -691,11 +699,10 @@ __global__ void __launch_bounds__(kLpThreads + 32, 3) logprobs_kernel(const LpAr
       bulk_load_hint(smem_addr(lp_ring) + s * kLpTile, P.vec + v0, bytes, smem_addr(&S.full[s]),
                      policy);
     }
-    if (k < P.niter) {  // gave up: let the copies land before the CTA may end
-      *reinterpret_cast<volatile int*>(&S.abort) = 1;
-      for (int j = max(0, k - kLpStages); j < k; ++j)
-        mbar_wait_for(smem_addr(&S.full[j % kLpStages]), (j / kLpStages) & 1);
-    }
+    if (k < P.niter) *reinterpret_cast<volatile int*>(&S.abort) = 1;   // gave up
+    // the last copies land before the CTA may end, whoever gave up and when
+    for (int j = max(0, k - kLpStages); j < k; ++j)
+      mbar_wait_for(smem_addr(&S.full[j % kLpStages]), (j / kLpStages) & 1);
     return;
   }
   if (!P.skip) {
@@ -810,8 +817,9 @@ size_t logprobs_workspace_bytes(int64_t rows) {
 cudaError_t launch_logprobs(const sv_logits& x, const int32_t* tokens, const float* temperature,
                             int n_top, float* logprob, float* entropy, float* mx, float* logsum,
                             int32_t* top_tok, float* top_lp, void* workspace, int sms,
-                            cudaStream_t s) {
+                            int test_expire, cudaStream_t s) {
   LpArgs A;
+  A.test_expire = test_expire;
   A.x = x.data;
   A.rows = x.rows;
   A.stride = x.row_stride;

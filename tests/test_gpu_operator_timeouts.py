@@ -99,3 +99,32 @@ def test_weights_report_an_expired_wait_and_recover(expire, D, dtype, block):
     for _ in range(3):
         assert torch.equal(call(), want)
         assert sv.attention_weights_error()[0] == 0
+
+
+# one block a row, in several waves; clusters of 8, 4 and 2 blocks
+@pytest.mark.parametrize("rows,V,dtype,cluster", [
+    (700, 50257, torch.bfloat16, 1), (200, 40000, torch.float32, 1),
+    (3, 151936, torch.bfloat16, 8), (30, 151936, torch.float32, 4), (8, 32000, torch.float32, 2)])
+@pytest.mark.parametrize("n_top", [0, 20])
+def test_logprobs_fail_the_row_of_an_expired_wait_only(expire, rows, V, dtype, cluster, n_top):
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    x = torch.randn(rows, V, device=DEV, generator=g).to(dtype)
+    tok = torch.randint(0, V, (rows,), dtype=torch.int32, device=DEV, generator=g)
+    take = 6 if n_top else 4
+    want = sv.logprobs(x, tok, None, n_top)[:take]
+    assert sv.logprobs_error()[0] == 0
+    for block in sorted({0, cluster - 1, rows // 2 * cluster, rows * cluster - 1}):
+        t0 = time.perf_counter()
+        expire(block + 1)
+        got = sv.logprobs(x, tok, None, n_top)[:take]
+        assert sv.logprobs_error() == (SV_ERR_TIMEOUT, -1, block // cluster)
+        assert time.perf_counter() - t0 < 5
+        other = torch.arange(rows, device=DEV) != block // cluster
+        for a, b in zip(want, got):
+            assert torch.equal(a[other], b[other])
+            failed = b[~other]
+            assert (torch.isnan(failed) if failed.is_floating_point() else failed == -1).all()
+        expire(0)
+        again = sv.logprobs(x, tok, None, n_top)[:take]
+        assert sv.logprobs_error()[0] == 0
+        assert all(torch.equal(a, b) for a, b in zip(want, again))
