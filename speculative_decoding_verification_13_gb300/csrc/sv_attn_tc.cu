@@ -120,7 +120,7 @@ struct Seg {
 
 struct TcShared {
   Seg seg[kSegs];
-  uint64_t announced[kSegs];
+  uint64_t announced[kSegs], noted[kSegs];   // noted: every page of the part was looked at
   uint64_t full[11], empty[11];
   uint64_t qfull[2], qempty[2], sfull[kBufs], pfull[kBufs], pvdone[kBufs], ofree;
   uint64_t looked[2], drain[2];  // softmax warps among themselves; products after a failure
@@ -322,7 +322,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       S.dirty[i] = 0;
     }
     mbar_init(smem_addr(&S.ofree), 4);
-    for (int i = 0; i < kSegs; ++i) mbar_init(smem_addr(&S.announced[i]), 1);
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(smem_addr(&S.announced[i]), 1);
+      mbar_init(smem_addr(&S.noted[i]), 2);
+    }
     mbar_init(smem_addr(&S.looked[0]), 4);
     mbar_init(smem_addr(&S.looked[1]), 4);
     mbar_init(smem_addr(&S.drain[0]), 1);
@@ -384,6 +387,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         at.step();
       }
       filled += t;
+      // Missing pages are noted while a tile's boxes are issued, after the lane's
+      // arrival (before it they would hold up the copies: long contexts 229 -> 234
+      // us); those who read the note wait for this arrival.
+      __syncwarp();
+      if (lane == 0 && !stop) mbar_arrive(smem_addr(&S.noted[unit % kSegs]));
     }
     if (lane == 0) {
       S.loaded[kv].at = at.at;
@@ -771,7 +779,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
       // ------------------------------------------------- the unit's rows
-      if (!stop) stop = !tc_wait_warp(&S.pvdone[done.at], done.phase, S);
+      if (!stop)
+        stop = !tc_wait_two(&S.pvdone[done.at], done.phase, &S.noted[unit % kSegs],
+                            (unit / kSegs) & 1, S);
       if (softmax_any(stop)) break;
       tc_fence_after();
       const bool bad = *reinterpret_cast<volatile int*>(&S.bad[unit % kSegs]) != 0;

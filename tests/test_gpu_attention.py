@@ -413,3 +413,21 @@ def test_the_widest_windows_hide_nothing(dtype, D, window):
            for w in (0, window)]
     assert sv.attention_weights_error()[0] == 0
     assert torch.equal(*got)
+
+
+@pytest.mark.parametrize("dtype,D", [(B16, 128), (F16, 64), (B16, 256)])
+def test_a_missing_page_of_a_whole_tile_fails_its_rows_every_time(dtype, D):
+    # the page is noted by the warp that loads, for those that wait for the tile
+    n = [128 * i for i in (1, 2, 3, 9, 40)]
+    c = Case(19, n, [0] * 5, 2, 4, D, 16, dtype, layers=1, junk=False)
+    args, sp = c.gpu()
+    want, want_lse = sv.attention(*args, sp)
+    for b, page in ((0, 7), (1, 8), (2, 23), (3, 71), (4, 0)):
+        table = args[4].clone()
+        table[b, page] = -1
+        for _ in range(40):
+            out, lse = sv.attention(*args[:4], table, args[5], sp)
+            assert torch.isnan(out[b]).all() and torch.isnan(lse[b]).all()
+            other = torch.arange(5, device=DEV) != b
+            assert torch.equal(out[other], want[other]) and torch.equal(lse[other], want_lse[other])
+        assert sv.attention_error()[:2] == (27, b)
