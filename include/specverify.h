@@ -455,10 +455,11 @@ int spec_attention_weights(const sv_kv_cache* cache, int32_t dtype, int32_t laye
  * order: kept position i moves to position i, K and V of every layer, its
  * score moves to out_score[b][i], scores from there to n become 0 and
  * out_len[b] the number kept.
- * In place (dst NULL): entries move within the request's own pages, which no
- * other request may share; pages past the new length are free.  Else the kept
- * entries are written to dst at dst_table's pages (another cache of the same
- * geometry, or other pages of this one) and the source stays as it is.
+ * In place (dst NULL, or this cache with block_table itself): entries move within
+ * the request's own pages, which no other request may share; pages past the new
+ * length are free.  Else the kept entries are written to dst at dst_table's pages
+ * (another cache of the same geometry, or pages of this one that no request's
+ * source lies in) and the source stays as it is.
  *   score       [B, score_cols] float, row stride score_stride
  *   out_score   [B, out_cols] float, row stride out_stride; may be score
  *   kv_len      [B] int32; out_len [B] int32, may be kv_len

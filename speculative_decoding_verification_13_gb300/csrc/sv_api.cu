@@ -527,13 +527,15 @@ int spec_kv_evict(const sv_kv_cache* cache, const int32_t* block_table, int32_t 
     return SV_ERR_ARG;
   if ((int64_t(c.entry_elems) * c.elem_bytes) % 16 != 0 || batch > 65535)
     return SV_ERR_UNSUPPORTED;
-  const bool in_place = dst == nullptr;
-  if (!in_place) {
+  if (dst) {
     if (dst->n_layers != c.n_layers || dst->page_size != c.page_size ||
         dst->entry_elems != c.entry_elems || dst->elem_bytes != c.elem_bytes ||
         dst->num_pages < 0 || dst_max_pages < 0)
       return SV_ERR_ARG;
   }
+  // the request's own pages, named as such or as the destination
+  const bool in_place = !dst || (dst->data == c.data && dst->num_pages == c.num_pages &&
+                                 dst_table == block_table && dst_max_pages == max_pages);
   const sv_kv_cache& d = in_place ? c : *dst;
   const int32_t* dt = in_place ? block_table : dst_table;
   const int32_t dcols = in_place ? max_pages : dst_max_pages;

@@ -329,7 +329,8 @@ def kv_evict(cache, score, kv_len, block_table, budget, sinks=0, recent=0, *, ou
     (:func:`attention_weights`) with them, and the length becomes the number
     kept.  Without ``out_table`` the entries move inside the request's own
     pages, which no other request may share; with it they are written to those
-    pages of ``out_cache`` (default: the same cache) and the source stays.
+    pages of ``out_cache`` (default: the same cache, where they have to be other
+    pages, or ``block_table`` itself for in place) and the source stays.
     ``out_score`` and ``out_len`` default to score and kv_len, in place.
 
     Returns ``(out_len [B] int32, kept [B, budget] int32 or None)``."""

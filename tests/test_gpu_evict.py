@@ -151,3 +151,20 @@ def test_graph_and_refusals():
         sv.kv_evict(*d, 10, out_table=d[3], out_cache=d[0][:, :1].contiguous())
     with pytest.raises(TypeError):
         sv.kv_evict(d[0], d[1].half(), *d[2:], 10)
+
+
+def test_the_own_pages_named_as_the_destination_are_in_place():
+    # many blocks would copy at once between pages that lie over one another
+    n, table, cache, score = case(13, [9001, 700, 2500], 16, 4, 1024)
+    d = [x.to(DEV) for x in (cache, score, torch.tensor(n, dtype=torch.int32), table)]
+    for dst in (None, d[0]):
+        here = [x.clone() for x in d]
+        if dst is not None:
+            dst = here[0]
+        lengths, kept = sv.kv_evict(*here, 2000, 4, 64, out_cache=dst, out_table=here[3],
+                                    with_kept=True)
+        assert sv.kv_evict_error()[0] == 0
+        own = [x.clone() for x in d]
+        want_lengths, want_kept = sv.kv_evict(*own, 2000, 4, 64, with_kept=True)
+        assert torch.equal(lengths, want_lengths) and torch.equal(kept, want_kept)
+        assert np.array_equal(bits(here[0]), bits(own[0])) and torch.equal(here[1], own[1])
