@@ -18,12 +18,18 @@
 // cut further, since nothing read is written.
 //
 // Measured, bf16, 36 layers of 2 x 1024 elements, pages of 16, 4 requests of 3001
-// to 9003 positions cut to 2000, in place: 394 us, of which the move 6.0 TB/s.  One
-// of 1041 positions cut to 512, 4 layers: 16 us, most of it the select's chain of
-// four histograms.  Positions a thread and round of the select: 1, 2, 4 and
-// 8 take it 9.9, 8.7, 10.5 and 13.4 us at 1041 positions, 20, 18, 19 and 21 at
-// 9003, the call 50, 47 and 43 us (1, 2, 4) at 30965.  Adding up a warp's equal
-// first digits by a match before the histogram cost 6 us there.
+// to 9003 positions cut to 2000, into other pages: 394 us, of which the move 6.0
+// TB/s.  One of 1041 positions cut to 512, 4 layers: 16 us, most of it the select's
+// chain of four histograms.  In place 4 of 3601 to 9003 positions take 766 us (3.1
+// TB/s) and that one 165: a group of lanes walks all positions of its slice, a chain
+// of dependent rounds of eight, and the one request has 32 warps in all.  (Slices
+// cut down to 128 bytes in place leave the number of threads and these times as
+// they are, and cost entries of 1040 bytes 737 -> 770 us.)
+// Positions a thread and round of the select: 1, 2, 4 and 8 take it 9.9, 8.7, 10.5
+// and 13.4 us at 1041 positions, 20, 18, 19 and 21 at 9003, the call 50, 47 and 43
+// us (1, 2, 4) at 30965: two win 1 to 2 us over four at the shorter lengths and lose
+// 4 at the longest.  Adding up a warp's equal first digits by a match before the
+// histogram cost 6 us there.
 #include "sv_internal.cuh"
 
 namespace sv {
@@ -335,15 +341,10 @@ cudaError_t launch_evict(const sv_kv_cache& src, const int32_t* src_table, int s
   A.range = reinterpret_cast<int2*>(w + o);
   o += align256(sizeof(int2) * size_t(B));
   A.kept = out_kept ? out_kept : reinterpret_cast<int32_t*>(w + o);
-  // 512-byte slices, halved while there are too few groups to fill the SMs
-  // (in place a slice's positions are walked by one group)
+  // slices of 512 bytes, a warp's, or of what covers a shorter entry
   const int64_t target = int64_t(sms) * (kMoveThreads / 32) * 4;  // warps
   int slice = 512;
   while (slice > 16 && slice / 2 >= A.entry_bytes) slice /= 2;
-  if (in_place)
-    while (slice > 128 &&
-           int64_t(B) * A.planes * ((A.entry_bytes + slice - 1) / slice) * (slice / 16) / 32 < target)
-      slice /= 2;
   A.slice_bytes = slice;
   A.slices = int((A.entry_bytes + slice - 1) / slice);
   const int64_t warps = int64_t(B) * A.planes * A.slices * (slice / 16) / 32 + 1;
