@@ -815,7 +815,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int row_at = s.R.at0 + (s.row0 + r) / A.G;
         const int lo = max(part0 * TN, A.window > 0 ? max(0, row_at - A.window + 1) : 0);
         const int hi = min(part1 * TN, min(row_at + 1, s.R.hi));
-        for (int p = lo; p < hi; ++p) {
+        for (int p = lo; p < hi && seen != 3; ++p) {
           if (p == in0 * TN) p = in1 * TN;
           const uint16_t* x = p < hi ? value_of(p) : nullptr;
           if (x) seen |= value_signs<T>(x[d]);

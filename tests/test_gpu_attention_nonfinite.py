@@ -122,3 +122,23 @@ def test_infinite_values_that_only_the_last_columns_of_a_tile_see(dtype, D, k, G
     put(c, 1, 40, 6, math.inf)         # in front of the window: seen by none
     args, sp = c.gpu()
     expect(c, *sv.attention(*args, sp, window=15), window=15)
+
+
+@pytest.mark.parametrize("dtype,D,G,k,window", [(B16, 256, 4, 32, 900), (B16, 128, 4, 0, 0),
+                                                (F16, 64, 16, 32, 700)])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+def test_nothing_but_infinite_or_nan_values(dtype, D, G, k, window, value):
+    # every row and column takes the second look, which has to end in a wait's time
+    n, Hk, S = 40000, 2, 16
+    g = torch.Generator(device=DEV).manual_seed(1)
+    cache = torch.randn(n // S, 1, 2, S, Hk * D, device=DEV, generator=g).to(dtype)
+    spec = torch.randn(1, k + 1, 1, 2, Hk * D, device=DEV, generator=g).to(dtype)
+    cache[:, :, 1], spec[:, :, :, 1] = value, value
+    q = torch.randn(k + 1, Hk * G, D, device=DEV, generator=g).to(dtype)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    out, lse = sv.attention(q, cache, 0, torch.tensor([n], **i32),
+                            torch.arange(n // S, **i32)[None], torch.tensor([k], **i32), spec,
+                            window=window)
+    assert sv.attention_error()[0] == 0
+    assert torch.isfinite(lse).all()
+    assert (torch.isnan(out) if math.isnan(value) else out == value).all()
