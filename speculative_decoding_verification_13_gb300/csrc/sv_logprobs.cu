@@ -23,10 +23,10 @@
 // 205 us without; element by element 266 us.
 //
 // Alternatives without keeping candidates during the pass: each thread
-// remembers the maximum of each sixteenth of its elements (a cell).  The 4
+// remembers the maximum of each eighth of its elements (a cell).  The 4
 // (8 where n > 24) largest thread maxima of every warp are elements of the row,
 // so the n-th largest of them bounds the row's n-th largest from below; only cells that
-// reach it are read again (little more than n of 4096 on random logits), and the
+// reach it are read again (little more than n of 2048 on random logits), and the
 // elements that reach it are ranked by (logit, index).  Parts where more cells
 // or elements than there is room for reach the bound (long ties) are scanned
 // once more by the warps, each keeping its 32 best in order.
