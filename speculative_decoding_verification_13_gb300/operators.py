@@ -6,8 +6,9 @@ given tokens with their gradient.
 Like the rest of the binding this only marshals arguments.  Calls are
 asynchronous on ``stream`` (default: the current stream) and allocate only
 their outputs and, once per stream, a workspace.  Data errors are found by the
-kernels and read back with the ``*_error`` functions.  Nothing here is recorded
-by autograd: the gradient of :func:`logprobs` is :func:`logprobs_grad`.
+kernels and read back with the ``*_error`` functions.  Calls may come from any
+thread.  Nothing here is recorded by autograd, also where an input requires a
+gradient: the gradient of :func:`logprobs` is :func:`logprobs_grad`.
 """
 
 from __future__ import annotations
@@ -278,7 +279,7 @@ def attention(q, cache, layer, kv_len, block_table, k_per_req, spec=None, *, sca
     own, with ``window`` > 0 only the last ``window`` of them.
 
     Returns ``(out [rows, q_heads, D], lse [rows, q_heads] float32)``; a token
-    that sees nothing has out 0 and lse -inf."""
+    that sees nothing has out 0 and lse -inf.  They carry no autograd history."""
     dev, dtype, B, rows, Hq, D, args = _attention_args(q, cache, layer, kv_len, block_table,
                                                        k_per_req, spec, scale, window)
     if out is None:
@@ -392,7 +393,12 @@ def logprobs(logits, tokens, temperature=None, n_top=0, *, stream=None):
     or None, 0 standing for 1.  Returns a :class:`LogProbs`: logprob, entropy,
     max, logsum [rows] float32 and top_tokens, top_logprobs [rows, n_top] (None
     without n_top; ties go to the lowest index; -1 and -inf where a row has
-    fewer tokens of nonzero probability)."""
+    fewer tokens of nonzero probability).
+
+    The results carry no autograd history, also where the logits require a
+    gradient: a loss made of them is constant to autograd.  Its gradient is
+    :func:`logprobs_grad`, to be handed to ``logits.backward`` (or
+    ``torch.autograd.backward`` next to a loss's other terms)."""
     x, dev, R, _ = _rows_desc(logits)
     t_ptr = _vector(tokens, "tokens", torch.int32, R, dev, optional=True)
     T_ptr = _vector(temperature, "temperature", torch.float32, R, dev, optional=True)
