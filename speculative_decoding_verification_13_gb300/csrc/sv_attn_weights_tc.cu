@@ -22,9 +22,9 @@
 // stay as they are.
 //
 // Measured, bf16, 8 KV heads of 128 with 4 query heads each, pages of 16: 32
-// requests of 2001 to 8190 positions with up to 15 drafts 61 us (4.9 TB/s; one row
+// requests of 2001 to 8190 positions with up to 15 drafts 58 us (5.2 TB/s; one row
 // warp with an address per copy 299, three with branches in their loops 70); 24
-// of 500 to 9001, one token, 35 us (4.2 TB/s, of which about 8 us until the first
+// of 500 to 9001, one token, 34 us (4.5 TB/s, of which about 8 us until the first
 // product).
 #include "sv_attn_tc.cuh"
 
