@@ -25,6 +25,7 @@ from . import SV_BF16, SV_F32, SV_OK, SpecVerifyError, _KvCache, _Logits, _check
 SV_F16 = 2
 SV_LOGPROBS_TOP_MAX = 32
 SV_HEAD_DIM_MAX = 256
+_INT_MAX = 2 ** 31 - 1
 
 _DTYPES = {torch.float32: SV_F32, torch.bfloat16: SV_BF16, torch.float16: SV_F16}
 
@@ -260,7 +261,7 @@ def _attention_args(q, cache, layer, kv_len, block_table, k_per_req, spec, scale
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     return dev, dtype, B, rows, Hq, D, (
         ctypes.byref(desc), code, layer, E // D, q.data_ptr(), ts, hs, Hq, rows, s_ptr, slots,
-        k_ptr, n_ptr, t_ptr, cols, scale, window)
+        k_ptr, n_ptr, t_ptr, cols, scale, min(window, _INT_MAX))   # a wider one hides nothing
 
 
 # ------------------------------------------------------------------ operators
@@ -340,8 +341,8 @@ def kv_evict(cache, score, kv_len, block_table, budget, sinks=0, recent=0, *, ou
     B = kv_len.shape[0]
     n_ptr = _vector(kv_len, "kv_len", torch.int32, B, dev)
     t_ptr, cols = _table(block_table, "block_table", B, dev)
-    if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget:
-        raise ValueError("budget must be positive and hold sinks and recent")
+    if not 1 <= budget <= _INT_MAX or sinks < 0 or recent < 0 or sinks + recent > budget:
+        raise ValueError("budget must be positive, below 2^31 and hold sinks and recent")
     s_ptr, stride, score_cols = _rows2d(score, "score", torch.float32, B, dev)
     if out_score is None:
         out_score = score
