@@ -86,6 +86,12 @@ extern "C" {
                                     /* missing from its block table               */
 #define SV_ERR_DATA_LENGTH 28       /* attention, eviction: kv_len negative or    */
                                     /* longer than the block table or the scores  */
+#define SV_ERR_DATA_TREE 29         /* a node's parent that is not an earlier     */
+                                    /* node; KV commit: a path with no such node  */
+#define SV_ERR_DATA_POOL 30         /* reservation: too few free pages for the    */
+                                    /* request; of the whole call: a free count   */
+                                    /* below 0, or past its list with what is     */
+                                    /* given back                                 */
 
 /* ---- limits -------------------------------------------------------------- */
 #define SV_MAX_K 32              /* drafts per request (one warp ballot)       */
@@ -95,6 +101,7 @@ extern "C" {
 #define SV_VOCAB_MAX (1 << 22)   /* largest vocabulary                         */
 #define SV_LOGPROBS_TOP_MAX 32   /* most alternatives per row (spec_logprobs)  */
 #define SV_HEAD_DIM_MAX 256      /* largest attention head (spec_attention)    */
+#define SV_TREE_MAX_K 63         /* drafts per request where they are a tree   */
 
 typedef enum { SV_F32 = 0, SV_BF16 = 1, SV_F16 = 2 } sv_dtype; /* logits: the first two */
 
@@ -299,6 +306,23 @@ int spec_kv_commit(const sv_kv_cache* cache, const void* spec, int32_t spec_slot
                    const int32_t* block_table, int32_t max_pages, void* stream, int32_t batch,
                    void* workspace, size_t workspace_bytes);
 
+/* The same for a tree of drafts (spec_verify_tree_greedy): of request b the
+ * entries path[t_off[b]] .. path[t_off[b] + L] are written, in this order, to
+ * positions kv_len[b] .. kv_len[b] + L, and k_b <= SV_TREE_MAX_K.
+ *   path       [rows] int32, rows = sum (k_b + 1), the layout of target rows
+ *   workspace  >= spec_kv_commit_path_workspace_size(batch) bytes
+ * A k_b outside [0, SV_TREE_MAX_K] or sum (k_b + 1) != rows leaves the whole
+ * batch untouched (SV_ERR_DATA_K / SV_ERR_DATA_ROWS); a request with a node
+ * outside [0, k_b] or not below spec_slots on its path fails with
+ * SV_ERR_DATA_TREE. */
+size_t spec_kv_commit_path_workspace_size(int32_t batch);
+
+int spec_kv_commit_path(const sv_kv_cache* cache, const void* spec, int32_t spec_slots,
+                        const int32_t* accept_len, const int32_t* k_per_req, const int32_t* path,
+                        int64_t rows, int32_t* kv_len, const int32_t* block_table,
+                        int32_t max_pages, void* stream, int32_t batch, void* workspace,
+                        size_t workspace_bytes);
+
 /* ---- LM-head GEMM with fused verification statistics ----------------------
  * The target's logits are its final hidden states times the unembedding
  * matrix, z = H W^T ("FlashMap: Flow Map Speculative Decoding…", section 1),
@@ -351,6 +375,33 @@ int spec_verify_greedy_from_argmax(const int32_t* target_argmax, const int32_t* 
                                    int32_t* out_tokens, void* stream, int32_t batch,
                                    int64_t target_rows, int32_t vocab, void* workspace,
                                    size_t workspace_bytes);
+
+/* ---- greedy verification of a tree of drafts --------------------------------
+ * Node 0 of a request is its last emitted token, nodes 1 .. k_b are its drafts,
+ * and draft j hangs from the earlier node parent[t_off[b] + j].  The walk begins
+ * at node 0 and goes on to the child whose token is the target's argmax at the
+ * node it is at (the lowest such child) until there is none: the rule of
+ * spec_verify at temperature 0 on the branch that the target takes.
+ *   target_argmax, parent [R_t] int32, rows t_off[b] + j of node j; node 0's
+ *                  parent is not read
+ *   draft_tokens   [R_t - B] int32, d_off[b] + j - 1 of node j
+ *   out_accept_len [B] int32 (L drafts, or -1)
+ *   out_tokens     [R_t] int32: the L accepted tokens and the argmax at the last
+ *                  node, then -1
+ *   out_path       [R_t] int32: the L + 1 nodes of the walk, then -1
+ *   workspace      >= spec_verify_tree_greedy_workspace_size(batch) bytes
+ * A k outside [0, SV_TREE_MAX_K] or sum(k + 1) != R_t fails the whole batch (all
+ * outputs -1, SV_ERR_DATA_K / SV_ERR_DATA_ROWS); a parent that is not an earlier
+ * node (SV_ERR_DATA_TREE), a token or argmax outside [0, V) (SV_ERR_DATA_TOKEN)
+ * fails its request.  Same ownership, stream and error conventions as
+ * spec_verify; with batch 0 nothing is launched or written. */
+size_t spec_verify_tree_greedy_workspace_size(int32_t batch);
+
+int spec_verify_tree_greedy(const int32_t* target_argmax, const int32_t* draft_tokens,
+                            const int32_t* parent, const int32_t* k_per_req,
+                            int32_t* out_accept_len, int32_t* out_tokens, int32_t* out_path,
+                            void* stream, int32_t batch, int64_t target_rows, int32_t vocab,
+                            void* workspace, size_t workspace_bytes);
 
 /* ---- adaptive speculation length -------------------------------------------
  * "Speculative decoding and multi-token prediction", section "Acceptance rate
@@ -415,6 +466,117 @@ int spec_attention(const sv_kv_cache* cache, int32_t dtype, int32_t layer, int32
                    const int32_t* kv_len, const int32_t* block_table, int32_t max_pages,
                    float scale, int32_t window, void* out, float* lse, void* stream,
                    int32_t batch, void* workspace, size_t workspace_bytes);
+
+/* The same over a tree of drafts: node j of request b (node 0 the last emitted
+ * token) hangs from the earlier node parent[t_off[b] + j], lies one position
+ * behind it (node 0 at kv_len[b]), and sees the cached positions, its ancestors
+ * and itself, with window W > 0 only the last W of them.  k_b <= SV_TREE_MAX_K,
+ * and `spec`, entry j of node j, is needed.  A request whose tree has a parent
+ * that is no earlier node gets NaN rows (SV_ERR_DATA_TREE); node 0's parent is
+ * not read.  All else as in spec_attention. */
+size_t spec_tree_attention_workspace_size(int32_t batch, int32_t head_dim);
+
+int spec_tree_attention(const sv_kv_cache* cache, int32_t dtype, int32_t layer, int32_t kv_heads,
+                        const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                        int32_t q_heads, int64_t rows, const void* spec, int32_t spec_slots,
+                        const int32_t* k_per_req, const int32_t* parent, const int32_t* kv_len,
+                        const int32_t* block_table, int32_t max_pages, float scale, int32_t window,
+                        void* out, float* lse, void* stream, int32_t batch, void* workspace,
+                        size_t workspace_bytes);
+
+/* ---- attention over packed prompts -----------------------------------------
+ * Causal attention within each of B sequences that lie one behind another in the
+ * rows of q, k and v; sequence b has rows offsets[b] .. offsets[b + 1] - 1.  For
+ * its token i and head hq, whose keys are those of KV head h = hq / G with
+ * G = q_heads / kv_heads:
+ *   s_j = scale * q_i . k_j        lse = ln sum_j exp(s_j)
+ *   out = sum_j exp(s_j - lse) v_j
+ * over its tokens j <= i, with window W > 0 only the last W of them.
+ *   q        [rows, q_heads, D], k, v [rows, kv_heads, D] of `dtype` (sv_dtype),
+ *            element strides of row and head, D contiguous, any alignment
+ *   offsets  [B + 1] int32
+ *   out      [rows, q_heads, D], contiguous;  lse  [rows, q_heads] float
+ *   workspace >= spec_prompt_attention_workspace_size(batch) bytes, 256-byte
+ *            aligned (its size depends on the current device's SM count)
+ * Rows of no sequence are neither read into a result nor written.  Infinite and
+ * NaN keys and values reach the tokens that see them only; such a value where the
+ * type holds no weight but 0 gives NaN.  Offsets that descend or leave [0, rows]
+ * fail the whole batch (SV_ERR_DATA_ROWS, every output NaN).  rows < 2^31 - 256.
+ * Results do not depend on the run.  Same ownership, stream and error
+ * conventions as spec_verify; with rows or batch 0 nothing is launched. */
+size_t spec_prompt_attention_workspace_size(int32_t batch);
+
+int spec_prompt_attention(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                          const void* k, int64_t k_row_stride, int64_t k_head_stride,
+                          const void* v, int64_t v_row_stride, int64_t v_head_stride,
+                          int32_t dtype, int64_t rows, int32_t q_heads, int32_t kv_heads,
+                          int32_t head_dim, const int32_t* offsets, float scale, int32_t window,
+                          void* out, float* lse, void* stream, int32_t batch, void* workspace,
+                          size_t workspace_bytes);
+
+/* ---- block tables from the requests' lengths ---------------------------------
+ * Gives every request the pages for length[b] positions: need[b] = ceil(length[b]
+ * / page_size) entries of its table row instead of held[b].  The free pages are a
+ * stack, free_pages[0 .. *free_count - 1].
+ *   - Columns need[b] .. held[b] - 1 of requests that hold more become -1, and
+ *     their pages go onto the stack in the order of the requests and columns.
+ *   - Requests that need more take pages off its end, request by request and
+ *     column by column, as long as what is wanted so far is there: a request from
+ *     which on it is not, and those behind it that want any, keep what they hold
+ *     (SV_ERR_DATA_POOL).
+ *   - Entries of the list from the new count up to the old one become -1; those
+ *     past both stay as they are.
+ *   table, out_table      [B, max_pages] int32; held, out_held, length [B] int32
+ *   free_pages, out_free  [capacity] int32; free_count, out_count [1] int32
+ *   workspace             >= spec_kv_reserve_workspace_size(batch, capacity)
+ * An output may be its input (in place) or a buffer of its own, which then gets
+ * the whole contents.  A request with held or need outside [0, max_pages] or a
+ * negative length is left as it is (SV_ERR_DATA_LENGTH).  A free count below 0,
+ * or above the capacity with what is given back, changes nothing for the whole
+ * batch (SV_ERR_DATA_POOL, request -1).  Same conventions as spec_verify; with
+ * batch 0 nothing is launched or written. */
+size_t spec_kv_reserve_workspace_size(int32_t batch, int64_t capacity);
+
+int spec_kv_reserve(const int32_t* table, int32_t* out_table, int32_t max_pages,
+                    const int32_t* held, int32_t* out_held, const int32_t* length,
+                    const int32_t* free_pages, int32_t* out_free, int64_t capacity,
+                    const int32_t* free_count, int32_t* out_count, int32_t page_size,
+                    void* stream, int32_t batch, void* workspace, size_t workspace_bytes);
+
+/* ---- slots of a step's new tokens ---------------------------------------------
+ * Row r of a step that appends count[b] tokens to request b, request by request
+ * (offsets[b] = sum of the counts before it), is token start[b] + r - offsets[b]
+ * of the request and lies in slot page * page_size + position % page_size.
+ *   out_slots    [rows] int64, -1 for rows past the last token
+ *   out_request, out_position  [rows] int32, -1 there
+ *   out_offsets  [B + 1] int32, as spec_prompt_attention takes them
+ *   workspace    >= spec_kv_slots_workspace_size(batch, rows)
+ * A request with a negative start or count, or with positions past its table row,
+ * has slots -1 (SV_ERR_DATA_LENGTH; a negative count is none); so has a row whose
+ * page is missing (SV_ERR_DATA_PAGE).  More tokens than rows fail the batch (every
+ * row -1, SV_ERR_DATA_ROWS).  Same conventions as spec_verify. */
+size_t spec_kv_slots_workspace_size(int32_t batch, int64_t rows);
+
+int spec_kv_slots(const int32_t* block_table, int32_t max_pages, const int32_t* start,
+                  const int32_t* count, int64_t rows, int32_t page_size, int64_t* out_slots,
+                  int32_t* out_request, int32_t* out_position, int32_t* out_offsets, void* stream,
+                  int32_t batch, void* workspace, size_t workspace_bytes);
+
+/* ---- keys and values into their slots -------------------------------------------
+ * cache[slot / page_size, layer, 0 | 1, slot % page_size] = k | v of each row.
+ *   k, v       [rows, kv_heads, D] of the cache's type, element strides of row and
+ *              head, D contiguous, any alignment
+ *   slots      [rows] int64, none twice; -1: the row is not written
+ *   workspace  >= spec_kv_write_workspace_size(rows) bytes
+ * A row with any other slot outside the pool is not written (SV_ERR_DATA_PAGE, and
+ * its row).  Of two rows with one slot either may stay, in pieces.  Same conventions
+ * as spec_verify; with rows 0 nothing is launched. */
+size_t spec_kv_write_workspace_size(int64_t rows);
+
+int spec_kv_write(const sv_kv_cache* cache, int32_t layer, int32_t kv_heads, const void* k,
+                  int64_t k_row_stride, int64_t k_head_stride, const void* v,
+                  int64_t v_row_stride, int64_t v_head_stride, const int64_t* slots, int64_t rows,
+                  void* stream, void* workspace, size_t workspace_bytes);
 
 /* ---- accumulated attention weights -----------------------------------------
  * How much each cached position is attended to, for spec_kv_evict:

@@ -32,7 +32,10 @@ __all__ = ["verify", "Verifier", "workspace_size", "get_error", "dump_rows", "st
            "adapt_k", "verify_greedy_from_argmax", "verify_greedy_error",
            "attention", "attention_error", "attention_weights", "attention_weights_error",
            "kv_evict", "kv_evict_error", "logprobs", "logprobs_error", "logprobs_grad",
-           "LogProbs", "SV_LOGPROBS_TOP_MAX", "SV_HEAD_DIM_MAX"]
+           "prompt_attention", "prompt_attention_error", "tree_attention", "tree_attention_error",
+           "verify_tree_greedy", "verify_tree_greedy_error", "kv_reserve", "kv_reserve_error",
+           "kv_slots", "kv_slots_error", "kv_write", "kv_write_error", "Reservation", "Slots",
+           "SV_TREE_MAX_K", "LogProbs", "SV_LOGPROBS_TOP_MAX", "SV_HEAD_DIM_MAX"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_lib", "libspecverify.so")
@@ -50,7 +53,8 @@ ERROR_NAMES = {
     18: "SV_ERR_DATA_TOP_P", 19: "SV_ERR_DATA_TOP_K", 20: "SV_ERR_DATA_TOKEN",
     21: "SV_ERR_DATA_ROWS", 22: "SV_ERR_DATA_LOGIT", 23: "SV_ERR_DATA_NO_DRAFT",
     24: "SV_ERR_TIMEOUT", 25: "SV_ERR_INTERNAL", 26: "SV_ERR_DATA_ACCEPT",
-    27: "SV_ERR_DATA_PAGE", 28: "SV_ERR_DATA_LENGTH",
+    27: "SV_ERR_DATA_PAGE", 28: "SV_ERR_DATA_LENGTH", 29: "SV_ERR_DATA_TREE",
+    30: "SV_ERR_DATA_POOL",
 }
 
 
@@ -130,6 +134,11 @@ def load_library():
             lib.spec_kv_commit.restype = ctypes.c_int
             lib.spec_kv_commit.argtypes = [ctypes.POINTER(_KvCache), P, i32, P, P, P, P, i32, P,
                                            i32, P, sz]
+            lib.spec_kv_commit_path_workspace_size.restype = sz
+            lib.spec_kv_commit_path_workspace_size.argtypes = [i32]
+            lib.spec_kv_commit_path.restype = ctypes.c_int
+            lib.spec_kv_commit_path.argtypes = [ctypes.POINTER(_KvCache), P, i32, P, P, P, i64, P,
+                                                P, i32, P, i32, P, sz]
             _lib = lib
     return _lib
 
@@ -477,13 +486,16 @@ def lmhead_stats_error(stream=None, device=None):
 _kv_ws = {}
 
 
-def kv_commit(cache, spec, accept_len, k_per_req, kv_len, block_table, stream=None):
+def kv_commit(cache, spec, accept_len, k_per_req, kv_len, block_table, stream=None, *, path=None):
     """Append the accepted K/V entries after verification (in place).
 
     cache: [num_pages, n_layers, 2, page_size, E] CUDA tensor (2- or 4-byte
     elements); spec: [B, spec_slots, n_layers, 2, E], same dtype; accept_len,
     k_per_req: [B] int32 (accept_len from verify, -1 = leave untouched);
-    kv_len: [B] int32, updated in place; block_table: [B, max_pages] int32."""
+    kv_len: [B] int32, updated in place; block_table: [B, max_pages] int32.
+    path: [rows] int32, of a tree of drafts the accepted nodes as
+    :func:`verify_tree_greedy` returns them (without it the drafts are a chain and
+    the entries 0 .. accept_len)."""
     lib = load_library()
     for t, n in ((accept_len, "accept_len"), (k_per_req, "k_per_req"), (kv_len, "kv_len")):
         _check(t, n, torch.int32)
@@ -500,10 +512,25 @@ def kv_commit(cache, spec, accept_len, k_per_req, kv_len, block_table, stream=No
         raise ValueError("spec must be [B, slots, n_layers, 2, E] matching the cache")
     desc = _KvCache(cache.data_ptr(), P_, L_, S_, E_, cache.element_size())
     dev = cache.device.index if cache.device.index is not None else torch.cuda.current_device()
-    need = int(lib.spec_kv_commit_workspace_size(B))
+    if path is not None:
+        _check(path, "path", torch.int32)
+        if path.device != cache.device:
+            raise ValueError(f"path is on {path.device}, the cache on {cache.device}")
+        need = int(lib.spec_kv_commit_path_workspace_size(B))
+    else:
+        need = int(lib.spec_kv_commit_workspace_size(B))
     ws = _kv_ws.get(dev)
     if ws is None or ws.numel() < need:
         ws = _kv_ws[dev] = torch.empty(max(need, 256), dtype=torch.uint8, device=cache.device)
+    if path is not None:
+        rc = lib.spec_kv_commit_path(ctypes.byref(desc), _ptr(spec), slots, _ptr(accept_len),
+                                     _ptr(k_per_req), _ptr(path), path.numel(), _ptr(kv_len),
+                                     _ptr(block_table),
+                                     int(block_table.shape[1]) if block_table is not None else 0,
+                                     _stream_handle(stream), B, _ptr(ws), ws.numel())
+        if rc != SV_OK:
+            raise SpecVerifyError(rc, "spec_kv_commit_path")
+        return kv_len
     rc = lib.spec_kv_commit(ctypes.byref(desc), _ptr(spec), slots, _ptr(accept_len),
                             _ptr(k_per_req), _ptr(kv_len), _ptr(block_table),
                             int(block_table.shape[1]) if block_table is not None else 0,
@@ -629,3 +656,7 @@ def verify_noalloc(target, draft, draft_tokens, k_per_req, temperature, uniforms
 from .operators import (LogProbs, SV_HEAD_DIM_MAX, SV_LOGPROBS_TOP_MAX, attention,  # noqa: E402
                         attention_error, attention_weights, attention_weights_error, kv_evict,
                         kv_evict_error, logprobs, logprobs_error, logprobs_grad)
+from .prompts import (Reservation, SV_TREE_MAX_K, Slots, kv_reserve, kv_reserve_error,  # noqa: E402
+                      kv_slots, kv_slots_error, kv_write, kv_write_error, prompt_attention,
+                      prompt_attention_error, tree_attention, tree_attention_error,
+                      verify_tree_greedy, verify_tree_greedy_error)

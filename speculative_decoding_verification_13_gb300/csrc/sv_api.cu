@@ -14,6 +14,7 @@
 
 #include "sv_attn.cuh"
 #include "sv_internal.cuh"
+#include "sv_prompt.cuh"
 
 namespace sv {
 cudaError_t rowpass_configure();
@@ -135,6 +136,7 @@ int attn_args(const sv_kv_cache* cache, int32_t dtype, int32_t layer, int32_t kv
   A.window = window < kMaxPositions ? window : 0;  // a wider one hides nothing
   A.Rt = rows;
   A.scale2 = scale * 1.4426950408889634f;
+  A.max_k = SV_MAX_K;
   A.test_expire = g_expire_wait.load(std::memory_order_relaxed);
   *out = A;
   return SV_OK;
@@ -336,13 +338,18 @@ int spec_draft_sample(const sv_logits* draft_logits, const int32_t* k_per_req,
 }
 
 size_t spec_kv_commit_workspace_size(int32_t batch) {
-  return batch < 0 ? 0 : kv_workspace_bytes(batch);
+  return batch < 0 ? 0 : kv_workspace_bytes(batch, SV_MAX_K);
 }
 
-int spec_kv_commit(const sv_kv_cache* cache, const void* spec, int32_t spec_slots,
-                   const int32_t* accept_len, const int32_t* k_per_req, int32_t* kv_len,
-                   const int32_t* block_table, int32_t max_pages, void* stream, int32_t batch,
-                   void* workspace, size_t workspace_bytes) {
+size_t spec_kv_commit_path_workspace_size(int32_t batch) {
+  return batch < 0 ? 0 : kv_workspace_bytes(batch, SV_TREE_MAX_K);
+}
+
+static int kv_commit(const sv_kv_cache* cache, const void* spec, int32_t spec_slots,
+                     const int32_t* accept_len, const int32_t* k_per_req, const int32_t* path,
+                     int64_t rows, int max_k, int32_t* kv_len, const int32_t* block_table,
+                     int32_t max_pages, void* stream, int32_t batch, void* workspace,
+                     size_t workspace_bytes) {
   if (!cache || batch < 0 || spec_slots < 1 || max_pages < 0) return SV_ERR_ARG;
   const sv_kv_cache& c = *cache;
   if (c.num_pages < 0 || c.n_layers < 1 || c.page_size < 1 || c.entry_elems < 1 ||
@@ -350,7 +357,8 @@ int spec_kv_commit(const sv_kv_cache* cache, const void* spec, int32_t spec_slot
     return SV_ERR_ARG;
   const int64_t entry_bytes = int64_t(c.entry_elems) * c.elem_bytes;
   if (entry_bytes % 16 != 0) return SV_ERR_UNSUPPORTED;
-  if (!workspace || misaligned(workspace, 256) || workspace_bytes < kv_workspace_bytes(batch))
+  if (!workspace || misaligned(workspace, 256) ||
+      workspace_bytes < kv_workspace_bytes(batch, max_k))
     return SV_ERR_WORKSPACE;
   if (batch == 0) return SV_OK;
   if (!c.data || !spec || !accept_len || !k_per_req || !kv_len || (max_pages > 0 && !block_table))
@@ -362,9 +370,28 @@ int spec_kv_commit(const sv_kv_cache* cache, const void* spec, int32_t spec_slot
     return SV_ERR_CUDA;
   if (launch_kv_commit(c.data, spec, c.num_pages, c.n_layers, c.page_size, entry_bytes,
                        spec_slots, accept_len, k_per_req, kv_len, block_table, max_pages, batch,
-                       workspace, sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+                       path, rows, max_k, workspace, sms,
+                       static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return SV_ERR_CUDA;
   return SV_OK;
+}
+
+int spec_kv_commit(const sv_kv_cache* cache, const void* spec, int32_t spec_slots,
+                   const int32_t* accept_len, const int32_t* k_per_req, int32_t* kv_len,
+                   const int32_t* block_table, int32_t max_pages, void* stream, int32_t batch,
+                   void* workspace, size_t workspace_bytes) {
+  return kv_commit(cache, spec, spec_slots, accept_len, k_per_req, nullptr, 0, SV_MAX_K, kv_len,
+                   block_table, max_pages, stream, batch, workspace, workspace_bytes);
+}
+
+int spec_kv_commit_path(const sv_kv_cache* cache, const void* spec, int32_t spec_slots,
+                        const int32_t* accept_len, const int32_t* k_per_req, const int32_t* path,
+                        int64_t rows, int32_t* kv_len, const int32_t* block_table,
+                        int32_t max_pages, void* stream, int32_t batch, void* workspace,
+                        size_t workspace_bytes) {
+  if (rows < batch || rows >= INT_MAX || (batch > 0 && !path)) return SV_ERR_ARG;
+  return kv_commit(cache, spec, spec_slots, accept_len, k_per_req, path, rows, SV_TREE_MAX_K,
+                   kv_len, block_table, max_pages, stream, batch, workspace, workspace_bytes);
 }
 
 size_t spec_lmhead_stats_workspace_size(int32_t rows, int32_t vocab) {
@@ -429,12 +456,55 @@ int spec_verify_greedy_from_argmax(const int32_t* target_argmax, const int32_t* 
              : SV_ERR_CUDA;
 }
 
+size_t spec_verify_tree_greedy_workspace_size(int32_t batch) {
+  return batch < 0 ? 0 : tree_greedy_workspace_bytes(batch);
+}
+
+int spec_verify_tree_greedy(const int32_t* target_argmax, const int32_t* draft_tokens,
+                            const int32_t* parent, const int32_t* k_per_req,
+                            int32_t* out_accept_len, int32_t* out_tokens, int32_t* out_path,
+                            void* stream, int32_t batch, int64_t target_rows, int32_t vocab,
+                            void* workspace, size_t workspace_bytes) {
+  if (batch < 0 || target_rows < batch || vocab < 1 || target_rows >= INT_MAX) return SV_ERR_ARG;
+  if (!workspace || misaligned(workspace, 256) ||
+      workspace_bytes < tree_greedy_workspace_bytes(batch))
+    return SV_ERR_WORKSPACE;
+  if (batch == 0) return SV_OK;
+  if (!target_argmax || !parent || !k_per_req || !out_accept_len || !out_tokens || !out_path ||
+      (target_rows > batch && !draft_tokens))
+    return SV_ERR_ARG;
+  return launch_tree_greedy(target_argmax, draft_tokens, parent, k_per_req, out_accept_len,
+                            out_tokens, out_path, batch, target_rows, vocab, workspace,
+                            static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
 void spec_test_expire_wait(int32_t n) { g_expire_wait.store(n, std::memory_order_relaxed); }
 
 size_t spec_attention_workspace_size(int32_t batch, int32_t head_dim) {
   const int sms = sm_count();
   if (batch < 0 || head_dim < 1 || head_dim > SV_HEAD_DIM_MAX || sms == 0) return 0;
   return attn_workspace_bytes(batch, head_dim, sms, false);
+}
+
+// What spec_attention and spec_tree_attention do with the arguments they have checked.
+static int attention_call(AttnArgs& A, int32_t dtype, void* out, float* lse, void* stream,
+                          void* workspace, size_t workspace_bytes) {
+  if (A.B == 0) return SV_OK;
+  if (!out || !lse) return SV_ERR_ARG;
+  if (!workspace || misaligned(workspace, 256)) return SV_ERR_WORKSPACE;
+  const int sms = sm_count();
+  if (sms == 0) return SV_ERR_CUDA;
+  if (workspace_bytes < attn_workspace_bytes(A.B, A.D, sms, false)) return SV_ERR_WORKSPACE;
+  A.out = out;
+  A.o_hs = A.D;
+  A.o_ts = int64_t(A.D) * A.Hq;
+  A.lse = lse;
+  return launch_attn(A, dtype, false, workspace, sms, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
 }
 
 int spec_attention(const sv_kv_cache* cache, int32_t dtype, int32_t layer, int32_t kv_heads,
@@ -448,18 +518,167 @@ int spec_attention(const sv_kv_cache* cache, int32_t dtype, int32_t layer, int32
                          rows, spec, spec_slots, k_per_req, kv_len, block_table, max_pages, scale,
                          window, batch, &A))
     return rc;
-  if (batch == 0) return SV_OK;
-  if (!out || !lse) return SV_ERR_ARG;
+  return attention_call(A, dtype, out, lse, stream, workspace, workspace_bytes);
+}
+
+size_t spec_tree_attention_workspace_size(int32_t batch, int32_t head_dim) {
+  return spec_attention_workspace_size(batch, head_dim);
+}
+
+int spec_tree_attention(const sv_kv_cache* cache, int32_t dtype, int32_t layer, int32_t kv_heads,
+                        const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                        int32_t q_heads, int64_t rows, const void* spec, int32_t spec_slots,
+                        const int32_t* k_per_req, const int32_t* parent, const int32_t* kv_len,
+                        const int32_t* block_table, int32_t max_pages, float scale, int32_t window,
+                        void* out, float* lse, void* stream, int32_t batch, void* workspace,
+                        size_t workspace_bytes) {
+  AttnArgs A;
+  if (int rc = attn_args(cache, dtype, layer, kv_heads, q, q_token_stride, q_head_stride, q_heads,
+                         rows, spec, spec_slots, k_per_req, kv_len, block_table, max_pages, scale,
+                         window, batch, &A))
+    return rc;
+  if (batch > 0 && (!spec || !parent)) return SV_ERR_ARG;
+  A.parent = parent;
+  A.max_k = SV_TREE_MAX_K;
+  return attention_call(A, dtype, out, lse, stream, workspace, workspace_bytes);
+}
+
+size_t spec_prompt_attention_workspace_size(int32_t batch) {
+  const int sms = sm_count();
+  return batch < 0 || sms == 0 ? 0 : prompt_workspace_bytes(batch, sms);
+}
+
+int spec_prompt_attention(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                          const void* k, int64_t k_row_stride, int64_t k_head_stride,
+                          const void* v, int64_t v_row_stride, int64_t v_head_stride,
+                          int32_t dtype, int64_t rows, int32_t q_heads, int32_t kv_heads,
+                          int32_t head_dim, const int32_t* offsets, float scale, int32_t window,
+                          void* out, float* lse, void* stream, int32_t batch, void* workspace,
+                          size_t workspace_bytes) {
+  if (batch < 0 || rows < 0 || rows >= INT_MAX - 255 || window < 0 || head_dim < 1 ||
+      kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0)
+    return SV_ERR_ARG;
+  if (dtype != SV_F32 && dtype != SV_BF16 && dtype != SV_F16) return SV_ERR_UNSUPPORTED;
+  if (!(scale > -INFINITY && scale < INFINITY)) return SV_ERR_ARG;
+  // (tiles of rows and heads are a grid's extents)
+  if (head_dim > SV_HEAD_DIM_MAX || kv_heads > 65535 ||
+      rows * (q_heads / kv_heads) / 64 + batch >= INT_MAX)
+    return SV_ERR_UNSUPPORTED;
+  if (rows == 0 || batch == 0) return SV_OK;
+  if (!q || !k || !v || !offsets || !out || !lse) return SV_ERR_ARG;
+  const size_t es = elem_size(dtype);
+  if (misaligned(q, es) || misaligned(k, es) || misaligned(v, es) || misaligned(out, es))
+    return SV_ERR_UNSUPPORTED;
   if (!workspace || misaligned(workspace, 256)) return SV_ERR_WORKSPACE;
   const int sms = sm_count();
   if (sms == 0) return SV_ERR_CUDA;
-  if (workspace_bytes < attn_workspace_bytes(batch, A.D, sms, false)) return SV_ERR_WORKSPACE;
+  if (workspace_bytes < prompt_workspace_bytes(batch, sms)) return SV_ERR_WORKSPACE;
+  PromptArgs A{};
+  A.q = q;
+  A.q_ts = q_row_stride;
+  A.q_hs = q_head_stride;
+  A.k = k;
+  A.k_ts = k_row_stride;
+  A.k_hs = k_head_stride;
+  A.v = v;
+  A.v_ts = v_row_stride;
+  A.v_hs = v_head_stride;
   A.out = out;
-  A.o_hs = A.D;
-  A.o_ts = int64_t(A.D) * q_heads;
   A.lse = lse;
-  return launch_attn(A, dtype, false, workspace, sms, static_cast<cudaStream_t>(stream)) ==
-                 cudaSuccess
+  A.offsets = offsets;
+  A.B = batch;
+  A.Hq = q_heads;
+  A.Hkv = kv_heads;
+  A.G = q_heads / kv_heads;
+  A.D = head_dim;
+  A.window = window < rows ? window : 0;   // a wider one hides nothing
+  A.rows = rows;
+  A.scale2 = scale * 1.4426950408889634f;
+  A.test_expire = g_expire_wait.load(std::memory_order_relaxed);
+  return launch_prompt(A, dtype, workspace, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
+size_t spec_kv_reserve_workspace_size(int32_t batch, int64_t capacity) {
+  return batch < 0 || capacity < 0 || capacity >= INT_MAX ? 0
+                                                          : reserve_workspace_bytes(batch, capacity);
+}
+
+int spec_kv_reserve(const int32_t* table, int32_t* out_table, int32_t max_pages,
+                    const int32_t* held, int32_t* out_held, const int32_t* length,
+                    const int32_t* free_pages, int32_t* out_free, int64_t capacity,
+                    const int32_t* free_count, int32_t* out_count, int32_t page_size,
+                    void* stream, int32_t batch, void* workspace, size_t workspace_bytes) {
+  if (batch < 0 || max_pages < 0 || page_size < 1 || capacity < 0 || capacity >= INT_MAX)
+    return SV_ERR_ARG;
+  if (!workspace || misaligned(workspace, 256) ||
+      workspace_bytes < reserve_workspace_bytes(batch, capacity))
+    return SV_ERR_WORKSPACE;
+  if (batch == 0) return SV_OK;
+  if ((max_pages > 0 && (!table || !out_table)) || !held || !out_held || !length ||
+      (capacity > 0 && (!free_pages || !out_free)) || !free_count || !out_count)
+    return SV_ERR_ARG;
+  const int sms = sm_count();
+  if (sms == 0) return SV_ERR_CUDA;
+  return launch_reserve(table, out_table, batch, max_pages, held, out_held, length, free_pages,
+                        out_free, capacity, free_count, out_count, page_size, workspace, sms,
+                        static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
+size_t spec_kv_slots_workspace_size(int32_t batch, int64_t rows) {
+  return batch < 0 || rows < 0 || rows >= INT_MAX ? 0 : slots_workspace_bytes(batch, rows);
+}
+
+int spec_kv_slots(const int32_t* block_table, int32_t max_pages, const int32_t* start,
+                  const int32_t* count, int64_t rows, int32_t page_size, int64_t* out_slots,
+                  int32_t* out_request, int32_t* out_position, int32_t* out_offsets, void* stream,
+                  int32_t batch, void* workspace, size_t workspace_bytes) {
+  if (batch < 0 || max_pages < 0 || page_size < 1 || rows < 0 || rows >= INT_MAX)
+    return SV_ERR_ARG;
+  if (!workspace || misaligned(workspace, 256) ||
+      workspace_bytes < slots_workspace_bytes(batch, rows))
+    return SV_ERR_WORKSPACE;
+  if (!out_offsets || (rows > 0 && (!out_slots || !out_request || !out_position)) ||
+      (batch > 0 && (!start || !count || (max_pages > 0 && !block_table))))
+    return SV_ERR_ARG;
+  if (misaligned(out_slots, 8)) return SV_ERR_UNSUPPORTED;
+  return launch_slots(block_table, batch, max_pages, start, count, rows, page_size, out_slots,
+                      out_request, out_position, out_offsets, workspace,
+                      static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
+size_t spec_kv_write_workspace_size(int64_t rows) {
+  const int sms = sm_count();
+  return rows < 0 || sms == 0 ? 0 : write_workspace_bytes(sms);
+}
+
+int spec_kv_write(const sv_kv_cache* cache, int32_t layer, int32_t kv_heads, const void* k,
+                  int64_t k_row_stride, int64_t k_head_stride, const void* v,
+                  int64_t v_row_stride, int64_t v_head_stride, const int64_t* slots, int64_t rows,
+                  void* stream, void* workspace, size_t workspace_bytes) {
+  if (!cache || rows < 0 || rows >= INT_MAX) return SV_ERR_ARG;
+  const sv_kv_cache& c = *cache;
+  if (c.num_pages < 0 || c.n_layers < 1 || c.page_size < 1 || c.entry_elems < 1 ||
+      (c.elem_bytes != 2 && c.elem_bytes != 4) || layer < 0 || layer >= c.n_layers ||
+      kv_heads < 1 || c.entry_elems % kv_heads != 0)
+    return SV_ERR_ARG;
+  if (rows == 0) return SV_OK;
+  if (!k || !v || !slots || (c.num_pages > 0 && !c.data)) return SV_ERR_ARG;
+  const size_t es = size_t(c.elem_bytes);
+  if (misaligned(c.data, es) || misaligned(k, es) || misaligned(v, es) || misaligned(slots, 8))
+    return SV_ERR_UNSUPPORTED;
+  const int sms = sm_count();
+  if (sms == 0) return SV_ERR_CUDA;
+  if (!workspace || misaligned(workspace, 256) || workspace_bytes < write_workspace_bytes(sms))
+    return SV_ERR_WORKSPACE;
+  return launch_write(c, layer, kv_heads, k, k_row_stride, k_head_stride, v, v_row_stride,
+                      v_head_stride, slots, rows, workspace, sms,
+                      static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? SV_OK
              : SV_ERR_CUDA;
 }
@@ -641,6 +860,8 @@ int spec_verify_get_error(const void* workspace, void* stream, int32_t* code, in
     size_t at = 0;
     while (at < n && st[at] == 0) ++at;
     int32_t c = at < n ? st[at] : 0;
+    if (at == n) at = INT32_MAX;   // none: as the entries that follow say it
+    const size_t trees = h.err_req == 2 ? n + extra / 2 : n + extra;
     for (size_t i = n; i < n + extra; ++i)
       if (st[i] < 0) {  // a CTA's failure, no request's
         *code = -st[i];
@@ -649,7 +870,7 @@ int spec_verify_get_error(const void* workspace, void* stream, int32_t* code, in
         return SV_OK;
       } else if (size_t(st[i]) < at) {
         at = size_t(st[i]);
-        c = SV_ERR_DATA_PAGE;
+        c = i < trees ? SV_ERR_DATA_PAGE : SV_ERR_DATA_TREE;
       }
     *code = c;
     if (request) *request = c && h.err_req ? int32_t(at) : -1;
@@ -729,6 +950,8 @@ const char* spec_verify_strerror(int code) {
     case SV_ERR_DATA_ACCEPT: return "KV commit: accept length above k";
     case SV_ERR_DATA_PAGE: return "a page missing from the block table, or negative kv_len";
     case SV_ERR_DATA_LENGTH: return "kv_len negative, or past the block table or the scores";
+    case SV_ERR_DATA_TREE: return "a tree's parent that is no earlier node, or a path without one";
+    case SV_ERR_DATA_POOL: return "too few free pages, or a free list that cannot hold them";
     default: return "unknown status";
   }
 }

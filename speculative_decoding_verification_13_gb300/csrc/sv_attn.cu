@@ -49,10 +49,12 @@ __device__ __forceinline__ void load_rows16(const AttnArgs& A, int b, int n, int
 
 // Scores of one tile: 2 threads per key, kRowsPerGroup rows each, in the log2
 // domain; -inf where the row does not see the key.
+// node: the rows' nodes where the drafts are a tree.
 template <class T>
 __device__ __forceinline__ void score_tile(const AttnArgs& A, const AttnReq& R, const char* sk,
                                            int stride, const float* sq, int row0, int rows, int p0,
-                                           float (&acc)[kRowsPerGroup]) {
+                                           float (&acc)[kRowsPerGroup],
+                                           const AttnNode* node = nullptr) {
   const int key = threadIdx.x % kTn, grp = threadIdx.x / kTn;
 #pragma unroll
   for (int r = 0; r < kRowsPerGroup; ++r) acc[r] = 0.f;
@@ -72,8 +74,9 @@ __device__ __forceinline__ void score_tile(const AttnArgs& A, const AttnReq& R, 
 #pragma unroll
   for (int r = 0; r < kRowsPerGroup; ++r) {
     const int row = grp * kRowsPerGroup + r;
-    const int at = R.at0 + (row0 + row) / A.G;
-    const bool see = row < rows && p <= at && p < R.hi && (A.window <= 0 || p > at - A.window);
+    const int at = node ? node[row].at : R.at0 + (row0 + row) / A.G;
+    bool see = row < rows && p <= at && p < R.hi && (A.window <= 0 || p > at - A.window);
+    if (node && p >= R.n) see = row < rows && p < R.hi && ((node[row].path >> (p - R.n)) & 1);
     acc[r] = see ? acc[r] * A.scale2 : -INFINITY;
   }
 }
@@ -92,7 +95,7 @@ __device__ __forceinline__ void load_q(const AttnArgs& A, int t_off, int h, int 
   }
 }
 
-template <class T>
+template <class T, bool TREE>
 __global__ void __launch_bounds__(kAtThreads) attn_kernel(const AttnArgs A) {
   extern __shared__ __align__(16) char at_smem[];
   const int stride = A.D * int(sizeof(T)) + 16;
@@ -103,13 +106,19 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const AttnArgs A) {
   float* s_m = sp + kMr * kTn;
   float* s_l = s_m + kMr;
   float* s_f = s_l + kMr;
-  __shared__ int s_bad;
+  __shared__ int s_bad, s_torn;
+  __shared__ AttnNode s_node[TREE ? kMr : 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const AttnPlan P = attn_plan<kTn, kMr, false, kAtThreads>(A);
-  int first_bad = INT32_MAX;
+  int first_bad = INT32_MAX, first_torn = INT32_MAX;
+  auto tell = [&] {
+    if (tid != 0) return;
+    A.status[A.B + blockIdx.x] = first_bad;
+    if (TREE) A.status[A.B + A.ctas + blockIdx.x] = first_torn;
+  };
   if (tid == 0) A.split[blockIdx.x].valid = 0;
   if (P.code) {
-    if (tid == 0) A.status[A.B + blockIdx.x] = INT32_MAX;
+    tell();
     fail_all<T>(A);
     return;
   }
@@ -131,7 +140,16 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const AttnArgs A) {
     const int h = unit / R.mtiles, row0 = (unit % R.mtiles) * kMr;
     const int rows = min(kMr, (R.k + 1) * A.G - row0);
     __syncthreads();
-    if (tid == 0) s_bad = R.code != 0;
+    if (tid == 0) {
+      s_bad = R.code != 0;
+      s_torn = 0;
+    }
+    if (TREE) {
+      const int32_t* parents = A.parent + t_off;
+      __syncthreads();
+      if (tid > 0 && tid <= R.k && !R.code && (parents[tid] < 0 || parents[tid] >= tid)) s_torn = 1;
+      if (tid < rows) s_node[tid] = attn_node(A, parents, R.n, (row0 + tid) / A.G);
+    }
     load_q<T>(A, t_off, h, row0, rows, sq);
     if (tid < kMr) {
       s_m[tid] = -INFINITY;
@@ -151,7 +169,7 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const AttnArgs A) {
       __syncthreads();
       {
         float s[kRowsPerGroup];
-        score_tile<T>(A, R, sk, stride, sq, row0, rows, p0, s);
+        score_tile<T>(A, R, sk, stride, sq, row0, rows, p0, s, TREE ? s_node : nullptr);
         const int key = tid % kTn, grp = tid / kTn;
 #pragma unroll
         for (int r = 0; r < kRowsPerGroup; ++r) sp[(grp * kRowsPerGroup + r) * kTn + key] = s[r];
@@ -199,8 +217,9 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const AttnArgs A) {
       }
     }
     __syncthreads();
-    const bool bad = s_bad != 0;
-    if (bad && first_bad == INT32_MAX && !R.code) first_bad = b;
+    const bool torn = TREE && s_torn != 0, bad = s_bad != 0 || torn;
+    if (torn && first_torn == INT32_MAX) first_torn = b;
+    else if (bad && first_bad == INT32_MAX && !R.code) first_bad = b;
     const float nan = __int_as_float(0x7fc00000);
     const bool whole = first == 0 && count == R.ntiles;
     const int slot = first == 0 ? 1 : 0;
@@ -243,7 +262,7 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const AttnArgs A) {
     }
     pos += count;
   }
-  if (tid == 0) A.status[A.B + blockIdx.x] = first_bad;
+  tell();
 }
 
 // Joins the partials of the unit that CTA blockIdx.x began and later ones
@@ -454,15 +473,17 @@ template <class T>
 cudaError_t run_attn(const AttnArgs& A, bool weights, cudaStream_t s) {
   const size_t smem = weights ? smem_weights<T>(A.D) : smem_attn<T>(A.D);
   // the most that any head size takes
-  static std::atomic<uint64_t> done_w{0}, done_a{0};
-  cudaError_t e = weights ? allow_smem(attn_weights_kernel<T>, smem_weights<T>(kMaxD), done_w)
-                          : allow_smem(attn_kernel<T>, smem_attn<T>(kMaxD), done_a);
+  static std::atomic<uint64_t> done_w{0}, done_a{0}, done_t{0};
+  cudaError_t e = weights    ? allow_smem(attn_weights_kernel<T>, smem_weights<T>(kMaxD), done_w)
+                  : A.parent ? allow_smem(attn_kernel<T, true>, smem_attn<T>(kMaxD), done_t)
+                             : allow_smem(attn_kernel<T, false>, smem_attn<T>(kMaxD), done_a);
   if (e != cudaSuccess) return e;
   if (weights) {
     attn_weights_kernel<T><<<A.ctas, kAtThreads, smem, s>>>(A);
     return cudaGetLastError();
   }
-  attn_kernel<T><<<A.ctas, kAtThreads, smem, s>>>(A);
+  if (A.parent) attn_kernel<T, true><<<A.ctas, kAtThreads, smem, s>>>(A);
+  else attn_kernel<T, false><<<A.ctas, kAtThreads, smem, s>>>(A);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_join(attn_join_kernel<T, kMr>, A, s);
@@ -487,7 +508,7 @@ AttnLayout attn_layout(int B, int D, int ctas, int mr) {
   AttnLayout L;
   size_t o = align256(sizeof(WsHeader));
   L.status = o;  // right behind the header, as spec_verify_get_error reads it
-  o += align256(4 * (size_t(B) + size_t(ctas)));
+  o += align256(4 * (size_t(B) + 2 * size_t(ctas)));
   L.split = o;
   o += align256(sizeof(AttnSplit) * size_t(ctas));
   L.ml = o;
@@ -528,7 +549,7 @@ cudaError_t launch_attn(AttnArgs A, int dtype, bool weights, void* workspace, in
     A.q_vec = aligned(A.q) && A.q_ts % 8 == 0 && A.q_hs % 8 == 0;
     A.out_vec = aligned(A.out);
     if (weights) return launch_attn_weights_tc(A, dtype, s);
-    const cudaError_t e = launch_attn_tc(A, dtype, s);
+    const cudaError_t e = A.parent ? launch_attn_tree_tc(A, dtype, s) : launch_attn_tc(A, dtype, s);
     if (e != cudaSuccess) return e;
     return dtype == SV_BF16 ? launch_join(attn_join_kernel<__nv_bfloat16, kTcRows>, A, s)
                             : launch_join(attn_join_kernel<__half, kTcRows>, A, s);

@@ -53,7 +53,8 @@ struct AttnArgs {
   float* part_o;                  // [CTAs, 2, MR, D]
   float2* part_ml;                // [CTAs, 2, MR]  maximum (log2 domain), sum
   AttnSplit* split;               // [CTAs]
-  int32_t* status;                // [B] then one entry per CTA (first request with a bad page)
+  int32_t* status;                // [B] then one entry per CTA (first request with a bad page),
+                                  // of trees then another (first request with a bad parent)
   WsHeader* hdr;
   // accumulated weights
   const int32_t* accept_len;      // may be null
@@ -69,6 +70,9 @@ struct AttnArgs {
   int32_t page_rows, layer_row;   // entries per page, entries before the layer's first
   int32_t q_vec, out_vec;         // 16-byte aligned heads
   int32_t test_expire;            // 1 + the block whose wait runs out, 0 in normal use
+  // a tree of drafts
+  const int32_t* parent;          // [Rt] each node's parent in its request, or null: a chain
+  int32_t max_k;                  // SV_MAX_K, of a tree SV_TREE_MAX_K
 };
 
 #ifdef __CUDACC__
@@ -110,7 +114,7 @@ __device__ __forceinline__ AttnReq attn_request(const AttnArgs& A, int b) {
   r.k = A.k_per_req[b];
   r.n = A.kv_len[b];
   r.code = 0;
-  const int k = min(max(r.k, 0), SV_MAX_K);
+  const int k = min(max(r.k, 0), A.max_k);
   if (r.k != k) r.code = SV_ERR_DATA_K;
   else if (r.n < 0 || int64_t(r.n) + k + 1 > kMaxPositions ||
            int64_t(r.n) > int64_t(A.max_pages) * A.S)
@@ -138,6 +142,28 @@ __device__ __forceinline__ AttnReq attn_request(const AttnArgs& A, int b) {
   r.ntiles = max((r.hi + TN - 1) / TN - r.tile0, WEIGHTS ? 0 : 1);
   if (WEIGHTS && r.take == 0) r.ntiles = 0;
   return r;
+}
+
+// A node of a request's tree of drafts.  Node 0 is the last emitted token, at
+// position n; a node lies one position behind its parent and sees the cache, its
+// ancestors and itself, as far as the window reaches.
+struct AttnNode {
+  uint64_t path;   // the nodes it sees
+  int at;          // its position
+};
+// parents: of this request's nodes; one that does not point back ends the walk
+__device__ __forceinline__ AttnNode attn_node(const AttnArgs& A, const int32_t* parents, int n,
+                                              int j) {
+  AttnNode x{0, n};
+  for (int depth = 0; depth <= SV_TREE_MAX_K; ++depth) {
+    if (A.window <= 0 || depth < A.window) x.path |= 1ull << j;
+    if (j == 0) break;
+    const int up = parents[j];
+    if (up < 0 || up >= j) break;
+    j = up;
+    ++x.at;
+  }
+  return x;
 }
 
 // Where a CTA starts, found by every CTA itself from the lengths.
@@ -259,8 +285,9 @@ __device__ AttnPlan attn_plan(const AttnArgs& A) {
   if (blockIdx.x == 0 && tid == 0) {
     A.hdr->err_code = kStatusList;
     A.hdr->err_row = A.B;
-    A.hdr->err_req = 1;           // entries are requests
-    A.hdr->n_active = A.ctas;     // followed by the CTAs' first bad-page requests
+    A.hdr->err_req = A.parent ? 2 : 1;   // entries are requests
+    // followed by the CTAs' first bad-page requests, of trees also the first torn ones
+    A.hdr->n_active = A.parent ? 2 * A.ctas : A.ctas;
   }
   return P;
 }
@@ -303,6 +330,7 @@ __device__ void fail_all(const AttnArgs& A) {
 
 // The tensor-core kernels' share of a call (MR = 128, one CTA per SM).
 cudaError_t launch_attn_tc(const AttnArgs& A, int dtype, cudaStream_t s);
+cudaError_t launch_attn_tree_tc(const AttnArgs& A, int dtype, cudaStream_t s);
 cudaError_t launch_attn_weights_tc(const AttnArgs& A, int dtype, cudaStream_t s);
 
 }  // namespace sv

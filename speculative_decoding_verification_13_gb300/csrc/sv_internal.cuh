@@ -67,8 +67,9 @@ struct WsHeader {
 // err_code of a header whose call keeps one status per entry instead (no
 // counter to clear before the call, the lowest failed entry whatever the order
 // of the CTAs): err_row entries follow the header, which are rows (err_req 0)
-// or requests (err_req 1), then n_active entries that name the first request
-// with a missing page (INT32_MAX for none) or, negative, their own error.
+// or requests (err_req 1 or 2), then n_active entries that name the first request
+// or row with a missing page (INT32_MAX for none) or, negative, their own error;
+// with err_req 2 the second half of them names requests with a torn tree.
 constexpr int32_t kStatusList = -1;
 
 struct RowStat {
@@ -210,7 +211,7 @@ cudaError_t launch_filter_decide(const Problem& P, bool bf16, int grid, cudaStre
 cudaError_t launch_draw(const Problem& P, bool bf16, int grid, cudaStream_t s);
 cudaError_t launch_locate(const Problem& P, bool bf16, int grid, cudaStream_t s);
 cudaError_t launch_sample_setup(const Problem& P, cudaStream_t s);
-size_t kv_workspace_bytes(int32_t B);
+size_t kv_workspace_bytes(int32_t B, int max_k);
 size_t lmhead_workspace_bytes(int M, int V);
 cudaError_t launch_adapt_k(const int32_t* accept_len, const int32_t* k_used, double* succ,
                            double* fail, double decay, double c, int k_min, int k_max,
@@ -223,7 +224,8 @@ cudaError_t launch_kv_commit(void* cache, const void* spec, int64_t num_pages, i
                              int page_size, int64_t entry_bytes, int spec_slots,
                              const int32_t* accept_len, const int32_t* k_per_req,
                              int32_t* kv_len, const int32_t* block_table, int max_pages, int B,
-                             void* workspace, int sms, cudaStream_t s);
+                             const int32_t* path, int64_t rows, int max_k, void* workspace,
+                             int sms, cudaStream_t s);
 cudaError_t launch_sample_post(const Problem& P, bool bf16, int grid, cudaStream_t s);
 cudaError_t launch_greedy_from_argmax(const int32_t* argmax, const int32_t* draft_tokens,
                                       const int32_t* k_per_req, int32_t* out_accept_len,
@@ -248,6 +250,30 @@ cudaError_t launch_evict(const sv_kv_cache& src, const int32_t* src_table, int s
                          const int32_t* kv_len, int32_t* out_len, int B, int budget, int sinks,
                          int recent, int32_t* out_kept, bool in_place, void* workspace, int sms,
                          cudaStream_t s);
+size_t tree_greedy_workspace_bytes(int32_t B);
+cudaError_t launch_tree_greedy(const int32_t* argmax, const int32_t* draft_tokens,
+                               const int32_t* parent, const int32_t* k_per_req,
+                               int32_t* accept_len, int32_t* tokens, int32_t* path, int B,
+                               int64_t Rt, int V, void* workspace, cudaStream_t s);
+size_t reserve_workspace_bytes(int32_t B, int64_t capacity);
+cudaError_t launch_reserve(const int32_t* table, int32_t* out_table, int B, int cols,
+                           const int32_t* held, int32_t* out_held, const int32_t* length,
+                           const int32_t* free_pages, int32_t* out_free, int64_t capacity,
+                           const int32_t* free_count, int32_t* out_count, int page_size,
+                           void* workspace, int sms, cudaStream_t s);
+size_t slots_workspace_bytes(int32_t B, int64_t rows);
+cudaError_t launch_slots(const int32_t* table, int B, int cols, const int32_t* start,
+                         const int32_t* count, int64_t rows, int page_size, int64_t* slots,
+                         int32_t* request, int32_t* position, int32_t* offsets, void* workspace,
+                         cudaStream_t s);
+size_t write_workspace_bytes(int sms);
+cudaError_t launch_write(const sv_kv_cache& c, int layer, int heads, const void* k, int64_t k_ts,
+                         int64_t k_hs, const void* v, int64_t v_ts, int64_t v_hs,
+                         const int64_t* slots, int64_t rows, void* workspace, int sms,
+                         cudaStream_t s);
+struct PromptArgs;
+size_t prompt_workspace_bytes(int32_t B, int sms);
+cudaError_t launch_prompt(PromptArgs A, int dtype, void* workspace, int sms, cudaStream_t s);
 struct AttnArgs;
 size_t attn_workspace_bytes(int32_t B, int32_t D, int sms, bool weights);
 cudaError_t launch_attn(AttnArgs A, int dtype, bool weights, void* workspace, int sms,

@@ -10,7 +10,7 @@
 // b lives in page block_table[b][p / page_size], slot p % page_size.  With
 // accept length L >= 0, spec entries 0..L (the last emitted token, then the L
 // accepted drafts) go to positions kv_len .. kv_len + L, and kv_len grows by
-// L + 1.
+// L + 1.  Of a tree of drafts the entries are those of the accepted path's nodes.
 //
 // Two launches: a validation CTA (accept lengths, destination pages, new
 // lengths, the list of tokens to copy), then a copy kernel in which one warp
@@ -37,10 +37,16 @@ struct KvProblem {
   const int32_t* block_table;
   int32_t max_pages;
   int32_t B;
+  const int32_t* path;     // [rows] nodes of the accepted paths, or null: entries in order
+  int64_t rows;
+  int32_t max_k;           // SV_MAX_K, of a tree SV_TREE_MAX_K
   WsHeader* hdr;
   int32_t* start;          // [B] kv_len before the commit
-  int2* tokens;            // [B * (SV_MAX_K + 1)] (request, entry) to copy
+  int2* tokens;            // [B * (max_k + 1)] (request, kv_move) to copy
 };
+
+// The entry that goes to the i-th position behind the request's last.
+__device__ __forceinline__ int kv_move(int i, int entry) { return i | entry << 16; }
 
 __device__ int kv_block_scan(int v, int* total) {
   __shared__ int s_w[kKvThreads / 32];
@@ -81,16 +87,45 @@ __global__ void __launch_bounds__(kKvThreads) kv_validate_kernel(const KvProblem
     Q.hdr->n_active = 0;
   }
   __syncthreads();
+  if (Q.path) {
+    // the rows of the paths: a batch whose rows do not add up is left alone
+    __shared__ int s_bad;
+    if (threadIdx.x == 0) s_bad = 0;
+    __syncthreads();
+    int64_t rows = 0;
+    for (int base = 0; base < Q.B; base += kKvThreads) {
+      const int b = base + threadIdx.x;
+      const int k = b < Q.B ? Q.k_per_req[b] : -1;
+      if (b < Q.B && (k < 0 || k > Q.max_k)) {
+        record_error(Q.hdr, SV_ERR_DATA_K, b, -1);
+        s_bad = 1;
+      }
+      int tot;
+      kv_block_scan(k >= 0 && k <= Q.max_k ? k + 1 : 0, &tot);
+      rows += tot;
+    }
+    if (s_bad || rows != Q.rows) {
+      if (threadIdx.x == 0 && !s_bad) record_error(Q.hdr, SV_ERR_DATA_ROWS, -1, -1);
+      return;   // no token to copy
+    }
+  }
   int carry = 0;
+  int64_t row0 = 0;
   for (int base = 0; base < Q.B; base += kKvThreads) {
     const int b = base + threadIdx.x;
     int cnt = 0;
+    int64_t row = 0;
+    if (Q.path) {
+      int tot;
+      row = row0 + kv_block_scan(b < Q.B ? Q.k_per_req[b] + 1 : 0, &tot);
+      row0 += tot;
+    }
     if (b < Q.B) {
       const int L = Q.accept_len[b];
       const int n = Q.kv_len[b];
       int code = 0;
       if (L >= 0) {
-        if (L > SV_MAX_K || L > Q.k_per_req[b] || L + 1 > Q.spec_slots) {
+        if (L > Q.max_k || L > Q.k_per_req[b] || L + 1 > Q.spec_slots) {
           code = SV_ERR_DATA_ACCEPT;
         } else if (n < 0) {
           code = SV_ERR_DATA_PAGE;
@@ -102,6 +137,10 @@ __global__ void __launch_bounds__(kKvThreads) kv_validate_kernel(const KvProblem
             if (page < 0 || page >= Q.num_pages) code = SV_ERR_DATA_PAGE;
           }
         }
+        for (int i = 0; Q.path && i <= L && !code; ++i) {
+          const int node = Q.path[row + i];
+          if (node < 0 || node > Q.k_per_req[b] || node >= Q.spec_slots) code = SV_ERR_DATA_TREE;
+        }
         if (code) record_error(Q.hdr, code, b, -1);
         else cnt = L + 1;
       }
@@ -110,7 +149,8 @@ __global__ void __launch_bounds__(kKvThreads) kv_validate_kernel(const KvProblem
     }
     int tot;
     const int t0 = carry + kv_block_scan(cnt, &tot);
-    for (int j = 0; j < cnt; ++j) Q.tokens[t0 + j] = make_int2(b, j);
+    for (int j = 0; j < cnt; ++j)
+      Q.tokens[t0 + j] = make_int2(b, kv_move(j, Q.path ? Q.path[row + j] : j));
     carry += tot;
   }
   if (threadIdx.x == 0) Q.hdr->n_active = carry;
@@ -128,11 +168,11 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const KvProblem Q
   for (int64_t it = wid; it < items; it += nw) {
     const int2 tk = Q.tokens[it / per_token];
     const int64_t lc = it % per_token;  // layer * 2 + (K or V)
-    const int64_t pos = int64_t(Q.start[tk.x]) + tk.y;
+    const int64_t pos = int64_t(Q.start[tk.x]) + (tk.y & 0xffff);
     const int64_t page = Q.block_table[int64_t(tk.x) * Q.max_pages + pos / Q.page_size];
     const int64_t slot = pos % Q.page_size;
     const uint4* src = reinterpret_cast<const uint4*>(
-        Q.spec + ((int64_t(tk.x) * Q.spec_slots + tk.y) * per_token + lc) * Q.entry_bytes);
+        Q.spec + ((int64_t(tk.x) * Q.spec_slots + (tk.y >> 16)) * per_token + lc) * Q.entry_bytes);
     uint4* dst = reinterpret_cast<uint4*>(
         Q.cache + ((page * per_token + lc) * Q.page_size + slot) * Q.entry_bytes);
     // four 16-byte vectors per lane in flight, then their stores
@@ -151,10 +191,10 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const KvProblem Q
 
 }  // namespace
 
-size_t kv_workspace_bytes(int32_t B) {
+size_t kv_workspace_bytes(int32_t B, int max_k) {
   size_t o = align256(sizeof(WsHeader));
   o = align256(o + sizeof(int32_t) * size_t(B > 0 ? B : 1));
-  o = align256(o + sizeof(int2) * size_t(B > 0 ? B : 1) * (SV_MAX_K + 1));
+  o = align256(o + sizeof(int2) * size_t(B > 0 ? B : 1) * size_t(max_k + 1));
   return o;
 }
 
@@ -162,7 +202,8 @@ cudaError_t launch_kv_commit(void* cache, const void* spec, int64_t num_pages, i
                              int page_size, int64_t entry_bytes, int spec_slots,
                              const int32_t* accept_len, const int32_t* k_per_req,
                              int32_t* kv_len, const int32_t* block_table, int max_pages, int B,
-                             void* workspace, int sms, cudaStream_t s) {
+                             const int32_t* path, int64_t rows, int max_k, void* workspace,
+                             int sms, cudaStream_t s) {
   KvProblem Q;
   Q.cache = static_cast<char*>(cache);
   Q.spec = static_cast<const char*>(spec);
@@ -177,6 +218,9 @@ cudaError_t launch_kv_commit(void* cache, const void* spec, int64_t num_pages, i
   Q.block_table = block_table;
   Q.max_pages = max_pages;
   Q.B = B;
+  Q.path = path;
+  Q.rows = rows;
+  Q.max_k = max_k;
   char* w = static_cast<char*>(workspace);
   size_t o = 0;
   Q.hdr = reinterpret_cast<WsHeader*>(w);
@@ -197,7 +241,7 @@ cudaError_t launch_kv_commit(void* cache, const void* spec, int64_t num_pages, i
   cudaError_t e = cudaLaunchKernelEx(&vc, kv_validate_kernel, Q);
   if (e != cudaSuccess) return e;
   // enough warps for every entry of the largest commit, at most 8 CTAs per SM
-  const int64_t items = int64_t(B) * (spec_slots < SV_MAX_K + 1 ? spec_slots : SV_MAX_K + 1) *
+  const int64_t items = int64_t(B) * (spec_slots < max_k + 1 ? spec_slots : max_k + 1) *
                         n_layers * 2;
   const int64_t want = (items + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
   const int64_t cap = int64_t(sms) * 8;

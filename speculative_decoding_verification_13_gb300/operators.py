@@ -264,6 +264,19 @@ def _attention_args(q, cache, layer, kv_len, block_table, k_per_req, spec, scale
         k_ptr, n_ptr, t_ptr, cols, scale, min(window, _INT_MAX))   # a wider one hides nothing
 
 
+def _attention_out(out, out_lse, rows, Hq, D, dtype, dev, stream):
+    """An attention's outputs, new where the caller brings none."""
+    if out is None:
+        out = _empty((rows, Hq, D), dtype, dev, stream)
+    else:
+        _matrix(out, "out", dtype, (rows, Hq, D), dev)
+    if out_lse is None:
+        out_lse = _empty((rows, Hq), torch.float32, dev, stream)
+    else:
+        _matrix(out_lse, "out_lse", torch.float32, (rows, Hq), dev)
+    return out, out_lse
+
+
 # ------------------------------------------------------------------ operators
 def attention(q, cache, layer, kv_len, block_table, k_per_req, spec=None, *, scale=None, window=0,
               out=None, out_lse=None, stream=None):
@@ -283,14 +296,7 @@ def attention(q, cache, layer, kv_len, block_table, k_per_req, spec=None, *, sca
     that sees nothing has out 0 and lse -inf.  They carry no autograd history."""
     dev, dtype, B, rows, Hq, D, args = _attention_args(q, cache, layer, kv_len, block_table,
                                                        k_per_req, spec, scale, window)
-    if out is None:
-        out = _empty((rows, Hq, D), dtype, dev, stream)
-    else:
-        _matrix(out, "out", dtype, (rows, Hq, D), dev)
-    if out_lse is None:
-        out_lse = _empty((rows, Hq), torch.float32, dev, stream)
-    else:
-        _matrix(out_lse, "out_lse", torch.float32, (rows, Hq), dev)
+    out, out_lse = _attention_out(out, out_lse, rows, Hq, D, dtype, dev, stream)
     _launch("attention", dev, stream, (B, D), (*args, out.data_ptr(), out_lse.data_ptr()), (B,))
     return out, out_lse
 
