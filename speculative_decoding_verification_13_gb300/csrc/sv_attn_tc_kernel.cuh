@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                (uint32_t(kTcMr >> 4) << 24);
     constexpr uint32_t kIdescS = kBase | (uint32_t(TN >> 3) << 17);
     const uint32_t idesc_o = kBase | (uint32_t(dim >> 3) << 17) | (1u << 16);
-    const uint32_t lead = lane == 0;
+    const uint32_t lead = elect_one();
     const bool scores = warp == kScoreWarp;
     Ring slot(scores ? 0 : C::kKSlots, scores ? C::kKSlots : C::kSlots - C::kKSlots, 0);
     Buf buf;

@@ -151,8 +151,10 @@ __global__ void __launch_bounds__(kPrThreads) prompt_kernel(const PromptArgs A) 
   for (int p0 = lo / kPrKeys * kPrKeys; p0 <= tok_last; p0 += kPrKeys) {
     const int live = min(kPrKeys, tok_last + 1 - p0);
     __syncthreads();
-    load_rows<T>(A, sk, stride, live, A.k_vec, [&](int r) { return k + int64_t(p0 + r) * A.k_ts; });
-    load_rows<T>(A, sv_, stride, live, A.v_vec, [&](int r) { return v + int64_t(p0 + r) * A.v_ts; });
+    load_rows<T>(A, sk, stride, live, A.k_vec,
+                 [&](int r) { return k + int64_t(p0 + r) * A.k_ts; });
+    load_rows<T>(A, sv_, stride, live, A.v_vec,
+                 [&](int r) { return v + int64_t(p0 + r) * A.v_ts; });
     __syncthreads();
     float s[4][4];
 #pragma unroll
@@ -164,13 +166,15 @@ __global__ void __launch_bounds__(kPrThreads) prompt_kernel(const PromptArgs A) 
 #pragma unroll
       for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<float4*>(sq + (ty * 4 + i) * stride + d);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<float4*>(sk + (tx + 16 * j) * stride + d);
+      for (int j = 0; j < 4; ++j)
+        b[j] = *reinterpret_cast<float4*>(sk + (tx + 16 * j) * stride + d);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          s[i][j] = fmaf(a[i].x, b[j].x, fmaf(a[i].y, b[j].y, fmaf(a[i].z, b[j].z,
-                                                                    fmaf(a[i].w, b[j].w, s[i][j]))));
+          s[i][j] = fmaf(a[i].x, b[j].x,
+                         fmaf(a[i].y, b[j].y,
+                              fmaf(a[i].z, b[j].z, fmaf(a[i].w, b[j].w, s[i][j]))));
     }
     const bool edge = p0 < all_lo || p0 + kPrKeys > tok_first + 1;
 #pragma unroll
@@ -273,7 +277,8 @@ size_t prompt_workspace_bytes(int32_t, int sms) {
 cudaError_t launch_prompt(PromptArgs A, int dtype, void* workspace, int sms, cudaStream_t s) {
   A.hdr = static_cast<WsHeader*>(workspace);
   A.status = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + align256(sizeof(WsHeader)));
-  A.out_vec = reinterpret_cast<uintptr_t>(A.out) % 16 == 0;
+  const uintptr_t to = reinterpret_cast<uintptr_t>(A.out);   // rows of A.D 16-bit elements
+  A.out_vec = to % 32 == 0 && A.D % 16 == 0 ? 2 : to % 16 == 0 ? 1 : 0;
   if (prompt_on_tensor_cores(A, dtype)) return launch_prompt_tc(A, dtype, sms, s);
   const size_t es = dtype == SV_F32 ? 4 : 2;
   auto fours = [&](const void* p, int64_t ts, int64_t hs) {

@@ -24,7 +24,9 @@
 //                   K and V into rings of slots, 128-byte swizzled.
 //   warp 9          issues the products.  The tensor cores run them in the order of
 //                   issue, so that S of the next tile may follow the product that
-//                   reads P in the same place.
+//                   reads P in the same place.  A warp for each row tile instead, with
+//                   or without turns, 1350 us -> 1480 to 1680 on the case below: their
+//                   products come between one another's.
 //   warps 10, 11    look through V of the tiles that some row of the unit sees in
 //                   part: masked weights are 0, but 0 times an infinite or NaN value
 //                   would still reach the row.  If such a tile holds any, each row
@@ -35,6 +37,12 @@
 //
 // Every wait is bounded; on expiry the CTA's status records it, its copies and
 // products land, TMEM is freed, and the rows of all its units become NaN.
+//
+// Measured, 32 + 8 heads of 128 in bf16: 16001 tokens 1.36 ms, 1540 TFLOP/s of the
+// 2.1 that the visible pairs take; 4 times 2048 tokens 125 us, 1100; 201 tokens 12.4
+// us.  Heads of 64 970 TFLOP/s, of 256 1200 (8 to 16 thousand tokens).  Bound by a row
+// tile's round of scores, softmax and products (3500 cycles where the products of
+// both row tiles take 2050): with the softmax taken out 1030 us of the 1360.
 #include <type_traits>
 
 #include "sv_attn_tc.cuh"
@@ -51,7 +59,7 @@ constexpr float kRescaleLog2 = 8.0f;
 constexpr uint32_t kTmemCols = 512;
 // Registers a thread: of the launch, of the softmax warps, of the others (three
 // warpgroups share 3 x 168).
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 120;
 
 template <int D>
 struct PtShape {
@@ -157,6 +165,7 @@ struct PtWalk {
   }
 };
 
+
 __device__ __forceinline__ void box_load3(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
                                           uint32_t bar) {
   asm volatile(
@@ -164,6 +173,12 @@ __device__ __forceinline__ void box_load3(uint32_t dst, const CUtensorMap* map, 
       "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
+}
+
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 // Descriptor of an MN-major 16-bit tile with 128-byte swizzling: rows (of K)
@@ -237,7 +252,8 @@ __device__ __noinline__ void pt_give_up(const PromptArgs& A, PtShared& S) {
     const int rows = (s.live[0] + s.live[1]) * A.G;
     for (int r = warp; r < rows; r += kPtThreads / 32) {
       const int64_t to = (int64_t(s.row0) + s.tok0 + r / A.G) * A.Hq + s.h * A.G + r % A.G;
-      for (int d = lane; d < A.D; d += 32) static_cast<T*>(A.out)[to * A.D + d] = from_float<T>(nan);
+      T* out = static_cast<T*>(A.out) + to * A.D;
+      for (int d = lane; d < A.D; d += 32) out[d] = from_float<T>(nan);
       if (lane == 0) A.lse[to] = nan;
     }
   }
@@ -247,7 +263,8 @@ template <class T, int D, bool PART>
 __global__ void __launch_bounds__(kPtThreads, 1)
     prompt_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                      const __grid_constant__ CUtensorMap k_map,
-                     const __grid_constant__ CUtensorMap v_map, const __grid_constant__ PromptArgs A) {
+                     const __grid_constant__ CUtensorMap v_map,
+                     const __grid_constant__ PromptArgs A) {
   using C = PtShape<D>;
   constexpr int TN = C::TN, NQ = C::NQ, NB = C::NB;
   constexpr int kSlotBytes = C::kSlotBytes;
@@ -389,7 +406,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       constexpr uint32_t kIdescS = kBase | (uint32_t(TN >> 3) << 17);
       const uint32_t wide = uint32_t(dim + 15) / 16;   // 16-element pieces of the head
       const uint32_t idesc_o = kBase | ((wide * 2) << 17) | (1u << 16);
-      const uint32_t lead = lane == 0;
+      const uint32_t lead = elect_one();
       Ring kr(0, C::kKSlots, 0), vr(C::kKSlots, C::kSlots - C::kKSlots, 0);
       const uint64_t q_desc = sw128_desc(smem0), k_desc = sw128_desc(ring0);
       const uint64_t v_desc = mn_desc(ring0, TN * 128);
@@ -547,6 +564,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t o_at = lanes + C::kOCol + g * D;
     const int mine = rr / A.G, head = rr % A.G;   // token of the tile, head of the group
+    int quad_row[4];                               // rows of out of the four lanes
+#pragma unroll
+    for (int i = 0; i < 4; ++i) quad_row[i] = ((rr & ~3) + i) / A.G * A.Hq + ((rr & ~3) + i) % A.G;
     uint32_t count = 0;                            // tiles of this row tile so far
     Ring vr(C::kKSlots, C::kSlots - C::kKSlots, 0);
     bool ok = true;
@@ -594,7 +614,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (lane == 0) mbar_arrive(smem_addr(&S.collected[g]));
           }
         }
-        const uint32_t buf = NB == 2 ? count & 1 : 0, phase = NB == 2 ? (count >> 1) & 1 : count & 1;
+        const uint32_t buf = NB == 2 ? count & 1 : 0;
+        const uint32_t phase = (NB == 2 ? count >> 1 : count) & 1;
         const uint32_t scol = lanes + (g * NB + buf) * TN;
         ok = tc_wait_warp(&S.sfull[g][buf], phase, S);
         if (!ok) break;
@@ -609,10 +630,14 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 #pragma unroll
           for (int c = 0; c < TN; ++c) x[c] = c >= lo && c < hi ? x[c] : -INFINITY;
         }
-        float high = x[0];
+        // four chains, two values a step
+        float top[4];
 #pragma unroll
-        for (int c = 1; c + 1 < TN; c += 2) high = fmaxf(high, fmaxf(x[c], x[c + 1]));
-        high = fmaxf(high, x[TN - 1]);
+        for (int c = 0; c < 4; ++c) top[c] = fmaxf(x[2 * c], x[2 * c + 1]);
+#pragma unroll
+        for (int c = 8; c < TN; c += 2)
+          asm("max.f32 %0, %0, %1, %2;" : "+f"(top[c / 2 & 3]) : "f"(x[c]), "f"(x[c + 1]));
+        const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         const float grown = fmaxf(m, high * A.scale2);   // scale2 > 0
         const bool rescale = live && grown > m + kRescaleLog2;
         if (__any_sync(0xffffffffu, rescale)) {
@@ -677,29 +702,72 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int64_t to = (int64_t(s.row0) + tok) * A.Hq + s.h * A.G + head;
       T* out = static_cast<T*>(A.out) + to * A.D;
+      if (A.out_vec == 2) {
+        // Four lanes exchange their rows' pieces of 32 bytes, so that each store
+        // writes 128 bytes of eight rows instead of 32 of 32 rows.
+        const int64_t unit_out = (int64_t(s.row0) + tok0) * A.Hq + s.h * A.G;
+        const int piece = lane & 3, live_rows = s.live[g] * A.G;
 #pragma unroll 1
-      for (int c = 0; c * 32 < dim; ++c) {
-        uint32_t o[32];
-        tmem_ld32(o_at + c * 32, o);
-        tmem_ld_wait();
-        if (!live) continue;
-        uint32_t w[16];
+        for (int c = 0; c * 64 < dim; ++c) {
+          uint32_t w[4][8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          w[e] = Bits<T>::pack(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-        if (A.out_vec) {
+          for (int i = 0; i < 2; ++i) {
+            uint32_t o[32];
+            tmem_ld32(o_at + c * 64 + i * 32, o);
+            tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (PART && c * 32 + e * 8 >= dim) break;
-            *reinterpret_cast<uint4*>(out + c * 32 + e * 8) =
-                make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            for (int e = 0; e < 16; ++e)
+              w[2 * i + (e >> 3)][e & 7] = Bits<T>::pack(__uint_as_float(o[2 * e]) * inv,
+                                                         __uint_as_float(o[2 * e + 1]) * inv);
           }
-        } else {
+          // w[i]: the lane's row's piece i, then row i's (of the four lanes') piece `piece`
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            if (PART && c * 32 + e >= dim) break;
-            const uint16_t y = uint16_t(w[e / 2] >> (16 * (e & 1)));
-            out[c * 32 + e] = *reinterpret_cast<const T*>(&y);
+          for (int step = 1; step < 4; step <<= 1) {
+            const bool up = piece & step;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (i & step) continue;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t give = up ? w[i][e] : w[i | step][e];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, give, step);
+                if (up) w[i][e] = got;
+                else w[i | step][e] = got;
+              }
+            }
+          }
+          const int col = c * 64 + piece * 16;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((rr & ~3) + i < live_rows && !(PART && col >= dim))
+              store32(static_cast<T*>(A.out) + (unit_out + quad_row[i]) * A.D + col, w[i]);
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c * 32 < dim; ++c) {
+          uint32_t o[32];
+          tmem_ld32(o_at + c * 32, o);
+          tmem_ld_wait();
+          if (!live) continue;
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w[e] =
+                Bits<T>::pack(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          if (A.out_vec) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (PART && c * 32 + e * 8 >= dim) break;
+              *reinterpret_cast<uint4*>(out + c * 32 + e * 8) =
+                  make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if (PART && c * 32 + e >= dim) break;
+              const uint16_t y = uint16_t(w[e / 2] >> (16 * (e & 1)));
+              out[c * 32 + e] = *reinterpret_cast<const T*>(&y);
+            }
           }
         }
       }
@@ -727,13 +795,14 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 
 // Rows of heads as boxes of 64 elements by `heads` heads by `rows` rows, 128-byte
 // swizzled.
-bool heads_map(CUtensorMap* map, const void* data, bool bf16, int D, int H, int64_t rows, int64_t ts,
-               int64_t hs, int heads, int box_rows) {
+bool heads_map(CUtensorMap* map, const void* data, bool bf16, int D, int H, int64_t rows,
+               int64_t ts, int64_t hs, int heads, int box_rows) {
   const EncodeTiledFn fn = tensor_map_encoder();
   if (!fn) return false;
   const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(rows)};
   // a stride that nothing is multiplied with may be anything
-  const cuuint64_t strides[2] = {cuuint64_t(H > 1 ? hs : 64) * 2, cuuint64_t(rows > 1 ? ts : 64) * 2};
+  const cuuint64_t strides[2] = {cuuint64_t(H > 1 ? hs : 64) * 2,
+                                 cuuint64_t(rows > 1 ? ts : 64) * 2};
   const cuuint32_t box[3] = {64, cuuint32_t(heads), cuuint32_t(box_rows)}, step[3] = {1, 1, 1};
   return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
             const_cast<void*>(data), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,

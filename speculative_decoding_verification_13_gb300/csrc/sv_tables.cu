@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(kTbThreads) reserve_release_kernel(const Reser
     __syncthreads();
   }
   if (Q.copy_free) {
-    const int64_t at = int64_t(blockIdx.x) * kTbThreads + tid, step = int64_t(gridDim.x) * kTbThreads;
+    const int64_t at = int64_t(blockIdx.x) * kTbThreads + tid;
+    const int64_t step = int64_t(gridDim.x) * kTbThreads;
     const int64_t vecs = Q.vec ? Q.capacity / 4 : 0;
     const int4* from = reinterpret_cast<const int4*>(Q.free_pages);
     for (int64_t i = at; i < vecs; i += step) reinterpret_cast<int4*>(Q.out_free)[i] = from[i];
