@@ -4,7 +4,8 @@
 //
 // All of it is bound by latency and by HBM: nothing is computed but prefix sums
 // over the requests, which every CTA forms by itself instead of waiting for a
-// kernel that does.
+// kernel that does.  The kernels are launched as dependents of what runs before
+// them and wait for it at their beginning.
 #include "sv_internal.cuh"
 
 namespace sv {
@@ -68,7 +69,9 @@ __device__ __forceinline__ int2 reserve_request(const ReserveProblem& Q, int b, 
   return *code ? make_int2(0, 0) : make_int2(held, need);
 }
 
-// The requests of CTA c: neighbouring ones, one warp each at a time.
+constexpr int kReserveCtasPerSm = 2;
+
+// The requests of CTA c: neighbouring ones.
 __device__ __forceinline__ int chunk_start(int B, int c) {
   return int(int64_t(B) * c / gridDim.x);
 }
@@ -77,7 +80,6 @@ __global__ void __launch_bounds__(kTbThreads) reserve_release_kernel(const Reser
   __shared__ int2 s_plan[kTbThreads];
   __shared__ int64_t s_first[kTbThreads];
   pdl_wait();
-  pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r0 = chunk_start(Q.B, blockIdx.x), r1 = chunk_start(Q.B, blockIdx.x + 1);
   const int n = *Q.free_count;
@@ -117,31 +119,46 @@ __global__ void __launch_bounds__(kTbThreads) reserve_release_kernel(const Reser
     s_plan[tid] = p;
     s_first[tid] = first;
     __syncthreads();
-    for (int i = warp; i < min(kTbThreads, r1 - c0); i += kTbWarps) {
-      const int64_t row = int64_t(c0 + i) * Q.cols;
-      const int lo = s_plan[i].y, hi = fail ? lo : s_plan[i].x;   // columns given up: [lo, hi)
-      if (Q.copy_table) {
-        if (Q.vec) {
-          const int4* from = reinterpret_cast<const int4*>(Q.table + row);
-          int4* to = reinterpret_cast<int4*>(Q.out_table + row);
+    const int rows = min(kTbThreads, r1 - c0);
+    // columns given up of row i: [lo, hi)
+    auto given_up = [&](int i, int* lo, int* hi) {
+      *lo = s_plan[i].y;
+      *hi = fail ? *lo : s_plan[i].x;
+    };
+    if (Q.copy_table) {
+      // all rows in one run of the threads: short rows and long ones alike
+      const int64_t first_row = int64_t(c0) * Q.cols;
+      int lo, hi;
+      if (Q.vec) {
+        const int per = Q.cols / 4;
+        const int4* from = reinterpret_cast<const int4*>(Q.table + first_row);
+        int4* to = reinterpret_cast<int4*>(Q.out_table + first_row);
 #pragma unroll 4
-          for (int c = lane; c < Q.cols / 4; c += 32) {
-            int4 v = from[c];
-            const int x = c * 4;
-            if (x + 3 >= lo && x < hi) {
-              if (x >= lo) v.x = -1;
-              if (x + 1 >= lo && x + 1 < hi) v.y = -1;
-              if (x + 2 >= lo && x + 2 < hi) v.z = -1;
-              if (x + 3 < hi) v.w = -1;
-            }
-            to[c] = v;
+        for (int64_t x = tid; x < int64_t(rows) * per; x += kTbThreads) {
+          const int i = int(x / per), c = int(x - int64_t(i) * per) * 4;
+          int4 v = from[x];
+          given_up(i, &lo, &hi);
+          if (c + 3 >= lo && c < hi) {
+            if (c >= lo) v.x = -1;
+            if (c + 1 >= lo && c + 1 < hi) v.y = -1;
+            if (c + 2 >= lo && c + 2 < hi) v.z = -1;
+            if (c + 3 < hi) v.w = -1;
           }
-        } else {
+          to[x] = v;
+        }
+      } else {
 #pragma unroll 4
-          for (int c = lane; c < Q.cols; c += 32)
-            Q.out_table[row + c] = c >= lo && c < hi ? -1 : Q.table[row + c];
+        for (int64_t x = tid; x < int64_t(rows) * Q.cols; x += kTbThreads) {
+          const int i = int(x / Q.cols), c = int(x - int64_t(i) * Q.cols);
+          given_up(i, &lo, &hi);
+          Q.out_table[first_row + x] = c >= lo && c < hi ? -1 : Q.table[first_row + x];
         }
       }
+    }
+    for (int i = warp; i < rows; i += kTbWarps) {
+      const int64_t row = int64_t(c0 + i) * Q.cols;
+      int lo, hi;
+      given_up(i, &lo, &hi);
       for (int c = lo + lane; c < hi; c += 32) {
         Q.released[s_first[i] + c - lo] = Q.table[row + c];
         if (!Q.copy_table) Q.out_table[row + c] = -1;
@@ -261,6 +278,7 @@ __global__ void __launch_bounds__(kTbThreads) slots_kernel(const SlotsProblem Q)
   __shared__ int s_req[kSlotRows], s_off[kSlotRows];
   __shared__ int s_last[kTbWarps];
   __shared__ int s_bad;
+  pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t r0 = int64_t(blockIdx.x) * kSlotRows, r1 = min(Q.rows, r0 + kSlotRows);
   if (tid == 0) s_bad = INT32_MAX;
@@ -364,6 +382,7 @@ __global__ void __launch_bounds__(kTbThreads) write_kernel(const WriteProblem Q)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) s_bad = INT32_MAX;
   __syncthreads();
+  pdl_wait();
   const int per_head = Q.head_bytes / int(sizeof(V));
   const int n = per_head * Q.heads;
   for (int64_t it = int64_t(blockIdx.x) * kTbWarps + warp; it < 2 * Q.rows;
@@ -480,8 +499,10 @@ cudaError_t launch_reserve(const int32_t* table, int32_t* out_table, int B, int 
   Q.plan = reinterpret_cast<int2*>(w + L.plan);
   Q.count = reinterpret_cast<int32_t*>(w + L.count);
   Q.released = reinterpret_cast<int32_t*>(w + L.released);
-  const int want = (B + kTbWarps - 1) / kTbWarps;
-  const int grid = want < 2 * sms ? want : 2 * sms;
+  // two requests a CTA while the CTAs fit (1024 rows of 2048 columns: 12.9 us with the
+  // second kernel; one CTA an SM 14.0, four 14.4)
+  const int want = (B + 1) / 2, cap = kReserveCtasPerSm * sms;
+  const int grid = want < cap ? want : cap;
   if (cudaError_t e = launch_pdl(reserve_release_kernel, grid, s, Q)) return e;
   return launch_pdl(reserve_grant_kernel, grid, s, Q);
 }
@@ -511,8 +532,7 @@ cudaError_t launch_slots(const int32_t* table, int B, int cols, const int32_t* s
   Q.hdr = static_cast<WsHeader*>(workspace);
   Q.status = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + align256(sizeof(WsHeader)));
   const int64_t ctas = (rows + kSlotRows - 1) / kSlotRows;
-  slots_kernel<<<unsigned(ctas > 0 ? ctas : 1), kTbThreads, 0, s>>>(Q);
-  return cudaGetLastError();
+  return launch_pdl(slots_kernel, int(ctas > 0 ? ctas : 1), s, Q);
 }
 
 size_t write_workspace_bytes(int sms) {
@@ -553,11 +573,10 @@ cudaError_t launch_write(const sv_kv_cache& c, int layer, int heads, const void*
                         uint64_t(Q.head_bytes) | (rows > 1 ? uint64_t(Q.k_ts | Q.v_ts) : 0) |
                         (Q.heads > 1 ? uint64_t(Q.k_hs | Q.v_hs) : 0);
   const int64_t want = (2 * rows + kTbWarps - 1) / kTbWarps, cap = int64_t(sms) * kWriteCtasPerSm;
-  const unsigned grid = unsigned(want < cap ? want : cap);
-  if (bits % 16 == 0) write_kernel<uint4><<<grid, kTbThreads, 0, s>>>(Q);
-  else if (es == 4 || bits % 4 == 0) write_kernel<uint32_t><<<grid, kTbThreads, 0, s>>>(Q);
-  else write_kernel<uint16_t><<<grid, kTbThreads, 0, s>>>(Q);
-  return cudaGetLastError();
+  const int grid = int(want < cap ? want : cap);
+  if (bits % 16 == 0) return launch_pdl(write_kernel<uint4>, grid, s, Q);
+  if (es == 4 || bits % 4 == 0) return launch_pdl(write_kernel<uint32_t>, grid, s, Q);
+  return launch_pdl(write_kernel<uint16_t>, grid, s, Q);
 }
 
 }  // namespace sv
