@@ -277,8 +277,7 @@ size_t prompt_workspace_bytes(int32_t, int sms) {
 cudaError_t launch_prompt(PromptArgs A, int dtype, void* workspace, int sms, cudaStream_t s) {
   A.hdr = static_cast<WsHeader*>(workspace);
   A.status = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + align256(sizeof(WsHeader)));
-  const uintptr_t to = reinterpret_cast<uintptr_t>(A.out);   // rows of A.D 16-bit elements
-  A.out_vec = to % 32 == 0 && A.D % 16 == 0 ? 2 : to % 16 == 0 ? 1 : 0;
+  A.out_vec = reinterpret_cast<uintptr_t>(A.out) % 16 == 0;
   if (prompt_on_tensor_cores(A, dtype)) return launch_prompt_tc(A, dtype, sms, s);
   const size_t es = dtype == SV_F32 ? 4 : 2;
   auto fours = [&](const void* p, int64_t ts, int64_t hs) {

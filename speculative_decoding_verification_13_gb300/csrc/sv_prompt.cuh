@@ -16,7 +16,7 @@ struct PromptArgs {
   int64_t rows;
   float scale2;                                 // scale * log2(e)
   int32_t q_vec, k_vec, v_vec;                  // four elements at a time (ordinary cores)
-  int32_t out_vec;                              // rows of the output lie on 16 bytes: 1, on 32: 2
+  int32_t out_vec;                              // 16-byte aligned output (tensor cores)
   int32_t test_expire;                          // as in AttnArgs
   int32_t* status;                              // [1 + CTAs]: the batch's, then each CTA's
   WsHeader* hdr;

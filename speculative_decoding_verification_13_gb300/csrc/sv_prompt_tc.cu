@@ -13,7 +13,8 @@
 //
 // One CTA per SM, over units u = c, 2 n - 1 - c, 2 n + c, ... (n CTAs, forth and back)
 // in the order of the tokens' place in their sequence, the last first: what a unit
-// costs falls with its number, so that the CTAs' sums stay close without a queue.
+// costs falls with its number, so that the CTAs' sums stay close without a queue (24
+// sequences of 1 to 4000 tokens: the most 97 tiles a CTA, the mean 93).
 //   warps 0-3, 4-7  softmax of the first and the second row tile, one row a thread
 //                   (the lanes of TMEM): scores from TMEM, running maximum, P rounded
 //                   to the type (half a step of it, the one rounding of a weight;
@@ -38,11 +39,13 @@
 // Every wait is bounded; on expiry the CTA's status records it, its copies and
 // products land, TMEM is freed, and the rows of all its units become NaN.
 //
-// Measured, 32 + 8 heads of 128 in bf16: 16001 tokens 1.36 ms, 1540 TFLOP/s of the
-// 2.1 that the visible pairs take; 4 times 2048 tokens 125 us, 1100; 201 tokens 12.4
-// us.  Heads of 64 970 TFLOP/s, of 256 1200 (8 to 16 thousand tokens).  Bound by a row
-// tile's round of scores, softmax and products (3500 cycles where the products of
-// both row tiles take 2050): with the softmax taken out 1030 us of the 1360.
+// Measured, 32 + 8 heads of 128 in bf16: 16001 tokens 1.34 ms, 1560 TFLOP/s of what the
+// visible pairs take; 4 times 2048 tokens 120 us, 1140; 201 tokens 12 us.  Heads of 64
+// 960 TFLOP/s, of 256 1300 (8 to 16 thousand tokens).  Bound by a row tile's round:
+// softmax 1200 to 1300 cycles, products 1050, and about 600 from barrier to barrier,
+// 2950 where the products of both row tiles take 2050; then by a unit's end (its last
+// product, 2500 cycles of output, the next unit's first scores: 6000 in all).  Heads of
+// 64: a product with V takes as long for 64 columns as for 128.
 #include <type_traits>
 
 #include "sv_attn_tc.cuh"
@@ -106,32 +109,40 @@ template <int NQ>
 struct PtWalk {
   int span;            // tokens of a unit
   int64_t u, step0, step1, base;   // unit number, the two strides in turn; units before the level
-  int level, cnt;      // tokens [level * span, ..) of sequences, and how many have such
+  // The level: units that begin at token level * span of their sequence.  cnt sequences have
+  // one, those with more than `level` units; so it is down to level `same`.
+  int level, cnt, same;
   __device__ __forceinline__ int units(const PromptArgs& A, int b) const {
     if (b >= A.B) return 0;
     int first, len;
     prompt_sequence(A, b, &first, &len);
     return (len + span - 1) / span;
   }
-  __device__ __forceinline__ int count(const PromptArgs& A) const {
+  __device__ __forceinline__ void look(const PromptArgs& A) {
     const int lane = threadIdx.x & 31;
-    int n = 0;
-    for (int b = 0; b < A.B; b += 32)
-      n += __popc(__ballot_sync(0xffffffffu, units(A, b + lane) > level));
-    return n;
+    cnt = same = 0;
+    for (int b = 0; b < A.B; b += 32) {
+      const int n = units(A, b + lane);
+      cnt += __popc(__ballot_sync(0xffffffffu, n > level));
+      same = max(same, __reduce_max_sync(0xffffffffu, n > level ? 0 : n));
+    }
   }
   // top: units of the longest sequence
   __device__ __forceinline__ PtWalk(const PromptArgs& A, int top)
       : span(NQ * (kM / A.G)), u(blockIdx.x), step0(2 * int64_t(gridDim.x) - 1 - 2 * blockIdx.x),
-        step1(1 + 2 * int64_t(blockIdx.x)), base(0), level(top - 1), cnt(0) {
-    if (level >= 0) cnt = count(A);
+        step1(1 + 2 * int64_t(blockIdx.x)), base(0), level(top - 1), cnt(0), same(0) {
+    if (level >= 0) look(A);
   }
   template <int TN>
   __device__ __forceinline__ bool next(const PromptArgs& A, PtSeg& s) {
     s.n = 0;
-    while (level >= 0 && u >= base + int64_t(cnt) * A.Hkv) {
-      base += int64_t(cnt) * A.Hkv;
-      if (--level >= 0) cnt = count(A);
+    while (level >= 0) {
+      const int64_t each = int64_t(cnt) * A.Hkv, off = (u - base) / each;
+      const int down = int(min(off, int64_t(level - same + 1)));
+      if (down == 0) break;
+      base += down * each;
+      level -= down;
+      if (level >= 0 && level < same) look(A);
     }
     if (level < 0) return false;
     const int local = int(u - base), lane = threadIdx.x & 31;
@@ -175,10 +186,10 @@ __device__ __forceinline__ void box_load3(uint32_t dst, const CUtensorMap* map, 
       : "memory");
 }
 
-__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
-               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // Descriptor of an MN-major 16-bit tile with 128-byte swizzling: rows (of K)
@@ -344,20 +355,19 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       bool stop = false;
       const uint32_t lead = lane == 0;
       PtWalk<NQ> walk(A, S.top);
-      for (int unit = 0; !stop; ++unit) {
-        PtSeg s;
-        const bool more = walk.template next<TN>(A, s);
-        if (!tc_wait_warp(&S.taken[unit % kSegs], ((unit / kSegs) & 1) ^ 1, S)) {
-          stop = true;
-          s.n = 0;
-        }
+      PtSeg next;
+      walk.template next<TN>(A, next);
+      for (int unit = 0;; ++unit) {
+        const PtSeg s = next;
+        // this entry's unit before has been taken over by every warp
+        stop = !tc_wait_warp(&S.taken[unit % kSegs], ((unit / kSegs) & 1) ^ 1, S);
+        if (stop) break;
         if (lead) {
           S.seg[unit % kSegs] = s;
           mbar_arrive(smem_addr(&S.announced[unit % kSegs]));
         }
         __syncwarp();
-        if (!more) break;
-        if (stop) s.n = s.cnt[0] = s.cnt[1] = 0;   // as below: what was issued lands
+        if (s.n == 0) break;
         auto load = [&](Ring& r, const CUtensorMap* map, int t) {
           if (!tc_wait_warp(&S.empty[r.at], r.phase, S)) return false;
           if (lead) {
@@ -391,13 +401,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             stop = !load(vr, &v_map, t);
             vfilled += !stop;
           }
+          if (t == 0) walk.template next<TN>(A, next);   // while the first tile is on its way
         }
-        if (stop) {   // let the copies that were issued land
-          ring_land(kr, kfilled, S.full);
-          ring_land(vr, vfilled, S.full);
-          for (int g = 0; g < NQ; ++g)
-            if (quse[g] > 0) mbar_wait_for(smem_addr(&S.qfull[g]), (quse[g] - 1) & 1, kTestWaitNs);
-        }
+        if (stop) break;
+      }
+      if (stop) {   // let the copies that were issued land
+        ring_land(kr, kfilled, S.full);
+        ring_land(vr, vfilled, S.full);
+        for (int g = 0; g < NQ; ++g)
+          if (quse[g] > 0) mbar_wait_for(smem_addr(&S.qfull[g]), (quse[g] - 1) & 1, kTestWaitNs);
       }
     } else if (warp == kMmaWarp) {
       // -------------------------------------------------------------- products
@@ -625,10 +637,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         for (int c = 0; c < TN / 32; ++c)
           tmem_ld32(scol + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[c * 32]));
         tmem_ld_wait();
-        if (p0 < own_lo || p0 + TN > own_hi) {
-          const int lo = row_lo - p0, hi = row_hi - p0;
+        if (p0 + TN > own_hi) {
+          const int hi = row_hi - p0;
 #pragma unroll
-          for (int c = 0; c < TN; ++c) x[c] = c >= lo && c < hi ? x[c] : -INFINITY;
+          for (int c = 0; c < TN; ++c) x[c] = c < hi ? x[c] : -INFINITY;
+        }
+        if (p0 < own_lo) {
+          const int lo = row_lo - p0;
+#pragma unroll
+          for (int c = 0; c < TN; ++c) x[c] = c >= lo ? x[c] : -INFINITY;
         }
         // four chains, two values a step
         float top[4];
@@ -702,23 +719,23 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int64_t to = (int64_t(s.row0) + tok) * A.Hq + s.h * A.G + head;
       T* out = static_cast<T*>(A.out) + to * A.D;
-      if (A.out_vec == 2) {
-        // Four lanes exchange their rows' pieces of 32 bytes, so that each store
-        // writes 128 bytes of eight rows instead of 32 of 32 rows.
-        const int64_t unit_out = (int64_t(s.row0) + tok0) * A.Hq + s.h * A.G;
-        const int piece = lane & 3, live_rows = s.live[g] * A.G;
+      if (A.out_vec) {
+        // Four lanes exchange their rows' pieces of 16 bytes, so that each store writes
+        // 64 bytes of eight rows instead of 16 of 32 rows.  A loop of few instructions:
+        // once a unit, it is their fetching that takes the time.
+        T* unit_out = static_cast<T*>(A.out) + ((int64_t(s.row0) + tok0) * A.Hq + s.h * A.G) * A.D;
+        const int piece = lane & 3, live_rows = s.live[g] * A.G - (rr & ~3);
+        const uint64_t inv2 = pk2(inv, inv);
 #pragma unroll 1
-        for (int c = 0; c * 64 < dim; ++c) {
-          uint32_t w[4][8];
+        for (int c = 0; c * 32 < dim; ++c) {
+          uint32_t o[32], w[4][4];
+          tmem_ld32(o_at + c * 32, o);
+          tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t o[32];
-            tmem_ld32(o_at + c * 64 + i * 32, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              w[2 * i + (e >> 3)][e & 7] = Bits<T>::pack(__uint_as_float(o[2 * e]) * inv,
-                                                         __uint_as_float(o[2 * e + 1]) * inv);
+          for (int e = 0; e < 16; ++e) {
+            float a, b;
+            upk2(mul2(pk2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), inv2), a, b);
+            w[e >> 2][e & 3] = Bits<T>::pack(a, b);
           }
           // w[i]: the lane's row's piece i, then row i's (of the four lanes') piece `piece`
 #pragma unroll
@@ -728,7 +745,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             for (int i = 0; i < 4; ++i) {
               if (i & step) continue;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
+              for (int e = 0; e < 4; ++e) {
                 const uint32_t give = up ? w[i][e] : w[i | step][e];
                 const uint32_t got = __shfl_xor_sync(0xffffffffu, give, step);
                 if (up) w[i][e] = got;
@@ -736,11 +753,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
               }
             }
           }
-          const int col = c * 64 + piece * 16;
+          const int col = c * 32 + piece * 8;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if ((rr & ~3) + i < live_rows && !(PART && col >= dim))
-              store32(static_cast<T*>(A.out) + (unit_out + quad_row[i]) * A.D + col, w[i]);
+            if (i < live_rows && !(PART && col >= dim))
+              *reinterpret_cast<uint4*>(unit_out + int64_t(quad_row[i]) * A.D + col) =
+                  make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
         }
       } else {
 #pragma unroll 1
@@ -754,20 +772,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           for (int e = 0; e < 16; ++e)
             w[e] =
                 Bits<T>::pack(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-          if (A.out_vec) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (PART && c * 32 + e * 8 >= dim) break;
-              *reinterpret_cast<uint4*>(out + c * 32 + e * 8) =
-                  make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if (PART && c * 32 + e >= dim) break;
-              const uint16_t y = uint16_t(w[e / 2] >> (16 * (e & 1)));
-              out[c * 32 + e] = *reinterpret_cast<const T*>(&y);
-            }
+          for (int e = 0; e < 32; ++e) {
+            if (PART && c * 32 + e >= dim) break;
+            const uint16_t y = uint16_t(w[e / 2] >> (16 * (e & 1)));
+            out[c * 32 + e] = *reinterpret_cast<const T*>(&y);
           }
         }
       }

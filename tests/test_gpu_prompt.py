@@ -252,3 +252,32 @@ def test_another_stream():
     side.synchronize()
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
     assert sv.prompt_attention_error() == (0, -1, -1)
+
+
+@pytest.mark.parametrize("D,Hk,G,window", [(128, 8, 4, 0), (64, 1, 7, 50), (256, 2, 2, 0)])
+def test_hundreds_of_sequences(D, Hk, G, window):
+    # every CTA has units of many sequences and of several lengths
+    rng = np.random.default_rng(D)
+    lengths = rng.integers(0, 60, 700).tolist()
+    lengths[13], lengths[600] = 1500, 300
+    q, k, v, at = make(1, lengths, Hk, G, D, B16)
+    a = gpu(q, k, v)
+    out, lse = sv.prompt_attention(*a, i32(at), window=window)
+    assert sv.prompt_attention_error() == (0, -1, -1)
+    want, mag = torch.empty(q.shape, dtype=torch.float64), torch.empty(q.shape, dtype=torch.float64)
+    ref = torch.empty(q.shape[:2], dtype=torch.float64)
+    for lo, hi in zip(at, at[1:]):
+        x, K, V = (y[lo:hi].double() for y in (q, k, v))
+        s = torch.einsum("ihgd,jhd->hgij", x.unflatten(1, (Hk, G)), K) * D ** -0.5
+        i = torch.arange(hi - lo)
+        see = (i[None] <= i[:, None]) & ((i[None] > i[:, None] - window) if window else True)
+        s = s.masked_fill(~see, -math.inf)
+        w = torch.softmax(s, -1)
+        want[lo:hi] = torch.einsum("hgij,jhd->ihgd", w, V).flatten(1, 2)
+        mag[lo:hi] = torch.einsum("hgij,jhd->ihgd", w, V.abs()).flatten(1, 2)
+        ref[lo:hi] = torch.logsumexp(s, -1).permute(2, 0, 1).flatten(1)
+    # a score is at most 60 here: e_s (D + 4) 2^-24 60 + 2^-21 at most 1e-3; a weight's half step
+    weight = 2e-3 + 2.0 ** -8
+    err = (out.double().cpu() - want).abs()
+    assert (err <= weight * mag + 2.0 ** -8 * (want.abs() + weight * mag) + 1e-30).all()
+    assert ((lse.double().cpu() - ref).abs() <= 1e-3 + 2.0 ** -20 * ref.abs()).all()
