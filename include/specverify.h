@@ -473,7 +473,9 @@ int spec_attention(const sv_kv_cache* cache, int32_t dtype, int32_t layer, int32
  * and itself, with window W > 0 only the last W of them.  k_b <= SV_TREE_MAX_K,
  * and `spec`, entry j of node j, is needed.  A request whose tree has a parent
  * that is no earlier node gets NaN rows (SV_ERR_DATA_TREE); node 0's parent is
- * not read.  All else as in spec_attention. */
+ * not read.  A row that sees an infinite value whose weight is 0 in the type may
+ * be NaN there, where the formula's weight is tiny and its result infinite.  All
+ * else as in spec_attention. */
 size_t spec_tree_attention_workspace_size(int32_t batch, int32_t head_dim);
 
 int spec_tree_attention(const sv_kv_cache* cache, int32_t dtype, int32_t layer, int32_t kv_heads,

@@ -20,9 +20,10 @@ SOURCES = ["sv_api.cu", "sv_setup.cu", "sv_rowpass.cu", "sv_finalize.cu", "sv_dr
            "sv_noalloc.cu", "sv_kv.cu", "sv_lmhead.cu", "sv_adapt.cu", "sv_greedy.cu",
            "sv_attn.cu", "sv_attn_tc.cu", "sv_attn_weights_tc.cu", "sv_evict.cu",
            "sv_logprobs.cu", "sv_attn_tree_tc.cu", "sv_prompt.cu", "sv_prompt_tc.cu",
-           "sv_tables.cu", "sv_tree.cu"]
+           "sv_tree_rows_tc.cu", "sv_tables.cu", "sv_tree.cu"]
 HEADERS = ["sv_internal.cuh", "sv_select.cuh", "sv_bigrow.cuh", "sv_weights.cuh", "sv_attn.cuh",
-           "sv_tcgen05.cuh", "sv_attn_tc.cuh", "sv_attn_tc_kernel.cuh", "sv_prompt.cuh"]
+           "sv_tcgen05.cuh", "sv_attn_tc.cuh", "sv_attn_tc_kernel.cuh", "sv_prompt.cuh",
+           "sv_row_tiles_tc.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
               "--expt-relaxed-constexpr"]

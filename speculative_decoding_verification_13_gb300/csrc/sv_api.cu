@@ -491,12 +491,13 @@ size_t spec_attention_workspace_size(int32_t batch, int32_t head_dim) {
 // What spec_attention and spec_tree_attention do with the arguments they have checked.
 static int attention_call(AttnArgs& A, int32_t dtype, void* out, float* lse, void* stream,
                           void* workspace, size_t workspace_bytes) {
+  const bool tree = A.parent != nullptr;
   if (A.B == 0) return SV_OK;
   if (!out || !lse) return SV_ERR_ARG;
   if (!workspace || misaligned(workspace, 256)) return SV_ERR_WORKSPACE;
   const int sms = sm_count();
   if (sms == 0) return SV_ERR_CUDA;
-  if (workspace_bytes < attn_workspace_bytes(A.B, A.D, sms, false)) return SV_ERR_WORKSPACE;
+  if (workspace_bytes < attn_workspace_bytes(A.B, A.D, sms, false, tree)) return SV_ERR_WORKSPACE;
   A.out = out;
   A.o_hs = A.D;
   A.o_ts = int64_t(A.D) * A.Hq;
@@ -522,7 +523,9 @@ int spec_attention(const sv_kv_cache* cache, int32_t dtype, int32_t layer, int32
 }
 
 size_t spec_tree_attention_workspace_size(int32_t batch, int32_t head_dim) {
-  return spec_attention_workspace_size(batch, head_dim);
+  const int sms = sm_count();
+  if (batch < 0 || head_dim < 1 || head_dim > SV_HEAD_DIM_MAX || sms == 0) return 0;
+  return attn_workspace_bytes(batch, head_dim, sms, false, true);
 }
 
 int spec_tree_attention(const sv_kv_cache* cache, int32_t dtype, int32_t layer, int32_t kv_heads,

@@ -501,6 +501,25 @@ bool on_tensor_cores(const AttnArgs& A, int dtype, bool weights) {
          A.num_pages * (A.page_bytes / A.entry_bytes) <= INT32_MAX;
 }
 
+// Whether a call's trees go to the kernel that has two row tiles of 128 rows over the
+// same keys.  It takes heads of 64 to 128 whose queries' rows lie on 16 bytes, and groups
+// that fill a row tile.  Two row tiles read the keys once and overlap; one alone takes
+// longer than in the other kernel.  32 requests of 2001 to 8190 positions, 8 KV heads of
+// 128 with 4 query heads each: 8 to 63 drafts (121 rows on average) 149 us with it, 176
+// without; 63 drafts (256 rows) 176 and 229; 47 (192) 165 and 233; 31 (128) 141 and 128;
+// 20 (84) 134 and 116.  So it takes the calls whose requests have room for more than a
+// row tile and fill more than kTwoRowTiles rows of one on average: the host knows no more
+// of the lengths.
+constexpr int kTwoRowTiles = 96;
+bool two_row_tiles(const AttnArgs& A) {
+  auto stride = [](int64_t x) { return x > 0 && x % 8 == 0 && x < (int64_t(1) << 38); };
+  return A.D <= 128 && kTcRows % A.G == 0 &&
+         int64_t(std::min(A.slots, A.max_k + 1)) * A.G > kTcRows &&
+         A.Rt * A.G > int64_t(kTwoRowTiles) * A.B &&
+         reinterpret_cast<uintptr_t>(A.q) % 16 == 0 && (A.Rt == 1 || stride(A.q_ts)) &&
+         (A.Hq == 1 || stride(A.q_hs));
+}
+
 struct AttnLayout {
   size_t status, split, ml, o, total;
 };
@@ -521,19 +540,20 @@ AttnLayout attn_layout(int B, int D, int ctas, int mr) {
 
 }  // namespace
 
-size_t attn_workspace_bytes(int32_t B, int32_t D, int sms, bool weights) {
+size_t attn_workspace_bytes(int32_t B, int32_t D, int sms, bool weights, bool tree) {
   const AttnLayout L = attn_layout(B, D, sms * kCtasPerSm, kMr);
   if (weights) return L.split;
-  const AttnLayout T = attn_layout(B, D, sms, kTcRows);
+  const AttnLayout T = attn_layout(B, D, sms, tree ? 2 * kTcRows : kTcRows);
   return L.total > T.total ? L.total : T.total;
 }
 
 cudaError_t launch_attn(AttnArgs A, int dtype, bool weights, void* workspace, int sms,
                         cudaStream_t s) {
   const bool tc = on_tensor_cores(A, dtype, weights);
+  const bool two = tc && A.parent && two_row_tiles(A);
   A.ctas = tc ? sms : sms * kCtasPerSm;
   A.hg = tc && !weights ? std::gcd(A.ctas, A.Hkv) : 1;
-  const AttnLayout L = attn_layout(A.B, A.D, A.ctas, tc ? kTcRows : kMr);
+  const AttnLayout L = attn_layout(A.B, A.D, A.ctas, two ? 2 * kTcRows : tc ? kTcRows : kMr);
   char* w = static_cast<char*>(workspace);
   A.hdr = reinterpret_cast<WsHeader*>(w);
   A.status = reinterpret_cast<int32_t*>(w + L.status);
@@ -549,8 +569,13 @@ cudaError_t launch_attn(AttnArgs A, int dtype, bool weights, void* workspace, in
     A.q_vec = aligned(A.q) && A.q_ts % 8 == 0 && A.q_hs % 8 == 0;
     A.out_vec = aligned(A.out);
     if (weights) return launch_attn_weights_tc(A, dtype, s);
-    const cudaError_t e = A.parent ? launch_attn_tree_tc(A, dtype, s) : launch_attn_tc(A, dtype, s);
+    const cudaError_t e = two        ? launch_tree_rows_tc(A, dtype, s)
+                          : A.parent ? launch_attn_tree_tc(A, dtype, s)
+                                     : launch_attn_tc(A, dtype, s);
     if (e != cudaSuccess) return e;
+    if (two)
+      return dtype == SV_BF16 ? launch_join(attn_join_kernel<__nv_bfloat16, 2 * kTcRows>, A, s)
+                              : launch_join(attn_join_kernel<__half, 2 * kTcRows>, A, s);
     return dtype == SV_BF16 ? launch_join(attn_join_kernel<__nv_bfloat16, kTcRows>, A, s)
                             : launch_join(attn_join_kernel<__half, kTcRows>, A, s);
   }

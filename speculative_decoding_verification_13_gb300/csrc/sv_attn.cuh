@@ -313,7 +313,7 @@ __device__ __forceinline__ const char* attn_key(const AttnArgs& A, int b, int n,
 }
 
 template <class T>
-__device__ void fail_all(const AttnArgs& A) {
+__device__ __noinline__ void fail_all(const AttnArgs& A) {
   // a batch whose rows cannot be told apart: every output is NaN
   const float nan = __int_as_float(0x7fc00000);
   const int64_t n = A.Rt * A.Hq;
@@ -331,6 +331,7 @@ __device__ void fail_all(const AttnArgs& A) {
 // The tensor-core kernels' share of a call (MR = 128, one CTA per SM).
 cudaError_t launch_attn_tc(const AttnArgs& A, int dtype, cudaStream_t s);
 cudaError_t launch_attn_tree_tc(const AttnArgs& A, int dtype, cudaStream_t s);
+cudaError_t launch_tree_rows_tc(const AttnArgs& A, int dtype, cudaStream_t s);  // MR = 256
 cudaError_t launch_attn_weights_tc(const AttnArgs& A, int dtype, cudaStream_t s);
 
 }  // namespace sv

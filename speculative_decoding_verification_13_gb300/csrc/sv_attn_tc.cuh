@@ -132,18 +132,32 @@ __device__ __forceinline__ uint64_t l2_evict_normal_policy() {
   return pol;
 }
 
+constexpr uint32_t kPollsPerLook = 256;
+
+// Whether a wait that has polled `polls` times, and its CTA, should give up: looked at
+// now and then.  Not inlined: a wait's own instructions are few, and a kernel has dozens
+// of them.
+template <class Sh>
+__device__ __noinline__ bool tc_expired(uint32_t polls, uint64_t* since, Sh& S) {
+  if (*reinterpret_cast<volatile int*>(&S.abort)) return true;
+  const uint64_t now = global_ns();
+  if (polls == kPollsPerLook) *since = now;
+  if (now - *since <= kWaitNs && polls < kWaitPolls) return false;
+  *reinterpret_cast<volatile int*>(&S.abort) = 1;
+  return true;
+}
+
 // Bounded wait on a barrier of a CTA whose shared record is S; false, with its
-// abort flag set, on expiry.  The clock of
-// the bound is read only after a number of polls: a wait here is short, and
-// reading the global timer would be most of it.
+// abort flag set, on expiry.
 template <class Sh>
 __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, Sh& S) {
   const uint32_t at = smem_addr(bar);
-  for (int i = 0; i < 128; ++i)
+  uint64_t since;
+#pragma unroll 1
+  for (uint32_t polls = 1;; ++polls) {
     if (mbar_try_wait(at, parity)) return true;
-  if (mbar_wait_for(at, parity, kWaitNs, &S.abort)) return true;
-  *reinterpret_cast<volatile int*>(&S.abort) = 1;
-  return false;
+    if (polls % kPollsPerLook == 0 && tc_expired(polls, &since, S)) return false;
+  }
 }
 // The same for a whole warp, one answer for all its lanes.
 template <class Sh>

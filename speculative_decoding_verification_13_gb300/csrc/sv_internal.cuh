@@ -275,7 +275,7 @@ struct PromptArgs;
 size_t prompt_workspace_bytes(int32_t B, int sms);
 cudaError_t launch_prompt(PromptArgs A, int dtype, void* workspace, int sms, cudaStream_t s);
 struct AttnArgs;
-size_t attn_workspace_bytes(int32_t B, int32_t D, int sms, bool weights);
+size_t attn_workspace_bytes(int32_t B, int32_t D, int sms, bool weights, bool tree = false);
 cudaError_t launch_attn(AttnArgs A, int dtype, bool weights, void* workspace, int sms,
                         cudaStream_t s);
 

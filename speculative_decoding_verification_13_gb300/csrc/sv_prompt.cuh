@@ -45,7 +45,7 @@ __device__ __forceinline__ void prompt_header(const PromptArgs& A, bool bad, int
 
 // A batch whose sequences cannot be told apart: every output is NaN.
 template <class T>
-__device__ void prompt_fail(const PromptArgs& A) {
+__device__ __noinline__ void prompt_fail(const PromptArgs& A) {
   const float nan = __int_as_float(0x7fc00000);
   const int64_t n = A.rows * A.Hq, at = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * blockDim.x,
                 step = int64_t(gridDim.x) * gridDim.y * blockDim.x;

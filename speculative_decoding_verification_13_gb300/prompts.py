@@ -116,6 +116,8 @@ def tree_attention(q, cache, layer, kv_len, block_table, k_per_req, parent, spec
     read.  A node lies one position behind its parent, node 0 at kv_len, and sees
     the cached positions, its ancestors and itself, with ``window`` > 0 only the
     last ``window`` of them.  spec: [B, slots, n_layers, 2, E], entry j of node j.
+    Where a row sees an infinite value whose weight is 0 in the type, its result may
+    be NaN instead of infinite.
 
     Returns ``(out [rows, q_heads, D], lse [rows, q_heads] float32)``."""
     if spec is None:

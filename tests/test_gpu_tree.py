@@ -99,6 +99,12 @@ CASES = [
     ([200, 40], [20, 40], 2, 2, 64, 16, F32, 4, "any"),
     ([300, 64], [50, 33], 3, 4, 144, 64, B16, 0, "any"),
     ([130, 127, 126, 65], [1, 2, 3, 63], 2, 2, 64, 16, B16, 0, "chain"),
+    # many rows a request: both row tiles of the kernel for them, its heads and groups
+    ([100, 31, 2], [45, 63, 30], 1, 4, 80, 16, B16, 0, "any"),
+    ([300, 0, 127], [50, 63, 39], 2, 4, 96, 7, F16, 40, "chain"),
+    ([129, 40], [20, 31], 1, 16, 128, 16, B16, 5, "any"),
+    ([260, 5, 1000], [3, 9, 0], 1, 128, 64, 64, F16, 0, "star"),
+    ([1500, 257, 0, 3], [63, 32, 31, 30], 3, 8, 128, 128, F16, 0, "any"),
 ]
 
 
