@@ -505,9 +505,9 @@ bool on_tensor_cores(const AttnArgs& A, int dtype, bool weights) {
 // same keys.  It takes heads of 64 to 128 whose queries' rows lie on 16 bytes, and groups
 // that fill a row tile.  Two row tiles read the keys once and overlap; one alone takes
 // longer than in the other kernel.  32 requests of 2001 to 8190 positions, 8 KV heads of
-// 128 with 4 query heads each: 8 to 63 drafts (121 rows on average) 149 us with it, 176
-// without; 63 drafts (256 rows) 176 and 229; 47 (192) 165 and 233; 31 (128) 141 and 128;
-// 20 (84) 134 and 116.  So it takes the calls whose requests have room for more than a
+// 128 with 4 query heads each: 8 to 63 drafts (121 rows on average) 138 us with it, 174
+// without; 63 drafts (256 rows) 160 and 226; 47 (192) 151 and 230; 31 (128) 129 and 126;
+// 20 (84) 120 and 115; one request of 900 positions, 63 drafts 26 and 23.  So it takes the calls whose requests have room for more than a
 // row tile and fill more than kTwoRowTiles rows of one on average: the host knows no more
 // of the lengths.
 constexpr int kTwoRowTiles = 96;
@@ -562,9 +562,12 @@ cudaError_t launch_attn(AttnArgs A, int dtype, bool weights, void* workspace, in
   A.part_o = reinterpret_cast<float*>(w + L.o);
   if (tc) {
     auto aligned = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
-    A.s_shift = -1;
-    for (int i = 0; i < 31; ++i)
-      if (A.S == 1 << i) A.s_shift = i;
+    // with 2^l the first power of two that S does not exceed, the factor's excess over
+    // 2^(31 + l) / S is below 1, so that of a product below p / 2^(31 + l) < 1 / S
+    int l = 0;
+    while (int64_t(A.S) > int64_t(1) << l) ++l;
+    A.s_shift = 31 + l;
+    A.s_mul = uint32_t(((uint64_t(1) << A.s_shift) + A.S - 1) / uint64_t(A.S));
     A.page_rows = int32_t(A.page_bytes / A.entry_bytes);
     A.q_vec = aligned(A.q) && A.q_ts % 8 == 0 && A.q_hs % 8 == 0;
     A.out_vec = aligned(A.out);

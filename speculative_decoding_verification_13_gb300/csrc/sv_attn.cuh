@@ -65,7 +65,8 @@ struct AttnArgs {
   int32_t ctas;                   // grid of the main kernel
   int32_t hg;                     // heads with a line of their own, 1 or more
   // the tensor-core kernel
-  int32_t s_shift;                // log2 of the page size, or -1
+  uint32_t s_mul;                 // p / S = p * s_mul >> s_shift for 0 <= p < 2^31
+  int32_t s_shift;
   int32_t box_rows;               // entries per box of the copy engine, 0: no boxes
   int32_t page_rows, layer_row;   // entries per page, entries before the layer's first
   int32_t q_vec, out_vec;         // 16-byte aligned heads
@@ -202,6 +203,7 @@ __device__ AttnPlan attn_plan(const AttnArgs& A) {
   const int b0 = min(A.B, tid * per), b1 = min(A.B, b0 + per);
   int64_t tiles = 0;
   int rows = 0;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     const AttnReq r = attn_request<TN, MR, WEIGHTS>(A, b);
     if (A.k_per_req[b] != r.k) atomicMin(&s_badk, b);
@@ -256,6 +258,7 @@ __device__ AttnPlan attn_plan(const AttnArgs& A) {
       s_toff = toff;
       s_base = base;
     }
+#pragma unroll 1
     for (int b = b0; per > 1 && b < b1; ++b) {
       const AttnReq r = attn_request<TN, MR, WEIGHTS>(A, b);
       const int64_t t = attn_tiles<TN, MR, WEIGHTS, PAD>(A, r);

@@ -214,7 +214,7 @@ struct TilePages {
 };
 
 __device__ __forceinline__ int page_column(const AttnArgs& A, int p) {
-  return A.s_shift >= 0 ? p >> A.s_shift : p / A.S;
+  return int(uint64_t(uint32_t(p)) * A.s_mul >> A.s_shift);
 }
 
 // A tile comes in boxes where it is whole and pages hold a multiple of 8 of its
@@ -224,23 +224,70 @@ __device__ __forceinline__ bool tile_boxed(const AttnArgs& A, int cached, int p0
   return A.box_rows > 0 && p0 + TN <= cached;
 }
 
+template <int TN, int SHARES>
+__device__ __forceinline__ TilePages<TN, SHARES> row_pages(const AttnArgs& A, const int32_t* table,
+                                                        int cached, int p0, int share) {
+  TilePages<TN, SHARES> t;
+#pragma unroll
+  for (int i = 0; i < TN / 32 / SHARES; ++i) {
+    const int p = p0 + share * (TN / SHARES) + (threadIdx.x & 31) + 32 * i;
+    t.page[i] = p < cached ? __ldg(table + page_column(A, p)) : 0;
+  }
+  return t;
+}
+
 template <int D, bool PART, int TN, int SHARES = 1>
 __device__ __forceinline__ TilePages<TN, SHARES> tile_pages(const AttnArgs& A,
                                                             const int32_t* table, int cached,
                                                             int p0, int share = 0) {
   const int lane = threadIdx.x & 31;
+  if (!tile_boxed<TN>(A, cached, p0)) return row_pages<TN, SHARES>(A, table, cached, p0, share);
   TilePages<TN, SHARES> t;
-  if (tile_boxed<TN>(A, cached, p0)) {
-    const int box0 = (lane * SHARES + share) / row_parts<D, PART>(A) * A.box_rows;
-    t.page[0] = box0 < TN ? __ldg(table + page_column(A, p0 + box0)) : 0;
-  } else {
-#pragma unroll
-    for (int i = 0; i < TN / 32 / SHARES; ++i) {
-      const int p = p0 + share * (TN / SHARES) + lane + 32 * i;
-      t.page[i] = p < cached ? __ldg(table + page_column(A, p)) : 0;
-    }
-  }
+  const int box0 = (lane * SHARES + share) / row_parts<D, PART>(A) * A.box_rows;
+  t.page[0] = box0 < TN ? __ldg(table + page_column(A, p0 + box0)) : 0;
   return t;
+}
+
+// The rows of a tile that does not come in boxes, 16 bytes at a time.  Like row_pages not
+// inlined: they are most of a load's instructions, and most tiles come in boxes.
+template <int D, bool PART, int TN, int SHARES>
+__device__ __noinline__ void load_rows(const AttnArgs& A, TilePages<TN, SHARES> pages, int b, int n,
+                                       int cached, int hi, int p0, int h, int kv, uint32_t dst,
+                                       int share) {
+  const int lane = threadIdx.x & 31;
+  const int dim = head_width<D, PART>(A);
+  // addresses of the lane's own rows; each round's lanes then fetch theirs from
+  // the lane that has it
+  constexpr int kOwn = TN / 32 / SHARES;
+  const int first = share * (TN / SHARES);
+  uint64_t own[kOwn];
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const int p = p0 + first + lane + 32 * i;
+    const char* a = nullptr;   // stays null for a row that is filled with zeros
+    if (p >= cached) {
+      if (p < hi)
+        a = A.spec + int64_t(b) * A.spec_req + int64_t(p - n) * A.spec_tok + kv * A.entry_bytes;
+    } else if (pages.page[i] >= 0) {
+      a = A.cache + pages.page[i] * A.page_bytes + kv * A.v_off +
+          (p - page_column(A, p) * A.S) * A.entry_bytes;
+    }
+    own[i] = a ? reinterpret_cast<uint64_t>(a + int64_t(h) * dim * 2) : 0;
+  }
+  constexpr int kChunks = D / 8, kStep = 32 / kChunks;   // 16-byte chunks of a row, rows a round
+  const int ch = lane % kChunks;
+  const char* none = A.spec ? A.spec : A.cache;   // not read, but on 16 bytes
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i)
+#pragma unroll 4
+    for (int j = 0; j < 32; j += kStep) {
+      const int from = j + lane / kChunks, r = first + 32 * i + from;
+      const uint64_t a = (uint64_t(__shfl_sync(0xffffffffu, uint32_t(own[i] >> 32), from)) << 32) |
+                         __shfl_sync(0xffffffffu, uint32_t(own[i]), from);
+      if (PART && ch * 8 >= dim) continue;
+      cp_async16(dst + (ch >> 3) * (TN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                 a ? reinterpret_cast<const char*>(a) + ch * 16 : none, a ? 16u : 0u);
+    }
 }
 
 // A warp loads its share of K (kv 0) or V (kv 1) of head h and positions p0 ..
@@ -279,38 +326,13 @@ __device__ __forceinline__ void load_tile(const AttnArgs& A, const CUtensorMap& 
     }
     return;
   }
-  // addresses of the lane's own rows; each round's lanes then fetch theirs from
-  // the lane that has it
-  constexpr int kOwn = TN / 32 / SHARES;
-  const int first = share * (TN / SHARES);
-  uint64_t own[kOwn];
+  TilePages<TN, SHARES> rows = pages;   // a missing page: -1
 #pragma unroll
-  for (int i = 0; i < kOwn; ++i) {
-    const int p = p0 + first + lane + 32 * i;
-    const char* a = nullptr;   // stays null for a row that is filled with zeros
-    if (p >= cached) {
-      if (p < hi)
-        a = A.spec + int64_t(b) * A.spec_req + int64_t(p - n) * A.spec_tok + kv * A.entry_bytes;
-    } else if (!missing(pages.page[i])) {
-      a = A.cache + pages.page[i] * A.page_bytes + kv * A.v_off +
-          (p - page_column(A, p) * A.S) * A.entry_bytes;
-    }
-    own[i] = a ? reinterpret_cast<uint64_t>(a + int64_t(h) * dim * 2) : 0;
+  for (int i = 0; i < TN / 32 / SHARES; ++i) {
+    const int p = p0 + share * (TN / SHARES) + (threadIdx.x & 31) + 32 * i;
+    if (p < cached && missing(rows.page[i])) rows.page[i] = -1;
   }
-  constexpr int kChunks = D / 8, kStep = 32 / kChunks;   // 16-byte chunks of a row, rows a round
-  const int ch = lane % kChunks;
-  const char* none = A.spec ? A.spec : A.cache;   // not read, but on 16 bytes
-#pragma unroll
-  for (int i = 0; i < kOwn; ++i)
-#pragma unroll 4
-    for (int j = 0; j < 32; j += kStep) {
-      const int from = j + lane / kChunks, r = first + 32 * i + from;
-      const uint64_t a = (uint64_t(__shfl_sync(0xffffffffu, uint32_t(own[i] >> 32), from)) << 32) |
-                         __shfl_sync(0xffffffffu, uint32_t(own[i]), from);
-      if (PART && ch * 8 >= dim) continue;
-      cp_async16(dst + (ch >> 3) * (TN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                 a ? reinterpret_cast<const char*>(a) + ch * 16 : none, a ? 16u : 0u);
-    }
+  load_rows<D, PART, TN, SHARES>(A, rows, b, n, cached, hi, p0, h, kv, dst, share);
   if (lane == 0) *copied = 1;
   cp_async_arrive(bar);
 }
@@ -344,6 +366,55 @@ inline bool rows_map(CUtensorMap* map, const AttnArgs& A, bool bf16) {
             const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A thread's signs of the infinite (NaN: both) values in a tile of V, of its positions
+// first .. last - 1 those from lo to hi - 1 and those of path's bits from node0 on: bits
+// of columns of the head, +inf then -inf.  This and add_signs are not inlined: what is
+// rare stands apart from what every tile runs, whose instructions then come from the
+// caches (230 KB of them with everything in one piece).
+template <class T, int D, int TN>
+__device__ __noinline__ void collect_signs(const uint32_t* v, int first, int last, int lo, int hi,
+                                           uint64_t path, int node0, uint32_t* signs) {
+  for (int i = 0; i < 2 * D / 32; ++i) signs[i] = 0;
+  for (int c = first; c < last; ++c) {
+    const bool node = c >= node0 && c - node0 < 64 && ((path >> (c - node0)) & 1);
+    if (!node && (c < lo || c >= hi)) continue;
+    for (int d = 0; d < D; d += 2) {
+      const uint32_t w =
+          v[(d >> 6) * (TN * 32) + c * 32 + ((((d & 63) >> 3) ^ (c & 7)) << 2) + ((d & 7) >> 1)];
+      if (!any_nonfinite<T>(w)) continue;
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t y = (w >> (16 * x)) & 0xffffu;
+        if ((y & Bits<T>::kExp1) != Bits<T>::kExp1) continue;
+        const bool isnan = (y & Bits<T>::kMan1) != 0;
+        const uint32_t bit = 1u << ((d + x) & 31);
+        if (isnan || !(y & 0x8000u)) signs[d >> 5] |= bit;
+        if (isnan || (y & 0x8000u)) signs[D / 32 + (d >> 5)] |= bit;
+      }
+    }
+  }
+}
+
+// Adds them to the thread's row of O.
+template <int D>
+__device__ __noinline__ void add_signs(uint32_t o_at, int dim, const uint32_t* signs) {
+  for (int c = 0; c * 16 < dim; ++c) {
+    uint32_t o[16];
+    tmem_ld16(o_at + c * 16, o);
+    tmem_ld_wait();
+    const uint32_t plus = signs[c >> 1] >> (16 * (c & 1)),
+                   minus = signs[D / 32 + (c >> 1)] >> (16 * (c & 1));
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float x = __uint_as_float(o[e]);
+      if ((plus >> e) & 1) x += INFINITY;
+      if ((minus >> e) & 1) x -= INFINITY;
+      o[e] = __float_as_uint(x);
+    }
+    tmem_st16(o_at + c * 16, o);
+  }
+  tmem_st_wait();
 }
 
 }  // namespace sv

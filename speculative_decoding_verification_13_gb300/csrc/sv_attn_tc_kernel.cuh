@@ -582,11 +582,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int row_lo = live && A.window > 0 ? max(0, at - A.window + 1) : 0;
       // behind row_hi: nodes that the row sees
       const uint64_t row_path = TREE && live && !s.R.code ? node.path : 0;
-      // whether the row sees position p
-      auto sees = [&](int p) {
-        if (p >= row_lo && p < row_hi) return true;
-        return TREE && p >= row_hi && p - row_hi < 64 && ((row_path >> (p - row_hi)) & 1);
-      };
       // the range that every row of the unit sees: tiles inside it need no mask
       const int at_first = s.R.at0 + s.row0 / A.G;
       // a tree is no deeper than its nodes are many
@@ -604,7 +599,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           break;
         }
         tc_fence_after();
-        uint32_t plus[D / 32], minus[D / 32];   // non-finite values that the row sees
+        uint32_t signs[2 * D / 32];   // non-finite values that the row sees
         bool dirty = false;
         if (edge) {
           // V of this tile: 128 bytes a thread
@@ -629,34 +624,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           looked ^= 1;
           dirty = *reinterpret_cast<volatile int*>(&S.dirty[buf]) == g + 1;
           if (dirty) {
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) plus[i] = minus[i] = 0;
-            const uint32_t* vw = reinterpret_cast<const uint32_t*>(v);
             // each copy has the signs of its own columns: one without weight has none
-            for (int c = copy * (TN / s.copies); live && c < (copy + 1) * (TN / s.copies); ++c) {
-              if (!sees(p0 + c)) continue;
-#pragma unroll
-              for (int i = 0; i < D / 32; ++i)
-                for (int e = 0; e < 32; e += 2) {
-                  const int d = i * 32 + e;
-                  const uint32_t w = vw[(d >> 6) * (TN * 32) + c * 32 +
-                                        ((((d & 63) >> 3) ^ (c & 7)) << 2) + ((d & 7) >> 1)];
-                  if (!any_nonfinite<T>(w)) continue;
-#pragma unroll
-                  for (int x = 0; x < 2; ++x) {
-                    const uint32_t y = (w >> (16 * x)) & 0xffffu;
-                    if ((y & Bits<T>::kExp1) != Bits<T>::kExp1) continue;
-                    const bool isnan = (y & Bits<T>::kMan1) != 0;
-                    if (isnan || !(y & 0x8000u)) plus[i] |= 1u << (e + x);
-                    if (isnan || (y & 0x8000u)) minus[i] |= 1u << (e + x);
-                  }
-                }
-            }
+            const int first = copy * (TN / s.copies);
+            collect_signs<T, D, TN>(reinterpret_cast<const uint32_t*>(v), first,
+                                    live ? first + TN / s.copies : first, row_lo - p0,
+                                    row_hi - p0, row_path, row_hi - p0, signs);
             if (!tc_sync(&S.looked[1], collected, S)) {
               stop = true;
               break;
             }
             collected ^= 1;
+#pragma unroll 1
             for (int i = 0; i < kSlotBytes / 16 / 128; ++i) {
               uint32_t* w = reinterpret_cast<uint32_t*>(v + i * 128 + tid);
 #pragma unroll
@@ -804,23 +782,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             break;
           }
           tc_fence_after();
-          if (active) {
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(lanes + C::kOCol + c * 32, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                float v = __uint_as_float(o[e]);
-                if ((plus[c] >> e) & 1) v += INFINITY;
-                if ((minus[c] >> e) & 1) v -= INFINITY;
-                o[e] = __float_as_uint(v);
-              }
-              tmem_st32(lanes + C::kOCol + c * 32, o);
-            }
-            tmem_st_wait();
-          }
+          if (active) add_signs<D>(lanes + C::kOCol, dim, signs);
           tc_fence_before();
         }
       }
@@ -975,8 +937,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               }
               if ((isnan(v0) || isnan(v1)) && stage.inv[r] == stage.inv[r]) {
                 if (settled) {
-                  v0 = settle(v0, r, c0 + e);
-                  v1 = settle(v1, r, c0 + e + 1);
+#pragma unroll 1
+                  for (int x = 0; x < 2; ++x) {
+                    const float v = settle(x ? v1 : v0, r, c0 + e + x);
+                    (x ? v1 : v0) = v;
+                  }
                 }
                 odd = true;
               }

@@ -25,8 +25,8 @@
 //                   product reads it as its A operand.  O is rescaled only when a
 //                   row's maximum has grown by more than 2^8 since the last time.
 //   warp 8          finds the units, announces them, and has the copy engine load Q,
-//                   K and V into rings of slots, 128-byte swizzled (of a cache, tiles
-//                   that are not whole by 16-byte copies: load_tile).
+//                   K and V into rings of slots, 128-byte swizzled (of a cache, V by
+//                   warp 10, tiles that are not whole by 16-byte copies: load_tile).
 //   warp 9          issues the products.  The tensor cores run them in the order of
 //                   issue, so that S of the next tile may follow the product that
 //                   reads P in the same place.  A warp for each row tile instead, with
@@ -51,10 +51,12 @@
 // product, 2500 cycles of output, the next unit's first scores: 6000 in all).  Heads of
 // 64: a product with V takes as long for 64 columns as for 128.  Every wait is a small
 // loop: unrolled, the kernel's 260 KB of instructions cost 5 to 9 %.
-// Trees, 32 requests of 2001 to 8190 positions with 8 to 63 drafts, the same heads: 149 us,
-// 4.1 TB/s of their entries.  Bound by the loads' and softmax's pace: a tile of 128
-// positions of both row tiles takes 4300 cycles, 1900 of them a warp's issue of its
-// boxes, 1000 the products.
+// Trees, 32 requests of 2001 to 8190 positions with 8 to 63 drafts, the same heads: 138 us,
+// 4.5 TB/s of their entries; 8 of 30000 with 63 drafts 200 us, 4.9.  Bound by the row
+// tiles' rounds: a tile of 128 positions of both takes 3700 cycles, 2050 of them products
+// (pages of 128 instead of 16 positions, boxes 8 times as large, change nothing; entries
+// that the L2 holds, 5 %).  Loads of K and V by the same instructions, and what is rare
+// out of line, 149 -> 138 us: the tensor cores' warp waits for instructions otherwise.
 #pragma once
 
 #include <type_traits>
@@ -331,53 +333,6 @@ __device__ __forceinline__ void exchange4(uint32_t (&w)[4][4]) {
   }
 }
 
-// A thread's signs of the infinite (NaN: both) values among the columns lo .. hi - 1,
-// and those of path's bits from column node0 on, of a tile of V: bits of columns of the
-// head, +inf then -inf.
-template <class T, int D, int TN>
-__device__ __noinline__ void collect_signs(const uint32_t* v, int lo, int hi, uint64_t path,
-                                           int node0, uint32_t* signs) {
-  for (int i = 0; i < 2 * D / 32; ++i) signs[i] = 0;
-  for (int c = 0; c < TN; ++c) {
-    const bool node = c >= node0 && c - node0 < 64 && ((path >> (c - node0)) & 1);
-    if (!node && (c < lo || c >= hi)) continue;
-    for (int d = 0; d < D; d += 2) {
-      const uint32_t w =
-          v[(d >> 6) * (TN * 32) + c * 32 + ((((d & 63) >> 3) ^ (c & 7)) << 2) + ((d & 7) >> 1)];
-      if (!any_nonfinite<T>(w)) continue;
-      for (int x = 0; x < 2; ++x) {
-        const uint32_t y = (w >> (16 * x)) & 0xffffu;
-        if ((y & Bits<T>::kExp1) != Bits<T>::kExp1) continue;
-        const bool isnan = (y & Bits<T>::kMan1) != 0;
-        const uint32_t bit = 1u << ((d + x) & 31);
-        if (isnan || !(y & 0x8000u)) signs[d >> 5] |= bit;
-        if (isnan || (y & 0x8000u)) signs[D / 32 + (d >> 5)] |= bit;
-      }
-    }
-  }
-}
-
-// Adds them to the thread's row of O.
-template <int D>
-__device__ __noinline__ void add_signs(uint32_t o_at, int dim, const uint32_t* signs) {
-  for (int c = 0; c * 16 < dim; ++c) {
-    uint32_t o[16];
-    tmem_ld16(o_at + c * 16, o);
-    tmem_ld_wait();
-    const uint32_t plus = signs[c >> 1] >> (16 * (c & 1)),
-                   minus = signs[D / 32 + (c >> 1)] >> (16 * (c & 1));
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      float x = __uint_as_float(o[e]);
-      if ((plus >> e) & 1) x += INFINITY;
-      if ((minus >> e) & 1) x -= INFINITY;
-      o[e] = __float_as_uint(x);
-    }
-    tmem_st16(o_at + c * 16, o);
-  }
-  tmem_st_wait();
-}
-
 // A thread's row of O where it does not lie on 16 bytes; none where out is null.
 template <class T>
 __device__ __noinline__ void rows_one_by_one(uint32_t o_at, int dim, float inv, T* out) {
@@ -527,43 +482,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     if (!go) prompt_fail<T>(A);
   }
 
-  // Trees: a warp loads a part's tiles of K (kv 0) or V (kv 1) into the ring; `then` runs
-  // while the first is on its way.
-  auto load_part = [&](const auto& s, int unit, int kv, Ring& r, int& filled, auto then) -> bool {
-    if constexpr (TREE) {
-      const int hi = s.R.code ? 0 : s.R.hi, cached = min(s.R.n, hi);
-      const int32_t* table = A.table + int64_t(s.b) * A.max_pages;
-      // keys that no other unit of the call reads leave the L2 first
-      const uint64_t policy = s.R.mtiles > 1 ? l2_evict_normal_policy() : l2_evict_first_policy();
-      auto missing = [&](int page) {
-        if (page >= 0 && page < A.num_pages) return false;
-        S.part_bad[unit % kSegs] = 1;
-        atomicMin(&S.first_bad, s.b);
-        return true;
-      };
-      // pages are read one tile ahead, so that nothing waits for the block table
-      TilePages<TN, 1> ahead = tile_pages<D, PART, TN>(A, table, cached, s.tile0 * TN);
-      for (int t = 0; t < s.n; ++t) {
-        const TilePages<TN, 1> pages = ahead;
-        const int p0 = (s.tile0 + t) * TN;
-        if (t + 1 < s.n) ahead = tile_pages<D, PART, TN>(A, table, cached, p0 + TN);
-        if (!tc_wait_warp(&S.empty[r.at], r.phase, S)) return false;
-        load_tile<D, PART, TN, 1>(A, k_map, pages, s.b, s.R.n, cached, hi, p0, s.h, kv,
-                                  ring0 + r.at * kSlotBytes, &S.full[r.at], &S.copied[r.at],
-                                  policy, 0, missing);
-        r.step();
-        ++filled;
-        if (t == 0) then();
-      }
-    }
-    return true;
-  };
-
   if (go && warp >= kLoadWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kLoadWarp) {
+    if (warp == kLoadWarp || (TREE && warp == kValueWarp)) {
       // ------------------------------------------------------- units and loads
-      Ring kr(0, C::kKSlots, 1), vr(C::kKSlots, C::kSlots - C::kKSlots, 1);
+      // (of trees one warp loads K, the other V, by the same instructions)
+      const bool leads = warp == kLoadWarp;
+      const int kv = leads ? 0 : 1;
+      Ring kr(kv ? C::kKSlots : 0, kv ? C::kSlots - C::kKSlots : C::kKSlots, 1);
+      Ring vr(C::kKSlots, C::kSlots - C::kKSlots, 1);   // of prompts
       int kfilled = 0, vfilled = 0, quse[2] = {0, 0};
       bool stop = false;
       const uint32_t lead = lane == 0;
@@ -578,47 +505,81 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       };
       find();
       for (int unit = 0;; ++unit) {
-        const Seg s = next;
-        stop = !tc_wait_warp(&S.taken[unit % kSegs], ((unit / kSegs) & 1) ^ 1, S);
-        if (stop) break;
-        if (lead) {
-          S.seg[unit % kSegs] = s;
-          if constexpr (TREE) S.part_bad[unit % kSegs] = s.n && s.R.code != 0;
-          mbar_arrive(smem_addr(&S.announced[unit % kSegs]));
-        }
-        __syncwarp();
-        if (s.n == 0) break;
-        auto load = [&](Ring& r, const CUtensorMap* map, int t) {
-          if (!tc_wait_warp(&S.empty[r.at], r.phase, S)) return false;
+        Seg s;
+        if (leads) {
+          s = next;
+          stop = !tc_wait_warp(&S.taken[unit % kSegs], ((unit / kSegs) & 1) ^ 1, S);
+          if (stop) break;
           if (lead) {
-            const uint32_t bar = smem_addr(&S.full[r.at]);
-            mbar_arrive_expect_tx(bar, uint32_t(parts * TN * 128));
-            for (int p = 0; p < parts; ++p)
-              box_load3(ring0 + r.at * kSlotBytes + p * (TN * 128), map, p * 64, s.h,
-                        s.row0 + (s.tile0 + t) * TN, bar);
+            S.seg[unit % kSegs] = s;
+            if constexpr (TREE) S.part_bad[unit % kSegs] = s.n && s.R.code != 0;
+            mbar_arrive(smem_addr(&S.announced[unit % kSegs]));
           }
           __syncwarp();
-          r.step();
-          return true;
-        };
+          if (s.n == 0) break;
 #pragma unroll
-        for (int g = 0; g < NQ; ++g) {
-          if (s.cnt[g] == 0 || stop) continue;
-          stop = !tc_wait_warp(&S.qempty[g], (quse[g]++ & 1) ^ 1, S);
-          if (lead && !stop) {
-            const uint32_t bar = smem_addr(&S.qfull[g]);
-            mbar_arrive_expect_tx(bar, uint32_t(parts * toks * A.G * 128));
-            for (int p = 0; p < parts; ++p)
-              box_load3(smem0 + g * C::kQBytes + p * (kM * 128), &q_map, p * 64, s.h * A.G,
-                        s.row0 + s.tok0 + g * toks, bar);
+          for (int g = 0; g < NQ; ++g) {
+            if (s.cnt[g] == 0 || stop) continue;
+            stop = !tc_wait_warp(&S.qempty[g], (quse[g]++ & 1) ^ 1, S);
+            if (lead && !stop) {
+              const uint32_t bar = smem_addr(&S.qfull[g]);
+              mbar_arrive_expect_tx(bar, uint32_t(parts * toks * A.G * 128));
+              for (int p = 0; p < parts; ++p)
+                box_load3(smem0 + g * C::kQBytes + p * (kM * 128), &q_map, p * 64, s.h * A.G,
+                          s.row0 + s.tok0 + g * toks, bar);
+            }
+            __syncwarp();
           }
-          __syncwarp();
+        } else if (!pt_next_seg(S, unit, s)) {
+          break;
         }
         if constexpr (TREE) {
-          stop = !load_part(s, unit, 0, kr, kfilled, find);
+          const int hi = s.R.code ? 0 : s.R.hi, cached = min(s.R.n, hi);
+          const int32_t* table = A.table + int64_t(s.b) * A.max_pages;
+          // keys that no other unit of the call reads leave the L2 first
+          const uint64_t policy =
+              s.R.mtiles > 1 ? l2_evict_normal_policy() : l2_evict_first_policy();
+          auto missing = [&](int page) {
+            if (page >= 0 && page < A.num_pages) return false;
+            S.part_bad[unit % kSegs] = 1;
+            atomicMin(&S.first_bad, s.b);
+            return true;
+          };
+          // pages are read one tile ahead, so that nothing waits for the block table
+          TilePages<TN, 1> ahead = tile_pages<D, PART, TN>(A, table, cached, s.tile0 * TN);
+          for (int t = 0; t < s.n && !stop; ++t) {
+            const TilePages<TN, 1> pages = ahead;
+            const int p0 = (s.tile0 + t) * TN;
+            if (t + 1 < s.n) ahead = tile_pages<D, PART, TN>(A, table, cached, p0 + TN);
+            stop = !tc_wait_warp(&S.empty[kr.at], kr.phase, S);
+            if (stop) break;
+            load_tile<D, PART, TN, 1>(A, k_map, pages, s.b, s.R.n, cached, hi, p0, s.h, kv,
+                                      ring0 + kr.at * kSlotBytes, &S.full[kr.at], &S.copied[kr.at],
+                                      policy, 0, missing);
+            kr.step();
+            ++kfilled;
+            if (t == 0 && leads) find();   // while the first tile is on its way
+          }
           __syncwarp();
-          if (lead && !stop) mbar_arrive(smem_addr(&S.noted[unit % kSegs]));
+          if (leads) {
+            if (lead && !stop) mbar_arrive(smem_addr(&S.noted[unit % kSegs]));
+          } else {
+            pt_taken(S, unit);
+          }
         } else {
+          auto load = [&](Ring& r, const CUtensorMap* map, int t) {
+            if (!tc_wait_warp(&S.empty[r.at], r.phase, S)) return false;
+            if (lead) {
+              const uint32_t bar = smem_addr(&S.full[r.at]);
+              mbar_arrive_expect_tx(bar, uint32_t(parts * TN * 128));
+              for (int p = 0; p < parts; ++p)
+                box_load3(ring0 + r.at * kSlotBytes + p * (TN * 128), map, p * 64, s.h,
+                          s.row0 + (s.tile0 + t) * TN, bar);
+            }
+            __syncwarp();
+            r.step();
+            return true;
+          };
           for (int t = 0; t < s.n && !stop; ++t) {
             stop = !load(kr, &k_map, t);
             kfilled += !stop;
@@ -631,27 +592,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
         if (stop) break;
       }
-      if (stop) {   // let the copies that were issued land
+      if (stop || S.abort) {   // let the copies that were issued land
         ring_land(kr, kfilled, S.full);
         ring_land(vr, vfilled, S.full);
         for (int g = 0; g < NQ; ++g)
           if (quse[g] > 0) mbar_wait_for(smem_addr(&S.qfull[g]), (quse[g] - 1) & 1, kTestWaitNs);
       }
       if constexpr (TREE) asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (TREE && warp == kValueWarp) {
-      // ------------------------------------------------------- trees: loads of V
-      Ring vr(C::kKSlots, C::kSlots - C::kKSlots, 1);
-      int filled = 0;
-      bool stop = false;
-      for (int unit = 0; !stop; ++unit) {
-        Seg s;
-        if (!pt_next_seg(S, unit, s)) break;
-        stop = !load_part(s, unit, 1, vr, filled, [] {});
-        __syncwarp();
-        pt_taken(S, unit);
-      }
-      if (S.abort) ring_land(vr, filled, S.full);
-      asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == kMmaWarp) {
       // -------------------------------------------------------------- products
       constexpr uint32_t kBase = (1u << 4) | (Bits<T>::kFmt << 7) | (Bits<T>::kFmt << 10) |
@@ -894,7 +841,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           if (dirty) {
             collect_signs<T, D, TN>(
                 reinterpret_cast<const uint32_t*>(smem_p + NQ * C::kQBytes + vr.at * kSlotBytes),
-                row_lo - p0, live ? row_hi - p0 : 0, path, row_hi - p0, signs);
+                0, TN, row_lo - p0, live ? row_hi - p0 : 0, path, row_hi - p0, signs);
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&S.collected[g]));
           }
