@@ -12,7 +12,9 @@
 // a request's keys are zero-filled, and a masked weight takes no part in the
 // product with V, so that what unused slots hold does not matter.
 #include <cmath>
+#include <cstring>
 #include <numeric>
+#include <type_traits>
 
 #include "sv_attn.cuh"
 
@@ -269,19 +271,36 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const AttnArgs A) {
 // continued, in order of position.  A warp has a row; where a unit lies in many
 // parts, a long context with few rows, the block's warps have a share of one row's
 // parts each.  Every lane finds the factor of a part, and the loads of eight
-// parts are under way at once: the time is that of a few dependent loads.  36000
-// positions, 4 heads of 256 in 38 parts each: the call 100 -> 43 us against one
-// warp that takes part after part.
+// parts are under way at once, the first before the maximum is known: the time is
+// that of a few dependent loads.  36000 positions, 4 heads of 256 in 38 parts each:
+// the call 100 -> 43 us against one warp that takes part after part.  Heads of up to
+// 128 have an instance of their own with 72 registers instead of 127: 32 requests of
+// 63 drafts, 18 units of 256 rows a KV head in two or three parts, 27 us of the call's
+// 160 -> 16 of 149.
 constexpr int kJoinThreads = 128;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinSplit = 16;  // blocks per unit
 constexpr int kJoinShare = 8;   // parts from which on the warps share a row
 constexpr int kJoinAhead = 8;
 
-template <class T, int MR>
+// Four elements of a row, at once (vec: the address allows it) or one by one.
+template <class T>
+__device__ __forceinline__ void store4(T* to, float4 x, bool vec) {
+  const T w[4] = {from_float<T>(x.x), from_float<T>(x.y), from_float<T>(x.z), from_float<T>(x.w)};
+  if (vec) {
+    using V = std::conditional_t<sizeof(T) == 4, uint4, uint2>;
+    V y;
+    memcpy(&y, w, sizeof(y));
+    *reinterpret_cast<V*>(to) = y;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) to[i] = w[i];
+}
+
+template <class T, int MR, int VECS>   // VECS: 16-byte vectors a lane
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs A) {
-  constexpr int kVecs = kMaxD / 4 / 32;   // 16-byte vectors a lane
-  __shared__ float4 s_acc[kJoinWarps][kMaxD / 4];
+  __shared__ float4 s_acc[kJoinWarps][VECS * 32];
   __shared__ float s_l[kJoinWarps];
   pdl_wait();
   const int c0 = blockIdx.x;
@@ -295,15 +314,27 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   for (int r = share ? blockIdx.y : blockIdx.y * kJoinWarps + warp; r < u.rows;
        r += share ? kJoinSplit : kJoinSplit * kJoinWarps) {
     auto slot = [&](int s) { return (int64_t(c0 + s * A.hg) * 2 + (s == 0 ? 1 : 0)) * MR + r; };
+    float4 v[kJoinAhead][VECS];
+    auto fetch = [&](int s0, int parts) {   // of parts s0 .. s0 + parts - 1, some
+#pragma unroll
+      for (int j = 0; j < kJoinAhead; ++j) {
+        if (j >= parts) break;
+        const float4* po = reinterpret_cast<const float4*>(A.part_o + slot(s0 + j) * A.D);
+#pragma unroll
+        for (int c = 0; c < VECS; ++c)
+          v[j][c] = c * 32 + lane < nvec ? po[c * 32 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    };
+    fetch(first, end - first);   // on their way while the maximum is found
     float m = -INFINITY;
     for (int s = lane; s < nseg; s += 32) m = fmax_nan(m, A.part_ml[slot(s)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float sh = m == -INFINITY ? 0.f : m;
-    float4 acc[kVecs];
+    float4 acc[VECS];
     float l = 0.f;
 #pragma unroll
-    for (int c = 0; c < kVecs; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < VECS; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s0 = first; s0 < end; s0 += 32) {
       const int parts = min(32, end - s0);
       float f = 0.f;   // 0: this part saw nothing
@@ -313,21 +344,13 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
         l = fmaf(ml.y, f, l);
       }
       for (int j0 = 0; j0 < parts; j0 += kJoinAhead) {
-        float4 v[kJoinAhead][kVecs];
-#pragma unroll
-        for (int j = 0; j < kJoinAhead; ++j) {
-          const float4* po =
-              reinterpret_cast<const float4*>(A.part_o + slot(s0 + min(j0 + j, parts - 1)) * A.D);
-#pragma unroll
-          for (int c = 0; c < kVecs; ++c)
-            v[j][c] = c * 32 + lane < nvec ? po[c * 32 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+        if (s0 + j0 > first) fetch(s0 + j0, parts - j0);
 #pragma unroll
         for (int j = 0; j < kJoinAhead; ++j) {
           const float fj = __shfl_sync(0xffffffffu, f, j0 + j);
           if (j0 + j >= parts) break;
 #pragma unroll
-          for (int c = 0; c < kVecs; ++c) {
+          for (int c = 0; c < VECS; ++c) {
             acc[c].x = fmaf(v[j][c].x, fj, acc[c].x);
             acc[c].y = fmaf(v[j][c].y, fj, acc[c].y);
             acc[c].z = fmaf(v[j][c].z, fj, acc[c].z);
@@ -340,7 +363,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (share) {   // the shares in order
 #pragma unroll
-      for (int c = 0; c < kVecs; ++c) s_acc[warp][c * 32 + lane] = acc[c];
+      for (int c = 0; c < VECS; ++c) s_acc[warp][c * 32 + lane] = acc[c];
       if (lane == 0) s_l[warp] = l;
       __syncthreads();
       if (warp == 0) {
@@ -348,7 +371,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
         for (int w = 1; w < kJoinWarps; ++w) {
           l += s_l[w];
 #pragma unroll
-          for (int c = 0; c < kVecs; ++c) {
+          for (int c = 0; c < VECS; ++c) {
             const float4 x = s_acc[w][c * 32 + lane];
             acc[c].x += x.x;
             acc[c].y += x.y;
@@ -367,13 +390,11 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
     const bool bad = !(m == m);
     const float inv = bad ? __int_as_float(0x7fc00000) : l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-    for (int c = 0; c < kVecs; ++c) {
+    for (int c = 0; c < VECS; ++c) {
       if (c * 32 + lane >= nvec) break;
-      T* to = o + (c * 32 + lane) * 4;
-      to[0] = from_float<T>(acc[c].x * inv);
-      to[1] = from_float<T>(acc[c].y * inv);
-      to[2] = from_float<T>(acc[c].z * inv);
-      to[3] = from_float<T>(acc[c].w * inv);
+      const float4 x = acc[c];
+      store4(o + (c * 32 + lane) * 4, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv),
+             A.out_vec);
     }
     if (lane == 0) A.lse[t * A.Hq + hq] = bad ? __int_as_float(0x7fc00000) : sh * kAttnLn2 + logf(l);
   }
@@ -455,8 +476,8 @@ size_t smem_weights(int D) {
   return size_t(kTn) * (D * sizeof(T) + 16) + sizeof(float) * (kMr * D + kMr + kTn);
 }
 
-template <class Kern>
-cudaError_t launch_join(Kern kernel, const AttnArgs& A, cudaStream_t s) {
+template <class T, int MR>
+cudaError_t launch_join(const AttnArgs& A, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(A.ctas), kJoinSplit);
   cfg.blockDim = dim3(kJoinThreads);
@@ -466,7 +487,8 @@ cudaError_t launch_join(Kern kernel, const AttnArgs& A, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, A);
+  return A.D <= kMaxD / 2 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<T, MR, kMaxD / 256>, A)
+                          : cudaLaunchKernelEx(&cfg, attn_join_kernel<T, MR, kMaxD / 128>, A);
 }
 
 template <class T>
@@ -486,7 +508,7 @@ cudaError_t run_attn(const AttnArgs& A, bool weights, cudaStream_t s) {
   else attn_kernel<T, false><<<A.ctas, kAtThreads, smem, s>>>(A);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_join(attn_join_kernel<T, kMr>, A, s);
+  return launch_join<T, kMr>(A, s);
 }
 
 constexpr int kCtasPerSm = 2;  // shared memory of the widest heads
@@ -507,9 +529,9 @@ bool on_tensor_cores(const AttnArgs& A, int dtype, bool weights) {
 // longer than in the other kernel.  32 requests of 2001 to 8190 positions, 8 KV heads of
 // 128 with 4 query heads each: 8 to 63 drafts (121 rows on average) 138 us with it, 174
 // without; 63 drafts (256 rows) 160 and 226; 47 (192) 151 and 230; 31 (128) 129 and 126;
-// 20 (84) 120 and 115; one request of 900 positions, 63 drafts 26 and 23.  So it takes the calls whose requests have room for more than a
-// row tile and fill more than kTwoRowTiles rows of one on average: the host knows no more
-// of the lengths.
+// 20 (84) 120 and 115; one request of 900 positions, 63 drafts 26 and 23.  So it takes
+// the calls whose requests have room for more than a row tile and fill more than
+// kTwoRowTiles rows of one on average: the host knows no more of the lengths.
 constexpr int kTwoRowTiles = 96;
 bool two_row_tiles(const AttnArgs& A) {
   auto stride = [](int64_t x) { return x > 0 && x % 8 == 0 && x < (int64_t(1) << 38); };
@@ -560,8 +582,9 @@ cudaError_t launch_attn(AttnArgs A, int dtype, bool weights, void* workspace, in
   A.split = reinterpret_cast<AttnSplit*>(w + L.split);
   A.part_ml = reinterpret_cast<float2*>(w + L.ml);
   A.part_o = reinterpret_cast<float*>(w + L.o);
+  auto aligned = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  A.out_vec = aligned(A.out);
   if (tc) {
-    auto aligned = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
     // with 2^l the first power of two that S does not exceed, the factor's excess over
     // 2^(31 + l) / S is below 1, so that of a product below p / 2^(31 + l) < 1 / S
     int l = 0;
@@ -570,17 +593,16 @@ cudaError_t launch_attn(AttnArgs A, int dtype, bool weights, void* workspace, in
     A.s_mul = uint32_t(((uint64_t(1) << A.s_shift) + A.S - 1) / uint64_t(A.S));
     A.page_rows = int32_t(A.page_bytes / A.entry_bytes);
     A.q_vec = aligned(A.q) && A.q_ts % 8 == 0 && A.q_hs % 8 == 0;
-    A.out_vec = aligned(A.out);
     if (weights) return launch_attn_weights_tc(A, dtype, s);
     const cudaError_t e = two        ? launch_tree_rows_tc(A, dtype, s)
                           : A.parent ? launch_attn_tree_tc(A, dtype, s)
                                      : launch_attn_tc(A, dtype, s);
     if (e != cudaSuccess) return e;
     if (two)
-      return dtype == SV_BF16 ? launch_join(attn_join_kernel<__nv_bfloat16, 2 * kTcRows>, A, s)
-                              : launch_join(attn_join_kernel<__half, 2 * kTcRows>, A, s);
-    return dtype == SV_BF16 ? launch_join(attn_join_kernel<__nv_bfloat16, kTcRows>, A, s)
-                            : launch_join(attn_join_kernel<__half, kTcRows>, A, s);
+      return dtype == SV_BF16 ? launch_join<__nv_bfloat16, 2 * kTcRows>(A, s)
+                              : launch_join<__half, 2 * kTcRows>(A, s);
+    return dtype == SV_BF16 ? launch_join<__nv_bfloat16, kTcRows>(A, s)
+                            : launch_join<__half, kTcRows>(A, s);
   }
   switch (dtype) {
     case SV_F32: return run_attn<float>(A, weights, s);
