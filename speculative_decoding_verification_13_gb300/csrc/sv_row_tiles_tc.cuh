@@ -43,7 +43,7 @@
 // Every wait is bounded; on expiry the CTA's status records it, its copies and
 // products land, TMEM is freed, and the rows of all its units become NaN.
 //
-// Measured, prompts, 32 + 8 heads of 128 in bf16: 16001 tokens 1.31 ms, 1590 TFLOP/s of
+// Measured, prompts, 32 + 8 heads of 128 in bf16: 16001 tokens 1.31 ms, 1600 TFLOP/s of
 // what the visible pairs take; 4 times 2048 tokens 110 us, 1250; 201 tokens 11 us.  Heads
 // of 64 985 TFLOP/s, of 256 1300 (8 to 16 thousand tokens).  Bound by a row tile's round:
 // softmax 1200 to 1300 cycles, products 1050, and about 600 from barrier to barrier,
@@ -667,10 +667,14 @@ __global__ void __launch_bounds__(kPtThreads, 1)
               if (!ok) break;
             }
             const uint32_t buf = NB == 2 ? pcount[g] & 1 : 0;
-            ok = tc_wait_two(&S.full[vr.at], vr.phase, &S.clean[vr.at], vr.phase, S) &&
+            // (tiles of K and V are waited for once, by the first row tile that has them:
+            // a wait that succeeds takes about 100 cycles; 16001 tokens 1335 -> 1317 us)
+            ok = ((g > 0 && t < s.cnt[0]) ||
+                  tc_wait_two(&S.full[vr.at], vr.phase, &S.clean[vr.at], vr.phase, S)) &&
                  tc_wait_warp(&S.pfull[g][buf], (NB == 2 ? pcount[g] >> 1 : pcount[g]) & 1, S);
             if (!ok) break;
-            fence_copied(vr.at);
+            if (g == 0 || t >= s.cnt[0]) fence_copied(vr.at);
+            else tc_fence_after();
             const uint64_t v = v_desc + vr.at * (kSlotBytes >> 4);
             const uint32_t p = tmem + (g * NB + buf) * TN;
 #pragma unroll
@@ -680,9 +684,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             mma_commit(lead, &S.pvdone[g][buf]);
             ++pcount[g];
             if (NB == 1 && t + 1 < s.cnt[g]) {
-              ok = tc_wait_warp(&S.full[kr.at], kr.phase, S);
-              if (!ok) break;
-              fence_copied(kr.at);
+              if (g == 0 || t + 1 >= s.cnt[0]) {
+                ok = tc_wait_warp(&S.full[kr.at], kr.phase, S);
+                if (!ok) break;
+                fence_copied(kr.at);
+              }
               score(g, s, t + 1);
             }
           }
