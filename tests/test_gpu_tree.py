@@ -176,6 +176,89 @@ def test_infinite_values_of_other_branches_stay_there():
         assert (out[4, :, 2] == -math.inf).all() and fin[:4, :, 2].all()
 
 
+# ------------------------------------------- many rows: two row tiles over the same keys
+def ancestors(parent, j):
+    path = [j]
+    while path[-1]:
+        path.append(parent[path[-1]])
+    return path
+
+
+@pytest.mark.parametrize("dtype,D,G", [(B16, 128, 4), (F16, 64, 8), (B16, 80, 4)])
+def test_a_torn_tree_of_many_rows_fails_its_request_alone(dtype, D, G):
+    k = [63, 50, 3, 60]
+    c = Case(15, [3000, 31, 0, 90], k, 1, G, D, 16, dtype)   # the first lies in several parts
+    want = c.oracle()
+    at = np.cumsum([0] + [x + 1 for x in k])
+    for b, j, up in ((0, 63, 63), (0, 1, -1), (3, 60, 61), (2, 2, 2)):
+        torn = list(c.parent)
+        torn[at[b] + j] = up
+        good, c.parent = c.parent, torn
+        out, lse = c.run()
+        assert sv.tree_attention_error() == (29, b, -1)
+        c.parent = good
+        rows = np.arange(at[-1])
+        bad = (rows >= at[b]) & (rows < at[b + 1])
+        assert torch.isnan(out[torch.tensor(bad)]).all() and torch.isnan(lse[torch.tensor(bad)]).all()
+        check(c, out, lse, want, rows[~bad])
+
+
+def test_other_errors_of_trees_of_many_rows():
+    k = [60, 63, 55]
+    c = Case(16, [1500, 50, 700], k, 2, 4, 128, 16, B16)
+    want = c.oracle()
+    rows = np.arange(sum(k) + 3)
+    first = rows < 61
+    for column, page in ((40, -1), (93, c.cache.shape[0]), (0, -7)):
+        keep = int(c.table[0, column])
+        c.table[0, column] = page
+        out, lse = c.run()
+        assert sv.tree_attention_error() == (27, 0, -1)
+        c.table[0, column] = keep
+        assert torch.isnan(out[:61]).all() and torch.isnan(lse[:61]).all()
+        check(c, out, lse, want, rows[~first])
+    for n in (-1, 10 ** 6):
+        c.n[1], keep = n, c.n[1]
+        out, lse = c.run()
+        assert sv.tree_attention_error() == (28, 1, -1)
+        c.n[1] = keep
+        second = (rows >= 61) & (rows < 125)
+        assert torch.isnan(out[61:125]).all()
+        check(c, out, lse, want, rows[~second])
+    for bad, code in (([60, 64, 54], 16), ([60, 63, 54], 21)):
+        c.k = bad
+        out, lse = c.run()
+        assert sv.tree_attention_error()[0] == code
+        assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.parametrize("dtype,D", [(B16, 128), (F16, 64), (F16, 112)])
+def test_values_that_are_no_numbers_among_many_rows(dtype, D):
+    n, W = 2000, 40
+    c = Case(17, [n], [63], 1, 4, D, 16, dtype)
+    parent, L = c.parent, c.layer
+    for node, col, x in ((5, 5, math.inf), (9, 6, math.nan), (20, 7, -math.inf)):
+        c.spec[0, node, L, 1, col] = x
+    at = lambda p: (int(c.table[0, p // 16]), L, 1, p % 16)   # noqa: E731  (V of position p)
+    c.cache[at(100)][9] = math.inf        # before every window
+    c.cache[at(n - 5)][10] = -math.inf    # seen from positions below n - 5 + W
+    c.cache[at(300)][11] = math.nan
+    c.cache[int(c.table[0, 18]), L, 0] = math.nan   # keys of positions 288 to 303
+    out, lse = c.run(window=W)
+    out = out.float().cpu().numpy()
+    assert torch.isfinite(lse).all()
+    for j in range(64):
+        path = ancestors(parent, j)
+        seen = path[:W]
+        here = out[j]
+        assert np.isfinite(here[:, [i for i in range(D) if i not in (5, 6, 7, 10)]]).all()
+        for node, col, test in ((5, 5, lambda x: x == math.inf), (9, 6, np.isnan),
+                                (20, 7, lambda x: x == -math.inf)):
+            assert (test if node in seen else np.isfinite)(here[:, col]).all(), (j, node)
+        sees = n - 5 > n + len(path) - 1 - W
+        assert ((here[:, 10] == -math.inf) if sees else np.isfinite(here[:, 10])).all(), j
+
+
 def test_strided_queries_in_a_graph_and_twice():
     c = Case(9, [700, 90], [40, 63], 2, 4, 128, 16, B16)
     want = c.run()
