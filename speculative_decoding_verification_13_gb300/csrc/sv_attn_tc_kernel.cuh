@@ -55,10 +55,10 @@
 // products land, TMEM is freed, and the rows of the CTA's parts become NaN.
 //
 // Measured, bf16, 8 KV heads of 128 with 4 query heads each, pages of 16: 64
-// requests of 1 to 16000 positions, one token, 81 us with the join (5.1 TB/s); 32
-// of 2001 to 8190 with up to 15 drafts 117 us (5.2 TB/s); one of 900 positions 16
+// requests of 1 to 16000 positions, one token, 77 us with the join (5.4 TB/s); 32
+// of 2001 to 8190 with up to 15 drafts 108 us (5.6 TB/s); one of 900 positions 15
 // us, all of it latency.  fp16, 16 heads of 64, 3 requests of 100001 to 131071
-// positions and 7 drafts, pages of 64: 232 us (6.6 TB/s).  What the first two lose
+// positions and 7 drafts, pages of 64: 219 us (7.0 TB/s).  What the first two lose
 // to the HBM's rate is the units' beginnings and ends: short requests have few
 // tiles for each.
 #pragma once

@@ -10,8 +10,8 @@
 // A warp has a request: a lane holds nodes `lane` and `lane + 32`, so a step of the
 // walk is two ballots and one shuffle.  Every CTA adds up the rows of the requests
 // before its own by itself (and checks the batch on the way), which takes one
-// launch instead of two.  Latency is what counts: 8 requests 2.4 us of the GPU,
-// 4096 with up to 63 drafts, 2.6 MB in and out, 5 us.
+// launch instead of two.  Latency is what counts: 8 requests 2.5 us of the GPU,
+// 4096 with up to 63 drafts, 2.6 MB in and out, 6.8 us.
 #include "sv_internal.cuh"
 
 namespace sv {
