@@ -277,6 +277,17 @@ def test_strided_queries_in_a_graph_and_twice():
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
+@pytest.mark.parametrize("dtype,D,k", [(B16, 128, [63, 40]), (F16, 64, [3, 9]), (B16, 256, [20, 5]),
+                                       (F32, 64, [30, 5])])
+def test_outputs_beside_memory_that_is_not_aligned(dtype, D, k):
+    c = Case(11, [5000, 90], k, 2, 4, D, 16, dtype)      # the first lies in several parts
+    want = c.run()
+    buf = torch.full((want[0].numel() + 2,), 7, dtype=dtype, device=DEV)
+    out = buf[1:-1].view(want[0].shape)
+    c.run(out=out, out_lse=want[1].clone())
+    assert torch.equal(out, want[0]) and buf[0] == 7 and buf[-1] == 7
+
+
 # ----------------------------------------------------------------- verification
 def verify_case(seed, k, V, agree=0.7):
     rng = random.Random(seed)
