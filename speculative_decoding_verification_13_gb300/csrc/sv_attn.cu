@@ -268,20 +268,24 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const AttnArgs A) {
 }
 
 // Joins the partials of the unit that CTA blockIdx.x began and later ones
-// continued, in order of position.  A warp has a row; where a unit lies in many
-// parts, a long context with few rows, the block's warps have a share of one row's
-// parts each.  Every lane finds the factor of a part, and the loads of eight
-// parts are under way at once, the first before the maximum is known: the time is
-// that of a few dependent loads.  36000 positions, 4 heads of 256 in 38 parts each:
-// the call 100 -> 43 us against one warp that takes part after part.  Heads of up to
-// 128 have an instance of their own with 72 registers instead of 127: 32 requests of
-// 63 drafts, 18 units of 256 rows a KV head in two or three parts, 27 us of the call's
-// 160 -> 16 of 149.
+// continued, in order of position: the time is that of a few dependent loads, a row's
+// first ones on their way before its maximum is known, and, where rows are many, of the
+// instructions around them.  A warp has a row; where a unit lies in many parts, a long
+// context with few rows, the block's warps have a share of one row's parts each (36000
+// positions, 4 heads of 256 in 38 parts each: the call 100 -> 43 us against one warp that
+// takes part after part).  In calls of more than kJoinManyRows rows a KV head and request
+// eight lanes have a row, each with the factor of one part: 32 requests of 63 drafts, 18
+// units of 256 rows a KV head in two or three parts, 149 -> 141 us, of 20 drafts 111 ->
+// 108; one request of 4 rows 14.8 -> 15.5.  Heads of up to 128 have instances of their
+// own with 72 to 80 registers instead of 126.
 constexpr int kJoinThreads = 128;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinSplit = 16;  // blocks per unit
 constexpr int kJoinShare = 8;   // parts from which on the warps share a row
-constexpr int kJoinAhead = 8;
+constexpr int kJoinAhead = 8;   // parts under way a warp
+constexpr int kJoinLanes = 8;   // of many rows, lanes a row
+constexpr int kJoinRowVecs = 8;   // and 16-byte vectors under way a lane
+constexpr int kJoinManyRows = 32;
 
 // Four elements of a row, at once (vec: the address allows it) or one by one.
 template <class T>
@@ -298,7 +302,8 @@ __device__ __forceinline__ void store4(T* to, float4 x, bool vec) {
   for (int i = 0; i < 4; ++i) to[i] = w[i];
 }
 
-template <class T, int MR, int VECS>   // VECS: 16-byte vectors a lane
+// VECS: 16-byte vectors that a lane of a warp has of a row
+template <class T, int MR, int VECS, bool MANY>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs A) {
   __shared__ float4 s_acc[kJoinWarps][VECS * 32];
   __shared__ float s_l[kJoinWarps];
@@ -308,18 +313,92 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   if (!u.valid) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nseg = (u.last - c0) / A.hg + 1, nvec = A.D / 4;
+  auto slot = [&](int s, int r) {
+    return (int64_t(c0 + s * A.hg) * 2 + (s == 0 ? 1 : 0)) * MR + r;
+  };
+  auto add = [](float4& a, float4 v, float f) {
+    a.x = fmaf(v.x, f, a.x);
+    a.y = fmaf(v.y, f, a.y);
+    a.z = fmaf(v.z, f, a.z);
+    a.w = fmaf(v.w, f, a.w);
+  };
+  // row r of the unit, of which the lane has vectors lane0 + c * lanes
+  auto finish = [&](int r, float m, float l, const float4* acc, int vecs, int lane0, int lanes) {
+    const int row = u.row0 + r;
+    const int64_t t = u.t_off + row / A.G;
+    const int hq = u.h * A.G + row % A.G;
+    T* o = static_cast<T*>(A.out) + t * A.o_ts + int64_t(hq) * A.o_hs;
+    const bool bad = !(m == m);
+    const float inv = bad ? __int_as_float(0x7fc00000) : l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int c = 0; c < vecs; ++c) {
+      if (c * lanes + lane0 >= nvec) break;
+      const float4 x = acc[c];
+      store4(o + (c * lanes + lane0) * 4,
+             make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv), A.out_vec);
+    }
+    if (lane0 == 0)
+      A.lse[t * A.Hq + hq] =
+          bad ? __int_as_float(0x7fc00000) : (m == -INFINITY ? 0.f : m) * kAttnLn2 + logf(l);
+  };
+  if (MANY && nseg <= kJoinShare) {   // eight lanes a row, each with the factor of one part
+    constexpr int kVecs = VECS * 32 / kJoinLanes, kAhead = kJoinRowVecs / kVecs;
+    const int sub = lane % kJoinLanes;
+    for (int r0 = (blockIdx.y * kJoinWarps + warp) * (32 / kJoinLanes); r0 < u.rows;
+         r0 += kJoinSplit * kJoinWarps * (32 / kJoinLanes)) {
+      const bool live = r0 + lane / kJoinLanes < u.rows;
+      const int r = live ? r0 + lane / kJoinLanes : r0;
+      float4 v[kAhead][kVecs];
+      auto fetch = [&](int s0) {   // of parts from s0 on, some
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          if (s0 + j >= nseg) break;
+          const float4* po = reinterpret_cast<const float4*>(A.part_o + slot(s0 + j, r) * A.D);
+#pragma unroll
+          for (int c = 0; c < kVecs; ++c)
+            v[j][c] = c * kJoinLanes + sub < nvec ? po[c * kJoinLanes + sub]
+                                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      };
+      fetch(0);   // on their way while the maximum is found
+      const float2 ml = sub < nseg ? A.part_ml[slot(sub, r)] : make_float2(-INFINITY, 0.f);
+      float m = ml.x;
+#pragma unroll
+      for (int o = kJoinLanes / 2; o > 0; o >>= 1)
+        m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+      // 0: this part saw nothing
+      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - (m == -INFINITY ? 0.f : m));
+      float l = sub < nseg ? ml.y * f : 0.f;
+#pragma unroll
+      for (int o = kJoinLanes / 2; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      float4 acc[kVecs];
+#pragma unroll
+      for (int c = 0; c < kVecs; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s0 = 0; s0 < nseg; s0 += kAhead) {
+        if (s0 > 0) fetch(s0);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          if (s0 + j >= nseg) break;
+          const float fj = __shfl_sync(0xffffffffu, f, s0 + j, kJoinLanes);
+#pragma unroll
+          for (int c = 0; c < kVecs; ++c) add(acc[c], v[j][c], fj);
+        }
+      }
+      if (live) finish(r, m, l, acc, kVecs, sub, kJoinLanes);
+    }
+    return;
+  }
   const bool share = nseg > kJoinShare;
   const int first = share ? nseg * warp / kJoinWarps : 0;
   const int end = share ? nseg * (warp + 1) / kJoinWarps : nseg;
   for (int r = share ? blockIdx.y : blockIdx.y * kJoinWarps + warp; r < u.rows;
        r += share ? kJoinSplit : kJoinSplit * kJoinWarps) {
-    auto slot = [&](int s) { return (int64_t(c0 + s * A.hg) * 2 + (s == 0 ? 1 : 0)) * MR + r; };
     float4 v[kJoinAhead][VECS];
     auto fetch = [&](int s0, int parts) {   // of parts s0 .. s0 + parts - 1, some
 #pragma unroll
       for (int j = 0; j < kJoinAhead; ++j) {
         if (j >= parts) break;
-        const float4* po = reinterpret_cast<const float4*>(A.part_o + slot(s0 + j) * A.D);
+        const float4* po = reinterpret_cast<const float4*>(A.part_o + slot(s0 + j, r) * A.D);
 #pragma unroll
         for (int c = 0; c < VECS; ++c)
           v[j][c] = c * 32 + lane < nvec ? po[c * 32 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -327,7 +406,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
     };
     fetch(first, end - first);   // on their way while the maximum is found
     float m = -INFINITY;
-    for (int s = lane; s < nseg; s += 32) m = fmax_nan(m, A.part_ml[slot(s)].x);
+    for (int s = lane; s < nseg; s += 32) m = fmax_nan(m, A.part_ml[slot(s, r)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float sh = m == -INFINITY ? 0.f : m;
@@ -339,7 +418,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
       const int parts = min(32, end - s0);
       float f = 0.f;   // 0: this part saw nothing
       if (lane < parts) {
-        const float2 ml = A.part_ml[slot(s0 + lane)];
+        const float2 ml = A.part_ml[slot(s0 + lane, r)];
         f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - sh);
         l = fmaf(ml.y, f, l);
       }
@@ -350,12 +429,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
           const float fj = __shfl_sync(0xffffffffu, f, j0 + j);
           if (j0 + j >= parts) break;
 #pragma unroll
-          for (int c = 0; c < VECS; ++c) {
-            acc[c].x = fmaf(v[j][c].x, fj, acc[c].x);
-            acc[c].y = fmaf(v[j][c].y, fj, acc[c].y);
-            acc[c].z = fmaf(v[j][c].z, fj, acc[c].z);
-            acc[c].w = fmaf(v[j][c].w, fj, acc[c].w);
-          }
+          for (int c = 0; c < VECS; ++c) add(acc[c], v[j][c], fj);
         }
       }
     }
@@ -383,20 +457,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
       __syncthreads();
       if (warp != 0) continue;
     }
-    const int row = u.row0 + r;
-    const int64_t t = u.t_off + row / A.G;
-    const int hq = u.h * A.G + row % A.G;
-    T* o = static_cast<T*>(A.out) + t * A.o_ts + int64_t(hq) * A.o_hs;
-    const bool bad = !(m == m);
-    const float inv = bad ? __int_as_float(0x7fc00000) : l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int c = 0; c < VECS; ++c) {
-      if (c * 32 + lane >= nvec) break;
-      const float4 x = acc[c];
-      store4(o + (c * 32 + lane) * 4, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv),
-             A.out_vec);
-    }
-    if (lane == 0) A.lse[t * A.Hq + hq] = bad ? __int_as_float(0x7fc00000) : sh * kAttnLn2 + logf(l);
+    finish(r, m, l, acc, VECS, lane, 32);
   }
 }
 
@@ -476,7 +537,10 @@ size_t smem_weights(int D) {
   return size_t(kTn) * (D * sizeof(T) + 16) + sizeof(float) * (kMr * D + kMr + kTn);
 }
 
-template <class T, int MR>
+constexpr int kCtasPerSm = 2;  // shared memory of the widest heads
+constexpr int kTcRows = 128;   // rows a unit of the tensor-core kernel
+
+template <class T, int MR, bool MANY>
 cudaError_t launch_join(const AttnArgs& A, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(A.ctas), kJoinSplit);
@@ -487,8 +551,10 @@ cudaError_t launch_join(const AttnArgs& A, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return A.D <= kMaxD / 2 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<T, MR, kMaxD / 256>, A)
-                          : cudaLaunchKernelEx(&cfg, attn_join_kernel<T, MR, kMaxD / 128>, A);
+  if constexpr (MR <= kTcRows)   // (two row tiles: heads of up to 128)
+    if (A.D > kMaxD / 2)
+      return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, MR, kMaxD / 128, MANY>, A);
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, MR, kMaxD / 256, MANY>, A);
 }
 
 template <class T>
@@ -508,11 +574,8 @@ cudaError_t run_attn(const AttnArgs& A, bool weights, cudaStream_t s) {
   else attn_kernel<T, false><<<A.ctas, kAtThreads, smem, s>>>(A);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_join<T, kMr>(A, s);
+  return launch_join<T, kMr, false>(A, s);
 }
-
-constexpr int kCtasPerSm = 2;  // shared memory of the widest heads
-constexpr int kTcRows = 128;   // rows a unit of the tensor-core kernel
 
 // Heads and types that the tensor-core kernels take; they number the cache's
 // entries in 32 bits.  Attention finds the largest score before the scaling, so
@@ -527,9 +590,9 @@ bool on_tensor_cores(const AttnArgs& A, int dtype, bool weights) {
 // same keys.  It takes heads of 64 to 128 whose queries' rows lie on 16 bytes, and groups
 // that fill a row tile.  Two row tiles read the keys once and overlap; one alone takes
 // longer than in the other kernel.  32 requests of 2001 to 8190 positions, 8 KV heads of
-// 128 with 4 query heads each: 8 to 63 drafts (121 rows on average) 138 us with it, 174
-// without; 63 drafts (256 rows) 160 and 226; 47 (192) 151 and 230; 31 (128) 129 and 126;
-// 20 (84) 120 and 115; one request of 900 positions, 63 drafts 26 and 23.  So it takes
+// 128 with 4 query heads each, before the join's last step: 8 to 63 drafts (121 rows on
+// average) 138 us with it, 174 without; 63 drafts (256 rows) 160 and 226; 47 (192) 151
+// and 230; 31 (128) 129 and 126; 20 (84) 120 and 115; one request of 900 positions, 63 drafts 26 and 23.  So it takes
 // the calls whose requests have room for more than a row tile and fill more than
 // kTwoRowTiles rows of one on average: the host knows no more of the lengths.
 constexpr int kTwoRowTiles = 96;
@@ -540,6 +603,13 @@ bool two_row_tiles(const AttnArgs& A) {
          A.Rt * A.G > int64_t(kTwoRowTiles) * A.B &&
          reinterpret_cast<uintptr_t>(A.q) % 16 == 0 && (A.Rt == 1 || stride(A.q_ts)) &&
          (A.Hq == 1 || stride(A.q_hs));
+}
+
+template <class T>
+cudaError_t join_tc(const AttnArgs& A, bool two, cudaStream_t s) {
+  if (two) return launch_join<T, 2 * kTcRows, true>(A, s);
+  return A.Rt * A.G > int64_t(kJoinManyRows) * A.B ? launch_join<T, kTcRows, true>(A, s)
+                                                   : launch_join<T, kTcRows, false>(A, s);
 }
 
 struct AttnLayout {
@@ -598,11 +668,7 @@ cudaError_t launch_attn(AttnArgs A, int dtype, bool weights, void* workspace, in
                           : A.parent ? launch_attn_tree_tc(A, dtype, s)
                                      : launch_attn_tc(A, dtype, s);
     if (e != cudaSuccess) return e;
-    if (two)
-      return dtype == SV_BF16 ? launch_join<__nv_bfloat16, 2 * kTcRows>(A, s)
-                              : launch_join<__half, 2 * kTcRows>(A, s);
-    return dtype == SV_BF16 ? launch_join<__nv_bfloat16, kTcRows>(A, s)
-                            : launch_join<__half, kTcRows>(A, s);
+    return dtype == SV_BF16 ? join_tc<__nv_bfloat16>(A, two, s) : join_tc<__half>(A, two, s);
   }
   switch (dtype) {
     case SV_F32: return run_attn<float>(A, weights, s);
