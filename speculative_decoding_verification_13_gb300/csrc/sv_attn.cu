@@ -590,9 +590,9 @@ bool on_tensor_cores(const AttnArgs& A, int dtype, bool weights) {
 // same keys.  It takes heads of 64 to 128 whose queries' rows lie on 16 bytes, and groups
 // that fill a row tile.  Two row tiles read the keys once and overlap; one alone takes
 // longer than in the other kernel.  32 requests of 2001 to 8190 positions, 8 KV heads of
-// 128 with 4 query heads each, before the join's last step: 8 to 63 drafts (121 rows on
-// average) 138 us with it, 174 without; 63 drafts (256 rows) 160 and 226; 47 (192) 151
-// and 230; 31 (128) 129 and 126; 20 (84) 120 and 115; one request of 900 positions, 63 drafts 26 and 23.  So it takes
+// 128 with 4 query heads each: 8 to 63 drafts (121 rows on average) 127 us with it, 165
+// without; 63 drafts (256 rows) 138 and 214; 47 (192) 135 and 221; 31 (128) 117 and 115;
+// 20 (84) 112 and 107; one request of 900 positions, 63 drafts 21 and 21.  So it takes
 // the calls whose requests have room for more than a row tile and fill more than
 // kTwoRowTiles rows of one on average: the host knows no more of the lengths.
 constexpr int kTwoRowTiles = 96;

@@ -52,8 +52,8 @@
 // 64: a product with V takes as long for 64 columns as for 128.  Every wait is a small
 // loop: unrolled, the kernel's 260 KB of instructions cost 5 to 9 %.
 // Trees, 32 requests of 2001 to 8190 positions with 8 to 63 drafts, the same heads: 127 us,
-// 4.9 TB/s of their entries; 8 of 30000 with 63 drafts 192 us, 5.1.  Bound by the row
-// tiles' rounds: a tile of 128 positions of both takes 3700 cycles, 2050 of them products
+// 4.9 TB/s of their entries; 8 of 30000 with 63 drafts 184 us, 5.3.  Bound by the row
+// tiles' rounds: a tile of 128 positions of both takes 3500 cycles, 2050 of them products
 // (pages of 128 instead of 16 positions, boxes 8 times as large, change nothing; entries
 // that the L2 holds, 5 %).  Loads of K and V by the same instructions, and what is rare
 // out of line, 149 -> 138 us: the tensor cores' warp waits for instructions otherwise.
