@@ -483,9 +483,6 @@ def lmhead_stats_error(stream=None, device=None):
                      stream)
 
 
-_kv_ws = {}
-
-
 def kv_commit(cache, spec, accept_len, k_per_req, kv_len, block_table, stream=None, *, path=None):
     """Append the accepted K/V entries after verification (in place).
 
@@ -495,8 +492,10 @@ def kv_commit(cache, spec, accept_len, k_per_req, kv_len, block_table, stream=No
     kv_len: [B] int32, updated in place; block_table: [B, max_pages] int32.
     path: [rows] int32, of a tree of drafts the accepted nodes as
     :func:`verify_tree_greedy` returns them (without it the drafts are a chain and
-    the entries 0 .. accept_len)."""
-    lib = load_library()
+    the entries 0 .. accept_len).
+
+    Asynchronous on ``stream`` (default: the current stream), with a workspace of that
+    stream's, of its own in a captured graph; calls may come from any thread."""
     for t, n in ((accept_len, "accept_len"), (k_per_req, "k_per_req"), (kv_len, "kv_len")):
         _check(t, n, torch.int32)
     _check(block_table, "block_table", torch.int32, ndim=2)
@@ -511,40 +510,23 @@ def kv_commit(cache, spec, accept_len, k_per_req, kv_len, block_table, stream=No
     if two != 2 or tuple(spec.shape[2:]) != (L_, 2, E_):
         raise ValueError("spec must be [B, slots, n_layers, 2, E] matching the cache")
     desc = _KvCache(cache.data_ptr(), P_, L_, S_, E_, cache.element_size())
-    dev = cache.device.index if cache.device.index is not None else torch.cuda.current_device()
+    kind, nodes = "kv_commit", ()
     if path is not None:
         _check(path, "path", torch.int32)
         if path.device != cache.device:
             raise ValueError(f"path is on {path.device}, the cache on {cache.device}")
-        need = int(lib.spec_kv_commit_path_workspace_size(B))
-    else:
-        need = int(lib.spec_kv_commit_workspace_size(B))
-    ws = _kv_ws.get(dev)
-    if ws is None or ws.numel() < need:
-        ws = _kv_ws[dev] = torch.empty(max(need, 256), dtype=torch.uint8, device=cache.device)
-    if path is not None:
-        rc = lib.spec_kv_commit_path(ctypes.byref(desc), _ptr(spec), slots, _ptr(accept_len),
-                                     _ptr(k_per_req), _ptr(path), path.numel(), _ptr(kv_len),
-                                     _ptr(block_table),
-                                     int(block_table.shape[1]) if block_table is not None else 0,
-                                     _stream_handle(stream), B, _ptr(ws), ws.numel())
-        if rc != SV_OK:
-            raise SpecVerifyError(rc, "spec_kv_commit_path")
-        return kv_len
-    rc = lib.spec_kv_commit(ctypes.byref(desc), _ptr(spec), slots, _ptr(accept_len),
-                            _ptr(k_per_req), _ptr(kv_len), _ptr(block_table),
-                            int(block_table.shape[1]) if block_table is not None else 0,
-                            _stream_handle(stream), B, _ptr(ws), ws.numel())
-    if rc != SV_OK:
-        raise SpecVerifyError(rc, "spec_kv_commit")
+        kind, nodes = "kv_commit_path", (_ptr(path), path.numel())
+    _operators._launch(kind, cache.device, stream, (B,),
+                       (ctypes.byref(desc), _ptr(spec), slots, _ptr(accept_len), _ptr(k_per_req),
+                        *nodes, _ptr(kv_len), _ptr(block_table),
+                        int(block_table.shape[1]) if block_table is not None else 0), (B,),
+                       errors="kv_commit")
     return kv_len
 
 
 def kv_commit_error(stream=None, device=None):
     """First data error of the last kv_commit on this device."""
-    d = torch.device(device or "cuda")
-    return get_error(_kv_ws[d.index if d.index is not None else torch.cuda.current_device()],
-                     stream)
+    return _operators._error("kv_commit", stream, device)
 
 
 def draft_sample(logits, k_per_req, temperature, uniforms, top_k=None, top_p=None, **kw):
@@ -653,6 +635,7 @@ def verify_noalloc(target, draft, draft_tokens, k_per_req, temperature, uniforms
     return out_accept_len, out_tokens
 
 
+from . import operators as _operators  # noqa: E402
 from .operators import (LogProbs, SV_HEAD_DIM_MAX, SV_LOGPROBS_TOP_MAX, attention,  # noqa: E402
                         attention_error, attention_weights, attention_weights_error, kv_evict,
                         kv_evict_error, logprobs, logprobs_error, logprobs_grad)

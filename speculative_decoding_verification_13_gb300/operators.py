@@ -146,14 +146,15 @@ def _call(name, dev, *args):
         raise SpecVerifyError(rc, name)
 
 
-def _launch(kind, dev, stream, size, args, batch=()):
-    """spec_<kind> on the stream, with its workspace."""
+def _launch(kind, dev, stream, size, args, batch=(), errors=None):
+    """spec_<kind> on the stream, with its workspace; errors: the kind under which its
+    status is found, its own by default."""
     handle = _stream_of(stream, dev)
     with _lock:
         ws = _scratch(kind, dev, stream, handle, size)
         _call("spec_" + kind, dev, *args, handle, *batch, ws.data_ptr(), ws.numel())
         # size[0] counts the requests or rows
-        _last[kind, dev.index] = ws if size[0] else None, handle
+        _last[errors or kind, dev.index] = ws if size[0] else None, handle
 
 
 # --------------------------------------------------------------------- checks
