@@ -271,7 +271,7 @@ __device__ __noinline__ void give_up(const AttnArgs& A, TcShared& S) {
     ring_land(at, S.loaded[kv].filled, S.full);
   } else if (warp == kScoreWarp || warp == kValueWarp) {
     uint64_t* drain = &S.drain[warp - kScoreWarp];
-    mma_commit(lane == 0, drain);
+    mma_commit(elect_one(), drain);   // of the lane that issued the products
     mbar_wait_for(smem_addr(drain), 0);
     __syncwarp();
   }
