@@ -520,7 +520,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 #pragma unroll
           for (int g = 0; g < NQ; ++g) {
             if (s.cnt[g] == 0 || stop) continue;
-            stop = !tc_wait_warp(&S.qempty[g], (quse[g]++ & 1) ^ 1, S);
+            stop = !tc_wait_warp(&S.qempty[g], (quse[g] & 1) ^ 1, S);
+            quse[g] += !stop;
             if (lead && !stop) {
               const uint32_t bar = smem_addr(&S.qfull[g]);
               mbar_arrive_expect_tx(bar, uint32_t(parts * toks * A.G * 128));
@@ -592,12 +593,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
         if (stop) break;
       }
-      if (stop || S.abort) {   // let the copies that were issued land
-        ring_land(kr, kfilled, S.full);
-        ring_land(vr, vfilled, S.full);
-        for (int g = 0; g < NQ; ++g)
-          if (quse[g] > 0) mbar_wait_for(smem_addr(&S.qfull[g]), (quse[g] - 1) & 1, kTestWaitNs);
-      }
+      // The copies that were issued land before the block ends, whatever the other warps
+      // do: one of them may give up after this one has left.
+      ring_land(kr, kfilled, S.full);
+      ring_land(vr, vfilled, S.full);
+      for (int g = 0; g < NQ; ++g)
+        if (quse[g] > 0) mbar_wait_for(smem_addr(&S.qfull[g]), (quse[g] - 1) & 1);
       if constexpr (TREE) asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == kMmaWarp) {
       // -------------------------------------------------------------- products
