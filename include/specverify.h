@@ -536,7 +536,8 @@ int spec_prompt_attention(const void* q, int64_t q_row_stride, int64_t q_head_st
  * negative length is left as it is (SV_ERR_DATA_LENGTH).  A free count below 0,
  * or above the capacity with what is given back, changes nothing for the whole
  * batch (SV_ERR_DATA_POOL, request -1).  Same conventions as spec_verify; with
- * batch 0 nothing is launched or written. */
+ * batch 0 the free list and its count are still copied to buffers of their own, and
+ * nothing is launched where they are in place. */
 size_t spec_kv_reserve_workspace_size(int32_t batch, int64_t capacity);
 
 int spec_kv_reserve(const int32_t* table, int32_t* out_table, int32_t max_pages,

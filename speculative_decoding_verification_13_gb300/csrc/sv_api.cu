@@ -618,8 +618,9 @@ int spec_kv_reserve(const int32_t* table, int32_t* out_table, int32_t max_pages,
   if (!workspace || misaligned(workspace, 256) ||
       workspace_bytes < reserve_workspace_bytes(batch, capacity))
     return SV_ERR_WORKSPACE;
-  if (batch == 0) return SV_OK;
-  if ((max_pages > 0 && (!table || !out_table)) || !held || !out_held || !length ||
+  // without requests there is a list to copy, or nothing to do
+  if (batch == 0 && free_pages == out_free && free_count == out_count) return SV_OK;
+  if ((batch > 0 && ((max_pages > 0 && (!table || !out_table)) || !held || !out_held || !length)) ||
       (capacity > 0 && (!free_pages || !out_free)) || !free_count || !out_count)
     return SV_ERR_ARG;
   const int sms = sm_count();

@@ -503,7 +503,7 @@ cudaError_t launch_reserve(const int32_t* table, int32_t* out_table, int B, int 
   Q.released = reinterpret_cast<int32_t*>(w + L.released);
   // two requests a CTA while the CTAs fit (1024 rows of 2048 columns: 12.9 us with the
   // second kernel; one CTA an SM 14.0, four 14.4)
-  const int want = (B + 1) / 2, cap = kReserveCtasPerSm * sms;
+  const int want = B > 0 ? (B + 1) / 2 : 1, cap = kReserveCtasPerSm * sms;
   const int grid = want < cap ? want : cap;
   if (cudaError_t e = launch_pdl(reserve_release_kernel, grid, s, Q)) return e;
   return launch_pdl(reserve_grant_kernel, grid, s, Q);

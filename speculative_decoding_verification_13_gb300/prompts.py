@@ -181,7 +181,8 @@ def kv_reserve(block_table, held, lengths, free_pages, free_count, page_size, *,
     request after the other, as long as there are enough for all so far: the first
     request for which there are not, and those behind it that need any, keep what
     they hold (error SV_ERR_DATA_POOL).  Without outputs everything is changed in
-    place; an output of its own gets the whole new contents.
+    place; an output of its own gets the whole new contents, also where there is
+    no request.
 
     Returns a :class:`Reservation` (block_table, held, free_pages, free_count)."""
     if not isinstance(block_table, torch.Tensor) or not block_table.is_cuda:
@@ -206,9 +207,12 @@ def kv_reserve(block_table, held, lengths, free_pages, free_count, page_size, *,
     of_ptr = _vector(got.free_pages, "out_free", i32, P, dev)
     if got.free_pages.numel() != P:
         raise ValueError(f"out_free must have {P} elements")
-    _launch("kv_reserve", dev, stream, (B, P),
+    oc_ptr = _vector(got.free_count, "out_count", i32, 1, dev)
+    # (without requests only a list or count of its own is written)
+    work = B or int((f_ptr, c_ptr) != (of_ptr, oc_ptr))
+    _launch("kv_reserve", dev, stream, (work, P),
             (t_ptr, ot_ptr, cols, h_ptr, _vector(got.held, "out_held", i32, B, dev), l_ptr, f_ptr,
-             of_ptr, P, c_ptr, _vector(got.free_count, "out_count", i32, 1, dev), page_size), (B,))
+             of_ptr, P, c_ptr, oc_ptr, page_size), (B,))
     return got
 
 
