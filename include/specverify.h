@@ -83,7 +83,8 @@ extern "C" {
 #define SV_ERR_DATA_PAGE 27         /* KV commit: a destination page missing from */
                                     /* the block table, or a negative kv_len;     */
                                     /* attention, eviction: a page of the request */
-                                    /* missing from its block table               */
+                                    /* missing from its block table; reservation: */
+                                    /* one that would be given back               */
 #define SV_ERR_DATA_LENGTH 28       /* attention, eviction: kv_len negative or    */
                                     /* longer than the block table or the scores  */
 #define SV_ERR_DATA_TREE 29         /* a node's parent that is not an earlier     */
@@ -533,9 +534,10 @@ int spec_prompt_attention(const void* q, int64_t q_row_stride, int64_t q_head_st
  *   workspace             >= spec_kv_reserve_workspace_size(batch, capacity)
  * An output may be its input (in place) or a buffer of its own, which then gets
  * the whole contents.  A request with held or need outside [0, max_pages] or a
- * negative length is left as it is (SV_ERR_DATA_LENGTH).  A free count below 0,
- * or above the capacity with what is given back, changes nothing for the whole
- * batch (SV_ERR_DATA_POOL, request -1).  Same conventions as spec_verify; with
+ * negative length is left as it is (SV_ERR_DATA_LENGTH), and so is one with an
+ * entry below 0 among those it would give back (SV_ERR_DATA_PAGE).  A free count
+ * below 0, or above the capacity with all that would be given back, changes nothing
+ * for the whole batch (SV_ERR_DATA_POOL, request -1).  Same conventions as spec_verify; with
  * batch 0 the free list and its count are still copied to buffers of their own, and
  * nothing is launched where they are in place. */
 size_t spec_kv_reserve_workspace_size(int32_t batch, int64_t capacity);

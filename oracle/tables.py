@@ -25,6 +25,10 @@ def reserve(table, held, lengths, free_pages, free_count, page_size):
     back = sum(max(0, int(held[b]) - need[b]) for b in ok)
     if n < 0 or n + back > len(free):
         return table, held, free, n, status, ERR_POOL
+    for b in ok:
+        if (table[b, need[b]:held[b]] < 0).any():   # not all of them are pages
+            status[b] = ERR_PAGE
+    ok = [b for b in ok if not status[b]]
     stack = list(free[:n])
     for b in ok:
         if held[b] > need[b]:

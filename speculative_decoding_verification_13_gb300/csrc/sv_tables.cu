@@ -59,7 +59,8 @@ struct ReserveProblem {
   int32_t vec;         // table rows and lists move 16 bytes at a time
   WsHeader* hdr;
   int32_t* status;     // [B], then one entry for the whole call
-  int2* plan;          // [B] pages held, pages needed (after checks)
+  int2* plan;          // [B] pages held, pages needed; of a request that fails -1, and
+                       // how many entries of `released` it has that are no pages to hand out
   int32_t* count;      // free pages before the call, or -1: the call fails
   int32_t* released;   // [capacity]
 };
@@ -157,13 +158,23 @@ __global__ void __launch_bounds__(kTbThreads) reserve_release_kernel(const Reser
         }
       }
     }
+    __syncthreads();
     for (int i = warp; i < rows; i += kTbWarps) {
       const int64_t row = int64_t(c0 + i) * Q.cols;
       int lo, hi;
       given_up(i, &lo, &hi);
+      bool torn = false;   // an entry is no page
       for (int c = lo + lane; c < hi; c += 32) {
-        Q.released[s_first[i] + c - lo] = Q.table[row + c];
-        if (!Q.copy_table) Q.out_table[row + c] = -1;
+        const int page = Q.table[row + c];
+        Q.released[s_first[i] + c - lo] = page;
+        torn |= page < 0;
+      }
+      torn = __any_sync(0xffffffffu, torn);
+      if (!torn && Q.copy_table) continue;
+      for (int c = lo + lane; c < hi; c += 32) Q.out_table[row + c] = torn ? Q.table[row + c] : -1;
+      if (torn && lane == 0) {
+        Q.status[c0 + i] = SV_ERR_DATA_PAGE;
+        Q.plan[c0 + i] = make_int2(-1, hi - lo);
       }
     }
     __syncthreads();
@@ -176,6 +187,19 @@ __global__ void __launch_bounds__(kTbThreads) reserve_release_kernel(const Reser
     for (int64_t i = at; i < vecs; i += step) reinterpret_cast<int4*>(Q.out_free)[i] = from[i];
     for (int64_t i = vecs * 4 + at; i < Q.capacity; i += step) Q.out_free[i] = Q.free_pages[i];
   }
+}
+
+// Where the i-th page that is handed on lies in `released`, of a call with requests
+// whose entries there are left out.
+__device__ __noinline__ int64_t released_at(const ReserveProblem& Q, int64_t i) {
+  int64_t upto = 0;   // entries of the requests so far
+  for (int b = 0; b < Q.B && upto <= i; ++b) {
+    const int2 p = Q.plan[b];
+    const int n = p.x < 0 ? p.y : max(p.x - p.y, 0);
+    if (p.x < 0) i += n;
+    upto += n;
+  }
+  return i;
 }
 
 __global__ void __launch_bounds__(kTbThreads) reserve_grant_kernel(const ReserveProblem Q) {
@@ -200,15 +224,21 @@ __global__ void __launch_bounds__(kTbThreads) reserve_grant_kernel(const Reserve
   int64_t want = 0, rel = 0, mine = 0, wants, released, before;
   for (int b = t0; b < t1; ++b) {
     const int2 p = Q.plan[b];
-    if (p.x < 0) continue;
+    if (p.x < 0) {
+      rel += int64_t(p.y) << 32;
+      continue;
+    }
     const int w = max(p.y - p.x, 0);
     want += w;
     rel += max(p.x - p.y, 0);
     if (b < r0) mine += w;
   }
   const int64_t upto = block_scan(want, &wants);
-  block_scan(rel, &released);
+  block_scan(rel, &released);   // (both counts are at most the list's entries)
   block_scan(mine, &before);
+  const bool torn = released >> 32;   // some entries of `released` are left out
+  released &= 0xffffffff;
+  auto given = [&](int64_t i) { return Q.released[torn ? released_at(Q, i) : i]; };
   const int64_t avail = n + released;
   int64_t taken = wants;
   if (wants > avail) {
@@ -246,7 +276,7 @@ __global__ void __launch_bounds__(kTbThreads) reserve_grant_kernel(const Reserve
       const int2 q = s_plan[i];
       for (int c = q.x + lane; c < q.y; c += 32) {
         const int64_t at = avail - 1 - (s_first[i] + c - q.x);
-        Q.out_table[row + c] = at >= n ? Q.released[at - n] : Q.free_pages[at];
+        Q.out_table[row + c] = at >= n ? given(at - n) : Q.free_pages[at];
         if (at < n) Q.out_free[at] = -1;   // read above, by this thread alone
       }
     }
@@ -255,7 +285,7 @@ __global__ void __launch_bounds__(kTbThreads) reserve_grant_kernel(const Reserve
   // what was released and not handed out again
   for (int64_t i = n + int64_t(blockIdx.x) * kTbThreads + tid; i < left;
        i += int64_t(gridDim.x) * kTbThreads)
-    Q.out_free[i] = Q.released[i - n];
+    Q.out_free[i] = given(i - n);
   if (blockIdx.x == 0 && tid == 0) *Q.out_count = int(left);
 }
 

@@ -180,9 +180,10 @@ def kv_reserve(block_table, held, lengths, free_pages, free_count, page_size, *,
     their place in the table; requests that need more take pages off its end, one
     request after the other, as long as there are enough for all so far: the first
     request for which there are not, and those behind it that need any, keep what
-    they hold (error SV_ERR_DATA_POOL).  Without outputs everything is changed in
-    place; an output of its own gets the whole new contents, also where there is
-    no request.
+    they hold (error SV_ERR_DATA_POOL).  A request with a missing page (below 0) among
+    those it would give back keeps them all (SV_ERR_DATA_PAGE).  Without outputs
+    everything is changed in place; an output of its own gets the whole new contents,
+    also where there is no request.
 
     Returns a :class:`Reservation` (block_table, held, free_pages, free_count)."""
     if not isinstance(block_table, torch.Tensor) or not block_table.is_cuda:
