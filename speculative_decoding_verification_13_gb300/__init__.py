@@ -496,26 +496,30 @@ def kv_commit(cache, spec, accept_len, k_per_req, kv_len, block_table, stream=No
 
     Asynchronous on ``stream`` (default: the current stream), with a workspace of that
     stream's, of its own in a captured graph; calls may come from any thread."""
-    for t, n in ((accept_len, "accept_len"), (k_per_req, "k_per_req"), (kv_len, "kv_len")):
-        _check(t, n, torch.int32)
-    _check(block_table, "block_table", torch.int32, ndim=2)
-    if block_table is not None and not block_table.is_contiguous():
-        raise ValueError("block_table must be contiguous")
     if cache.dim() != 5 or spec.dim() != 5 or not cache.is_contiguous() or not spec.is_contiguous():
         raise ValueError("cache and spec must be contiguous 5-D tensors")
     if cache.dtype != spec.dtype or cache.element_size() not in (2, 4):
         raise TypeError("cache and spec must share a 2- or 4-byte dtype")
+    if not cache.is_cuda or spec.device != cache.device:
+        raise TypeError("cache and spec must be CUDA tensors of one device")
     P_, L_, two, S_, E_ = cache.shape
     B, slots = int(spec.shape[0]), int(spec.shape[1])
     if two != 2 or tuple(spec.shape[2:]) != (L_, 2, E_):
         raise ValueError("spec must be [B, slots, n_layers, 2, E] matching the cache")
+    # the kernels read and write what B implies
+    for t, n in ((accept_len, "accept_len"), (k_per_req, "k_per_req"), (kv_len, "kv_len")):
+        _operators._vector(t, n, torch.int32, B, cache.device)
+    _check(block_table, "block_table", torch.int32, ndim=2)
+    if block_table is not None and not block_table.is_contiguous():
+        raise ValueError("block_table must be contiguous")
+    if block_table is not None and (block_table.device != cache.device or
+                                    block_table.shape[0] < B):
+        raise ValueError(f"block_table must have {B} rows on {cache.device}")
     desc = _KvCache(cache.data_ptr(), P_, L_, S_, E_, cache.element_size())
     kind, nodes = "kv_commit", ()
     if path is not None:
-        _check(path, "path", torch.int32)
-        if path.device != cache.device:
-            raise ValueError(f"path is on {path.device}, the cache on {cache.device}")
-        kind, nodes = "kv_commit_path", (_ptr(path), path.numel())
+        kind = "kv_commit_path"
+        nodes = (_operators._vector(path, "path", torch.int32, 0, cache.device), path.numel())
     _operators._launch(kind, cache.device, stream, (B,),
                        (ctypes.byref(desc), _ptr(spec), slots, _ptr(accept_len), _ptr(k_per_req),
                         *nodes, _ptr(kv_len), _ptr(block_table),
