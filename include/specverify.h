@@ -103,6 +103,7 @@ extern "C" {
 #define SV_LOGPROBS_TOP_MAX 32   /* most alternatives per row (spec_logprobs)  */
 #define SV_HEAD_DIM_MAX 256      /* largest attention head (spec_attention)    */
 #define SV_TREE_MAX_K 63         /* drafts per request where they are a tree   */
+                                 /* (and then less than 2^25 requests)         */
 
 typedef enum { SV_F32 = 0, SV_BF16 = 1, SV_F16 = 2 } sv_dtype; /* logits: the first two */
 
@@ -504,7 +505,8 @@ int spec_tree_attention(const sv_kv_cache* cache, int32_t dtype, int32_t layer, 
  * Rows of no sequence are neither read into a result nor written.  Infinite and
  * NaN keys and values reach the tokens that see them only; such a value where the
  * type holds no weight but 0 gives NaN.  Offsets that descend or leave [0, rows]
- * fail the whole batch (SV_ERR_DATA_ROWS, every output NaN).  rows < 2^31 - 256.
+ * fail the whole batch (SV_ERR_DATA_ROWS, every output NaN).  rows < 2^31 - 256,
+ * batch * kv_heads < 2^31 - 1.
  * Results do not depend on the run.  Same ownership, stream and error
  * conventions as spec_verify; with rows or batch 0 nothing is launched. */
 size_t spec_prompt_attention_workspace_size(int32_t batch);

@@ -384,12 +384,16 @@ int spec_kv_commit(const sv_kv_cache* cache, const void* spec, int32_t spec_slot
                    block_table, max_pages, stream, batch, workspace, workspace_bytes);
 }
 
+// Batches of trees whose rows a 32-bit sum holds whatever their lengths say.
+static bool tree_batch(int32_t batch) { return batch <= INT_MAX / (SV_TREE_MAX_K + 1); }
+
 int spec_kv_commit_path(const sv_kv_cache* cache, const void* spec, int32_t spec_slots,
                         const int32_t* accept_len, const int32_t* k_per_req, const int32_t* path,
                         int64_t rows, int32_t* kv_len, const int32_t* block_table,
                         int32_t max_pages, void* stream, int32_t batch, void* workspace,
                         size_t workspace_bytes) {
   if (rows < batch || rows >= INT_MAX || (batch > 0 && !path)) return SV_ERR_ARG;
+  if (!tree_batch(batch)) return SV_ERR_UNSUPPORTED;
   return kv_commit(cache, spec, spec_slots, accept_len, k_per_req, path, rows, SV_TREE_MAX_K,
                    kv_len, block_table, max_pages, stream, batch, workspace, workspace_bytes);
 }
@@ -466,6 +470,7 @@ int spec_verify_tree_greedy(const int32_t* target_argmax, const int32_t* draft_t
                             void* stream, int32_t batch, int64_t target_rows, int32_t vocab,
                             void* workspace, size_t workspace_bytes) {
   if (batch < 0 || target_rows < batch || vocab < 1 || target_rows >= INT_MAX) return SV_ERR_ARG;
+  if (!tree_batch(batch)) return SV_ERR_UNSUPPORTED;
   if (!workspace || misaligned(workspace, 256) ||
       workspace_bytes < tree_greedy_workspace_bytes(batch))
     return SV_ERR_WORKSPACE;
@@ -541,6 +546,7 @@ int spec_tree_attention(const sv_kv_cache* cache, int32_t dtype, int32_t layer, 
                          window, batch, &A))
     return rc;
   if (batch > 0 && (!spec || !parent)) return SV_ERR_ARG;
+  if (!tree_batch(batch)) return SV_ERR_UNSUPPORTED;
   A.parent = parent;
   A.max_k = SV_TREE_MAX_K;
   return attention_call(A, dtype, out, lse, stream, workspace, workspace_bytes);
@@ -563,9 +569,9 @@ int spec_prompt_attention(const void* q, int64_t q_row_stride, int64_t q_head_st
     return SV_ERR_ARG;
   if (dtype != SV_F32 && dtype != SV_BF16 && dtype != SV_F16) return SV_ERR_UNSUPPORTED;
   if (!(scale > -INFINITY && scale < INFINITY)) return SV_ERR_ARG;
-  // (tiles of rows and heads are a grid's extents)
+  // (tiles of rows and heads are a grid's extents, and a sequence has a unit a KV head)
   if (head_dim > SV_HEAD_DIM_MAX || kv_heads > 65535 ||
-      rows * (q_heads / kv_heads) / 64 + batch >= INT_MAX)
+      rows * (q_heads / kv_heads) / 64 + batch >= INT_MAX || int64_t(batch) * kv_heads >= INT_MAX)
     return SV_ERR_UNSUPPORTED;
   if (rows == 0 || batch == 0) return SV_OK;
   if (!q || !k || !v || !offsets || !out || !lse) return SV_ERR_ARG;
