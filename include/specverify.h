@@ -504,7 +504,8 @@ int spec_tree_attention(const sv_kv_cache* cache, int32_t dtype, int32_t layer, 
  *            aligned (its size depends on the current device's SM count)
  * Rows of no sequence are neither read into a result nor written.  Infinite and
  * NaN keys and values reach the tokens that see them only; such a value where the
- * type holds no weight but 0 gives NaN.  Offsets that descend or leave [0, rows]
+ * type holds no weight but 0 gives NaN.  A product of +inf makes its row NaN, a
+ * position of -inf weighs nothing.  Offsets that descend or leave [0, rows]
  * fail the whole batch (SV_ERR_DATA_ROWS, every output NaN).  rows < 2^31 - 256,
  * batch * kv_heads < 2^31 - 1.
  * Results do not depend on the run.  Same ownership, stream and error

@@ -275,8 +275,8 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const AttnArgs A) {
 // positions, 4 heads of 256 in 38 parts each: the call 100 -> 43 us against one warp that
 // takes part after part).  In calls of more than kJoinManyRows rows a KV head and request
 // eight lanes have a row, each with the factor of one part: 32 requests of 63 drafts, 18
-// units of 256 rows a KV head in two or three parts, 149 -> 141 us, of 20 drafts 111 ->
-// 108; one request of 4 rows 14.8 -> 15.5.  Heads of up to 128 have instances of their
+// units of 256 rows a KV head in two or three parts, 149 -> 141 us (138 to 140 on other
+// boxes), of 20 drafts 111 -> 108; one request of 4 rows 14.8 -> 15.5.  Heads of up to 128 have instances of their
 // own with 72 to 80 registers instead of 126.
 constexpr int kJoinThreads = 128;
 constexpr int kJoinWarps = kJoinThreads / 32;

@@ -76,6 +76,11 @@ def prompt_attention(q, k, v, offsets, *, scale=None, window=0, out=None, out_ls
     (:func:`kv_slots` gives them).  A token sees its sequence up to itself, with
     ``window`` > 0 only the last ``window`` tokens of that.
 
+    Masked keys and values may be anything.  Infinite and NaN values reach the tokens
+    that see them; where the type holds the weight of such a value as 0 (more than 2^126
+    below the token's largest, 2^31 in fp16) the result is NaN.  A product of +inf makes
+    its row NaN, a position of -inf weighs nothing.
+
     Returns ``(out [rows, q_heads, D], lse [rows, q_heads] float32)``; rows of no
     sequence are left as they were.  They carry no autograd history."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
